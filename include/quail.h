@@ -136,6 +136,111 @@ void quail_trie_free(quail_trie* trie);
  * allocation and copy out of a later call. */
 quail_status quail_trie_upload(quail_trie* trie, quail_stream_t stream);
 
+/* ------------------------------------------------------------ document cache
+ * The paged K/V cache the classify calls read ("a fixed pool of KV pages in
+ * HBM", Quail intro, sec. 3.2.3; "fuse small operations", "Building an
+ * Ultra-High Throughput AI-SQL Engine", sec. 3.2.4): writing it, reading it
+ * back, and attention over it for sequences that share their first tokens. A
+ * bf16 cache filled by quail_cache_append is what quail_paged_kv describes
+ * (same pools, same page table).
+ *
+ * dtype QUAIL_DTYPE_BF16: k_pool, v_pool bf16 [num_pages, n_kv_heads, 16, 128];
+ *                k_scale, v_scale NULL.
+ * dtype QUAIL_DTYPE_E4M3: the pools hold e4m3 codes in one byte, and k_scale,
+ *                v_scale [num_pages, n_kv_heads, 16] one byte e (1..254) per
+ *                (page, head, slot): element = code * 2^(e - 127), a bf16 value
+ *                exactly.
+ * page_table:    device int32 [num_seqs, max_pages]; entry (b, p) = physical
+ *                page of positions [16p, 16p + 16) of sequence b. */
+typedef enum { QUAIL_DTYPE_BF16 = 0, QUAIL_DTYPE_F32 = 1, QUAIL_DTYPE_E4M3 = 2 } quail_dtype;
+
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  void* k_scale;
+  void* v_scale;
+  int32_t dtype;      /* QUAIL_DTYPE_BF16 or QUAIL_DTYPE_E4M3 */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* must be 128 */
+  int32_t num_pages;
+  int32_t page_size;  /* must be 16 */
+  const int32_t* page_table;
+  int32_t num_seqs;
+  int32_t max_pages;
+} quail_cache_desc;
+
+/* Normalises, rotates and stores the projections of num_tokens tokens.
+ * Row t of qkv (QUAIL_DTYPE_BF16 or QUAIL_DTYPE_F32, row stride ld elements, a
+ * multiple of 8) holds n_q_heads query heads, then n_kv_heads key heads, then
+ * n_kv_heads value heads, 128 wide each (n_q_heads may be 0).
+ *   q, k: x / sqrt(mean(x^2) + rms_eps) * gain when the gain (bf16 [128]) is not
+ *         NULL; then rotate-half RoPE at position token_pos[t] when rope_theta is
+ *         not 0 (pair (j, j + 64) by the angle pos * rope_theta^(-2j/128)); all in
+ *         fp32, rounded once.
+ *   q_out: bf16 [num_tokens, n_q_heads, 128], or NULL.
+ *   k, v: to slot token_pos[t] % 16 of page page_table[token_seq[t]][token_pos[t] / 16].
+ *         In an e4m3 cache each (token, head) row gets the smallest 2^e, at least
+ *         2^-100, with max |x| <= 448 * 2^e over its finite elements, and
+ *         x / 2^e rounded to the nearest code (ties to even); an infinity
+ *         saturates, a NaN stays one.
+ * token_seq[t] < 0 marks a padding token: nothing of it is written. A
+ * (sequence, position) pair may occur once per call, and a page that two
+ * sequences share is written through one of them. A sequence, position or
+ * page id out of range sets QUAIL_ERR_DEVICE_BOUNDS and drops that token. */
+quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
+                                int32_t num_tokens, int32_t n_q_heads, const int32_t* token_seq,
+                                const int32_t* token_pos, const void* q_norm, const void* k_norm, float rms_eps,
+                                float rope_theta, void* q_out, quail_stream_t stream);
+
+/* Reads the cached K and V of num_tokens (sequence, position) pairs, in any
+ * order and any number of times each, as bf16 [num_tokens, n_kv_heads, 128]:
+ * exactly what an e4m3 cache stands for. k_out or v_out may be NULL.
+ * token_seq[t] < 0: row t is left as it was. Errors as quail_cache_append. */
+quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* token_seq, const int32_t* token_pos,
+                              int32_t num_tokens, void* k_out, void* v_out, quail_stream_t stream);
+
+/* Bytes of device workspace quail_attention_shared needs for these bounds
+ * (256-byte aligned base required); 0 on invalid arguments. */
+size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
+                                      int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len);
+
+/* GQA attention over the cache for num_seqs sequences whose first prefix_len
+ * positions are the same pages (the instructions every document's prompt
+ * starts with): o = softmax(scale q K^T) V, lse = log sum exp(scale q K^T).
+ * Where a sequence's own queries fill only a small part of a tile, the shared
+ * keys are read and multiplied once for the whole batch, and the two parts
+ * join by log-sum-exp.
+ *   prefix_pages: device int32 [prefix_len / 16], pages of positions
+ *                 [0, prefix_len); prefix_len a multiple of 16, 0: nothing is
+ *                 shared (NULL then). Positions from prefix_len on come from
+ *                 page_table; its first prefix_len / 16 columns are not read.
+ *   seq_len:      device int32 [num_seqs], keys of each sequence, the shared ones
+ *                 included, at most max_seq_len; 0: no keys at all (its rows get
+ *                 o = 0, lse = -inf), else at least prefix_len (+ the sequence's
+ *                 queries when causal).
+ *   q, out:       device bf16 [total_q, n_q_heads, 128]; q as quail_cache_append
+ *                 writes it. Query head h reads KV head h / (n_q_heads / n_kv_heads).
+ *   q_offsets:    device int32 [num_seqs + 1]: sequence b's queries are rows
+ *                 [q_offsets[b], q_offsets[b+1]), at most max_q_len of them; NULL:
+ *                 one query per sequence (total_q = num_seqs, max_q_len = 1).
+ *                 Rows outside every range are left as they were.
+ *   causal:       1: the queries are the sequence's last tokens, cached already,
+ *                 and each sees the keys up to its own position; 0: every query
+ *                 sees every key.
+ *   scale:        0: 1/sqrt(128)
+ *   lse:          device fp32 [total_q, n_q_heads] (natural logarithm), or NULL.
+ * Sums and softmax statistics are fp32; the weights are rounded to bf16 (fp16
+ * over e4m3 keys read directly) for the product with V. Keys past a sequence's
+ * end are never used, whatever their slots hold. Bounds that only the device
+ * can see set QUAIL_ERR_DEVICE_BOUNDS and void that sequence's rows (all rows,
+ * for a prefix page). Nothing in the workspace needs to start at zero; calls
+ * that may run at the same time need one each. */
+quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
+                                    const int32_t* seq_len, int32_t max_seq_len, const void* q,
+                                    const int32_t* q_offsets, int32_t total_q, int32_t max_q_len, int32_t n_q_heads,
+                                    int32_t causal, float scale, void* workspace, size_t workspace_bytes, void* out,
+                                    float* lse, quail_stream_t stream);
+
 /* ------------------------------------------------------------------ model
  * One decoder layer's attention block plus the output head, as used at the
  * answer positions: x = E[tok]; x^ = RMSNorm(x)*in_norm; q,k,v = x^ W^T;

@@ -24,6 +24,10 @@ Entry points (same names as the C ABI, without the quail_ prefix):
   Shortlist(...)                 -> quail_shortlist_create / quail_shortlist_groups / quail_shortlist_free
   workspace_size_shortlist(...), classify_trie_tree_shortlist(...)
                                  -> quail_workspace_size_shortlist / quail_classify_trie_tree_shortlist
+  KVCache(...), cache_append(...), cache_read(...)
+                                 -> quail_cache_append / quail_cache_read
+  workspace_size_attention(...), attention_shared(...)
+                                 -> quail_workspace_size_attention / quail_attention_shared
 """
 from __future__ import annotations
 
@@ -114,6 +118,13 @@ class PagedKV(ctypes.Structure):
                 ("doc_len", ctypes.c_void_p), ("max_doc_len", ctypes.c_int32)]
 
 
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 class TrieCSR(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_int32), ("num_labels", ctypes.c_int32), ("n_eval", ctypes.c_int32),
                 ("n_eval_children", ctypes.c_int32), ("max_depth", ctypes.c_int32),
@@ -172,6 +183,19 @@ _SIGNATURES = {
                                                           ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
                                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                           ctypes.c_void_p, ctypes.c_void_p]),
+    "quail_cache_append": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_float,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    "quail_cache_read": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "quail_workspace_size_attention": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc), ctypes.c_int32, ctypes.c_int32,
+                                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "quail_attention_shared": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_void_p, ctypes.c_int32,
+                                              ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_void_p]),
     "quail_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "quail_set_stage_events": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
     "quail_launch_count": (ctypes.c_int32, []),
@@ -526,3 +550,114 @@ def classify_trie_tree_ml(model: ModelML, kv: KVML, trie: Trie, num_docs: int, w
         ctypes.byref(model.desc), ctypes.byref(kv.desc), trie.handle, int(num_docs), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(label_logscore), _ptr(label_prob), _ptr(label_argmax),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ document cache
+DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
+
+
+def _need(ok: bool, message: str) -> None:
+    if not ok:
+        raise QuailError(-1, message)
+
+
+def _is(t, dtype, shape=None) -> bool:
+    return t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)
+
+
+class KVCache:
+    """quail_cache_desc over device tensors: pools [P, H_kv, 16, 128] (bf16, or e4m3
+    codes as float8_e4m3fn or uint8 with uint8 scales [P, H_kv, 16]) and the
+    page_table [num_seqs, max_pages] int32. A bf16 cache is read by the classify
+    calls as KV(k_pool, v_pool, page_table, seq_len, max_len)."""
+
+    def __init__(self, k_pool, v_pool, page_table, k_scale=None, v_scale=None):
+        import torch
+        shape = k_pool.shape
+        _need(len(shape) == 4 and shape[2] == 16 and shape[3] == 128, "pools must be [pages, kv heads, 16, 128]")
+        codes = k_pool.dtype in (torch.uint8, torch.float8_e4m3fn)
+        _need(codes or k_pool.dtype is torch.bfloat16, "pools must be bfloat16, float8_e4m3fn or uint8")
+        _need(_is(k_pool, k_pool.dtype) and _is(v_pool, k_pool.dtype, shape), "pools must be contiguous and alike")
+        _need((k_scale is not None and v_scale is not None) if codes else (k_scale is None and v_scale is None),
+              "an e4m3 cache has two scale tensors, a bf16 cache none")
+        for t in (k_scale, v_scale):
+            _need(t is None or _is(t, torch.uint8, shape[:3]), "scales must be contiguous uint8 [pages, kv heads, 16]")
+        _need(page_table.dim() == 2 and _is(page_table, torch.int32), "page_table must be contiguous int32 [seqs, pages]")
+        for t in (v_pool, k_scale, v_scale, page_table):
+            _need(t is None or t.device == k_pool.device, "the cache's tensors must share one device")
+        self.tensors = (k_pool, v_pool, page_table, k_scale, v_scale)
+        self.n_kv_heads = int(shape[1])
+        self.num_seqs = int(page_table.shape[0])
+        self.device = k_pool.device
+        self.desc = CacheDesc(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                              DTYPE_E4M3 if codes else DTYPE_BF16, self.n_kv_heads, 128, int(shape[0]), 16,
+                              _ptr(page_table), self.num_seqs, int(page_table.shape[1]))
+
+
+def cache_append(cache: KVCache, qkv, n_q_heads: int, token_seq, token_pos, q_out=None, q_norm=None, k_norm=None,
+                 rms_eps: float = 1e-6, rope_theta: float = 0.0, stream=None) -> None:
+    """qkv [T, >= (n_q_heads + 2 H_kv) * 128] bf16 or fp32 (rows contiguous, any row stride that is a
+    multiple of 8): the normed, rotated K and the V of token t go to position token_pos[t] of sequence
+    token_seq[t] (negative: padding), its q to q_out [T, n_q_heads, 128] bf16."""
+    import torch
+    n = qkv.shape[0]
+    _need(qkv.dim() == 2 and qkv.stride(1) == 1 and
+          qkv.shape[1] >= (n_q_heads + 2 * cache.n_kv_heads) * 128, "qkv must be rows of (hq + 2 hkv) * 128 elements")
+    _need(qkv.dtype is torch.bfloat16 or qkv.dtype is torch.float32, "qkv must be bfloat16 or float32")
+    _need(_is(token_seq, torch.int32, (n,)) and _is(token_pos, torch.int32, (n,)), "token_seq, token_pos: int32 [tokens]")
+    _need(q_out is None or _is(q_out, torch.bfloat16, (n, n_q_heads, 128)), "q_out must be bfloat16 [tokens, hq, 128]")
+    for g in (q_norm, k_norm):
+        _need(g is None or _is(g, torch.bfloat16, (128,)), "gains must be bfloat16 [128]")
+    for t in (qkv, token_seq, token_pos, q_out, q_norm, k_norm):
+        _need(t is None or t.device == cache.device, "every tensor must be on the cache's device")
+    _check(lib().quail_cache_append(
+        ctypes.byref(cache.desc), _ptr(qkv), DTYPE_F32 if qkv.dtype is torch.float32 else DTYPE_BF16,
+        qkv.stride(0) if n > 1 else max(qkv.stride(0), qkv.shape[1]), n, n_q_heads, _ptr(token_seq), _ptr(token_pos),
+        _ptr(q_norm), _ptr(k_norm), rms_eps, rope_theta, _ptr(q_out), _stream(stream)))
+
+
+def cache_read(cache: KVCache, token_seq, token_pos, k_out, v_out, stream=None) -> None:
+    """k_out, v_out [T, H_kv, 128] bf16 (either may be None): the cached rows of (token_seq[t], token_pos[t])."""
+    import torch
+    n = token_seq.shape[0]
+    _need(_is(token_seq, torch.int32, (n,)) and _is(token_pos, torch.int32, (n,)), "token_seq, token_pos: int32 [tokens]")
+    for t in (k_out, v_out):
+        _need(t is None or _is(t, torch.bfloat16, (n, cache.n_kv_heads, 128)),
+              "outputs must be bfloat16 [tokens, kv heads, 128]")
+    for t in (token_seq, token_pos, k_out, v_out):
+        _need(t is None or t.device == cache.device, "every tensor must be on the cache's device")
+    _check(lib().quail_cache_read(ctypes.byref(cache.desc), _ptr(token_seq), _ptr(token_pos), n, _ptr(k_out),
+                                  _ptr(v_out), _stream(stream)))
+
+
+def workspace_size_attention(cache: KVCache, n_q_heads: int, total_q: int, max_q_len: int, max_seq_len: int,
+                             prefix_len: int = 0) -> int:
+    n = lib().quail_workspace_size_attention(ctypes.byref(cache.desc), int(n_q_heads), int(total_q), int(max_q_len),
+                                             int(max_seq_len), int(prefix_len))
+    if n == 0:
+        _check(-1)
+    return int(n)
+
+
+def attention_shared(cache: KVCache, q, q_offsets, seq_len, max_q_len: int, max_seq_len: int, prefix_pages, out,
+                     workspace, lse=None, causal: bool = True, scale: float | None = None, stream=None) -> None:
+    """q, out [total_q, hq, 128] bf16; q_offsets int32 [num_seqs + 1] or None (one query per sequence);
+    seq_len int32 [num_seqs], the shared keys included; prefix_pages int32 [prefix_len / 16] or None;
+    lse fp32 [total_q, hq] or None."""
+    import torch
+    n, hq, B = q.shape[0], q.shape[1], cache.num_seqs
+    _need(_is(q, torch.bfloat16, (n, hq, 128)) and _is(out, torch.bfloat16, (n, hq, 128)),
+          "q and out must be contiguous bfloat16 [total_q, hq, 128]")
+    _need(q_offsets is None or _is(q_offsets, torch.int32, (B + 1,)), "q_offsets must be int32 [num_seqs + 1]")
+    _need(_is(seq_len, torch.int32, (B,)), "seq_len must be int32 [num_seqs]")
+    _need(prefix_pages is None or (prefix_pages.dim() == 1 and _is(prefix_pages, torch.int32)),
+          "prefix_pages must be int32 [prefix_len / 16]")
+    _need(lse is None or _is(lse, torch.float32, (n, hq)), "lse must be float32 [total_q, hq]")
+    _need(workspace.is_contiguous(), "workspace must be contiguous")
+    for t in (q, out, q_offsets, seq_len, prefix_pages, lse, workspace):
+        _need(t is None or t.device == cache.device, "every tensor must be on the cache's device")
+    _check(lib().quail_attention_shared(
+        ctypes.byref(cache.desc), _ptr(prefix_pages), 0 if prefix_pages is None else prefix_pages.shape[0] * 16,
+        _ptr(seq_len), int(max_seq_len), _ptr(q), _ptr(q_offsets), n, int(max_q_len), hq, 1 if causal else 0,
+        0.0 if scale is None else float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(out), _ptr(lse), _stream(stream)))

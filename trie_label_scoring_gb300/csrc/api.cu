@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "cache.h"
 #include "kernels.h"
 #include "umma_gemm.cuh"
 #include "quail_internal.h"
@@ -814,6 +815,84 @@ size_t plan_shortlist(uint8_t* base, const quail_model_desc* m, const quail_shor
   x.am1 = c.take<int>(N);
   if (out) *out = x;
   return shared + c.off + 256;
+}
+
+// ------------------------------------------------------------------ document cache
+// A device pointer of the current device (or NULL where `opt`).
+quail_status check_device_ptr(const void* p, const char* name, int dev, bool opt = false) {
+  if (p == nullptr) return opt ? QUAIL_OK : fail(QUAIL_ERR_INVALID_ARG, "%s is null", name);
+  if (!aligned16(p)) return fail(QUAIL_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  cudaPointerAttributes at;
+  CUDA_TRY(cudaPointerGetAttributes(&at, p));
+  if (at.type == cudaMemoryTypeDevice && at.device != dev)
+    return fail(QUAIL_ERR_INVALID_ARG, "%s lies on device %d, the current device is %d", name, at.device, dev);
+  if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
+    return fail(QUAIL_ERR_INVALID_ARG, "%s is not device memory", name);
+  return QUAIL_OK;
+}
+
+quail_status check_cache_shape(const quail_cache_desc* c) {
+  if (c == nullptr) return fail(QUAIL_ERR_INVALID_ARG, "cache is null");
+  if (c->head_dim != 128) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "head_dim must be 128 (got %d)", c->head_dim);
+  if (c->page_size != 16) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "page_size must be 16 (got %d)", c->page_size);
+  if (c->dtype != QUAIL_DTYPE_BF16 && c->dtype != QUAIL_DTYPE_E4M3)
+    return fail(QUAIL_ERR_INVALID_ARG, "cache dtype must be bf16 or e4m3");
+  if (c->n_kv_heads <= 0 || c->n_kv_heads > 128)
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "n_kv_heads must be in [1, 128]");
+  if (c->num_pages <= 0 || c->num_seqs < 0 || c->max_pages <= 0 || c->max_pages > (1 << 27))
+    return fail(QUAIL_ERR_INVALID_ARG, "bad num_pages, num_seqs or max_pages");
+  if (static_cast<int64_t>(c->num_pages) * c->n_kv_heads * 16 > (int64_t(1) << 31) - 1)
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "cache too large for 32-bit row coordinates");
+  if (c->num_seqs > 65535) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most 65535 sequences per call");
+  return QUAIL_OK;
+}
+
+// Host checks of the cache; fills the kernels' view of it.
+quail_status open_cache(const quail_cache_desc* c, DeviceState** ds, int* dev, CacheView* v) {
+  quail_status s = check_cache_shape(c);
+  if (s != QUAIL_OK) return s;
+  const bool codes = c->dtype == QUAIL_DTYPE_E4M3;
+  if (c->k_pool == nullptr || c->v_pool == nullptr || c->page_table == nullptr ||
+      (codes && (c->k_scale == nullptr || c->v_scale == nullptr)))
+    return fail(QUAIL_ERR_INVALID_ARG, "a cache pointer is null");
+  if (!codes && (c->k_scale != nullptr || c->v_scale != nullptr))
+    return fail(QUAIL_ERR_INVALID_ARG, "a bf16 cache has no scales");
+  for (const void* p : {c->k_pool, c->v_pool, c->k_scale, c->v_scale})
+    if (!aligned16(p)) return fail(QUAIL_ERR_INVALID_ARG, "cache pools must be 16-byte aligned");
+  s = device_state(ds);
+  if (s != QUAIL_OK) return s;
+  CUDA_TRY(cudaGetDevice(dev));
+  s = check_device_ptr(c->k_pool, "k_pool", *dev);
+  if (s != QUAIL_OK) return s;
+  *v = CacheView{c->k_pool,
+                 c->v_pool,
+                 static_cast<uint8_t*>(c->k_scale),
+                 static_cast<uint8_t*>(c->v_scale),
+                 codes,
+                 c->n_kv_heads,
+                 c->num_pages,
+                 c->num_seqs,
+                 c->max_pages,
+                 c->page_table,
+                 (*ds)->err};
+  return QUAIL_OK;
+}
+
+quail_status check_attention_shape(const quail_cache_desc* c, int n_q_heads, int total_q, int max_q_len,
+                                   int max_seq_len, int prefix_len) {
+  quail_status s = check_cache_shape(c);
+  if (s != QUAIL_OK) return s;
+  if (n_q_heads <= 0 || n_q_heads > 128 || n_q_heads % c->n_kv_heads != 0)
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "n_q_heads must be a multiple of n_kv_heads, at most 128");
+  if (total_q < 0 || max_q_len < 1) return fail(QUAIL_ERR_INVALID_ARG, "bad total_q or max_q_len");
+  if (static_cast<int64_t>(total_q) * n_q_heads > (int64_t(1) << 30))
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "too many query rows");
+  if (prefix_len < 0 || prefix_len % 16 != 0)
+    return fail(QUAIL_ERR_INVALID_ARG, "prefix_len must be a multiple of 16 (got %d)", prefix_len);
+  if (max_seq_len < 1 || max_seq_len < prefix_len ||
+      static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(c->max_pages) * 16)
+    return fail(QUAIL_ERR_INVALID_ARG, "max_seq_len must cover prefix_len and fit max_pages");
+  return QUAIL_OK;
 }
 
 }  // namespace
@@ -1677,6 +1756,124 @@ quail_status quail_classify_trie_tree_shortlist(const quail_model_desc* model, c
   if (group_selected != nullptr)
     CUDA_TRY(cudaMemcpyAsync(group_selected, x.sel, static_cast<size_t>(num_docs) * B * sizeof(int),
                              cudaMemcpyDeviceToDevice, st));
+  return QUAIL_OK;
+}
+
+quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
+                                int32_t num_tokens, int32_t n_q_heads, const int32_t* token_seq,
+                                const int32_t* token_pos, const void* q_norm, const void* k_norm, float rms_eps,
+                                float rope_theta, void* q_out, quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_cache_shape(cache);
+  if (s != QUAIL_OK) return s;
+  if (qkv_dtype != QUAIL_DTYPE_BF16 && qkv_dtype != QUAIL_DTYPE_F32)
+    return fail(QUAIL_ERR_INVALID_ARG, "qkv dtype must be bf16 or f32");
+  if (num_tokens < 0) return fail(QUAIL_ERR_INVALID_ARG, "num_tokens < 0");
+  if (n_q_heads < 0 || n_q_heads > 128) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "n_q_heads must be in [0, 128]");
+  if (ld % 8 != 0 || ld < static_cast<int64_t>(n_q_heads + 2 * cache->n_kv_heads) * 128)
+    return fail(QUAIL_ERR_INVALID_ARG, "ld must be a multiple of 8 that holds every head");
+  if (!(rms_eps > 0.f) && (q_norm != nullptr || k_norm != nullptr))
+    return fail(QUAIL_ERR_INVALID_ARG, "rms_eps must be positive");
+  if (rope_theta != 0.f && !(rope_theta > 1.f && rope_theta < INFINITY))
+    return fail(QUAIL_ERR_INVALID_ARG, "rope_theta must be 0 or above 1");
+  if (cache->max_pages > (1 << 20) && rope_theta != 0.f)
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "rotation is exact for positions below 2^24 only");
+  if (num_tokens == 0) return QUAIL_OK;
+  if (qkv == nullptr || token_seq == nullptr || token_pos == nullptr)
+    return fail(QUAIL_ERR_INVALID_ARG, "a token pointer is null");
+  for (const void* p : {qkv, q_norm, k_norm, static_cast<const void*>(q_out)})
+    if (!aligned16(p)) return fail(QUAIL_ERR_INVALID_ARG, "qkv, the gains and q_out must be 16-byte aligned");
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  AppendArgs a{};
+  s = open_cache(cache, &ds, &dev, &a.c);
+  if (s != QUAIL_OK) return s;
+  s = check_device_ptr(qkv, "qkv", dev);
+  if (s != QUAIL_OK) return s;
+  a.qkv = qkv;
+  a.ld = ld;
+  a.num_tokens = num_tokens;
+  a.hq = n_q_heads;
+  a.seq = token_seq;
+  a.pos = token_pos;
+  a.gq = static_cast<const bf16*>(q_norm);
+  a.gk = static_cast<const bf16*>(k_norm);
+  a.eps = rms_eps;
+  a.theta = rope_theta;
+  a.q_out = static_cast<bf16*>(q_out);
+  CUDA_TRY(launch_cache_append(a, qkv_dtype == QUAIL_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)));
+  return QUAIL_OK;
+}
+
+quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* token_seq, const int32_t* token_pos,
+                              int32_t num_tokens, void* k_out, void* v_out, quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_cache_shape(cache);
+  if (s != QUAIL_OK) return s;
+  if (num_tokens < 0) return fail(QUAIL_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_tokens == 0) return QUAIL_OK;
+  if (token_seq == nullptr || token_pos == nullptr) return fail(QUAIL_ERR_INVALID_ARG, "a token pointer is null");
+  if (k_out == nullptr && v_out == nullptr) return fail(QUAIL_ERR_INVALID_ARG, "k_out and v_out are null");
+  if (!aligned16(k_out) || !aligned16(v_out))
+    return fail(QUAIL_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  CacheView v;
+  s = open_cache(cache, &ds, &dev, &v);
+  if (s != QUAIL_OK) return s;
+  s = check_device_ptr(k_out != nullptr ? k_out : v_out, "the output", dev);
+  if (s != QUAIL_OK) return s;
+  CUDA_TRY(launch_cache_read(v, token_seq, token_pos, num_tokens, static_cast<bf16*>(k_out), static_cast<bf16*>(v_out),
+                             reinterpret_cast<cudaStream_t>(stream)));
+  return QUAIL_OK;
+}
+
+size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
+                                      int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
+  if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
+  return 256;
+}
+
+quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
+                                    const int32_t* seq_len, int32_t max_seq_len, const void* q,
+                                    const int32_t* q_offsets, int32_t total_q, int32_t max_q_len, int32_t n_q_heads,
+                                    int32_t causal, float scale, void* workspace, size_t workspace_bytes, void* out,
+                                    float* lse, quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len);
+  if (s != QUAIL_OK) return s;
+  if (!(scale >= 0.f && scale < INFINITY)) return fail(QUAIL_ERR_INVALID_ARG, "scale must be finite and not negative");
+  if (causal != 0 && causal != 1) return fail(QUAIL_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (q_offsets == nullptr && (total_q != cache->num_seqs || max_q_len != 1))
+    return fail(QUAIL_ERR_INVALID_ARG, "without q_offsets there is one query per sequence");
+  if (total_q == 0 || cache->num_seqs == 0) return QUAIL_OK;
+  if (q == nullptr || out == nullptr || seq_len == nullptr || (prefix_len > 0 && prefix_pages == nullptr))
+    return fail(QUAIL_ERR_INVALID_ARG, "q, out, seq_len or prefix_pages is null");
+  if (!aligned16(q) || !aligned16(out)) return fail(QUAIL_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  s = check_workspace(workspace, workspace_bytes,
+                      quail_workspace_size_attention(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len));
+  if (s != QUAIL_OK) return s;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  SharedAttnArgs a{};
+  s = open_cache(cache, &ds, &dev, &a.c);
+  if (s != QUAIL_OK) return s;
+  s = check_device_ptr(q, "q", dev);
+  if (s != QUAIL_OK) return s;
+  a.hq = n_q_heads;
+  a.q = static_cast<const bf16*>(q);
+  a.q_offsets = q_offsets;
+  a.total_q = total_q;
+  a.max_q = std::min(max_q_len, total_q);
+  a.seq_len = seq_len;
+  a.max_seq_len = max_seq_len;
+  a.prefix_pages = prefix_pages;
+  a.prefix_len = prefix_len;
+  a.causal = causal;
+  a.scale_log2 = (scale > 0.f ? scale : 0.08838834764831845f) * 1.4426950408889634f;
+  a.out = static_cast<bf16*>(out);
+  a.lse = lse;
+  CUDA_TRY(launch_attention_simple(a, reinterpret_cast<cudaStream_t>(stream)));
   return QUAIL_OK;
 }
 
