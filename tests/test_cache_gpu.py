@@ -522,7 +522,7 @@ def test_python_checks_of_tensors():
     pool = Pool("bf16", 2, [64, 64])
     q = torch.zeros((2, 8, D), dtype=torch.bfloat16, device="cuda")
     L = torch.tensor([3, 4], dtype=torch.int32, device="cuda")
-    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(Q.workspace_size_attention(pool.cache, 8, 2, 1, 64), dtype=torch.uint8, device="cuda")
     good = dict(cache=pool.cache, q=q, q_offsets=None, seq_len=L, max_q_len=1, max_seq_len=64, prefix_pages=None,
                 out=torch.empty_like(q), workspace=ws)
     Q.attention_shared(**good)

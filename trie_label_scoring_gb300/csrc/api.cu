@@ -103,6 +103,19 @@ quail_status encode_2d_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint
   return QUAIL_OK;
 }
 
+// e4m3 codes [rows, 128] (one byte each), boxes of 128 x box_rows, 128-byte swizzle.
+quail_status encode_2d_codes(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
+  cuuint64_t dims[2] = {128, rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QUAIL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return QUAIL_OK;
+}
+
 // ------------------------------------------------------------------ profiling hook
 std::mutex g_ev_mu;
 std::vector<cudaEvent_t> g_events;
@@ -895,6 +908,33 @@ quail_status check_attention_shape(const quail_cache_desc* c, int n_q_heads, int
   return QUAIL_OK;
 }
 
+// How one attention call is carried out, and its workspace.
+size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
+                      int prefix_len, SharedAttnArgs* a) {
+  const int G = hq / c->n_kv_heads;
+  const size_t rows = static_cast<size_t>(total_q) * hq;
+  SharedAttnArgs t{};
+  const long seq_rows = static_cast<long>(max_q) * G;  // query rows of a sequence per KV head
+  t.stream_rows = seq_rows <= 16 ? 16 : seq_rows <= 32 ? 32 : 0;
+  Carver k{base};
+  if (t.stream_rows > 0) {
+    const size_t workers = stream_workers(planning_sms());
+    t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
+    if (prefix_len > 0) {
+      t.prefix_row_tiles =
+          static_cast<int>((static_cast<size_t>(total_q) * G + t.stream_rows - 1) / t.stream_rows);
+      t.prefix_o = k.take<float>(rows * 128);
+      t.prefix_st = k.take<PartStat>(rows);
+    }
+    t.own_o = k.take<float>(rows * 128);
+    t.own_st = k.take<PartStat>(rows);
+    t.cont_o = k.take<float>(workers * t.stream_rows * 128);
+    t.cont_st = k.take<PartStat>(workers * t.stream_rows);
+  }
+  if (a != nullptr) *a = t;
+  return k.off + 256;
+}
+
 }  // namespace
 
 // ================================================================== C ABI
@@ -1433,6 +1473,7 @@ quail_status quail_test_set_pipeline_wait_limit(long long cycles) {
   CUDA_TRY(set_pipeline_wait_limit_gemm(v));
   CUDA_TRY(set_pipeline_wait_limit_attention(v));
   CUDA_TRY(set_pipeline_wait_limit_attention_tc(v));
+  CUDA_TRY(set_pipeline_wait_limit_cache_attention(v));
   CUDA_TRY(cudaDeviceSynchronize());
   return QUAIL_OK;
 }
@@ -1831,7 +1872,7 @@ quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* toke
 size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
-  return 256;
+  return plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
 }
 
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
@@ -1856,6 +1897,7 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   DeviceState* ds = nullptr;
   int dev = 0;
   SharedAttnArgs a{};
+  plan_attention(static_cast<uint8_t*>(workspace), cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, &a);
   s = open_cache(cache, &ds, &dev, &a.c);
   if (s != QUAIL_OK) return s;
   s = check_device_ptr(q, "q", dev);
@@ -1873,7 +1915,21 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   a.scale_log2 = (scale > 0.f ? scale : 0.08838834764831845f) * 1.4426950408889634f;
   a.out = static_cast<bf16*>(out);
   a.lse = lse;
-  CUDA_TRY(launch_attention_simple(a, reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.stream_rows == 0) {
+    CUDA_TRY(launch_attention_simple(a, st));
+    return QUAIL_OK;
+  }
+  CUtensorMap tK, tV;
+  const uint64_t pool_rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+  for (int i = 0; i < 2; ++i) {
+    const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
+    CUtensorMap* m = i == 0 ? &tK : &tV;
+    s = a.c.codes ? encode_2d_codes(m, pool, pool_rows, 16) : encode_2d_bf16(m, pool, pool_rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+  }
+  CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
+  CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
   return QUAIL_OK;
 }
 

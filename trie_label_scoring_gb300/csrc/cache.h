@@ -1,6 +1,6 @@
-// Launch wrappers of the document cache kernels (cache.cu, cache_attention.cu,
-// cache_attention_tc.cu). Device pointers throughout; every launch goes to
-// `st` and returns the launch status.
+// Launch wrappers of the document cache kernels (cache.cu, cache_attention.cu).
+// Device pointers throughout; every launch goes to `st` and returns the launch
+// status.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,6 +45,13 @@ cudaError_t launch_cache_append(const AppendArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens,
                               __nv_bfloat16* k_out, __nv_bfloat16* v_out, cudaStream_t st);
 
+// One softmax part of a query row: o = sum 2^(t_j - m_o) v_j and
+// l = sum 2^(s_j - m_l), with s the scores in base 2 and t = s, or s plus the
+// power of two of key j's value row where v_j are bare codes.
+struct __align__(16) PartStat {
+  float m_o, m_l, l, pad;
+};
+
 struct SharedAttnArgs {
   CacheView c;
   int hq;
@@ -59,7 +66,30 @@ struct SharedAttnArgs {
   float scale_log2;  // score factor times log2(e)
   __nv_bfloat16* out;
   float* lse;  // nullable
+
+  // The streaming kernel's work list: row_tiles x hkv passes over the prefix
+  // pages (0: the prefix is not its work), then every sequence's own pages,
+  // cut into equal chunks over the workers. plan: [0] units, [1] chunk, [2 + b]
+  // first unit of sequence b, [2 + num_seqs] past the last.
+  int stream_rows;       // rows of a tile, 16 or 32
+  int prefix_row_tiles;
+  long long* plan;
+  // Parts, each [rows, 128] fp32 and a PartStat per row; rows are (token, head)
+  // except in `cont`, the pieces of work items that began at an earlier worker.
+  float* prefix_o;       // pieces that begin a (row tile, head) pass over the prefix
+  PartStat* prefix_st;
+  float* own_o;          // pieces that begin a sequence's own keys
+  PartStat* own_st;
+  float* cont_o;         // [workers, stream_rows, 128]
+  PartStat* cont_st;
 };
+
+constexpr int kStreamWarps = 8;
+int stream_workers(int num_sms);
+cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    int num_sms, cudaStream_t st);
+cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_attention_simple(const SharedAttnArgs& a, cudaStream_t st);
+cudaError_t set_pipeline_wait_limit_cache_attention(long long cycles);
 
 }  // namespace quail

@@ -1,7 +1,12 @@
 // Attention over the paged document cache for a batch whose sequences share
 // their first prefix_len tokens:
 //   o = softmax(scale q K^T) V,  lse = log sum exp(scale q K^T)
+// The keys of a row are cut into parts (the shared prefix, pieces of the
+// sequence's own pages); each part keeps (max, sum, sum of weighted values)
+// and the join rescales them to one maximum.
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "attn_common.cuh"
 #include "cache.h"
@@ -87,12 +92,834 @@ __global__ void attention_simple_kernel(SharedAttnArgs a) {
   }
 }
 
+
+// ------------------------------------------------------------------ streaming kernel
+// Few query rows per KV head (a decoded token: G of them), so the work is
+// reading keys and values once: every warp of the grid is a worker of its own
+// with a private ring of pages, and the work list (all pages of all sequences
+// and KV heads, in order) is cut into equal contiguous chunks, one per worker,
+// whatever the lengths are. A worker's lane 0 issues the TMA copies of a page
+// STAGES pages ahead, across the borders of work items, so the stream of loads
+// never drains; no barrier joins warps. Pieces of an item that several workers
+// share are joined by the second kernel.
+//
+// Per page of 16 keys: S = Q K^T and O += P V on mma.sync m16n8k16 with the 16
+// (or 2 x 16) query rows as M. Over bf16 pages q and P are bf16; over e4m3
+// pages the codes widen exactly to fp16, q is scaled by a power of two per row
+// (exact) and P is rounded to fp16. The key's power of two multiplies its score,
+// the value's is added to the exponent of its weight: o and l keep separate
+// maxima, so that value rows of any scale neither overflow P nor starve the sum.
+template <bool CODES, int MT>
+struct StreamCfg {
+  static constexpr uint32_t kPlane = CODES ? 2048 : 4096;  // K or V of one (page, head)
+  static constexpr uint32_t kStage = 2 * kPlane;
+  static constexpr int kStages = (CODES ? 2 : 1) * (MT == 1 ? 3 : 2);
+  static constexpr uint32_t kRing = kStreamWarps * kStages * kStage;
+  static constexpr uint32_t kQ = MT == 1 ? 0 : kStreamWarps * MT * 4096;  // q fragments (16 rows: in registers)
+  static constexpr uint32_t kScales = CODES ? kStreamWarps * kStages * 32 : 0;  // 16 key, 16 value exponents
+  static constexpr uint32_t kBars = kStreamWarps * kStages * 8;
+  static constexpr uint32_t kScan = (kStreamWarps * 32 + 1) * 8;
+  static constexpr size_t kSmem = 1024 + kRing + kQ + kScales + kBars + kScan + 16;
+};
+static_assert(StreamCfg<false, 1>::kSmem <= 227 * 1024 && StreamCfg<false, 2>::kSmem <= 227 * 1024 &&
+                  StreamCfg<true, 1>::kSmem <= 227 * 1024 && StreamCfg<true, 2>::kSmem <= 227 * 1024,
+              "shared memory");
+constexpr int kStreamThreads = 32 * kStreamWarps;
+constexpr int kMinChunk = 4;  // pages a worker takes at least
+
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (low 16 bits of v) as fp16.
+__device__ __forceinline__ uint32_t widen2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ float pow2_byte(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Pages of sequence b's own keys that its queries read (0: none, or a bad sequence).
+__device__ __forceinline__ int own_pages(const SharedAttnArgs& a, int b) {
+  const QueryRange r = query_range(a, b);
+  return r.ok && r.hi > r.lo && r.len > a.prefix_len ? (r.len - a.prefix_len + kPage - 1) / kPage : 0;
+}
+
+// A page of the work list: page j of the n of an item. Items: (row tile, head)
+// over the prefix, then (sequence, head) over own pages.
+struct Cursor {
+  bool own;
+  int b;  // row tile or sequence
+  int g;
+  int j, n;
+};
+
+// First sequence at or after b with own pages (n of them); num_seqs if none.
+__device__ __forceinline__ void seek_own(const SharedAttnArgs& a, Cursor& c, int b, int lane) {
+  c.own = true;
+  c.g = c.j = 0;
+  for (; b < a.c.num_seqs; b += 32) {
+    const int n = b + lane < a.c.num_seqs ? own_pages(a, b + lane) : 0;
+    const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+    if (some != 0) {
+      const int first = __ffs(some) - 1;
+      c.b = b + first;
+      c.n = __shfl_sync(0xffffffffu, n, first);
+      return;
+    }
+  }
+  c.b = a.c.num_seqs;
+  c.n = 0;
+}
+__device__ __forceinline__ void next_page(const SharedAttnArgs& a, Cursor& c, int lane) {
+  if (++c.j < c.n) return;
+  c.j = 0;
+  if (++c.g < a.c.hkv) return;
+  c.g = 0;
+  if (c.own) {
+    seek_own(a, c, c.b + 1, lane);
+  } else if (++c.b >= a.prefix_row_tiles) {
+    seek_own(a, c, 0, lane);
+  }
+}
+
+template <bool CODES, int MT>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    attention_stream_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
+                            const __grid_constant__ CUtensorMap tmV) {
+  using Cfg = StreamCfg<CODES, MT>;
+  constexpr int kStages = Cfg::kStages;
+  constexpr int kRows = 16 * MT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = base + warp * kStages * Cfg::kStage;
+  uint4* qs = reinterpret_cast<uint4*>(base + Cfg::kRing + warp * MT * 4096) + lane;  // [tile][ks][lane]
+  uint4 qr8[8] = {};
+  auto q_frag = [&](int t, int ks) {
+    if constexpr (MT == 1)
+      return qr8[ks];
+    else
+      return qs[(t * 8 + ks) * 32];
+  };
+  uint8_t* scales = base + Cfg::kRing + Cfg::kQ + warp * kStages * 32;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Cfg::kRing + Cfg::kQ + Cfg::kScales) + warp * kStages;
+  long long* scan = reinterpret_cast<long long*>(base + Cfg::kRing + Cfg::kQ + Cfg::kScales + Cfg::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + Cfg::kRing + Cfg::kQ + Cfg::kScales + Cfg::kBars +
+                                                             Cfg::kScan);
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    if (warp == 0) *abort_flag = 0;
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- the plan: thread i counts the units of its own run of sequences
+  const int B = a.c.num_seqs, G = a.hq / a.c.hkv;
+  const int per = (B + kStreamThreads - 1) / kStreamThreads;
+  const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (blockIdx.x == 0 && !query_range(a, b).ok) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, b);
+    mine += static_cast<long long>(own_pages(a, b)) * a.c.hkv;
+  }
+  const int pp = a.prefix_len / kPage;
+  const long long prefix_units = static_cast<long long>(a.prefix_row_tiles) * a.c.hkv * pp;
+  {
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    scan[threadIdx.x + 1] = x;  // inclusive within the warp
+    if (threadIdx.x == 0) scan[0] = 0;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += scan[32 * w + 32];
+    __syncthreads();
+    scan[threadIdx.x + 1] = x + before;
+    __syncthreads();
+  }
+  const long long units = prefix_units + scan[kStreamThreads];
+  const long long workers = static_cast<long long>(gridDim.x) * kStreamWarps;
+  const long long chunk = max(static_cast<long long>(kMinChunk), (units + workers - 1) / workers);
+  if (blockIdx.x == 0) {
+    long long at = prefix_units + scan[threadIdx.x];
+    for (int b = b0; b < b1; ++b) {
+      a.plan[2 + b] = at;
+      at += static_cast<long long>(own_pages(a, b)) * a.c.hkv;
+    }
+    if (threadIdx.x == 0) {
+      a.plan[0] = units;
+      a.plan[1] = chunk;
+      a.plan[2 + B] = units;
+    }
+  }
+  // workers of one SM sit far apart in the list, so long items spread over the SMs
+  const long long worker = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
+  const long long u0 = worker * chunk;
+  const int count = static_cast<int>(max(0LL, min(units, u0 + chunk) - u0));
+  if (count == 0) return;
+
+  // ---- where the chunk begins
+  Cursor cc;
+  if (u0 < prefix_units) {
+    const long long item = u0 / pp;
+    cc.own = false;
+    cc.b = static_cast<int>(item / a.c.hkv);
+    cc.g = static_cast<int>(item % a.c.hkv);
+    cc.j = static_cast<int>(u0 % pp);
+    cc.n = pp;
+  } else {
+    const long long v = u0 - prefix_units;
+    int lo = 0, hi = kStreamThreads;  // scan[lo] <= v < scan[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (scan[mid] <= v)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    long long at = scan[lo];
+    for (int b = lo * per;; b += 32) {
+      const int n = b + lane < B ? own_pages(a, b + lane) : 0;
+      long long x = static_cast<long long>(n) * a.c.hkv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, at + x > v);
+      if (past != 0) {
+        const int f = __ffs(past) - 1;
+        const long long end = __shfl_sync(0xffffffffu, at + x, f);
+        cc.own = true;
+        cc.b = b + f;
+        cc.n = __shfl_sync(0xffffffffu, n, f);
+        const long long rem = v - (end - static_cast<long long>(cc.n) * a.c.hkv);
+        cc.g = static_cast<int>(rem / cc.n);
+        cc.j = static_cast<int>(rem % cc.n);
+        break;
+      }
+      at = __shfl_sync(0xffffffffu, at + x, 31);
+      if (b >= B) return;  // not reached: v lies before the end of the list
+    }
+  }
+
+  // ---- producer: page `issued` of the chunk into stage issued % kStages. Page
+  // ids are read 32 at a time, one per lane.
+  Cursor pc = cc;
+  int issued = 0, win = -1, ids = 0;
+  uint32_t armed = 0;  // stages whose latest phase carries copies
+  auto produce = [&]() {
+    if (win < 0 || pc.j - win >= 32) {
+      win = pc.j;
+      const int j = pc.j + lane;
+      const int* list = pc.own ? a.c.table + static_cast<size_t>(pc.b) * a.c.max_pages + pp : a.prefix_pages;
+      ids = j < pc.n ? list[j] : -1;
+    }
+    const int page = __shfl_sync(0xffffffffu, ids, pc.j - win);
+    const int s = issued % kStages;
+    const bool ok = page >= 0 && page < a.c.num_pages;
+    if (lane == 0) {
+      if (ok) {
+        uint8_t* dst = ring + s * Cfg::kStage;
+        const int row = (page * a.c.hkv + pc.g) * kPage;
+        mbar_arrive_expect_tx(&bars[s], Cfg::kStage + (CODES ? 32 : 0));
+        if constexpr (CODES) {
+          tma_load_2d(dst, &tmK, &bars[s], 0, row);
+          tma_load_2d(dst + Cfg::kPlane, &tmV, &bars[s], 0, row);
+          bulk_load(scales + s * 32, a.c.k_scale + row, 16, &bars[s]);
+          bulk_load(scales + s * 32 + 16, a.c.v_scale + row, 16, &bars[s]);
+        } else {
+          tma_load_2d(dst, &tmK, &bars[s], 0, row);
+          tma_load_2d(dst + 2048, &tmK, &bars[s], 64, row);
+          tma_load_2d(dst + 4096, &tmV, &bars[s], 0, row);
+          tma_load_2d(dst + 6144, &tmV, &bars[s], 64, row);
+        }
+      } else {
+        raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, pc.own ? pc.b : 0);
+        mbar_arrive(&bars[s]);  // the stage's old contents are consumed; the rows are void
+      }
+    }
+    armed = ok ? armed | 1u << s : armed & ~(1u << s);
+    ++issued;
+    const bool own = pc.own;
+    const int b = pc.b, g = pc.g;
+    next_page(a, pc, lane);
+    if (pc.own != own || pc.b != b || pc.g != g) win = -1;
+  };
+  for (int s = 0; s < kStages && s < count; ++s) produce();
+
+  // ---- consumer
+  const int gq = lane >> 2, tq = lane & 3;
+  float o[MT][16][4], m_o[MT][2], m_l[MT][2], l[MT][2], f_row[MT][2];
+  int limit[MT][2];  // keys that rows gq and gq + 8 of the tile see, counted from the item's first
+  QueryRange qr{0, 0, 0, true};
+  int first_page = 0, n_rows = 0;
+  bool ok = true;
+
+  // the item's query rows: fragments, score factors, limits; an empty state
+  auto open_item = [&]() {
+    if (cc.own) {
+      qr = query_range(a, cc.b);
+      n_rows = (qr.hi - qr.lo) * G;
+    } else {
+      qr.lo = 0;
+      n_rows = min(kRows, a.total_q * G - cc.b * kRows);
+    }
+    first_page = cc.j;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const __nv_bfloat16* src[2];
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int r = t * 16 + gq + 8 * hr;
+        src[hr] = nullptr;
+        limit[t][hr] = cc.own ? qr.len - a.prefix_len : a.prefix_len;
+        if (r < n_rows) {
+          const int flat = cc.own ? r : cc.b * kRows + r;
+          src[hr] = a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + cc.g * G + flat % G) * 128;
+          if (cc.own && a.causal) limit[t][hr] -= qr.hi - qr.lo - 1 - flat / G;
+        }
+        m_o[t][hr] = m_l[t][hr] = -INFINITY;
+        l[t][hr] = 0.f;
+        f_row[t][hr] = a.scale_log2;
+      }
+#pragma unroll
+      for (int n = 0; n < 16; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+      // A fragment of 16 dims: registers 0 and 2 are row gq's first and second
+      // half of the dims that lane tq's B registers hold, 1 and 3 row gq + 8's.
+      uint2 w[2][8];
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          w[hr][ks] = make_uint2(0u, 0u);
+          if (src[hr] != nullptr) {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(src[hr] + ks * 16);
+            w[hr][ks] = CODES ? make_uint2(p[2 * tq], p[2 * tq + 1]) : make_uint2(p[tq], p[tq + 4]);
+          }
+        }
+      }
+      if constexpr (CODES) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          float am = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
+            am = fmaxf(fmaxf(fmaxf(am, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
+          }
+          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+          // 2^e <= max |q| < 2^(e+1): q / 2^e is exact in fp16 down to 2^-24 of the row's maximum
+          const int e = am > 0.f ? min(127, static_cast<int>(__float_as_uint(am) >> 23) - 127) : 0;
+          const float down = ldexpf(1.f, -e);
+          f_row[t][hr] = a.scale_log2 * ldexpf(1.f, e);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
+            w[hr][ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
+          }
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint4 f = make_uint4(w[0][ks].x, w[1][ks].x, w[0][ks].y, w[1][ks].y);
+        if constexpr (MT == 1)
+          qr8[ks] = f;
+        else
+          qs[(t * 8 + ks) * 32] = f;  // read by this lane only
+      }
+    }
+  };
+
+  // the piece's rows: final when it is the whole of what they attend to, else parts
+  auto close_item = [&]() {
+    const bool whole = cc.own && a.prefix_len == 0 && first_page == 0 && cc.j == cc.n - 1;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        float sum = l[t][hr];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = t * 16 + gq + 8 * hr;
+        if (r >= n_rows) continue;
+        const int flat = cc.own ? r : cc.b * kRows + r;
+        const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + cc.g * G + flat % G;
+        if (whole) {
+          // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
+          const float f = (m_o[t][hr] == m_l[t][hr] ? 1.f : exp2f(m_o[t][hr] - m_l[t][hr])) / sum;
+#pragma unroll
+          for (int n = 0; n < 16; n += 2) {
+            __nv_bfloat16* d = a.out + row * 128;
+            if constexpr (CODES) {
+              *reinterpret_cast<uint2*>(d + n * 8 + 4 * tq) =
+                  make_uint2(pack_bf16(o[t][n][2 * hr] * f, o[t][n + 1][2 * hr] * f),
+                             pack_bf16(o[t][n][2 * hr + 1] * f, o[t][n + 1][2 * hr + 1] * f));
+            } else {
+              *reinterpret_cast<uint32_t*>(d + n * 8 + 2 * tq) = pack_bf16(o[t][n][2 * hr] * f, o[t][n][2 * hr + 1] * f);
+              *reinterpret_cast<uint32_t*>(d + n * 8 + 8 + 2 * tq) =
+                  pack_bf16(o[t][n + 1][2 * hr] * f, o[t][n + 1][2 * hr + 1] * f);
+            }
+          }
+          if (tq == 0 && a.lse != nullptr) a.lse[row] = (m_l[t][hr] + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          float* d;
+          PartStat* st;
+          if (first_page > 0) {
+            const size_t at = static_cast<size_t>(worker) * kRows + r;
+            d = a.cont_o + at * 128;
+            st = a.cont_st + at;
+          } else {
+            d = (cc.own ? a.own_o : a.prefix_o) + row * 128;
+            st = (cc.own ? a.own_st : a.prefix_st) + row;
+          }
+#pragma unroll
+          for (int n = 0; n < 16; n += 2) {
+            if constexpr (CODES) {
+              *reinterpret_cast<float4*>(d + n * 8 + 4 * tq) =
+                  make_float4(o[t][n][2 * hr], o[t][n + 1][2 * hr], o[t][n][2 * hr + 1], o[t][n + 1][2 * hr + 1]);
+            } else {
+              *reinterpret_cast<float2*>(d + n * 8 + 2 * tq) = make_float2(o[t][n][2 * hr], o[t][n][2 * hr + 1]);
+              *reinterpret_cast<float2*>(d + n * 8 + 8 + 2 * tq) =
+                  make_float2(o[t][n + 1][2 * hr], o[t][n + 1][2 * hr + 1]);
+            }
+          }
+          if (tq == 0) *st = PartStat{m_o[t][hr], m_l[t][hr], sum, 0.f};
+        }
+      }
+    }
+  };
+
+  for (int i = 0; i < count; ++i) {
+    const int s = i % kStages;
+    if (i == 0 || cc.j == 0) open_item();
+    // warp-uniform wait: the collectives below need every lane
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], static_cast<uint32_t>((i / kStages) & 1), abort_flag))) {
+      ok = false;
+      break;
+    }
+    const uint32_t kb = smem_u32(ring + s * Cfg::kStage), vb = kb + Cfg::kPlane;
+    const int key0 = cc.j * kPage;
+    const int valid = (cc.own ? qr.len - a.prefix_len : a.prefix_len) - key0;  // slots of the page that hold keys
+    float sc[MT][2][4];
+    {
+      float acc[MT][2][2][4];  // two chains per key tile
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[t][x >> 1][x & 1][c] = 0.f;
+      const uint32_t mi = lane >> 3, ri = lane & 7;
+      if constexpr (CODES) {
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2) {  // 32 dims
+          uint32_t r[4];  // (keys 0-7, 8-15) of chunk 2 k2, then of the next
+          ldsm_x4(kb + swz((mi & 1) * 8 + ri, 2 * k2 + (mi >> 1)), r);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const uint32_t lo = widen2(r[2 * h + nt]), hi = widen2(r[2 * h + nt] >> 16);
+#pragma unroll
+              for (int t = 0; t < MT; ++t) mma16816<true>(acc[t][nt][h], q_frag(t, 2 * k2 + h), lo, hi);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          uint32_t r[4];  // keys 0-7: dims 0-7, 8-15 of the 16; keys 8-15 likewise
+          ldsm_x4(kb + (ks >> 2) * 2048 + swz((mi >> 1) * 8 + ri, (ks & 3) * 2 + (mi & 1)), r);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const uint4 qf = q_frag(t, ks);
+            mma16816<false>(acc[t][0][ks & 1], qf, r[0], r[1]);
+            mma16816<false>(acc[t][1][ks & 1], qf, r[2], r[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[t][nt][c] = acc[t][nt][0][c] + acc[t][nt][1][c];
+    }
+    float kf[2][2], ve[2][2];  // key factor, value exponent of this lane's keys
+    if constexpr (CODES) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const uint32_t k2 = *reinterpret_cast<const uint16_t*>(scales + s * 32 + nt * 8 + 2 * tq);
+        const uint32_t v2 = *reinterpret_cast<const uint16_t*>(scales + s * 32 + 16 + nt * 8 + 2 * tq);
+        kf[nt][0] = pow2_byte(k2 & 0xffu);
+        kf[nt][1] = pow2_byte(k2 >> 8);
+        ve[nt][0] = static_cast<float>(static_cast<int>(v2 & 0xffu) - 127);
+        ve[nt][1] = static_cast<float>(static_cast<int>(v2 >> 8) - 127);
+      }
+    }
+    uint4 pa[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      float mo[2] = {-INFINITY, -INFINITY}, ml[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = key0 + nt * 8 + tq * 2 + (c & 1);
+          float x = sc[t][nt][c] * f_row[t][c >> 1];
+          if constexpr (CODES) x *= kf[nt][c & 1];
+          x = key < limit[t][c >> 1] ? x : -INFINITY;
+          sc[t][nt][c] = x;
+          ml[c >> 1] = fmaxf(ml[c >> 1], x);
+          if constexpr (CODES) mo[c >> 1] = fmaxf(mo[c >> 1], x + ve[nt][c & 1]);
+        }
+      }
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 1));
+        ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 2));
+        if constexpr (CODES) {
+          mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 1));
+          mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 2));
+        } else {
+          mo[hr] = ml[hr];
+        }
+      }
+      // The reference maxima move only when a page exceeds them by more than
+      // 2^8: weights stay below 256 and the rescale is skipped on most pages.
+      if (__any_sync(0xffffffffu, mo[0] > m_o[t][0] + 8.f || mo[1] > m_o[t][1] + 8.f || ml[0] > m_l[t][0] + 8.f ||
+                                      ml[1] > m_l[t][1] + 8.f)) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const float no = fmaxf(m_o[t][hr], mo[hr]), nl = fmaxf(m_l[t][hr], ml[hr]);
+          const float fo = no == -INFINITY ? 1.f : exp2f(m_o[t][hr] - no);
+          l[t][hr] *= nl == -INFINITY ? 1.f : exp2f(m_l[t][hr] - nl);
+          m_o[t][hr] = no;
+          m_l[t][hr] = nl;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            o[t][n][2 * hr] *= fo;
+            o[t][n][2 * hr + 1] *= fo;
+          }
+        }
+      }
+      uint32_t pr[4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          // no key seen yet: the reference is still -inf, and every weight is 0
+          const float rl = m_l[t][hr] == -INFINITY ? 0.f : m_l[t][hr];
+          const float x0 = sc[t][nt][2 * hr], x1 = sc[t][nt][2 * hr + 1];
+          const float e0 = fast_exp2(x0 - rl), e1 = fast_exp2(x1 - rl);
+          l[t][hr] += e0 + e1;
+          if constexpr (CODES) {
+            const float ro = m_o[t][hr] == -INFINITY ? 0.f : m_o[t][hr];
+            pr[nt * 2 + hr] = pack_f16(fast_exp2(x0 + ve[nt][0] - ro), fast_exp2(x1 + ve[nt][1] - ro));
+          } else {
+            pr[nt * 2 + hr] = pack_bf16(e0, e1);
+          }
+        }
+      }
+      pa[t] = make_uint4(pr[0], pr[1], pr[2], pr[3]);
+    }
+    // O += P V. Slots past the sequence's end may hold anything: their values
+    // are zeroed in registers, since 0 * NaN would reach O.
+    {
+      const uint32_t mi = lane >> 3, ri = lane & 7;
+      uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
+      if (valid < kPage) {
+        const int k0 = tq * 2, k1 = k0 + 8;
+        m0 = (k0 < valid ? 0x0000ffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
+        m1 = (k1 < valid ? 0x0000ffffu : 0u) | (k1 + 1 < valid ? 0xffff0000u : 0u);
+      }
+      if constexpr (CODES) {
+#pragma unroll
+        for (int c2 = 0; c2 < 4; ++c2) {  // 32 dims: chunks 2 c2 and 2 c2 + 1
+          uint32_t r[4];  // (keys 0-7, 8-15) of the first chunk, then of the second
+          ldsm_x4_t(vb + swz((mi & 1) * 8 + ri, 2 * c2 + (mi >> 1)), r);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // bytes (k0 d0, k0 d1, k1 d0, k1 d1) -> even dims (k0, k1), odd dims (k0, k1)
+            const uint32_t a0 = __byte_perm(r[2 * h] & m0, 0u, 0x3120), a1 = __byte_perm(r[2 * h + 1] & m1, 0u, 0x3120);
+            const uint32_t e0 = widen2(a0), d0 = widen2(a0 >> 16), e1 = widen2(a1), d1 = widen2(a1 >> 16);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              mma16816<true>(o[t][(2 * c2 + h) * 2], pa[t], e0, e1);
+              mma16816<true>(o[t][(2 * c2 + h) * 2 + 1], pa[t], d0, d1);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int np = 0; np < 8; ++np) {
+          uint32_t r[4];
+          ldsm_x4_t(vb + (np >> 2) * 2048 + swz((mi & 1) * 8 + ri, (np & 3) * 2 + (mi >> 1)), r);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            mma16816<false>(o[t][np * 2], pa[t], r[0] & m0, r[1] & m1);
+            mma16816<false>(o[t][np * 2 + 1], pa[t], r[2] & m0, r[3] & m1);
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+    if (issued < count) produce();
+    if (cc.j == cc.n - 1 || i == count - 1) close_item();
+    if (i < count - 1) next_page(a, cc, lane);
+  }
+
+  if (!ok && lane == 0) {
+    // gave up: wait for the copies in flight, which may still land in this block's memory
+    for (int s = 0; s < kStages; ++s) {
+      if (!(armed >> s & 1u)) continue;
+      const int last = (issued - 1 - s) / kStages;  // index of the stage's latest phase
+      const long long t0 = clock64();
+      while (!mbar_try_wait(smem_u32(&bars[s]), static_cast<uint32_t>(last & 1)) && clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
+    raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 4000);
+  }
+}
+
+// ------------------------------------------------------------------ join
+// Warps of a block share one (token, head) row (all of them where rows are few
+// and parts many, else each warp has its own): every warp folds its parts into
+// (m, l, o), then the first adds them up.
+constexpr int kJoinWarps = 4;
+
+__device__ __forceinline__ float pow2_or_0(float x, float ref) {  // 2^(x - ref); 0 where nothing was seen
+  return x == -INFINITY ? 0.f : exp2f(x - ref);
+}
+
+struct Parts {
+  int prefix_n, own_n;  // pieces of the prefix / of the own keys
+  size_t prefix_w, own_w;  // worker of the first piece
+  int prefix_r, own_r;  // row within the items' tiles
+};
+
+template <int WPR>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(SharedAttnArgs a) {
+  grid_dependency_wait();
+  __shared__ float so[kJoinWarps][128];
+  __shared__ PartStat ss[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
+  const int sub = warp % WPR;
+  const int G = a.hq / a.c.hkv;
+  bool live = row < static_cast<long long>(a.total_q) * a.hq;
+  const int t = live ? static_cast<int>(row / a.hq) : 0, h = live ? static_cast<int>(row % a.hq) : 0, g = h / G;
+  int b = t;
+  if (live && a.q_offsets != nullptr) {  // last sequence that begins at or before t
+    int lo = 0, hi = a.c.num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.q_offsets[mid] <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+  }
+  QueryRange qr{0, 0, 0, false};
+  if (live) qr = query_range(a, b);
+  live = live && qr.ok && t >= qr.lo && t < qr.hi;
+  Parts p{0, 0, 0, 0, 0, 0};
+  if (live && qr.len > 0) {
+    const long long chunk = a.plan[1];
+    if (a.prefix_row_tiles > 0) {
+      const int flat = t * G + h % G;
+      const int pp = a.prefix_len / kPage;
+      const long long u = (static_cast<long long>(flat / a.stream_rows) * a.c.hkv + g) * pp;
+      p.prefix_w = static_cast<size_t>(u / chunk);
+      p.prefix_n = static_cast<int>((u + pp - 1) / chunk - u / chunk) + 1;
+      p.prefix_r = flat % a.stream_rows;
+    }
+    const int n = own_pages(a, b);
+    if (n > 0) {
+      const long long u = a.plan[2 + b] + static_cast<long long>(g) * n;
+      p.own_w = static_cast<size_t>(u / chunk);
+      p.own_n = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
+      p.own_r = (t - qr.lo) * G + h % G;
+    }
+    if (a.prefix_len == 0 && p.own_n == 1) live = false;  // written by its only worker
+  }
+  const int parts = p.prefix_n + p.own_n;
+  float m_l = -INFINITY, m_o = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    auto locate = [&](int i, const float*& o, const PartStat*& st) {
+      const bool pre = i < p.prefix_n;
+      const int k = pre ? i : i - p.prefix_n;
+      if (k == 0) {
+        o = (pre ? a.prefix_o : a.own_o) + row * 128;
+        st = (pre ? a.prefix_st : a.own_st) + row;
+      } else {
+        const size_t at = ((pre ? p.prefix_w : p.own_w) + k) * a.stream_rows + (pre ? p.prefix_r : p.own_r);
+        o = a.cont_o + at * 128;
+        st = a.cont_st + at;
+      }
+    };
+    constexpr int kBatch = 4;
+    for (int i0 = sub; i0 < parts; i0 += WPR * kBatch) {
+      PartStat st[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        st[k] = PartStat{-INFINITY, -INFINITY, 0.f, 0.f};
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + k * WPR < parts) {
+          const float* o;
+          const PartStat* sp;
+          locate(i0 + k * WPR, o, sp);
+          st[k] = *sp;
+          v[k] = *reinterpret_cast<const float4*>(o + 4 * lane);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float nl = fmaxf(m_l, st[k].m_l), no = fmaxf(m_o, st[k].m_o);
+        l = l * pow2_or_0(m_l, nl) + st[k].l * (st[k].l != st[k].l ? 1.f : pow2_or_0(st[k].m_l, nl));
+        const float fo = pow2_or_0(m_o, no), fk = pow2_or_0(st[k].m_o, no);
+        acc.x = acc.x * fo + v[k].x * fk;
+        acc.y = acc.y * fo + v[k].y * fk;
+        acc.z = acc.z * fo + v[k].z * fk;
+        acc.w = acc.w * fo + v[k].w * fk;
+        m_l = nl;
+        m_o = no;
+      }
+    }
+  }
+  if constexpr (WPR > 1) {
+    *reinterpret_cast<float4*>(&so[warp][4 * lane]) = acc;
+    if (lane == 0) ss[warp] = PartStat{m_o, m_l, l, 0.f};
+    __syncthreads();
+    if (sub != 0) return;
+    float nl = -INFINITY, no = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      nl = fmaxf(nl, ss[warp + w].m_l);
+      no = fmaxf(no, ss[warp + w].m_o);
+    }
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const PartStat st = ss[warp + w];
+      l += st.l * (st.l != st.l ? 1.f : pow2_or_0(st.m_l, nl));
+      const float f = pow2_or_0(st.m_o, no);
+      const float4 v = *reinterpret_cast<const float4*>(&so[warp + w][4 * lane]);
+      acc.x += v.x * f;
+      acc.y += v.y * f;
+      acc.z += v.z * f;
+      acc.w += v.w * f;
+    }
+    m_l = nl;
+    m_o = no;
+  }
+  if (!live) return;
+  // no key at all: 0 and -inf. A NaN sum makes the row NaN, as the formula has it.
+  const bool none = qr.len == 0;
+  const float f = none ? 0.f : (l != l ? l : exp2f(m_o - m_l) / l);
+  const float4 r = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+  *reinterpret_cast<uint2*>(a.out + row * 128 + 4 * lane) = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : (m_l + log2f(l)) * 0.6931471805599453f;
+}
+
 }  // namespace
+
+int stream_workers(int num_sms) { return num_sms * kStreamWarps; }
+
+namespace {
+
+template <bool CODES, int MT>
+cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
+                          cudaStream_t st) {
+  auto kern = attention_stream_kernel<CODES, MT>;
+  constexpr size_t smem = StreamCfg<CODES, MT>::kSmem;
+  static std::atomic<bool> configured[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_release);
+  }
+  count_launch();
+  return launch_pdl(kern, dim3(num_sms), dim3(kStreamThreads), smem, st, a, tmK, tmV);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    int num_sms, cudaStream_t st) {
+  if (a.stream_rows == 16)
+    return a.c.codes ? launch_stream<true, 1>(a, tmK, tmV, num_sms, st)
+                     : launch_stream<false, 1>(a, tmK, tmV, num_sms, st);
+  return a.c.codes ? launch_stream<true, 2>(a, tmK, tmV, num_sms, st)
+                   : launch_stream<false, 2>(a, tmK, tmV, num_sms, st);
+}
+
+cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.total_q) * a.hq;
+  count_launch();
+  // few rows: many parts each, so a block's warps share a row
+  if (rows <= 16LL * num_sms)
+    return launch_pdl(attention_join_kernel<kJoinWarps>, dim3(static_cast<unsigned>(rows)), dim3(32 * kJoinWarps), 0, st, a);
+  return launch_pdl(attention_join_kernel<1>, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
+                    dim3(32 * kJoinWarps), 0, st, a);
+}
 
 cudaError_t launch_attention_simple(const SharedAttnArgs& a, cudaStream_t st) {
   if (a.total_q <= 0 || a.c.num_seqs <= 0) return cudaSuccess;
   count_launch();
   return launch_pdl(attention_simple_kernel, dim3(a.max_q, a.c.hkv, a.c.num_seqs), dim3(128), 0, st, a);
+}
+
+// Test hook: this translation unit's copy of the pipeline wait limit.
+cudaError_t set_pipeline_wait_limit_cache_attention(long long cycles) {
+  return cudaMemcpyToSymbol(g_pipeline_wait_limit, &cycles, sizeof(cycles));
 }
 
 }  // namespace quail
