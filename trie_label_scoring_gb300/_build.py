@@ -15,7 +15,7 @@ LIB = os.path.join(OUT_DIR, "libquail.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 CUDA_SOURCES = ["api.cu", "gemm.cu", "attention.cu", "attention_tc.cu", "layer.cu", "mlp.cu", "shortlist.cu",
-                "cache.cu", "cache_attention.cu"]
+                "cache.cu", "cache_attention.cu", "cache_attention_tc.cu"]
 CXX_SOURCES = ["trie.cpp", "cost.cpp", "shortlist.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -908,21 +908,64 @@ quail_status check_attention_shape(const quail_cache_desc* c, int n_q_heads, int
   return QUAIL_OK;
 }
 
+// Key ranges (whole 128-key blocks) that `items` tiles of nb blocks are cut
+// into: the cut that minimises waves x (blocks + the fixed cost of a tile, in
+// blocks: its queries, the pipeline's fill and its rows out).
+void choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
+  constexpr int kFixed = 4;
+  long best = -1;
+  *split = 128;
+  *splits = nb;
+  for (int p = 1; p <= nb; ++p) {
+    const int blocks = (nb + p - 1) / p;
+    const int n = (nb + blocks - 1) / blocks;
+    const long cost = (items * n + sms - 1) / sms * (blocks + kFixed);
+    if (best < 0 || cost < best) {
+      best = cost;
+      *split = blocks * 128;
+      *splits = n;
+    }
+    if (blocks == 1 || items * n > 4L * sms) break;
+  }
+}
+
 // How one attention call is carried out, and its workspace.
+//   up to 32 query rows per sequence and KV head: streamed (memory bound); the
+//       prefix too while the whole batch has no more rows than that, else on tiles
+//   fewer rows than half a tile, and a prefix: prefix and sequences on tiles apart
+//   else: every sequence's rows fill tiles by themselves, prefix and own keys in one pass
 size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
                       int prefix_len, SharedAttnArgs* a) {
-  const int G = hq / c->n_kv_heads;
+  const int hkv = c->n_kv_heads, G = hq / hkv, sms = planning_sms();
   const size_t rows = static_cast<size_t>(total_q) * hq;
+  const bool codes = c->dtype == QUAIL_DTYPE_E4M3;
   SharedAttnArgs t{};
-  const long seq_rows = static_cast<long>(max_q) * G;  // query rows of a sequence per KV head
+  const long seq_rows = static_cast<long>(std::min(max_q, total_q)) * G;  // query rows of a sequence per KV head
+  const long all_rows = static_cast<long>(total_q) * G;
   t.stream_rows = seq_rows <= 16 ? 16 : seq_rows <= 32 ? 32 : 0;
+  const bool stream = t.stream_rows > 0;
+  const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > t.stream_rows : seq_rows < 128 && c->num_seqs > 1);
+  if (tile_prefix)
+    choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, &t.prefix_split,
+                      &t.prefix_splits);
+  if (!stream) {
+    t.seq_begin = tile_prefix ? prefix_len : 0;
+    t.seq_split = 128;
+    t.seq_splits = 1;
+    if (max_seq_len > t.seq_begin)
+      choose_key_splits((seq_rows + kTileRows - 1) / kTileRows * hkv * c->num_seqs,
+                        (max_seq_len - t.seq_begin + 127) / 128, sms, &t.seq_split, &t.seq_splits);
+  }
+  t.dense_parts = t.prefix_splits + t.seq_splits;
+  if (t.dense_parts == 1 && !tile_prefix) t.dense_parts = 0;
+  t.pool_pages = c->num_pages;
+  t.wide_pages = codes && (tile_prefix || !stream);
   Carver k{base};
-  if (t.stream_rows > 0) {
-    const size_t workers = stream_workers(planning_sms());
+  if (stream) {
+    const size_t workers = stream_workers(sms);
     t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
-    if (prefix_len > 0) {
-      t.prefix_row_tiles =
-          static_cast<int>((static_cast<size_t>(total_q) * G + t.stream_rows - 1) / t.stream_rows);
+    if (prefix_len > 0 && !tile_prefix) {
+      t.prefix_row_tiles = static_cast<int>((all_rows + t.stream_rows - 1) / t.stream_rows);
       t.prefix_o = k.take<float>(rows * 128);
       t.prefix_st = k.take<PartStat>(rows);
     }
@@ -930,6 +973,19 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     t.own_st = k.take<PartStat>(rows);
     t.cont_o = k.take<float>(workers * t.stream_rows * 128);
     t.cont_st = k.take<PartStat>(workers * t.stream_rows);
+  }
+  if (t.dense_parts > 0) {
+    t.dense_o = k.take<float>(t.dense_parts * rows * 128);
+    t.dense_st = k.take<PartStat>(t.dense_parts * rows);
+  }
+  if (t.wide_pages) {
+    t.wide_own = stream ? 0 : (max_seq_len - prefix_len + 15) / 16;
+    const size_t pages = static_cast<size_t>(prefix_len / 16) + static_cast<size_t>(c->num_seqs) * t.wide_own;
+    // row coordinates of the widened pool stay below 2^31
+    if (pages * hkv * 16 > (size_t(1) << 31) - 1) return 0;
+    t.pool_pages = static_cast<int>(std::max<size_t>(pages, 1));
+    t.wide_k = k.take<bf16>(static_cast<size_t>(t.pool_pages) * hkv * 16 * 128);
+    t.wide_v = k.take<bf16>(static_cast<size_t>(t.pool_pages) * hkv * 16 * 128);
   }
   if (a != nullptr) *a = t;
   return k.off + 256;
@@ -1474,6 +1530,7 @@ quail_status quail_test_set_pipeline_wait_limit(long long cycles) {
   CUDA_TRY(set_pipeline_wait_limit_attention(v));
   CUDA_TRY(set_pipeline_wait_limit_attention_tc(v));
   CUDA_TRY(set_pipeline_wait_limit_cache_attention(v));
+  CUDA_TRY(set_pipeline_wait_limit_cache_attention_tc(v));
   CUDA_TRY(cudaDeviceSynchronize());
   return QUAIL_OK;
 }
@@ -1872,7 +1929,9 @@ quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* toke
 size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
-  return plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
+  const size_t n = plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
+  if (n == 0) fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "num_seqs x max_seq_len is too large for an e4m3 cache");
+  return n;
 }
 
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
@@ -1891,8 +1950,9 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   if (q == nullptr || out == nullptr || seq_len == nullptr || (prefix_len > 0 && prefix_pages == nullptr))
     return fail(QUAIL_ERR_INVALID_ARG, "q, out, seq_len or prefix_pages is null");
   if (!aligned16(q) || !aligned16(out)) return fail(QUAIL_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  s = check_workspace(workspace, workspace_bytes,
-                      quail_workspace_size_attention(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len));
+  const size_t need = plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
+  if (need == 0) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "num_seqs x max_seq_len is too large for an e4m3 cache");
+  s = check_workspace(workspace, workspace_bytes, need);
   if (s != QUAIL_OK) return s;
   DeviceState* ds = nullptr;
   int dev = 0;
@@ -1916,20 +1976,30 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   a.out = static_cast<bf16*>(out);
   a.lse = lse;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (a.stream_rows == 0) {
-    CUDA_TRY(launch_attention_simple(a, st));
-    return QUAIL_OK;
-  }
-  CUtensorMap tK, tV;
-  const uint64_t pool_rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
-  for (int i = 0; i < 2; ++i) {
-    const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
-    CUtensorMap* m = i == 0 ? &tK : &tV;
-    s = a.c.codes ? encode_2d_codes(m, pool, pool_rows, 16) : encode_2d_bf16(m, pool, pool_rows, 128, 128, 64, 16);
+  const bool streamed = a.stream_rows > 0;
+  if (a.wide_pages) CUDA_TRY(launch_cache_widen(a, st));
+  if (a.prefix_splits > 0 || !streamed) {
+    CUtensorMap tK, tV;
+    const uint64_t pool_rows = static_cast<uint64_t>(a.pool_pages) * cache->n_kv_heads * 16;
+    s = encode_2d_bf16(&tK, a.wide_pages ? a.wide_k : cache->k_pool, pool_rows, 128, 128, 64, 16);
     if (s != QUAIL_OK) return s;
+    s = encode_2d_bf16(&tV, a.wide_pages ? a.wide_v : cache->v_pool, pool_rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
+    if (!streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
   }
-  CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
-  CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
+  if (streamed) {
+    CUtensorMap tK, tV;
+    const uint64_t pool_rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+    for (int i = 0; i < 2; ++i) {
+      const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
+      CUtensorMap* m = i == 0 ? &tK : &tV;
+      s = a.c.codes ? encode_2d_codes(m, pool, pool_rows, 16) : encode_2d_bf16(m, pool, pool_rows, 128, 128, 64, 16);
+      if (s != QUAIL_OK) return s;
+    }
+    CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
+  }
+  if (streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
   return QUAIL_OK;
 }
 

@@ -84,19 +84,6 @@ __device__ __forceinline__ void tmem_st_16cols_nowait(uint32_t taddr, const floa
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D (+)= A * B^T with A in TMEM (M rows = lanes, K packed two bf16 per column)
-// and the B shared-memory descriptor given as its two 32-bit words.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 bd, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // One TMA page ring (K or V): block j's 8 pages into stage j % kTcStages, both
 // 64-dim halves, once the stage's previous block has been consumed.
 __device__ __forceinline__ void load_ring(uint8_t* ring, uint64_t* full, uint64_t* empty, const CUtensorMap* tm,

@@ -59,6 +59,19 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// D (+)= A * B^T with A in TMEM (M rows = lanes, K packed two bf16 per column)
+// and the B shared-memory descriptor given as its two 32-bit words.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ int row_doc(const RowMap& m, int slot) { return m.slot_doc ? m.slot_doc[slot] : slot; }
 __device__ __forceinline__ int row_node(const RowMap& m, int slot, int e) {
   if (m.slot_base) {

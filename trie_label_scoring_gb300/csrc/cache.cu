@@ -213,6 +213,19 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t two, float scale) {
   return pack_bf16(f.x * scale, f.y * scale);
 }
 
+// Elements 16 l .. 16 l + 15 of a row: sixteen codes w times sc.
+__device__ __forceinline__ void store_codes_bf16(bf16* out, int l, const uint4& w, float sc) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = codes_to_bf16x2(in[i], sc);
+    o[2 * i + 1] = codes_to_bf16x2(in[i] >> 16, sc);
+  }
+  *reinterpret_cast<uint4*>(out + 16 * l) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(out + 16 * l + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 __global__ void __launch_bounds__(kReadThreads)
     cache_read_kernel(CacheView c, const int* seq, const int* pos, int num_tokens, bf16* k_out, bf16* v_out) {
   grid_dependency_wait();
@@ -242,19 +255,50 @@ __global__ void __launch_bounds__(kReadThreads)
     const uint4 w = ldg_stream(static_cast<const uint8_t*>(is_k ? c.k : c.v) + at * 128 + 16 * l);
     const int e = (is_k ? c.k_scale : c.v_scale)[at];
     const float sc = __uint_as_float(static_cast<uint32_t>(e) << 23);
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = codes_to_bf16x2(in[i], sc);
-      o[2 * i + 1] = codes_to_bf16x2(in[i] >> 16, sc);
-    }
-    *reinterpret_cast<uint4*>(out + 16 * l) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(out + 16 * l + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    store_codes_bf16(out, l, w, sc);
+  }
+}
+
+// ------------------------------------------------------------------ widen
+// Block = one page of the list (the prefix, then wide_own pages per sequence):
+// its K and V rows as bf16 for the tensor-core tiles. Exact, and small next to
+// their work: the tiles have 256 rows to multiply with every key.
+__global__ void __launch_bounds__(kReadThreads) cache_widen_kernel(SharedAttnArgs a) {
+  grid_dependency_wait();
+  const int pp = a.prefix_len / kPage, p = blockIdx.x;
+  int page;
+  if (p < pp) {
+    page = a.prefix_pages[p];
+  } else {
+    const int b = (p - pp) / a.wide_own, j = (p - pp) % a.wide_own;
+    const int len = a.seq_len[b];
+    if (len > a.max_seq_len || (pp + j) * kPage >= len) return;
+    page = a.c.table[static_cast<size_t>(b) * a.c.max_pages + pp + j];
+  }
+  if (page < 0 || page >= a.c.num_pages) {
+    if (threadIdx.x == 0) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, p);
+    return;  // the rows that read this page are void
+  }
+  const int l = threadIdx.x % kRowLanes;
+  const int rows = a.c.hkv * kPage;
+  for (int u = threadIdx.x / kRowLanes; u < 2 * rows; u += kReadGroups) {
+    const bool is_k = u < rows;
+    const int r = is_k ? u : u - rows;
+    const size_t at = static_cast<size_t>(page) * rows + r;
+    const uint4 w = ldg_stream(static_cast<const uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128 + 16 * l);
+    const float sc = __uint_as_float(static_cast<uint32_t>((is_k ? a.c.k_scale : a.c.v_scale)[at]) << 23);
+    store_codes_bf16((is_k ? a.wide_k : a.wide_v) + (static_cast<size_t>(p) * rows + r) * 128, l, w, sc);
   }
 }
 
 }  // namespace
+
+cudaError_t launch_cache_widen(const SharedAttnArgs& a, cudaStream_t st) {
+  const long long pages = a.prefix_len / kPage + static_cast<long long>(a.c.num_seqs) * a.wide_own;
+  if (pages <= 0) return cudaSuccess;
+  count_launch();
+  return launch_pdl(cache_widen_kernel, dim3(static_cast<unsigned>(pages)), dim3(kReadThreads), 0, st, a);
+}
 
 cudaError_t launch_cache_append(const AppendArgs& a, bool f32, cudaStream_t st) {
   if (a.num_tokens <= 0) return cudaSuccess;

@@ -1,5 +1,5 @@
-// Launch wrappers of the document cache kernels (cache.cu, cache_attention.cu).
-// Device pointers throughout; every launch goes to `st` and returns the launch
+// Launch wrappers of the document cache kernels (cache.cu, cache_attention.cu,
+// cache_attention_tc.cu). Device pointers throughout; every launch goes to `st` and returns the launch
 // status.
 #pragma once
 #include <cuda.h>
@@ -82,14 +82,38 @@ struct SharedAttnArgs {
   PartStat* own_st;
   float* cont_o;         // [workers, stream_rows, 128]
   PartStat* cont_st;
+
+  // The tensor-core tiles' work: the prefix for all rows in prefix_splits key
+  // ranges of prefix_split (0: not its work), then every sequence's keys from
+  // seq_begin on in seq_splits ranges of seq_split (0: streamed instead).
+  // Part s of a row is dense_o[s], the prefix's first; dense_parts 0: a single
+  // part, written to out directly.
+  int prefix_split, prefix_splits;
+  int seq_begin, seq_split, seq_splits;
+  int dense_parts;
+  float* dense_o;  // [dense_parts, total_q * hq, 128]
+  PartStat* dense_st;
+  // The pool that the tiles read: the cache, or (codes) its pages widened to
+  // bf16 in list order, the prefix and then wide_own pages for every sequence.
+  bool wide_pages;
+  int wide_own, pool_pages;
+  __nv_bfloat16* wide_k;
+  __nv_bfloat16* wide_v;
 };
 
+constexpr int kTileRows = 256;  // query rows of a tensor-core CTA
 constexpr int kStreamWarps = 8;
 int stream_workers(int num_sms);
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     int num_sms, cudaStream_t st);
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st);
-cudaError_t launch_attention_simple(const SharedAttnArgs& a, cudaStream_t st);
+cudaError_t launch_attention_prefix(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    cudaStream_t st);
+cudaError_t launch_attention_sequences(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                       cudaStream_t st);
+// wide_k / wide_v from the prefix pages and, when wide_own > 0, every sequence's own.
+cudaError_t launch_cache_widen(const SharedAttnArgs& a, cudaStream_t st);
 cudaError_t set_pipeline_wait_limit_cache_attention(long long cycles);
+cudaError_t set_pipeline_wait_limit_cache_attention_tc(long long cycles);
 
 }  // namespace quail

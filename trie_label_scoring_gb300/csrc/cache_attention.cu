@@ -9,7 +9,7 @@
 #include <atomic>
 
 #include "attn_common.cuh"
-#include "cache.h"
+#include "cache_attn.cuh"
 #include "launch.cuh"
 #include "quail_internal.h"
 #include "sm103.cuh"
@@ -17,81 +17,6 @@
 namespace quail {
 
 namespace {
-
-constexpr int kPage = 16;
-
-struct QueryRange {
-  int lo, hi;  // rows of the sequence's queries
-  int len;     // keys
-  bool ok;
-};
-
-__device__ __forceinline__ QueryRange query_range(const SharedAttnArgs& a, int b) {
-  QueryRange r;
-  r.lo = a.q_offsets ? a.q_offsets[b] : b;
-  r.hi = a.q_offsets ? a.q_offsets[b + 1] : b + 1;
-  r.len = a.seq_len[b];
-  const int n = r.hi - r.lo;
-  r.ok = r.lo >= 0 && n >= 0 && n <= a.max_q && r.hi <= a.total_q && r.len >= 0 && r.len <= a.max_seq_len &&
-         (r.len == 0 || r.len - (a.causal ? n : 0) >= a.prefix_len);
-  return r;
-}
-
-// Block = (query of a sequence, KV head), one warp per query head of the group.
-__global__ void attention_simple_kernel(SharedAttnArgs a) {
-  grid_dependency_wait();
-  const int b = blockIdx.z, g = blockIdx.y, i = blockIdx.x;
-  const QueryRange r = query_range(a, b);
-  const int G = a.hq / a.c.hkv, lane = threadIdx.x & 31;
-  if (!r.ok) {
-    if (threadIdx.x == 0) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, b);
-    return;
-  }
-  if (i >= r.hi - r.lo) return;
-  const size_t row = r.lo + i;
-  const int n = a.causal && r.len > 0 ? r.len - (r.hi - r.lo) + i + 1 : r.len;
-  for (int hl = threadIdx.x >> 5; hl < G; hl += blockDim.x >> 5) {
-    const size_t h = row * a.hq + g * G + hl;
-    float q[4];
-    for (int d = 0; d < 4; ++d) q[d] = __bfloat162float(a.q[h * 128 + 4 * lane + d]);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < n; ++j) {
-      const int page = j < a.prefix_len ? a.prefix_pages[j / kPage]
-                                        : a.c.table[static_cast<size_t>(b) * a.c.max_pages + j / kPage];
-      if (page < 0 || page >= a.c.num_pages) {
-        raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, b);
-        return;
-      }
-      const size_t at = (static_cast<size_t>(page) * a.c.hkv + g) * kPage + j % kPage;
-      float k[4], v[4];
-      for (int d = 0; d < 4; ++d) {
-        const size_t e = at * 128 + 4 * lane + d;
-        if (a.c.codes) {
-          __nv_fp8_e4m3 kc, vc;
-          kc.__x = static_cast<const uint8_t*>(a.c.k)[e];
-          vc.__x = static_cast<const uint8_t*>(a.c.v)[e];
-          k[d] = static_cast<float>(kc) * __uint_as_float(static_cast<uint32_t>(a.c.k_scale[at]) << 23);
-          v[d] = static_cast<float>(vc) * __uint_as_float(static_cast<uint32_t>(a.c.v_scale[at]) << 23);
-        } else {
-          k[d] = __bfloat162float(static_cast<const bf16*>(a.c.k)[e]);
-          v[d] = __bfloat162float(static_cast<const bf16*>(a.c.v)[e]);
-        }
-      }
-      float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= a.scale_log2;
-      const float nm = fmaxf(m, s);
-      const float ref = nm == -INFINITY ? 0.f : nm;
-      const float f = exp2f(m - ref), p = exp2f(s - ref);
-      m = nm;
-      l = l * f + p;
-      for (int d = 0; d < 4; ++d) o[d] = o[d] * f + p * v[d];
-    }
-    for (int d = 0; d < 4; ++d) a.out[h * 128 + 4 * lane + d] = __float2bfloat16(n > 0 ? o[d] / l : 0.f);
-    if (lane == 0 && a.lse) a.lse[h] = n > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-  }
-}
-
 
 // ------------------------------------------------------------------ streaming kernel
 // Few query rows per KV head (a decoded token: G of them), so the work is
@@ -170,12 +95,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 __device__ __forceinline__ float pow2_byte(uint32_t e) { return __uint_as_float(e << 23); }
-
-// Pages of sequence b's own keys that its queries read (0: none, or a bad sequence).
-__device__ __forceinline__ int own_pages(const SharedAttnArgs& a, int b) {
-  const QueryRange r = query_range(a, b);
-  return r.ok && r.hi > r.lo && r.len > a.prefix_len ? (r.len - a.prefix_len + kPage - 1) / kPage : 0;
-}
 
 // A page of the work list: page j of the n of an item. Items: (row tile, head)
 // over the prefix, then (sequence, head) over own pages.
@@ -731,10 +650,12 @@ __device__ __forceinline__ float pow2_or_0(float x, float ref) {  // 2^(x - ref)
   return x == -INFINITY ? 0.f : exp2f(x - ref);
 }
 
+// A row's parts, in this order: the prefix by key range (tiles), the prefix in
+// pieces (streamed), the own keys in pieces (streamed) or by key range (tiles).
 struct Parts {
-  int prefix_n, own_n;  // pieces of the prefix / of the own keys
+  int prefix_dense, prefix_n, own_n, own_dense;
   size_t prefix_w, own_w;  // worker of the first piece
-  int prefix_r, own_r;  // row within the items' tiles
+  int prefix_r, own_r;     // row within the items' tiles
 };
 
 template <int WPR>
@@ -763,41 +684,60 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(SharedA
   QueryRange qr{0, 0, 0, false};
   if (live) qr = query_range(a, b);
   live = live && qr.ok && t >= qr.lo && t < qr.hi;
-  Parts p{0, 0, 0, 0, 0, 0};
+  Parts p{};
   if (live && qr.len > 0) {
-    const long long chunk = a.plan[1];
-    if (a.prefix_row_tiles > 0) {
-      const int flat = t * G + h % G;
-      const int pp = a.prefix_len / kPage;
-      const long long u = (static_cast<long long>(flat / a.stream_rows) * a.c.hkv + g) * pp;
-      p.prefix_w = static_cast<size_t>(u / chunk);
-      p.prefix_n = static_cast<int>((u + pp - 1) / chunk - u / chunk) + 1;
-      p.prefix_r = flat % a.stream_rows;
+    const int r = (t - qr.lo) * G + h % G;
+    p.prefix_dense = a.prefix_splits;
+    if (a.stream_rows > 0) {
+      const long long chunk = a.plan[1];
+      if (a.prefix_row_tiles > 0) {
+        const int flat = t * G + h % G;
+        const int pp = a.prefix_len / kPage;
+        const long long u = (static_cast<long long>(flat / a.stream_rows) * a.c.hkv + g) * pp;
+        p.prefix_w = static_cast<size_t>(u / chunk);
+        p.prefix_n = static_cast<int>((u + pp - 1) / chunk - u / chunk) + 1;
+        p.prefix_r = flat % a.stream_rows;
+      }
+      const int n = own_pages(a, b);
+      if (n > 0) {
+        const long long u = a.plan[2 + b] + static_cast<long long>(g) * n;
+        p.own_w = static_cast<size_t>(u / chunk);
+        p.own_n = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
+        p.own_r = r;
+      }
+      if (a.prefix_len == 0 && p.own_n == 1) live = false;  // written by its only worker
+    } else {
+      const int keys = tile_key_end(a, qr, r) - a.seq_begin;
+      p.own_dense = keys > 0 ? (keys + a.seq_split - 1) / a.seq_split : 0;
     }
-    const int n = own_pages(a, b);
-    if (n > 0) {
-      const long long u = a.plan[2 + b] + static_cast<long long>(g) * n;
-      p.own_w = static_cast<size_t>(u / chunk);
-      p.own_n = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
-      p.own_r = (t - qr.lo) * G + h % G;
-    }
-    if (a.prefix_len == 0 && p.own_n == 1) live = false;  // written by its only worker
   }
-  const int parts = p.prefix_n + p.own_n;
+  const int parts = p.prefix_dense + p.prefix_n + p.own_n + p.own_dense;
   float m_l = -INFINITY, m_o = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (live) {
     auto locate = [&](int i, const float*& o, const PartStat*& st) {
-      const bool pre = i < p.prefix_n;
-      const int k = pre ? i : i - p.prefix_n;
-      if (k == 0) {
-        o = (pre ? a.prefix_o : a.own_o) + row * 128;
-        st = (pre ? a.prefix_st : a.own_st) + row;
+      const float* po;
+      const PartStat* ps;
+      size_t at = static_cast<size_t>(row);
+      const int k = i - p.prefix_dense;
+      if (k < 0 || k >= p.prefix_n + p.own_n) {
+        const int s = k < 0 ? i : a.prefix_splits + k - p.prefix_n - p.own_n;
+        po = a.dense_o;
+        ps = a.dense_st;
+        at += static_cast<size_t>(s) * a.total_q * a.hq;
       } else {
-        const size_t at = ((pre ? p.prefix_w : p.own_w) + k) * a.stream_rows + (pre ? p.prefix_r : p.own_r);
-        o = a.cont_o + at * 128;
-        st = a.cont_st + at;
+        const bool pre = k < p.prefix_n;
+        const int piece = pre ? k : k - p.prefix_n;
+        po = pre ? a.prefix_o : a.own_o;
+        ps = pre ? a.prefix_st : a.own_st;
+        if (piece > 0) {
+          at = ((pre ? p.prefix_w : p.own_w) + piece) * a.stream_rows + (pre ? p.prefix_r : p.own_r);
+          po = a.cont_o;
+          ps = a.cont_st;
+        }
       }
+      o = po + at * 128;
+      st = ps + at;
     };
     constexpr int kBatch = 4;
     for (int i0 = sub; i0 < parts; i0 += WPR * kBatch) {
@@ -909,12 +849,6 @@ cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStre
     return launch_pdl(attention_join_kernel<kJoinWarps>, dim3(static_cast<unsigned>(rows)), dim3(32 * kJoinWarps), 0, st, a);
   return launch_pdl(attention_join_kernel<1>, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
                     dim3(32 * kJoinWarps), 0, st, a);
-}
-
-cudaError_t launch_attention_simple(const SharedAttnArgs& a, cudaStream_t st) {
-  if (a.total_q <= 0 || a.c.num_seqs <= 0) return cudaSuccess;
-  count_launch();
-  return launch_pdl(attention_simple_kernel, dim3(a.max_q, a.c.hkv, a.c.num_seqs), dim3(128), 0, st, a);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.

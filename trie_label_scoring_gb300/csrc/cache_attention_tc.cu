@@ -1,0 +1,503 @@
+// Attention over the paged document cache on tcgen05, for many query rows per
+// KV head. Two uses of one kernel:
+//   shared prefix -- the rows of every sequence of the batch side by side, so
+//                    the prefix keys are read and multiplied once for all;
+//   sequences     -- a sequence's own rows over its keys (all of them, or those
+//                    past the prefix), each row up to its causal limit.
+// A CTA owns 256 query rows as two 128-row tiles that share every K and V
+// block of 128 keys (8 pages):
+//   S_t = Q_t K^T   M 128, N 128 keys, K 128 dims; Q_t and K in shared memory
+//   O_t += P_t V    M 128, N 128 dims, K 128 keys; P_t (bf16) in TMEM over S_t
+// with fp32 S and O in TMEM (2 x (128 + 128) columns, all 512). The issue order
+// PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) keeps the tensor pipe on one tile while the
+// softmax warpgroup of the other works: a product is 512 tensor cycles, so each
+// softmax has 1,024 cycles for its 128 x 128 block.
+//
+// Roles (384 threads): warp 0 loads pages into one ring K0 V0 K1 V1 .., warp 1
+// owns TMEM and issues the MMAs, warps 4-7 and 8-11 are the softmax of tile 0
+// and 1, one thread per row (no exchange between threads), which also load
+// their Q row and write their O row.
+#include <atomic>
+
+#include "cache_attn.cuh"
+#include "launch.cuh"
+
+namespace quail {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kBlkKeys = 128;
+constexpr int kBlkPages = kBlkKeys / kPage;
+constexpr int kStages = 5;
+constexpr uint32_t kHalf = kBlkKeys * 128;  // 128 rows x 64 bf16, 128-byte rows, swizzled
+constexpr uint32_t kStage = 2 * kHalf;
+constexpr uint32_t kOffQ = 0;  // two tiles
+constexpr uint32_t kOffRing = 2 * kStage;
+constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
+constexpr uint32_t kTmemO = 256;
+// A block starts with 384 x 168 registers; the softmax keeps a whole row of S.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "the split draws on the launch's registers");
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+constexpr size_t kSmem = 1024 + kOffBar + sizeof(Bars);
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void tmem_ld_32cols_nowait(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+struct Item {
+  int row0, n_rows;  // this CTA's first row and the rows there are, per KV head
+  int k_lo, k_hi;    // keys
+  int b;             // sequence, or -1: the shared prefix for all rows
+  int g, split;
+};
+
+template <bool PREFIX>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tile_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(base + kOffBar);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.hq / a.c.hkv;
+  grid_dependency_wait();
+
+  Item it;
+  QueryRange qr{0, 0, 0, true};
+  it.g = blockIdx.y;
+  if constexpr (PREFIX) {
+    it.b = -1;
+    it.row0 = blockIdx.x * kTileRows;
+    it.n_rows = a.total_q * G;
+    it.split = blockIdx.z;
+    it.k_lo = it.split * a.prefix_split;
+    it.k_hi = min(a.prefix_len, it.k_lo + a.prefix_split);
+  } else {
+    // the rows that see the most keys first
+    it.b = blockIdx.z;
+    it.split = blockIdx.x % a.seq_splits;
+    it.row0 = (gridDim.x / a.seq_splits - 1 - blockIdx.x / a.seq_splits) * kTileRows;
+    qr = query_range(a, it.b);
+    if (!qr.ok) {
+      if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+        raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, it.b);
+      return;
+    }
+    it.n_rows = (qr.hi - qr.lo) * G;
+    if (it.row0 >= it.n_rows) return;
+    if (qr.len == 0) {  // no key: zeros, here or in the join
+      if (a.dense_parts == 0) {
+        for (int i = threadIdx.x; i < min(kTileRows, it.n_rows - it.row0) * 16; i += kThreads) {
+          const int r = it.row0 + i / 16;
+          const size_t row = static_cast<size_t>(qr.lo + r / G) * a.hq + it.g * G + r % G;
+          reinterpret_cast<uint4*>(a.out + row * 128)[i % 16] = make_uint4(0u, 0u, 0u, 0u);
+          if (i % 16 == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
+        }
+      }
+      return;
+    }
+    it.k_lo = a.seq_begin + it.split * a.seq_split;
+    it.k_hi = min(tile_key_end(a, qr, it.row0), it.k_lo + a.seq_split);
+    if (it.k_hi <= it.k_lo) return;
+  }
+  const bool two = it.n_rows - it.row0 > 128;
+  const int n_pages = (it.k_hi - it.k_lo + kPage - 1) / kPage;
+  const int n_blocks = (n_pages + kBlkPages - 1) / kBlkPages;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 128);
+      mbar_init(&bars->pv_done[t], 1);
+    }
+    mbar_init(&bars->q_full, 256);
+    mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = bars->tmem_slot;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0) {
+      // ---------------------------------------------- loader: lane q takes page q of a block
+      const int p0 = it.k_lo / kPage;
+      uint32_t armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int blk = 0; blk < n_blocks && ok; ++blk) {
+        const int np = min(kBlkPages, n_pages - blk * kBlkPages);
+        int page = -1;
+        if (lane < np) {
+          const int p = p0 + blk * kBlkPages + lane, pp = a.prefix_len / kPage;
+          if (a.wide_pages) {  // pages widened to bf16 in list order: the prefix, then each sequence's own
+            page = p < pp ? p : pp + it.b * a.wide_own + (p - pp);
+          } else {
+            page = p < pp ? a.prefix_pages[p] : a.c.table[static_cast<size_t>(it.b) * a.c.max_pages + p];
+          }
+          if (page < 0 || page >= a.pool_pages) {
+            raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, PREFIX ? 0 : it.b);
+            page = -1;  // not copied: the stage's old contents are consumed, the rows are void
+          }
+        }
+        const uint32_t good = __popc(__ballot_sync(0xffffffffu, page >= 0));
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const int idx = 2 * blk + kv, s = idx % kStages, use = idx / kStages;
+          if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty[s], static_cast<uint32_t>((use - 1) & 1), abort_flag))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (good > 0)
+              mbar_arrive_expect_tx(&bars->full[s], good * 2 * 2048);
+            else
+              mbar_arrive(&bars->full[s]);
+          }
+          __syncwarp();
+          if (page >= 0) {
+            uint8_t* dst = base + kOffRing + s * kStage + lane * 2048;
+            const int y = (page * a.c.hkv + it.g) * kPage;
+            const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
+            tma_load_2d(dst, tm, &bars->full[s], 0, y);
+            tma_load_2d(dst + kHalf, tm, &bars->full[s], 64, y);
+          }
+          armed = good > 0 ? armed | 1u << s : armed & ~(1u << s);
+          armed_parity = (use & 1) ? armed_parity | 1u << s : armed_parity & ~(1u << s);
+        }
+      }
+      if (lane == 0) {  // no copy may still be landing when the CTA exits
+        for (int s = 0; s < kStages; ++s) {
+          if (!(armed >> s & 1u)) continue;
+          const long long t0 = clock64();
+          while (!mbar_try_wait(smem_u32(&bars->full[s]), armed_parity >> s & 1u)) {
+            if (clock64() - t0 > kWaitLimitCycles) {
+              *abort_flag = 1;
+              break;
+            }
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ---------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, kBlkKeys);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16_f32_bmn(128, 128);
+      const uint64_t dq = smem_desc_sw128(smem_u32(base + kOffQ));
+      const uint64_t dk = smem_desc_sw128(smem_u32(base + kOffRing));
+      const uint64_t dv = smem_desc_sw128_mn(smem_u32(base + kOffRing), kHalf, 1024);
+      const uint32_t dv_lo = static_cast<uint32_t>(dv), dv_hi = static_cast<uint32_t>(dv >> 32);
+      auto issue_s = [&](int t, int j) {
+        const uint64_t k = dk + (((2 * j) % kStages * kStage) >> 4), q = dq + ((t * kStage) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+          umma_bf16(tmem_base + t * 128, q + off, k + off, idesc_s, ks != 0 ? 1u : 0u);
+        }
+        umma_commit(&bars->s_full[t]);
+      };
+      auto issue_pv = [&](int t, int j) {
+        const uint32_t v = dv_lo + (((2 * j + 1) % kStages * kStage) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // 16 keys = one page per instruction
+          umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
+                  (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&bars->pv_done[t]);
+      };
+      auto wait_full = [&](int idx) {
+        return mbar_wait(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag);
+      };
+      bool ok = mbar_wait(&bars->q_full, 0u, abort_flag) && wait_full(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        if (two) issue_s(1, 0);
+        umma_commit(&bars->empty[0]);
+      }
+      for (int j = 0; ok && j < n_blocks; ++j) {
+        const bool more = j + 1 < n_blocks;
+        const uint32_t par = static_cast<uint32_t>(j & 1);
+        ok = mbar_wait(&bars->p_full[0], par, abort_flag) && wait_full(2 * j + 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(0, j);
+        if (more) {
+          ok = wait_full(2 * j + 2);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, j + 1);
+        }
+        if (two) {
+          ok = mbar_wait(&bars->p_full[1], par, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, j);
+        }
+        umma_commit(&bars->empty[(2 * j + 1) % kStages]);
+        if (more) {
+          if (two) issue_s(1, j + 1);
+          umma_commit(&bars->empty[(2 * j + 2) % kStages]);
+        }
+      }
+      // every MMA of this thread completes before TMEM is released
+      umma_commit(&bars->drain);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(smem_u32(&bars->drain), 0u)) {
+        if (clock64() - t0 > kWaitLimitCycles) {
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ------------------------------------------------ softmax: thread <-> row of tile t
+    const int t = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;           // row of the tile = TMEM lane
+    const int rr = it.row0 + t * 128 + r;        // row of the item
+    const bool row_ok = rr < it.n_rows;
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    const size_t out_row =
+        row_ok ? static_cast<size_t>(qr.lo + rr / G) * a.hq + it.g * G + rr % G : 0;  // (token, head)
+    uint8_t* q_tile = base + kOffQ + t * kStage;
+    if (t == 0 || two) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row * 128);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint4 x = row_ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(q_tile + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+      }
+      fence_proxy_async_smem();
+    }
+    mbar_arrive(&bars->q_full);
+    if (t == 0 || two) {
+      const int limit = PREFIX || !row_ok ? it.k_hi : min(it.k_hi, row_limit(a, qr, rr));
+      const float scale = a.scale_log2;
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < n_blocks; ++j) {
+        const uint32_t par = static_cast<uint32_t>(j & 1);
+        const int key0 = it.k_lo + j * kBlkKeys;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], par, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32cols_nowait(lane_addr + t * 128 + c * 32, s + c * 32);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        const int valid = limit - key0;
+        if (__any_sync(0xffffffffu, valid < kBlkKeys)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = i < valid ? s[i] : -INFINITY;
+        }
+        float mx = -INFINITY;  // of the raw scores: the factor is positive
+#pragma unroll
+        for (int i = 0; i < 128; ++i) mx = fmaxf(mx, s[i]);
+        mx *= scale;
+        // the reference maximum moves only past +8 in base 2 (weights stay below 256)
+        const bool need = mx > m_ref + 8.f;
+        float alpha = 1.f;
+        if (need) {
+          alpha = exp2f(m_ref - mx);
+          m_ref = mx;
+          l *= alpha;
+        }
+        if (j >= 1 && __any_sync(0xffffffffu, need)) {
+          // O holds every product up to block j - 1 before it is rescaled
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], par ^ 1u, abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tmem_ld_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
+          }
+        }
+        // no key seen yet: the reference is still -inf, and every weight is 0
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        float p0 = 0.f, p1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // 64 keys: 32 columns of bf16 pairs
+          float w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e0 = fast_exp2(fmaf(s[c * 64 + 2 * i], scale, -ref));
+            const float e1 = fast_exp2(fmaf(s[c * 64 + 2 * i + 1], scale, -ref));
+            p0 += e0;
+            p1 += e1;
+            w[i] = __uint_as_float(pack_bf16(e0, e1));
+          }
+          tmem_st_32cols(lane_addr + t * 128 + c * 32, w);
+        }
+        l += p0 + p1;
+        // Keys past the range (tail of the last page, pages not loaded): their V
+        // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
+        // Tile 0 does it for both: its product is issued first.
+        const int in_range = it.k_hi - key0;
+        if (t == 0 && in_range < kBlkKeys) {
+          const int idx = 2 * j + 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag))) {
+            ok = false;
+            break;
+          }
+          uint8_t* v = base + kOffRing + (idx % kStages) * kStage;
+          for (int i = r; i < (kBlkKeys - in_range) * 16; i += 128) {
+            const int row = in_range + i / 16, c = i % 16;
+            *reinterpret_cast<uint4*>(v + (c / 8) * kHalf + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
+      }
+      // ---- rows out, through this tile's Q buffer (no MMA reads it any more):
+      // a warp's 32 rows as whole 256-byte lines
+      if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag))) {
+        tc_fence_after();
+        uint8_t* stage = q_tile + quarter * 8192;
+        const bool final = a.dense_parts == 0;
+        const float inv = 1.f / l;
+        const size_t part = (PREFIX ? it.split : a.prefix_splits + it.split) * static_cast<size_t>(a.total_q) * a.hq;
+        const int passes = final ? 1 : 2;  // 128 bf16, or twice 64 fp32
+#pragma unroll 1
+        for (int ps = 0; ps < passes; ++ps) {
+          __syncwarp();
+          if (final) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                const int chunk = c * 4 + i / 8;
+                *reinterpret_cast<uint4*>(stage + lane * 256 + ((chunk ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                               pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float o[32];
+              tmem_ld_32cols(lane_addr + kTmemO + t * 128 + ps * 64 + c * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const int chunk = c * 8 + i / 4;
+                *reinterpret_cast<float4*>(stage + lane * 256 + ((chunk ^ (lane & 7)) << 4)) =
+                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              }
+            }
+          }
+          __syncwarp();
+          for (int i = 0; i < 32; i += 2) {  // 16 lanes a row
+            const int row = i + (lane >> 4), c = lane & 15;
+            const size_t dst = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(out_row), row);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 256 + ((c ^ (row & 7)) << 4));
+            if (it.row0 + t * 128 + quarter * 32 + row >= it.n_rows) continue;
+            if (final)
+              reinterpret_cast<uint4*>(a.out + dst * 128)[c] = x;
+            else
+              reinterpret_cast<uint4*>(a.dense_o + (part + dst) * 128 + ps * 64)[c] = x;
+          }
+        }
+        if (row_ok) {
+          if (!final)
+            a.dense_st[part + out_row] = PartStat{m_ref, m_ref, l, 0.f};
+          else if (a.lse != nullptr)
+            a.lse[out_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 5000);
+}
+
+template <bool PREFIX>
+cudaError_t launch_tile(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, dim3 grid,
+                        cudaStream_t st) {
+  auto kern = attention_tile_kernel<PREFIX>;
+  static std::atomic<bool> configured[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;  // the register split would not add up
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_release);
+  }
+  count_launch();
+  return launch_pdl(kern, grid, dim3(kThreads), kSmem, st, a, tmK, tmV);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prefix(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                    cudaStream_t st) {
+  const long rows = static_cast<long>(a.total_q) * (a.hq / a.c.hkv);
+  return launch_tile<true>(a, tmK, tmV, dim3((rows + kTileRows - 1) / kTileRows, a.c.hkv, a.prefix_splits), st);
+}
+
+cudaError_t launch_attention_sequences(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                       cudaStream_t st) {
+  const long rows = static_cast<long>(a.max_q) * (a.hq / a.c.hkv);
+  return launch_tile<false>(a, tmK, tmV,
+                            dim3((rows + kTileRows - 1) / kTileRows * a.seq_splits, a.c.hkv, a.c.num_seqs), st);
+}
+
+// Test hook: this translation unit's copy of the pipeline wait limit.
+cudaError_t set_pipeline_wait_limit_cache_attention_tc(long long cycles) {
+  return cudaMemcpyToSymbol(g_pipeline_wait_limit, &cycles, sizeof(cycles));
+}
+
+}  // namespace quail
