@@ -942,9 +942,8 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   SharedAttnArgs t{};
   const long seq_rows = static_cast<long>(std::min(max_q, total_q)) * G;  // query rows of a sequence per KV head
   const long all_rows = static_cast<long>(total_q) * G;
-  t.stream_rows = seq_rows <= 16 ? 16 : seq_rows <= 32 ? 32 : 0;
-  const bool stream = t.stream_rows > 0;
-  const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > t.stream_rows : seq_rows < 128 && c->num_seqs > 1);
+  const bool stream = t.streamed = seq_rows <= 32;
+  const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > 16 : seq_rows < 128 && c->num_seqs > 1);
   if (tile_prefix)
     choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, &t.prefix_split,
                       &t.prefix_splits);
@@ -965,14 +964,14 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     const size_t workers = stream_workers(sms);
     t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
     if (prefix_len > 0 && !tile_prefix) {
-      t.prefix_row_tiles = static_cast<int>((all_rows + t.stream_rows - 1) / t.stream_rows);
+      t.prefix_row_tiles = static_cast<int>((all_rows + kStreamRows - 1) / kStreamRows);
       t.prefix_o = k.take<float>(rows * 128);
       t.prefix_st = k.take<PartStat>(rows);
     }
     t.own_o = k.take<float>(rows * 128);
     t.own_st = k.take<PartStat>(rows);
-    t.cont_o = k.take<float>(workers * t.stream_rows * 128);
-    t.cont_st = k.take<PartStat>(workers * t.stream_rows);
+    t.cont_o = k.take<float>(workers * kStreamRows * 128);
+    t.cont_st = k.take<PartStat>(workers * kStreamRows);
   }
   if (t.dense_parts > 0) {
     t.dense_o = k.take<float>(t.dense_parts * rows * 128);
@@ -1899,7 +1898,7 @@ quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, 
   a.eps = rms_eps;
   a.theta = rope_theta;
   a.q_out = static_cast<bf16*>(q_out);
-  CUDA_TRY(launch_cache_append(a, qkv_dtype == QUAIL_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)));
+  CUDA_TRY(launch_cache_append(a, qkv_dtype == QUAIL_DTYPE_F32, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
   return QUAIL_OK;
 }
 
@@ -1976,7 +1975,7 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   a.out = static_cast<bf16*>(out);
   a.lse = lse;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool streamed = a.stream_rows > 0;
+  const bool streamed = a.streamed;
   if (a.wide_pages) CUDA_TRY(launch_cache_widen(a, st));
   if (a.prefix_splits > 0 || !streamed) {
     CUtensorMap tK, tV;

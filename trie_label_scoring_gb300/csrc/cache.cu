@@ -30,44 +30,34 @@ constexpr int kRowLanes = 8;
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
-__device__ __forceinline__ void widen8(const uint4& u, float* x) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_bf16(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-
-// x[0..7] = dims 8l.., x[8..15] = dims 64 + 8l.. of the head row at p.
+// A lane's 16 elements of a head row as pairs: x[0..3] = dims 8l.., x[4..7] =
+// dims 64 + 8l.. ; Raw holds them as loaded.
 template <typename T>
-__device__ __forceinline__ void load_row(const T* p, int l, float (&x)[16]);
-template <>
-__device__ __forceinline__ void load_row<bf16>(const bf16* p, int l, float (&x)[16]) {
-  const uint4 a = ldg_stream(p + 8 * l), b = ldg_stream(p + 64 + 8 * l);
-  widen8(a, x);
-  widen8(b, x + 8);
-}
-template <>
-__device__ __forceinline__ void load_row<float>(const float* p, int l, float (&x)[16]) {
+struct Raw {
+  uint4 v[sizeof(T)];  // 2 x 16 bytes of bf16, 4 of fp32
+  __device__ __forceinline__ void load(const T* p, int l) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = __ldcs(reinterpret_cast<const float4*>(p + (i < 2 ? 0 : 64) + 8 * l + 4 * (i & 1)));
-    x[4 * i] = f.x;
-    x[4 * i + 1] = f.y;
-    x[4 * i + 2] = f.z;
-    x[4 * i + 3] = f.w;
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+      v[i] = ldg_stream(p + (2 * i < static_cast<int>(sizeof(T)) ? 0 : 64) + 8 * l + (sizeof(T) == 4 ? 4 * (i & 1) : 0));
   }
-}
+  __device__ __forceinline__ void pairs(float2 (&x)[8]) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2)
+        x[i] = unpack_bf16(w[i]);
+      else
+        x[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+  }
+};
 
-__device__ __forceinline__ void store_row_bf16(bf16* p, int l, const float (&x)[16]) {
+__device__ __forceinline__ void store_row_bf16(bf16* p, int l, const float2 (&x)[8]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float* y = x + 8 * h;
+  for (int h = 0; h < 2; ++h)
     *reinterpret_cast<uint4*>(p + 64 * h + 8 * l) =
-        make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-  }
+        make_uint4(pack_bf16(x[4 * h].x, x[4 * h].y), pack_bf16(x[4 * h + 1].x, x[4 * h + 1].y),
+                   pack_bf16(x[4 * h + 2].x, x[4 * h + 2].y), pack_bf16(x[4 * h + 3].x, x[4 * h + 3].y));
 }
 
 // Sum / maximum over the eight lanes of a row.
@@ -94,7 +84,7 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 
 // Row x as codes and scale; m is the row's largest finite |x|. An infinity
 // saturates to +-448 * 2^e, a NaN stays one.
-__device__ __forceinline__ void store_row_codes(uint8_t* p, uint8_t* scale, int l, const float (&x)[16], float m) {
+__device__ __forceinline__ void store_row_codes(uint8_t* p, uint8_t* scale, int l, const float2 (&x)[8], float m) {
   const int e = scale_exponent(m);
   const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 #pragma unroll
@@ -102,9 +92,9 @@ __device__ __forceinline__ void store_row_codes(uint8_t* p, uint8_t* scale, int 
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float* y = x + 8 * h + 4 * i;
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE, __NV_E4M3);
+      const float2 a = x[4 * h + 2 * i], b = x[4 * h + 2 * i + 1];
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a.x * inv, a.y * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(b.x * inv, b.y * inv), __NV_SATFINITE, __NV_E4M3);
       w[i] = lo | hi << 16;
     }
     *reinterpret_cast<uint2*>(p + 64 * h + 8 * l) = make_uint2(w[0], w[1]);
@@ -125,79 +115,112 @@ __device__ __forceinline__ int page_of(const CacheView& c, int seq, int pos, int
 }
 
 // ------------------------------------------------------------------ append
-// Block = one token: 16 row groups of eight lanes walk its hq + 2 hkv heads,
-// so the 64 angles of a position are computed once per group and shared by
-// the heads that the group takes.
-constexpr int kAppendThreads = 128;
+// Block = TOK tokens: thread i first computes angle i % 64 of token i / 64 and
+// looks up its page while the first rows are on their way, then 32 row groups
+// of eight lanes walk the tokens' hq + 2 hkv heads, each one row ahead with its
+// loads. (One angle per thread and block: with the angles of a position
+// computed by every group, the kernel was bound by its instructions.)
+constexpr int kAppendThreads = 256;
 constexpr int kAppendGroups = kAppendThreads / kRowLanes;
 
-template <typename T>
+template <typename T, int TOK>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs a, RopeTable rt) {
+  __shared__ __align__(16) float s_cos[TOK][64], s_sin[TOK][64];
+  __shared__ int s_page[TOK], s_slot[TOK];  // page -1: nothing of the token is written
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = blockIdx.x;
-  const int group = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
-  const int seq = a.seq[t];
-  if (seq < 0) return;  // a padding token: nothing of it is written
-  const int pos = a.pos[t];
-  const int page = page_of(a.c, seq, pos, t);
-  if (page < 0) return;
-  const int heads = a.hq + 2 * a.c.hkv;
-  const T* row = static_cast<const T*>(a.qkv) + static_cast<long long>(t) * a.ld;
-  float cs[8], sn[8];
-  if (a.theta > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rope_cs(pos, rt.w[8 * l + i], cs[i], sn[i]);
-  }
-  // whole warps take the loop together: the row sums shuffle over all lanes
-  for (int h0 = 0; h0 < heads; h0 += kAppendGroups) {
-    const int h = h0 + group;
-    const bool live = h < heads;
-    const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.c.hkv;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    if (live) load_row(row + h * 128, l, x);
-    const bf16* gain = is_q ? a.gq : is_k ? a.gk : nullptr;
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    ss = row_sum(ss);
-    if (gain != nullptr) {
-      const float r = rsqrtf(ss * (1.f / 128.f) + a.eps);
-      float g[16];
-      widen8(*reinterpret_cast<const uint4*>(gain + 8 * l), g);
-      widen8(*reinterpret_cast<const uint4*>(gain + 64 + 8 * l), g + 8);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = x[i] * r * g[i];
+  const int t0 = blockIdx.x * TOK;
+  const int l = threadIdx.x % kRowLanes, heads = a.hq + 2 * a.c.hkv;
+  const int rows = min(TOK, a.num_tokens - t0) * heads;
+  int r = threadIdx.x / kRowLanes, tok = r / heads, h = r - tok * heads;
+  const T* qkv = static_cast<const T*>(a.qkv);
+  Raw<T> next;
+  if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, l);
+  if (threadIdx.x < 64 * TOK) {
+    const int i = threadIdx.x / 64, j = threadIdx.x % 64, t = t0 + i;
+    const int seq = t < a.num_tokens ? a.seq[t] : -1;
+    const int pos = seq >= 0 ? a.pos[t] : 0;
+    if (j == 0) {
+      s_page[i] = seq < 0 ? -1 : page_of(a.c, seq, pos, t);
+      s_slot[i] = pos % kPage;
     }
-    if (a.theta > 0.f && (is_q || is_k)) {
+    float c = 1.f, sn = 0.f;
+    if (a.theta > 0.f) rope_cs(pos, rt.w[j], c, sn);
+    s_cos[i][j] = c;
+    s_sin[i][j] = sn;
+  }
+  uint4 gain[2][2];  // of queries, keys
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x1 = x[i], x2 = x[i + 8];
-        x[i] = x1 * cs[i] - x2 * sn[i];
-        x[i + 8] = x2 * cs[i] + x1 * sn[i];
+  for (int i = 0; i < 2; ++i) {
+    const bf16* g = i == 0 ? a.gq : a.gk;
+    gain[i][0] = gain[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (g != nullptr) {
+      gain[i][0] = *reinterpret_cast<const uint4*>(g + 8 * l);
+      gain[i][1] = *reinterpret_cast<const uint4*>(g + 64 + 8 * l);
+    }
+  }
+  __syncthreads();
+  const int rounds = (rows + kAppendGroups - 1) / kAppendGroups;
+  // whole warps take every round: the row sums shuffle over all lanes
+  for (int it = 0; it < rounds; ++it) {
+    const Raw<T> raw = next;
+    const bool in = r < rows;
+    const int ct = in ? tok : 0, ch = h;  // rows past the end index the tables of token 0, and write nothing
+    r += kAppendGroups;
+    h += kAppendGroups;
+    while (h >= heads) {
+      h -= heads;
+      ++tok;
+    }
+    if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, l);
+    const int page = in ? s_page[ct] : -1;
+    const bool live = page >= 0;
+    const bool is_q = ch < a.hq, is_k = !is_q && ch < a.hq + a.c.hkv, is_v = !is_q && !is_k;
+    float2 x[8];
+    raw.pairs(x);
+    if (__any_sync(0xffffffffu, live && !is_v)) {
+      const bool norm = is_q ? a.gq != nullptr : a.gk != nullptr;
+      float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) ss = fma2(x[i], x[i], ss);
+      const float f = row_sum(ss.x + ss.y);
+      if (norm && !is_v) {
+        const float rs = rsqrtf(f * (1.f / 128.f) + a.eps);
+        const float2 r2 = make_float2(rs, rs);
+        const uint4 g0 = is_q ? gain[0][0] : gain[1][0], g1 = is_q ? gain[0][1] : gain[1][1];
+        const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(x[i], r2), unpack_bf16(gw[i]));
+      }
+      if (a.theta > 0.f && !is_v) {
+        const float2* c2 = reinterpret_cast<const float2*>(&s_cos[ct][8 * l]);
+        const float2* s2 = reinterpret_cast<const float2*>(&s_sin[ct][8 * l]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x1 = x[i], x2 = x[i + 4], c = c2[i], sn = s2[i];
+          x[i] = fma2(x1, c, mul2(make_float2(-x2.x, -x2.y), sn));
+          x[i + 4] = fma2(x2, c, mul2(x1, sn));
+        }
       }
     }
-    if (live && is_q) {
-      if (a.q_out != nullptr) store_row_bf16(a.q_out + (static_cast<size_t>(t) * a.hq + h) * 128, l, x);
-    }
-    // the codes' row maximum shuffles: every lane of the warp goes through it
-    const int g = h - a.hq - (is_k ? 0 : a.c.hkv);
-    const size_t at = (static_cast<size_t>(page) * a.c.hkv + g) * kPage + pos % kPage;
+    if (live && is_q && a.q_out != nullptr)
+      store_row_bf16(a.q_out + (static_cast<size_t>(t0 + ct) * a.hq + ch) * 128, l, x);
     const bool kv = live && !is_q;
+    const int g = ch - a.hq - (is_k ? 0 : a.c.hkv);
+    const size_t at = (static_cast<size_t>(page) * a.c.hkv + g) * kPage + s_slot[ct];
     if (!a.c.codes) {
       if (kv) store_row_bf16(static_cast<bf16*>(is_k ? a.c.k : a.c.v) + at * 128, l, x);
-    } else {
+    } else if (__any_sync(0xffffffffu, kv)) {
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = fabsf(x[i]);
-        m = fmaxf(m, v < INFINITY ? v : 0.f);
+      for (int i = 0; i < 8; ++i) {
+        const float u = fabsf(x[i].x), v = fabsf(x[i].y);
+        m = fmaxf(m, fmaxf(u < INFINITY ? u : 0.f, v < INFINITY ? v : 0.f));
       }
       m = row_max(m);
-      if (kv) store_row_codes(static_cast<uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128,
-                              (is_k ? a.c.k_scale : a.c.v_scale) + at, l, x, m);
+      if (kv)
+        store_row_codes(static_cast<uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128, (is_k ? a.c.k_scale : a.c.v_scale) + at,
+                        l, x, m);
     }
   }
 }
@@ -226,42 +249,76 @@ __device__ __forceinline__ void store_codes_bf16(bf16* out, int l, const uint4& 
   *reinterpret_cast<uint4*>(out + 16 * l + 8) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// Block = a few consecutive tokens: their pages are looked up once, then every
+// group copies kReadRows rows at a time, loads first.
+constexpr int kReadRows = 4;
+constexpr int kReadTokens = 64;  // at most
+
+inline __host__ __device__ int read_tokens(int hkv) {  // tokens of a block: about 4 x 32 rows
+  const int n = kReadRows * kReadGroups / (2 * hkv);
+  return n < 1 ? 1 : n > kReadTokens ? kReadTokens : n;
+}
+
+template <bool CODES>
 __global__ void __launch_bounds__(kReadThreads)
     cache_read_kernel(CacheView c, const int* seq, const int* pos, int num_tokens, bf16* k_out, bf16* v_out) {
+  __shared__ long long first_row[kReadTokens];  // row of the token's slot for head 0; -1: nothing to read
   grid_dependency_wait();
   grid_launch_dependents();
-  const int l = threadIdx.x % kRowLanes;
-  const long long u = static_cast<long long>(blockIdx.x) * kReadGroups + threadIdx.x / kRowLanes;
-  const int per = 2 * c.hkv;
-  const int t = static_cast<int>(u / per), r = static_cast<int>(u % per);
-  if (t >= num_tokens) return;
-  const int s = seq[t];
-  if (s < 0) return;
-  const int p = pos[t];
-  const int page = page_of(c, s, p, t);
-  if (page < 0) return;
-  const bool is_k = r < c.hkv;
-  const int h = is_k ? r : r - c.hkv;
-  bf16* out = is_k ? k_out : v_out;
-  if (out == nullptr) return;
-  out += (static_cast<size_t>(t) * c.hkv + h) * 128;
-  const size_t at = (static_cast<size_t>(page) * c.hkv + h) * kPage + p % kPage;
-  if (!c.codes) {
-    const bf16* in = static_cast<const bf16*>(is_k ? c.k : c.v) + at * 128;
-    const uint4 a = ldg_stream(in + 8 * l), b = ldg_stream(in + 64 + 8 * l);
-    *reinterpret_cast<uint4*>(out + 8 * l) = a;
-    *reinterpret_cast<uint4*>(out + 64 + 8 * l) = b;
-  } else {
-    const uint4 w = ldg_stream(static_cast<const uint8_t*>(is_k ? c.k : c.v) + at * 128 + 16 * l);
-    const int e = (is_k ? c.k_scale : c.v_scale)[at];
-    const float sc = __uint_as_float(static_cast<uint32_t>(e) << 23);
-    store_codes_bf16(out, l, w, sc);
+  const int tokens = read_tokens(c.hkv);
+  const int t0 = blockIdx.x * tokens;
+  if (threadIdx.x < tokens) {
+    const int t = t0 + threadIdx.x;
+    long long at = -1;
+    if (t < num_tokens) {
+      const int s = seq[t], p = pos[t];
+      const int page = s < 0 ? -1 : page_of(c, s, p, t);
+      if (page >= 0) at = static_cast<long long>(page) * c.hkv * kPage + p % kPage;
+    }
+    first_row[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int l = threadIdx.x % kRowLanes, per = 2 * c.hkv, rows = tokens * per;
+  for (int r0 = threadIdx.x / kRowLanes; r0 < rows; r0 += kReadRows * kReadGroups) {
+    uint4 x[kReadRows][CODES ? 1 : 2];
+    float sc[kReadRows];
+    bf16* out[kReadRows];
+#pragma unroll
+    for (int k = 0; k < kReadRows; ++k) {
+      const int r = r0 + k * kReadGroups;
+      const int t = r / per, kvh = r - t * per;
+      const bool is_k = kvh < c.hkv;
+      const int h = is_k ? kvh : kvh - c.hkv;
+      out[k] = is_k ? k_out : v_out;
+      if (r >= rows || first_row[r < rows ? t : 0] < 0) out[k] = nullptr;
+      if (out[k] == nullptr) continue;
+      out[k] += (static_cast<size_t>(t0 + t) * c.hkv + h) * 128;
+      const size_t at = static_cast<size_t>(first_row[t]) + static_cast<size_t>(h) * kPage;
+      if constexpr (CODES) {
+        x[k][0] = ldg_stream(static_cast<const uint8_t*>(is_k ? c.k : c.v) + at * 128 + 16 * l);
+        sc[k] = __uint_as_float(static_cast<uint32_t>((is_k ? c.k_scale : c.v_scale)[at]) << 23);
+      } else {
+        const bf16* in = static_cast<const bf16*>(is_k ? c.k : c.v) + at * 128;
+        x[k][0] = ldg_stream(in + 8 * l);
+        x[k][1] = ldg_stream(in + 64 + 8 * l);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kReadRows; ++k) {
+      if (out[k] == nullptr) continue;
+      if constexpr (CODES) {
+        store_codes_bf16(out[k], l, x[k][0], sc[k]);
+      } else {
+        *reinterpret_cast<uint4*>(out[k] + 8 * l) = x[k][0];
+        *reinterpret_cast<uint4*>(out[k] + 64 + 8 * l) = x[k][1];
+      }
+    }
   }
 }
 
 // ------------------------------------------------------------------ widen
-// Block = one page of the list (the prefix, then wide_own pages per sequence):
-// its K and V rows as bf16 for the tensor-core tiles. Exact, and small next to
+// Block = one head of a page of the list (the prefix, then wide_own pages per
+// sequence): its K and V rows as bf16 for the tensor-core tiles. Exact, and small next to
 // their work: the tiles have 256 rows to multiply with every key.
 __global__ void __launch_bounds__(kReadThreads) cache_widen_kernel(SharedAttnArgs a) {
   grid_dependency_wait();
@@ -279,11 +336,12 @@ __global__ void __launch_bounds__(kReadThreads) cache_widen_kernel(SharedAttnArg
     if (threadIdx.x == 0) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, p);
     return;  // the rows that read this page are void
   }
-  const int l = threadIdx.x % kRowLanes;
+  // y: 32 rows of the page, K and V of one head (16 slots each)
+  const int l = threadIdx.x % kRowLanes, u = threadIdx.x / kRowLanes;
   const int rows = a.c.hkv * kPage;
-  for (int u = threadIdx.x / kRowLanes; u < 2 * rows; u += kReadGroups) {
-    const bool is_k = u < rows;
-    const int r = is_k ? u : u - rows;
+  {
+    const bool is_k = u < kPage;
+    const int r = blockIdx.y * kPage + (is_k ? u : u - kPage);
     const size_t at = static_cast<size_t>(page) * rows + r;
     const uint4 w = ldg_stream(static_cast<const uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128 + 16 * l);
     const float sc = __uint_as_float(static_cast<uint32_t>((is_k ? a.c.k_scale : a.c.v_scale)[at]) << 23);
@@ -297,24 +355,36 @@ cudaError_t launch_cache_widen(const SharedAttnArgs& a, cudaStream_t st) {
   const long long pages = a.prefix_len / kPage + static_cast<long long>(a.c.num_seqs) * a.wide_own;
   if (pages <= 0) return cudaSuccess;
   count_launch();
-  return launch_pdl(cache_widen_kernel, dim3(static_cast<unsigned>(pages)), dim3(kReadThreads), 0, st, a);
+  return launch_pdl(cache_widen_kernel, dim3(static_cast<unsigned>(pages), a.c.hkv), dim3(kReadThreads), 0, st, a);
 }
 
-cudaError_t launch_cache_append(const AppendArgs& a, bool f32, cudaStream_t st) {
+namespace {
+
+template <typename T>
+cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t st) {
+  const RopeTable rt = a.theta > 0.f ? make_rope_table(a.theta) : RopeTable{};
+  // few tokens: a block each, so that they spread over the SMs
+  if (a.num_tokens <= 4 * num_sms)
+    return launch_pdl(cache_append_kernel<T, 1>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt);
+  return launch_pdl(cache_append_kernel<T, 4>, dim3((a.num_tokens + 3) / 4), dim3(kAppendThreads), 0, st, a, rt);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendArgs& a, bool f32, int num_sms, cudaStream_t st) {
   if (a.num_tokens <= 0) return cudaSuccess;
   count_launch();
-  const RopeTable rt = a.theta > 0.f ? make_rope_table(a.theta) : RopeTable{};
-  return f32 ? launch_pdl(cache_append_kernel<float>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt)
-             : launch_pdl(cache_append_kernel<bf16>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt);
+  return f32 ? launch_append<float>(a, num_sms, st) : launch_append<bf16>(a, num_sms, st);
 }
 
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens, bf16* k_out,
                               bf16* v_out, cudaStream_t st) {
-  const long long rows = static_cast<long long>(num_tokens) * 2 * c.hkv;
-  if (rows <= 0) return cudaSuccess;
+  if (num_tokens <= 0) return cudaSuccess;
+  const int tokens = read_tokens(c.hkv);
+  const dim3 grid(static_cast<unsigned>((num_tokens + static_cast<long long>(tokens) - 1) / tokens));
   count_launch();
-  return launch_pdl(cache_read_kernel, dim3(static_cast<unsigned>((rows + kReadGroups - 1) / kReadGroups)),
-                    dim3(kReadThreads), 0, st, c, seq, pos, num_tokens, k_out, v_out);
+  return c.codes ? launch_pdl(cache_read_kernel<true>, grid, dim3(kReadThreads), 0, st, c, seq, pos, num_tokens, k_out, v_out)
+                 : launch_pdl(cache_read_kernel<false>, grid, dim3(kReadThreads), 0, st, c, seq, pos, num_tokens, k_out, v_out);
 }
 
 }  // namespace quail

@@ -39,7 +39,7 @@ struct AppendArgs {
   float theta;  // 0: no rotation
   __nv_bfloat16* q_out;  // nullable
 };
-cudaError_t launch_cache_append(const AppendArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_cache_append(const AppendArgs& a, bool f32, int num_sms, cudaStream_t st);
 
 // k_out / v_out [num_tokens, hkv, 128] bf16 (either may be null).
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens,
@@ -67,11 +67,12 @@ struct SharedAttnArgs {
   __nv_bfloat16* out;
   float* lse;  // nullable
 
-  // The streaming kernel's work list: row_tiles x hkv passes over the prefix
-  // pages (0: the prefix is not its work), then every sequence's own pages,
-  // cut into equal chunks over the workers. plan: [0] units, [1] chunk, [2 + b]
+  // The streaming kernel's work list: prefix_row_tiles x hkv passes over the
+  // prefix pages (0: the prefix is not its work), then every sequence's own pages
+  // per KV head and row tile, in units of stream_unit_pages, cut into equal chunks over the
+  // workers. plan: [0] units, [1] chunk, [2 + b]
   // first unit of sequence b, [2 + num_seqs] past the last.
-  int stream_rows;       // rows of a tile, 16 or 32
+  bool streamed;
   int prefix_row_tiles;
   long long* plan;
   // Parts, each [rows, 128] fp32 and a PartStat per row; rows are (token, head)
@@ -80,7 +81,7 @@ struct SharedAttnArgs {
   PartStat* prefix_st;
   float* own_o;          // pieces that begin a sequence's own keys
   PartStat* own_st;
-  float* cont_o;         // [workers, stream_rows, 128]
+  float* cont_o;         // [workers, kStreamRows, 128]
   PartStat* cont_st;
 
   // The tensor-core tiles' work: the prefix for all rows in prefix_splits key
@@ -102,7 +103,10 @@ struct SharedAttnArgs {
 };
 
 constexpr int kTileRows = 256;  // query rows of a tensor-core CTA
-constexpr int kStreamWarps = 8;
+constexpr int kStreamWarps = 12;
+constexpr int kStreamRows = 16;  // query rows of a streamed item
+// Pages that a streaming worker takes at a time.
+__host__ __device__ constexpr int stream_unit_pages(bool codes) { return codes ? 2 : 1; }
 int stream_workers(int num_sms);
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     int num_sms, cudaStream_t st);

@@ -4,8 +4,6 @@
 // The keys of a row are cut into parts (the shared prefix, pieces of the
 // sequence's own pages); each part keeps (max, sum, sum of weighted values)
 // and the join rescales them to one maximum.
-#include <cuda_fp8.h>
-
 #include <atomic>
 
 #include "attn_common.cuh"
@@ -28,29 +26,29 @@ namespace {
 // never drains; no barrier joins warps. Pieces of an item that several workers
 // share are joined by the second kernel.
 //
-// Per page of 16 keys: S = Q K^T and O += P V on mma.sync m16n8k16 with the 16
-// (or 2 x 16) query rows as M. Over bf16 pages q and P are bf16; over e4m3
+// Per page of 16 keys (two e4m3 pages at a time, so that the bookkeeping and the
+// row reductions are shared by 32 keys): S = Q K^T and O += P V on mma.sync
+// m16n8k16 with 16 query rows as M. A sequence with more rows is several items
+// in a row, so its pages come from L2 after the first. Over bf16 pages q and P are bf16; over e4m3
 // pages the codes widen exactly to fp16, q is scaled by a power of two per row
 // (exact) and P is rounded to fp16. The key's power of two multiplies its score,
 // the value's is added to the exponent of its weight: o and l keep separate
 // maxima, so that value rows of any scale neither overflow P nor starve the sum.
-template <bool CODES, int MT>
+template <bool CODES>
 struct StreamCfg {
+  static constexpr int kUnit = stream_unit_pages(CODES);   // pages a stage
   static constexpr uint32_t kPlane = CODES ? 2048 : 4096;  // K or V of one (page, head)
-  static constexpr uint32_t kStage = 2 * kPlane;
-  static constexpr int kStages = (CODES ? 2 : 1) * (MT == 1 ? 3 : 2);
+  static constexpr uint32_t kStage = 2 * kPlane * kUnit;
+  static constexpr int kStages = 2;
   static constexpr uint32_t kRing = kStreamWarps * kStages * kStage;
-  static constexpr uint32_t kQ = MT == 1 ? 0 : kStreamWarps * MT * 4096;  // q fragments (16 rows: in registers)
-  static constexpr uint32_t kScales = CODES ? kStreamWarps * kStages * 32 : 0;  // 16 key, 16 value exponents
+  static constexpr uint32_t kScales = CODES ? kStreamWarps * kStages * kUnit * 32 : 0;  // key, value exponents
   static constexpr uint32_t kBars = kStreamWarps * kStages * 8;
   static constexpr uint32_t kScan = (kStreamWarps * 32 + 1) * 8;
-  static constexpr size_t kSmem = 1024 + kRing + kQ + kScales + kBars + kScan + 16;
+  static constexpr size_t kSmem = 1024 + kRing + kScales + kBars + kScan + 16;
 };
-static_assert(StreamCfg<false, 1>::kSmem <= 227 * 1024 && StreamCfg<false, 2>::kSmem <= 227 * 1024 &&
-                  StreamCfg<true, 1>::kSmem <= 227 * 1024 && StreamCfg<true, 2>::kSmem <= 227 * 1024,
-              "shared memory");
+static_assert(StreamCfg<false>::kSmem <= 227 * 1024 && StreamCfg<true>::kSmem <= 227 * 1024, "shared memory");
 constexpr int kStreamThreads = 32 * kStreamWarps;
-constexpr int kMinChunk = 4;  // pages a worker takes at least
+constexpr int kMinChunk = 2;  // units a worker takes at least
 
 __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
 
@@ -79,10 +77,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes (low 16 bits of v) as fp16.
-__device__ __forceinline__ uint32_t widen2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -96,67 +98,82 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 }
 __device__ __forceinline__ float pow2_byte(uint32_t e) { return __uint_as_float(e << 23); }
 
-// A page of the work list: page j of the n of an item. Items: (row tile, head)
-// over the prefix, then (sequence, head) over own pages.
+// A unit of the work list (a stage: UNIT pages, fewer at an item's end): unit j
+// of the n of an item. Items: (row tile, head) over the prefix, then (sequence,
+// head) over own pages.
 struct Cursor {
   bool own;
-  int b;  // row tile or sequence
-  int g;
+  int b;        // sequence, or row tile of the whole batch
+  int x, X;     // item: x = head * tiles + row tile of the sequence (prefix: the head), of X
   int j, n;
 };
 
-// First sequence at or after b with own pages (n of them); num_seqs if none.
+template <int UNIT>
+__device__ __forceinline__ int own_units(const SharedAttnArgs& a, int b) {
+  return (own_pages(a, b) + UNIT - 1) / UNIT;
+}
+// Items of sequence b: its row tiles for every KV head.
+__device__ __forceinline__ int own_items(const SharedAttnArgs& a, int b) {
+  const int n = a.q_offsets ? a.q_offsets[b + 1] - a.q_offsets[b] : 1;
+  return (n * (a.hq / a.c.hkv) + kStreamRows - 1) / kStreamRows * a.c.hkv;
+}
+// All units of sequence b; b may lie past the last.
+template <int UNIT>
+__device__ __forceinline__ long long seq_units(const SharedAttnArgs& a, int b, int* n) {
+  *n = b < a.c.num_seqs ? own_units<UNIT>(a, b) : 0;
+  return *n > 0 ? static_cast<long long>(*n) * own_items(a, b) : 0;
+}
+// First sequence at or after b with own pages; num_seqs if none.
+template <int UNIT>
 __device__ __forceinline__ void seek_own(const SharedAttnArgs& a, Cursor& c, int b, int lane) {
   c.own = true;
-  c.g = c.j = 0;
+  c.x = c.j = 0;
   for (; b < a.c.num_seqs; b += 32) {
-    const int n = b + lane < a.c.num_seqs ? own_pages(a, b + lane) : 0;
+    const int n = b + lane < a.c.num_seqs ? own_units<UNIT>(a, b + lane) : 0;
     const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
     if (some != 0) {
       const int first = __ffs(some) - 1;
       c.b = b + first;
       c.n = __shfl_sync(0xffffffffu, n, first);
+      c.X = own_items(a, c.b);
       return;
     }
   }
   c.b = a.c.num_seqs;
-  c.n = 0;
+  c.n = c.X = 0;
 }
-__device__ __forceinline__ void next_page(const SharedAttnArgs& a, Cursor& c, int lane) {
+template <int UNIT>
+__device__ __forceinline__ void next_unit(const SharedAttnArgs& a, Cursor& c, int lane) {
   if (++c.j < c.n) return;
   c.j = 0;
-  if (++c.g < a.c.hkv) return;
-  c.g = 0;
+  if (++c.x < c.X) return;
+  c.x = 0;
   if (c.own) {
-    seek_own(a, c, c.b + 1, lane);
+    seek_own<UNIT>(a, c, c.b + 1, lane);
   } else if (++c.b >= a.prefix_row_tiles) {
-    seek_own(a, c, 0, lane);
+    seek_own<UNIT>(a, c, 0, lane);
   }
 }
+// KV head of the cursor's item.
+__device__ __forceinline__ int item_head(const SharedAttnArgs& a, const Cursor& c) {
+  return c.own ? c.x / (c.X / a.c.hkv) : c.x;
+}
 
-template <bool CODES, int MT>
+template <bool CODES>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     attention_stream_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV) {
-  using Cfg = StreamCfg<CODES, MT>;
-  constexpr int kStages = Cfg::kStages;
-  constexpr int kRows = 16 * MT;
+  using Cfg = StreamCfg<CODES>;
+  constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit;
+  constexpr int kKeys = kUnit * kPage;  // keys of a unit
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = base + warp * kStages * Cfg::kStage;
-  uint4* qs = reinterpret_cast<uint4*>(base + Cfg::kRing + warp * MT * 4096) + lane;  // [tile][ks][lane]
-  uint4 qr8[8] = {};
-  auto q_frag = [&](int t, int ks) {
-    if constexpr (MT == 1)
-      return qr8[ks];
-    else
-      return qs[(t * 8 + ks) * 32];
-  };
-  uint8_t* scales = base + Cfg::kRing + Cfg::kQ + warp * kStages * 32;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Cfg::kRing + Cfg::kQ + Cfg::kScales) + warp * kStages;
-  long long* scan = reinterpret_cast<long long*>(base + Cfg::kRing + Cfg::kQ + Cfg::kScales + Cfg::kBars);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + Cfg::kRing + Cfg::kQ + Cfg::kScales + Cfg::kBars +
+  uint8_t* scales = base + Cfg::kRing + warp * kStages * kUnit * 32;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + Cfg::kRing + Cfg::kScales) + warp * kStages;
+  long long* scan = reinterpret_cast<long long*>(base + Cfg::kRing + Cfg::kScales + Cfg::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + Cfg::kRing + Cfg::kScales + Cfg::kBars +
                                                              Cfg::kScan);
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
@@ -173,10 +190,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     if (blockIdx.x == 0 && !query_range(a, b).ok) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, b);
-    mine += static_cast<long long>(own_pages(a, b)) * a.c.hkv;
+    int n;
+    mine += seq_units<kUnit>(a, b, &n);
   }
-  const int pp = a.prefix_len / kPage;
-  const long long prefix_units = static_cast<long long>(a.prefix_row_tiles) * a.c.hkv * pp;
+  const int pp = a.prefix_len / kPage, pu = (pp + kUnit - 1) / kUnit;
+  const long long prefix_units = static_cast<long long>(a.prefix_row_tiles) * a.c.hkv * pu;
   {
     long long x = mine;
 #pragma unroll
@@ -200,7 +218,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     long long at = prefix_units + scan[threadIdx.x];
     for (int b = b0; b < b1; ++b) {
       a.plan[2 + b] = at;
-      at += static_cast<long long>(own_pages(a, b)) * a.c.hkv;
+      int n;
+      at += seq_units<kUnit>(a, b, &n);
     }
     if (threadIdx.x == 0) {
       a.plan[0] = units;
@@ -217,12 +236,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // ---- where the chunk begins
   Cursor cc;
   if (u0 < prefix_units) {
-    const long long item = u0 / pp;
+    const long long item = u0 / pu;
     cc.own = false;
     cc.b = static_cast<int>(item / a.c.hkv);
-    cc.g = static_cast<int>(item % a.c.hkv);
-    cc.j = static_cast<int>(u0 % pp);
-    cc.n = pp;
+    cc.x = static_cast<int>(item % a.c.hkv);
+    cc.X = a.c.hkv;
+    cc.j = static_cast<int>(u0 % pu);
+    cc.n = pu;
   } else {
     const long long v = u0 - prefix_units;
     int lo = 0, hi = kStreamThreads;  // scan[lo] <= v < scan[hi]
@@ -235,8 +255,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     long long at = scan[lo];
     for (int b = lo * per;; b += 32) {
-      const int n = b + lane < B ? own_pages(a, b + lane) : 0;
-      long long x = static_cast<long long>(n) * a.c.hkv;
+      int n;
+      long long x = seq_units<kUnit>(a, b + lane, &n);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -249,8 +269,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         cc.own = true;
         cc.b = b + f;
         cc.n = __shfl_sync(0xffffffffu, n, f);
-        const long long rem = v - (end - static_cast<long long>(cc.n) * a.c.hkv);
-        cc.g = static_cast<int>(rem / cc.n);
+        cc.X = own_items(a, cc.b);
+        const long long rem = v - (end - static_cast<long long>(cc.n) * cc.X);
+        cc.x = static_cast<int>(rem / cc.n);
         cc.j = static_cast<int>(rem % cc.n);
         break;
       }
@@ -259,171 +280,192 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
   }
 
-  // ---- producer: page `issued` of the chunk into stage issued % kStages. Page
-  // ids are read 32 at a time, one per lane.
+  // ---- producer: unit `issued` of the chunk into stage issued % kStages. Page
+  // ids are read 32 at a time, one per lane, while the units before are at work.
   Cursor pc = cc;
-  int issued = 0, win = -1, ids = 0;
+  int issued = 0, win = 0, ids = 0, pages = 0, head = 0;  // ids: pages win .. win + 31 of the item's `pages`
+  const int* list = nullptr;
   uint32_t armed = 0;  // stages whose latest phase carries copies
+  auto open_list = [&]() {
+    list = pc.own ? a.c.table + static_cast<size_t>(pc.b) * a.c.max_pages + pp : a.prefix_pages;
+    pages = pc.own ? own_pages(a, pc.b) : pp;
+    head = item_head(a, pc);
+    win = pc.j * kUnit;
+    ids = win + lane < pages ? list[win + lane] : -1;
+  };
+  if (pc.n > 0) open_list();
   auto produce = [&]() {
-    if (win < 0 || pc.j - win >= 32) {
-      win = pc.j;
-      const int j = pc.j + lane;
-      const int* list = pc.own ? a.c.table + static_cast<size_t>(pc.b) * a.c.max_pages + pp : a.prefix_pages;
-      ids = j < pc.n ? list[j] : -1;
-    }
-    const int page = __shfl_sync(0xffffffffu, ids, pc.j - win);
+    const int j0 = pc.j * kUnit;
     const int s = issued % kStages;
-    const bool ok = page >= 0 && page < a.c.num_pages;
+    int page[kUnit];
+    bool any = false, bad = false;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      page[u] = __shfl_sync(0xffffffffu, ids, j0 - win + u);
+      const bool ok = page[u] >= 0 && page[u] < a.c.num_pages;
+      bad = bad || (!ok && j0 + u < pages);
+      if (!ok) page[u] = -1;
+      any = any || ok;
+      bytes += ok ? 2 * Cfg::kPlane + (CODES ? 32 : 0) : 0;
+    }
     if (lane == 0) {
-      if (ok) {
-        uint8_t* dst = ring + s * Cfg::kStage;
-        const int row = (page * a.c.hkv + pc.g) * kPage;
-        mbar_arrive_expect_tx(&bars[s], Cfg::kStage + (CODES ? 32 : 0));
+      if (bad) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, pc.own ? pc.b : 0);
+      if (any)
+        mbar_arrive_expect_tx(&bars[s], bytes);
+      else
+        mbar_arrive(&bars[s]);  // the stage's old contents are consumed; the rows are void
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) {
+        if (page[u] < 0) continue;
+        uint8_t* dst = ring + s * Cfg::kStage + u * 2 * Cfg::kPlane;
+        const int row = (page[u] * a.c.hkv + head) * kPage;
         if constexpr (CODES) {
           tma_load_2d(dst, &tmK, &bars[s], 0, row);
           tma_load_2d(dst + Cfg::kPlane, &tmV, &bars[s], 0, row);
-          bulk_load(scales + s * 32, a.c.k_scale + row, 16, &bars[s]);
-          bulk_load(scales + s * 32 + 16, a.c.v_scale + row, 16, &bars[s]);
+          bulk_load(scales + (s * kUnit + u) * 32, a.c.k_scale + row, 16, &bars[s]);
+          bulk_load(scales + (s * kUnit + u) * 32 + 16, a.c.v_scale + row, 16, &bars[s]);
         } else {
           tma_load_2d(dst, &tmK, &bars[s], 0, row);
           tma_load_2d(dst + 2048, &tmK, &bars[s], 64, row);
           tma_load_2d(dst + 4096, &tmV, &bars[s], 0, row);
           tma_load_2d(dst + 6144, &tmV, &bars[s], 64, row);
         }
-      } else {
-        raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, pc.own ? pc.b : 0);
-        mbar_arrive(&bars[s]);  // the stage's old contents are consumed; the rows are void
       }
     }
-    armed = ok ? armed | 1u << s : armed & ~(1u << s);
+    armed = any ? armed | 1u << s : armed & ~(1u << s);
     ++issued;
-    const bool own = pc.own;
-    const int b = pc.b, g = pc.g;
-    next_page(a, pc, lane);
-    if (pc.own != own || pc.b != b || pc.g != g) win = -1;
+    if (issued == count) return;
+    const int j = pc.j;
+    next_unit<kUnit>(a, pc, lane);
+    if (pc.j != j + 1) {
+      open_list();
+    } else if (pc.j * kUnit - win >= 32) {
+      win += 32;
+      ids = win + lane < pages ? list[win + lane] : -1;
+    }
   };
   for (int s = 0; s < kStages && s < count; ++s) produce();
 
   // ---- consumer
   const int gq = lane >> 2, tq = lane & 3;
-  float o[MT][16][4], m_o[MT][2], m_l[MT][2], l[MT][2], f_row[MT][2];
-  int limit[MT][2];  // keys that rows gq and gq + 8 of the tile see, counted from the item's first
+  uint4 qf[8];
+  float o[16][4], m_o[2], m_l[2], l[2], f_row[2];
+  int limit[2];  // keys that rows gq and gq + 8 of the tile see, counted from the item's first
   QueryRange qr{0, 0, 0, true};
-  int first_page = 0, n_rows = 0;
+  int g = 0, flat0 = 0, n_rows = 0;  // KV head, first row (within the sequence or the batch), rows
+  int first_unit = 0;
+  int keys = 0, safe = 0;  // the item's keys; those that every row sees
   bool ok = true;
 
   // the item's query rows: fragments, score factors, limits; an empty state
   auto open_item = [&]() {
+    g = item_head(a, cc);
     if (cc.own) {
       qr = query_range(a, cc.b);
-      n_rows = (qr.hi - qr.lo) * G;
+      flat0 = cc.x % (cc.X / a.c.hkv) * kStreamRows;
+      n_rows = min(kStreamRows, (qr.hi - qr.lo) * G - flat0);
+      keys = qr.len - a.prefix_len;
+      safe = a.causal ? keys - (qr.hi - qr.lo - 1) + flat0 / G : keys;
     } else {
       qr.lo = 0;
-      n_rows = min(kRows, a.total_q * G - cc.b * kRows);
+      flat0 = cc.b * kStreamRows;
+      n_rows = min(kStreamRows, a.total_q * G - flat0);
+      keys = safe = a.prefix_len;
     }
-    first_page = cc.j;
+    first_unit = cc.j;
+    const __nv_bfloat16* src[2];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const __nv_bfloat16* src[2];
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int r = t * 16 + gq + 8 * hr;
-        src[hr] = nullptr;
-        limit[t][hr] = cc.own ? qr.len - a.prefix_len : a.prefix_len;
-        if (r < n_rows) {
-          const int flat = cc.own ? r : cc.b * kRows + r;
-          src[hr] = a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + cc.g * G + flat % G) * 128;
-          if (cc.own && a.causal) limit[t][hr] -= qr.hi - qr.lo - 1 - flat / G;
-        }
-        m_o[t][hr] = m_l[t][hr] = -INFINITY;
-        l[t][hr] = 0.f;
-        f_row[t][hr] = a.scale_log2;
+    for (int hr = 0; hr < 2; ++hr) {
+      const int r = gq + 8 * hr, flat = flat0 + r;
+      src[hr] = nullptr;
+      limit[hr] = keys;
+      if (r < n_rows) {
+        src[hr] = a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G) * 128;
+        if (cc.own && a.causal) limit[hr] -= qr.hi - qr.lo - 1 - flat / G;
       }
+      m_o[hr] = m_l[hr] = -INFINITY;
+      l[hr] = 0.f;
+      f_row[hr] = a.scale_log2;
+    }
 #pragma unroll
-      for (int n = 0; n < 16; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
-      // A fragment of 16 dims: registers 0 and 2 are row gq's first and second
-      // half of the dims that lane tq's B registers hold, 1 and 3 row gq + 8's.
-      uint2 w[2][8];
+    for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    // A fragment of 16 dims: registers 0 and 2 are row gq's first and second
+    // half of the dims that lane tq's B registers hold, 1 and 3 row gq + 8's.
+    uint2 w[2][8];
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          w[hr][ks] = make_uint2(0u, 0u);
-          if (src[hr] != nullptr) {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(src[hr] + ks * 16);
-            w[hr][ks] = CODES ? make_uint2(p[2 * tq], p[2 * tq + 1]) : make_uint2(p[tq], p[tq + 4]);
-          }
-        }
-      }
-      if constexpr (CODES) {
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          float am = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
-            am = fmaxf(fmaxf(fmaxf(am, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
-          }
-          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-          am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-          // 2^e <= max |q| < 2^(e+1): q / 2^e is exact in fp16 down to 2^-24 of the row's maximum
-          const int e = am > 0.f ? min(127, static_cast<int>(__float_as_uint(am) >> 23) - 127) : 0;
-          const float down = ldexpf(1.f, -e);
-          f_row[t][hr] = a.scale_log2 * ldexpf(1.f, e);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
-            w[hr][ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
-          }
-        }
-      }
+    for (int hr = 0; hr < 2; ++hr) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const uint4 f = make_uint4(w[0][ks].x, w[1][ks].x, w[0][ks].y, w[1][ks].y);
-        if constexpr (MT == 1)
-          qr8[ks] = f;
-        else
-          qs[(t * 8 + ks) * 32] = f;  // read by this lane only
+        w[hr][ks] = make_uint2(0u, 0u);
+        if (src[hr] != nullptr) {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(src[hr] + ks * 16);
+          w[hr][ks] = CODES ? *reinterpret_cast<const uint2*>(p + 2 * tq) : make_uint2(p[tq], p[tq + 4]);
+        }
       }
     }
+    if constexpr (CODES) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        float am = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
+          am = fmaxf(fmaxf(fmaxf(am, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
+        }
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        // 2^e <= max |q| < 2^(e+1), e in [-126, 126]: q / 2^e is exact in fp16
+        // down to 2^-24 of the row's maximum
+        const int e = am > 0.f ? min(126, max(-126, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 0;
+        const float down = pow2_byte(127 - e);
+        f_row[hr] = a.scale_log2 * pow2_byte(127 + e);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
+          w[hr][ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
+        }
+      }
+    }
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) qf[ks] = make_uint4(w[0][ks].x, w[1][ks].x, w[0][ks].y, w[1][ks].y);
   };
 
   // the piece's rows: final when it is the whole of what they attend to, else parts
   auto close_item = [&]() {
-    const bool whole = cc.own && a.prefix_len == 0 && first_page == 0 && cc.j == cc.n - 1;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
+    const bool whole = cc.own && a.prefix_len == 0 && first_unit == 0 && cc.j == cc.n - 1;
+    {
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
-        float sum = l[t][hr];
+        float sum = l[hr];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = t * 16 + gq + 8 * hr;
+        const int r = gq + 8 * hr;
         if (r >= n_rows) continue;
-        const int flat = cc.own ? r : cc.b * kRows + r;
-        const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + cc.g * G + flat % G;
+        const int flat = flat0 + r;
+        const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G;
         if (whole) {
           // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
-          const float f = (m_o[t][hr] == m_l[t][hr] ? 1.f : exp2f(m_o[t][hr] - m_l[t][hr])) / sum;
+          const float f = (m_o[hr] == m_l[hr] ? 1.f : exp2f(m_o[hr] - m_l[hr])) / sum;
 #pragma unroll
           for (int n = 0; n < 16; n += 2) {
             __nv_bfloat16* d = a.out + row * 128;
             if constexpr (CODES) {
               *reinterpret_cast<uint2*>(d + n * 8 + 4 * tq) =
-                  make_uint2(pack_bf16(o[t][n][2 * hr] * f, o[t][n + 1][2 * hr] * f),
-                             pack_bf16(o[t][n][2 * hr + 1] * f, o[t][n + 1][2 * hr + 1] * f));
+                  make_uint2(pack_bf16(o[n][2 * hr] * f, o[n + 1][2 * hr] * f),
+                             pack_bf16(o[n][2 * hr + 1] * f, o[n + 1][2 * hr + 1] * f));
             } else {
-              *reinterpret_cast<uint32_t*>(d + n * 8 + 2 * tq) = pack_bf16(o[t][n][2 * hr] * f, o[t][n][2 * hr + 1] * f);
+              *reinterpret_cast<uint32_t*>(d + n * 8 + 2 * tq) = pack_bf16(o[n][2 * hr] * f, o[n][2 * hr + 1] * f);
               *reinterpret_cast<uint32_t*>(d + n * 8 + 8 + 2 * tq) =
-                  pack_bf16(o[t][n + 1][2 * hr] * f, o[t][n + 1][2 * hr + 1] * f);
+                  pack_bf16(o[n + 1][2 * hr] * f, o[n + 1][2 * hr + 1] * f);
             }
           }
-          if (tq == 0 && a.lse != nullptr) a.lse[row] = (m_l[t][hr] + log2f(sum)) * 0.6931471805599453f;
+          if (tq == 0 && a.lse != nullptr) a.lse[row] = (m_l[hr] + log2f(sum)) * 0.6931471805599453f;
         } else {
           float* d;
           PartStat* st;
-          if (first_page > 0) {
-            const size_t at = static_cast<size_t>(worker) * kRows + r;
+          if (first_unit > 0) {
+            const size_t at = static_cast<size_t>(worker) * kStreamRows + r;
             d = a.cont_o + at * 128;
             st = a.cont_st + at;
           } else {
@@ -434,14 +476,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           for (int n = 0; n < 16; n += 2) {
             if constexpr (CODES) {
               *reinterpret_cast<float4*>(d + n * 8 + 4 * tq) =
-                  make_float4(o[t][n][2 * hr], o[t][n + 1][2 * hr], o[t][n][2 * hr + 1], o[t][n + 1][2 * hr + 1]);
+                  make_float4(o[n][2 * hr], o[n + 1][2 * hr], o[n][2 * hr + 1], o[n + 1][2 * hr + 1]);
             } else {
-              *reinterpret_cast<float2*>(d + n * 8 + 2 * tq) = make_float2(o[t][n][2 * hr], o[t][n][2 * hr + 1]);
+              *reinterpret_cast<float2*>(d + n * 8 + 2 * tq) = make_float2(o[n][2 * hr], o[n][2 * hr + 1]);
               *reinterpret_cast<float2*>(d + n * 8 + 8 + 2 * tq) =
-                  make_float2(o[t][n + 1][2 * hr], o[t][n + 1][2 * hr + 1]);
+                  make_float2(o[n + 1][2 * hr], o[n + 1][2 * hr + 1]);
             }
           }
-          if (tq == 0) *st = PartStat{m_o[t][hr], m_l[t][hr], sum, 0.f};
+          if (tq == 0) *st = PartStat{m_o[hr], m_l[hr], sum, 0.f};
         }
       }
     }
@@ -455,81 +497,88 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       ok = false;
       break;
     }
-    const uint32_t kb = smem_u32(ring + s * Cfg::kStage), vb = kb + Cfg::kPlane;
-    const int key0 = cc.j * kPage;
-    const int valid = (cc.own ? qr.len - a.prefix_len : a.prefix_len) - key0;  // slots of the page that hold keys
-    float sc[MT][2][4];
+    const uint32_t stage = smem_u32(ring + s * Cfg::kStage);
+    const int key0 = cc.j * kKeys;
+    const bool border = key0 + kKeys > safe;  // some row does not see some key of the unit
+    const uint32_t mi = lane >> 3, ri = lane & 7;
+    float sc[2 * kUnit][4];  // scores of the unit's key tiles (8 keys each)
     {
-      float acc[MT][2][2][4];  // two chains per key tile
+      constexpr int kChains = kUnit == 1 ? 2 : 1;  // accumulators per key tile, for independent products
+      float acc[2 * kUnit][kChains][4] = {};
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int u = 0; u < kUnit; ++u) {
+        const uint32_t kb = stage + u * 2 * Cfg::kPlane;
+        if constexpr (CODES) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+          for (int k2 = 0; k2 < 4; ++k2) {  // 32 dims
+            uint32_t r[4];  // (keys 0-7, 8-15) of chunk 2 k2, then of the next
+            ldsm_x4(kb + swz((mi & 1) * 8 + ri, 2 * k2 + (mi >> 1)), r);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[t][x >> 1][x & 1][c] = 0.f;
-      const uint32_t mi = lane >> 3, ri = lane & 7;
-      if constexpr (CODES) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int k2 = 0; k2 < 4; ++k2) {  // 32 dims
-          uint32_t r[4];  // (keys 0-7, 8-15) of chunk 2 k2, then of the next
-          ldsm_x4(kb + swz((mi & 1) * 8 + ri, 2 * k2 + (mi >> 1)), r);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const uint32_t lo = widen2(r[2 * h + nt]), hi = widen2(r[2 * h + nt] >> 16);
-#pragma unroll
-              for (int t = 0; t < MT; ++t) mma16816<true>(acc[t][nt][h], q_frag(t, 2 * k2 + h), lo, hi);
+              for (int nt = 0; nt < 2; ++nt) {
+                uint32_t lo, hi;
+                widen4(r[2 * h + nt], lo, hi);
+                  mma16816<true>(acc[2 * u + nt][h % kChains], qf[2 * k2 + h], lo, hi);
+              }
             }
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          uint32_t r[4];  // keys 0-7: dims 0-7, 8-15 of the 16; keys 8-15 likewise
-          ldsm_x4(kb + (ks >> 2) * 2048 + swz((mi >> 1) * 8 + ri, (ks & 3) * 2 + (mi & 1)), r);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            const uint4 qf = q_frag(t, ks);
-            mma16816<false>(acc[t][0][ks & 1], qf, r[0], r[1]);
-            mma16816<false>(acc[t][1][ks & 1], qf, r[2], r[3]);
+          for (int ks = 0; ks < 8; ++ks) {
+            uint32_t r[4];  // keys 0-7: dims 0-7, 8-15 of the 16; keys 8-15 likewise
+            ldsm_x4(kb + (ks >> 2) * 2048 + swz((mi >> 1) * 8 + ri, (ks & 3) * 2 + (mi & 1)), r);
+            {
+                mma16816<false>(acc[2 * u][ks % kChains], qf[ks], r[0], r[1]);
+              mma16816<false>(acc[2 * u + 1][ks % kChains], qf[ks], r[2], r[3]);
+            }
           }
         }
       }
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+        for (int nt = 0; nt < 2 * kUnit; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[t][nt][c] = acc[t][nt][0][c] + acc[t][nt][1][c];
+          for (int c = 0; c < 4; ++c)
+            sc[nt][c] = kChains == 2 ? acc[nt][0][c] + acc[nt][kChains - 1][c] : acc[nt][0][c];
     }
-    float kf[2][2], ve[2][2];  // key factor, value exponent of this lane's keys
+    float kf[2 * kUnit][2], ve[2 * kUnit][2];  // key factor, value exponent of this lane's keys
     if constexpr (CODES) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint32_t k2 = *reinterpret_cast<const uint16_t*>(scales + s * 32 + nt * 8 + 2 * tq);
-        const uint32_t v2 = *reinterpret_cast<const uint16_t*>(scales + s * 32 + 16 + nt * 8 + 2 * tq);
+      for (int nt = 0; nt < 2 * kUnit; ++nt) {
+        const uint8_t* e = scales + (s * kUnit + (nt >> 1)) * 32 + (nt & 1) * 8 + 2 * tq;
+        const uint32_t k2 = *reinterpret_cast<const uint16_t*>(e), v2 = *reinterpret_cast<const uint16_t*>(e + 16);
         kf[nt][0] = pow2_byte(k2 & 0xffu);
         kf[nt][1] = pow2_byte(k2 >> 8);
         ve[nt][0] = static_cast<float>(static_cast<int>(v2 & 0xffu) - 127);
         ve[nt][1] = static_cast<float>(static_cast<int>(v2 >> 8) - 127);
       }
     }
-    uint4 pa[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
+    uint4 pa[kUnit];
+    {
       float mo[2] = {-INFINITY, -INFINITY}, ml[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int nt = 0; nt < 2 * kUnit; ++nt) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int key = key0 + nt * 8 + tq * 2 + (c & 1);
-          float x = sc[t][nt][c] * f_row[t][c >> 1];
-          if constexpr (CODES) x *= kf[nt][c & 1];
-          x = key < limit[t][c >> 1] ? x : -INFINITY;
-          sc[t][nt][c] = x;
-          ml[c >> 1] = fmaxf(ml[c >> 1], x);
-          if constexpr (CODES) mo[c >> 1] = fmaxf(mo[c >> 1], x + ve[nt][c & 1]);
+          if constexpr (CODES)
+            sc[nt][c] *= f_row[c >> 1] * kf[nt][c & 1];
+          else
+            sc[nt][c] *= f_row[c >> 1];
+        }
+      }
+      if (border) {
+#pragma unroll
+        for (int nt = 0; nt < 2 * kUnit; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (key0 + nt * 8 + tq * 2 + (c & 1) >= limit[c >> 1]) sc[nt][c] = -INFINITY;
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2 * kUnit; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ml[c >> 1] = fmaxf(ml[c >> 1], sc[nt][c]);
+          if constexpr (CODES) mo[c >> 1] = fmaxf(mo[c >> 1], sc[nt][c] + ve[nt][c & 1]);
         }
       }
 #pragma unroll
@@ -543,48 +592,57 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           mo[hr] = ml[hr];
         }
       }
-      // The reference maxima move only when a page exceeds them by more than
-      // 2^8: weights stay below 256 and the rescale is skipped on most pages.
-      if (__any_sync(0xffffffffu, mo[0] > m_o[t][0] + 8.f || mo[1] > m_o[t][1] + 8.f || ml[0] > m_l[t][0] + 8.f ||
-                                      ml[1] > m_l[t][1] + 8.f)) {
+      // The reference maxima move only when a unit exceeds them by more than
+      // 2^8: weights stay below 256 and the rescale is skipped on most units.
+      if (__any_sync(0xffffffffu, mo[0] > m_o[0] + 8.f || mo[1] > m_o[1] + 8.f || ml[0] > m_l[0] + 8.f ||
+                                      ml[1] > m_l[1] + 8.f)) {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          const float no = fmaxf(m_o[t][hr], mo[hr]), nl = fmaxf(m_l[t][hr], ml[hr]);
-          const float fo = no == -INFINITY ? 1.f : exp2f(m_o[t][hr] - no);
-          l[t][hr] *= nl == -INFINITY ? 1.f : exp2f(m_l[t][hr] - nl);
-          m_o[t][hr] = no;
-          m_l[t][hr] = nl;
+          const float no = fmaxf(m_o[hr], mo[hr]), nl = fmaxf(m_l[hr], ml[hr]);
+          const float fo = no == -INFINITY ? 1.f : exp2f(m_o[hr] - no);
+          l[hr] *= nl == -INFINITY ? 1.f : exp2f(m_l[hr] - nl);
+          m_o[hr] = no;
+          m_l[hr] = nl;
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            o[t][n][2 * hr] *= fo;
-            o[t][n][2 * hr + 1] *= fo;
+            o[n][2 * hr] *= fo;
+            o[n][2 * hr + 1] *= fo;
           }
         }
       }
-      uint32_t pr[4];
+      // no key seen yet: the reference is still -inf, and every weight is 0
+      float rl[2], ro[2];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int hr = 0; hr < 2; ++hr) {
+        rl[hr] = m_l[hr] == -INFINITY ? 0.f : m_l[hr];
+        ro[hr] = m_o[hr] == -INFINITY ? 0.f : m_o[hr];
+      }
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          // no key seen yet: the reference is still -inf, and every weight is 0
-          const float rl = m_l[t][hr] == -INFINITY ? 0.f : m_l[t][hr];
-          const float x0 = sc[t][nt][2 * hr], x1 = sc[t][nt][2 * hr + 1];
-          const float e0 = fast_exp2(x0 - rl), e1 = fast_exp2(x1 - rl);
-          l[t][hr] += e0 + e1;
-          if constexpr (CODES) {
-            const float ro = m_o[t][hr] == -INFINITY ? 0.f : m_o[t][hr];
-            pr[nt * 2 + hr] = pack_f16(fast_exp2(x0 + ve[nt][0] - ro), fast_exp2(x1 + ve[nt][1] - ro));
-          } else {
-            pr[nt * 2 + hr] = pack_bf16(e0, e1);
+      for (int u = 0; u < kUnit; ++u) {
+        uint32_t pr[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int nt = 2 * u + h;
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr) {
+            const float x0 = sc[nt][2 * hr], x1 = sc[nt][2 * hr + 1];
+            const float e0 = fast_exp2(x0 - rl[hr]), e1 = fast_exp2(x1 - rl[hr]);
+            l[hr] += e0 + e1;
+            if constexpr (CODES)
+              pr[h * 2 + hr] = pack_f16(fast_exp2(x0 + (ve[nt][0] - ro[hr])), fast_exp2(x1 + (ve[nt][1] - ro[hr])));
+            else
+              pr[h * 2 + hr] = pack_bf16(e0, e1);
           }
         }
+        pa[u] = make_uint4(pr[0], pr[1], pr[2], pr[3]);
       }
-      pa[t] = make_uint4(pr[0], pr[1], pr[2], pr[3]);
     }
     // O += P V. Slots past the sequence's end may hold anything: their values
     // are zeroed in registers, since 0 * NaN would reach O.
-    {
-      const uint32_t mi = lane >> 3, ri = lane & 7;
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      const uint32_t vb = stage + u * 2 * Cfg::kPlane + Cfg::kPlane;
+      const int valid = keys - key0 - u * kPage;
       uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
       if (valid < kPage) {
         const int k0 = tq * 2, k1 = k0 + 8;
@@ -596,15 +654,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         for (int c2 = 0; c2 < 4; ++c2) {  // 32 dims: chunks 2 c2 and 2 c2 + 1
           uint32_t r[4];  // (keys 0-7, 8-15) of the first chunk, then of the second
           ldsm_x4_t(vb + swz((mi & 1) * 8 + ri, 2 * c2 + (mi >> 1)), r);
+          if (valid < kPage) {
+            r[0] &= m0;
+            r[1] &= m1;
+            r[2] &= m0;
+            r[3] &= m1;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // bytes (k0 d0, k0 d1, k1 d0, k1 d1) -> even dims (k0, k1), odd dims (k0, k1)
-            const uint32_t a0 = __byte_perm(r[2 * h] & m0, 0u, 0x3120), a1 = __byte_perm(r[2 * h + 1] & m1, 0u, 0x3120);
-            const uint32_t e0 = widen2(a0), d0 = widen2(a0 >> 16), e1 = widen2(a1), d1 = widen2(a1 >> 16);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              mma16816<true>(o[t][(2 * c2 + h) * 2], pa[t], e0, e1);
-              mma16816<true>(o[t][(2 * c2 + h) * 2 + 1], pa[t], d0, d1);
+            uint32_t e0, d0, e1, d1;
+            widen4(__byte_perm(r[2 * h], 0u, 0x3120), e0, d0);
+            widen4(__byte_perm(r[2 * h + 1], 0u, 0x3120), e1, d1);
+            {
+              mma16816<true>(o[(2 * c2 + h) * 2], pa[u], e0, e1);
+              mma16816<true>(o[(2 * c2 + h) * 2 + 1], pa[u], d0, d1);
             }
           }
         }
@@ -613,10 +677,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         for (int np = 0; np < 8; ++np) {
           uint32_t r[4];
           ldsm_x4_t(vb + (np >> 2) * 2048 + swz((mi & 1) * 8 + ri, (np & 3) * 2 + (mi >> 1)), r);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            mma16816<false>(o[t][np * 2], pa[t], r[0] & m0, r[1] & m1);
-            mma16816<false>(o[t][np * 2 + 1], pa[t], r[2] & m0, r[3] & m1);
+          if (valid < kPage) {
+            r[0] &= m0;
+            r[1] &= m1;
+            r[2] &= m0;
+            r[3] &= m1;
+          }
+          {
+            mma16816<false>(o[np * 2], pa[u], r[0], r[1]);
+            mma16816<false>(o[np * 2 + 1], pa[u], r[2], r[3]);
           }
         }
       }
@@ -624,7 +693,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     __syncwarp();  // every lane has read the stage
     if (issued < count) produce();
     if (cc.j == cc.n - 1 || i == count - 1) close_item();
-    if (i < count - 1) next_page(a, cc, lane);
+    if (i < count - 1) next_unit<kUnit>(a, cc, lane);
   }
 
   if (!ok && lane == 0) {
@@ -641,10 +710,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// Warps of a block share one (token, head) row (all of them where rows are few
-// and parts many, else each warp has its own): every warp folds its parts into
-// (m, l, o), then the first adds them up.
-constexpr int kJoinWarps = 4;
+// WPR warps share one (token, head) row (many where rows are few and parts many,
+// else each warp has its own): every warp folds its parts into (m, l, o), then
+// the first adds them up. Bound by the latency of three dependent reads
+// (lengths, plan, parts), so a warp reads up to kBatch parts at once.
+__host__ __device__ constexpr int join_warps(int wpr) { return wpr > 4 ? wpr : 4; }  // of a block
 
 __device__ __forceinline__ float pow2_or_0(float x, float ref) {  // 2^(x - ref); 0 where nothing was seen
   return x == -INFINITY ? 0.f : exp2f(x - ref);
@@ -659,7 +729,8 @@ struct Parts {
 };
 
 template <int WPR>
-__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(SharedAttnArgs a) {
+__global__ void __launch_bounds__(32 * join_warps(WPR)) attention_join_kernel(SharedAttnArgs a) {
+  constexpr int kJoinWarps = join_warps(WPR);
   grid_dependency_wait();
   __shared__ float so[kJoinWarps][128];
   __shared__ PartStat ss[kJoinWarps];
@@ -688,22 +759,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(SharedA
   if (live && qr.len > 0) {
     const int r = (t - qr.lo) * G + h % G;
     p.prefix_dense = a.prefix_splits;
-    if (a.stream_rows > 0) {
+    if (a.streamed) {
       const long long chunk = a.plan[1];
+      const int unit = stream_unit_pages(a.c.codes);
       if (a.prefix_row_tiles > 0) {
         const int flat = t * G + h % G;
-        const int pp = a.prefix_len / kPage;
-        const long long u = (static_cast<long long>(flat / a.stream_rows) * a.c.hkv + g) * pp;
+        const int pu = (a.prefix_len / kPage + unit - 1) / unit;
+        const long long u = (static_cast<long long>(flat / kStreamRows) * a.c.hkv + g) * pu;
         p.prefix_w = static_cast<size_t>(u / chunk);
-        p.prefix_n = static_cast<int>((u + pp - 1) / chunk - u / chunk) + 1;
-        p.prefix_r = flat % a.stream_rows;
+        p.prefix_n = static_cast<int>((u + pu - 1) / chunk - u / chunk) + 1;
+        p.prefix_r = flat % kStreamRows;
       }
-      const int n = own_pages(a, b);
+      const int n = (own_pages(a, b) + unit - 1) / unit;
       if (n > 0) {
-        const long long u = a.plan[2 + b] + static_cast<long long>(g) * n;
+        const int tiles = own_items(a, b) / a.c.hkv;
+        const long long u = a.plan[2 + b] + (static_cast<long long>(g) * tiles + r / kStreamRows) * n;
         p.own_w = static_cast<size_t>(u / chunk);
         p.own_n = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
-        p.own_r = r;
+        p.own_r = r % kStreamRows;
       }
       if (a.prefix_len == 0 && p.own_n == 1) live = false;  // written by its only worker
     } else {
@@ -731,7 +804,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(SharedA
         po = pre ? a.prefix_o : a.own_o;
         ps = pre ? a.prefix_st : a.own_st;
         if (piece > 0) {
-          at = ((pre ? p.prefix_w : p.own_w) + piece) * a.stream_rows + (pre ? p.prefix_r : p.own_r);
+          at = ((pre ? p.prefix_w : p.own_w) + piece) * kStreamRows + (pre ? p.prefix_r : p.own_r);
           po = a.cont_o;
           ps = a.cont_st;
         }
@@ -739,7 +812,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(SharedA
       o = po + at * 128;
       st = ps + at;
     };
-    constexpr int kBatch = 4;
+    constexpr int kBatch = WPR == 1 ? 6 : 4;
     for (int i0 = sub; i0 < parts; i0 += WPR * kBatch) {
       PartStat st[kBatch];
       float4 v[kBatch];
@@ -811,11 +884,11 @@ int stream_workers(int num_sms) { return num_sms * kStreamWarps; }
 
 namespace {
 
-template <bool CODES, int MT>
+template <bool CODES>
 cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
                           cudaStream_t st) {
-  auto kern = attention_stream_kernel<CODES, MT>;
-  constexpr size_t smem = StreamCfg<CODES, MT>::kSmem;
+  auto kern = attention_stream_kernel<CODES>;
+  constexpr size_t smem = StreamCfg<CODES>::kSmem;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -834,21 +907,26 @@ cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const
 
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     int num_sms, cudaStream_t st) {
-  if (a.stream_rows == 16)
-    return a.c.codes ? launch_stream<true, 1>(a, tmK, tmV, num_sms, st)
-                     : launch_stream<false, 1>(a, tmK, tmV, num_sms, st);
-  return a.c.codes ? launch_stream<true, 2>(a, tmK, tmV, num_sms, st)
-                   : launch_stream<false, 2>(a, tmK, tmV, num_sms, st);
+  return a.c.codes ? launch_stream<true>(a, tmK, tmV, num_sms, st) : launch_stream<false>(a, tmK, tmV, num_sms, st);
 }
+
+namespace {
+
+template <int WPR>
+cudaError_t launch_join(const SharedAttnArgs& a, long long rows, cudaStream_t st) {
+  constexpr int per_block = join_warps(WPR) / WPR;
+  return launch_pdl(attention_join_kernel<WPR>, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)),
+                    dim3(32 * join_warps(WPR)), 0, st, a);
+}
+
+}  // namespace
 
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.total_q) * a.hq;
   count_launch();
-  // few rows: many parts each, so a block's warps share a row
-  if (rows <= 16LL * num_sms)
-    return launch_pdl(attention_join_kernel<kJoinWarps>, dim3(static_cast<unsigned>(rows)), dim3(32 * kJoinWarps), 0, st, a);
-  return launch_pdl(attention_join_kernel<1>, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
-                    dim3(32 * kJoinWarps), 0, st, a);
+  if (rows <= num_sms) return launch_join<16>(a, rows, st);
+  if (rows <= 16LL * num_sms) return launch_join<4>(a, rows, st);
+  return launch_join<1>(a, rows, st);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.

@@ -49,22 +49,44 @@ struct Bars {
 constexpr size_t kSmem = 1024 + kOffBar + sizeof(Bars);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ void tmem_ld_32cols_nowait(uint32_t taddr, float* v) {
-  uint32_t r[32];
+// Starts the load of 32 columns; the registers hold them after tmem_ld_wait,
+// which names them so that no use can move ahead of it.
+__device__ __forceinline__ void tmem_ld_32cols_nowait(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      :
+        "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               :
+        "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+        "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+        "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
+        "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+        "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_32cols_nowait(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
 struct Item {
   int row0, n_rows;  // this CTA's first row and the rows there are, per KV head
   int k_lo, k_hi;    // keys
@@ -315,19 +337,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32cols_nowait(lane_addr + t * 128 + c * 32, s + c * 32);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        uint32_t su[4][32];
         const int valid = limit - key0;
-        if (__any_sync(0xffffffffu, valid < kBlkKeys)) {
+        const bool border = __any_sync(0xffffffffu, valid < kBlkKeys);
+        // The maximum of one quarter runs under the load of the next, on eight
+        // chains: a single chain of 128 dependent maxima would take longer than
+        // the exponentials.
+        float mq[8];
 #pragma unroll
-          for (int i = 0; i < 128; ++i) s[i] = i < valid ? s[i] : -INFINITY;
+        for (int i = 0; i < 8; ++i) mq[i] = -INFINITY;
+        tmem_ld_32cols_nowait(lane_addr + t * 128, su[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait(su[c]);
+          if (c < 3) tmem_ld_32cols_nowait(lane_addr + t * 128 + (c + 1) * 32, su[c + 1]);
+          if (border) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) su[c][i] = c * 32 + i < valid ? su[c][i] : 0xff800000u;  // -infinity
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mq[i & 7] = fmaxf(mq[i & 7], __uint_as_float(su[c][i]));
         }
-        float mx = -INFINITY;  // of the raw scores: the factor is positive
-#pragma unroll
-        for (int i = 0; i < 128; ++i) mx = fmaxf(mx, s[i]);
-        mx *= scale;
+        const float mx = scale * fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
+                                       fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
         // the reference maximum moves only past +8 in base 2 (weights stay below 256)
         const bool need = mx > m_ref + 8.f;
         float alpha = 1.f;
@@ -354,21 +386,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // no key seen yet: the reference is still -inf, and every weight is 0
         const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-        float p0 = 0.f, p1 = 0.f;
+        const float2 sc2 = make_float2(scale, scale), nr2 = make_float2(-ref, -ref);
+        float2 sum[4] = {};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // 64 keys: 32 columns of bf16 pairs
-          float w[32];
+          uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float e0 = fast_exp2(fmaf(s[c * 64 + 2 * i], scale, -ref));
-            const float e1 = fast_exp2(fmaf(s[c * 64 + 2 * i + 1], scale, -ref));
-            p0 += e0;
-            p1 += e1;
-            w[i] = __uint_as_float(pack_bf16(e0, e1));
+            const uint32_t* s = &su[2 * c + (i >> 4)][2 * i & 31];
+            const float2 x = fma2(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2, nr2);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum[i & 3] = add2(sum[i & 3], e);
+            w[i] = pack_bf16(e.x, e.y);
           }
-          tmem_st_32cols(lane_addr + t * 128 + c * 32, w);
+          tmem_st_32cols_nowait(lane_addr + t * 128 + c * 32, w);
         }
-        l += p0 + p1;
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
         // Keys past the range (tail of the last page, pages not loaded): their V
         // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
         // Tile 0 does it for both: its product is issued first.
