@@ -103,7 +103,7 @@ struct SharedAttnArgs {
 };
 
 constexpr int kTileRows = 256;  // query rows of a tensor-core CTA
-constexpr int kStreamWarps = 12;
+constexpr int kStreamWarps = 8;
 constexpr int kStreamRows = 16;  // query rows of a streamed item
 // Pages that a streaming worker takes at a time.
 __host__ __device__ constexpr int stream_unit_pages(bool codes) { return codes ? 2 : 1; }

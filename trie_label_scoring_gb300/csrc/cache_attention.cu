@@ -39,7 +39,8 @@ struct StreamCfg {
   static constexpr int kUnit = stream_unit_pages(CODES);   // pages a stage
   static constexpr uint32_t kPlane = CODES ? 2048 : 4096;  // K or V of one (page, head)
   static constexpr uint32_t kStage = 2 * kPlane * kUnit;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = 3;
+  static constexpr int kScaleLanes = CODES ? 2 * kUnit : 0;  // lanes that copy 16 scale bytes each
   static constexpr uint32_t kRing = kStreamWarps * kStages * kStage;
   static constexpr uint32_t kScales = CODES ? kStreamWarps * kStages * kUnit * 32 : 0;  // key, value exponents
   static constexpr uint32_t kBars = kStreamWarps * kStages * 8;
@@ -90,11 +91,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// 16 bytes to shared memory, and this thread's arrival on `bar` once its copies
+// have landed (counted in the barrier's expected arrivals).
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ float pow2_byte(uint32_t e) { return __uint_as_float(e << 23); }
 
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + Cfg::kRing + Cfg::kScales + Cfg::kBars +
                                                              Cfg::kScan);
   if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1 + Cfg::kScaleLanes);
     fence_mbar_init();
     if (warp == 0) *abort_flag = 0;
   }
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       bad = bad || (!ok && j0 + u < pages);
       if (!ok) page[u] = -1;
       any = any || ok;
-      bytes += ok ? 2 * Cfg::kPlane + (CODES ? 32 : 0) : 0;
+      bytes += ok ? 2 * Cfg::kPlane : 0;
     }
     if (lane == 0) {
       if (bad) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, pc.own ? pc.b : 0);
@@ -320,18 +323,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (page[u] < 0) continue;
         uint8_t* dst = ring + s * Cfg::kStage + u * 2 * Cfg::kPlane;
         const int row = (page[u] * a.c.hkv + head) * kPage;
-        if constexpr (CODES) {
-          tma_load_2d(dst, &tmK, &bars[s], 0, row);
-          tma_load_2d(dst + Cfg::kPlane, &tmV, &bars[s], 0, row);
-          bulk_load(scales + (s * kUnit + u) * 32, a.c.k_scale + row, 16, &bars[s]);
-          bulk_load(scales + (s * kUnit + u) * 32 + 16, a.c.v_scale + row, 16, &bars[s]);
-        } else {
-          tma_load_2d(dst, &tmK, &bars[s], 0, row);
-          tma_load_2d(dst + 2048, &tmK, &bars[s], 64, row);
-          tma_load_2d(dst + 4096, &tmV, &bars[s], 0, row);
-          tma_load_2d(dst + 6144, &tmV, &bars[s], 64, row);
-        }
+        tma_load_2d(dst, &tmK, &bars[s], 0, row);
+        if (!CODES) tma_load_2d(dst + 2048, &tmK, &bars[s], 64, row);
+        tma_load_2d(dst + Cfg::kPlane, &tmV, &bars[s], 0, row);
+        if (!CODES) tma_load_2d(dst + Cfg::kPlane + 2048, &tmV, &bars[s], 64, row);
       }
+    }
+    if (CODES && lane < Cfg::kScaleLanes) {  // lane 2u: the keys' exponents of page u, 2u + 1: the values'
+      const int p = lane < 2 ? page[0] : page[kUnit - 1];
+      if (p >= 0)
+        copy16_async(scales + s * kUnit * 32 + lane * 16,
+                     ((lane & 1) ? a.c.v_scale : a.c.k_scale) + static_cast<size_t>(p * a.c.hkv + head) * kPage);
+      arrive_after_copies(&bars[s]);
     }
     armed = any ? armed | 1u << s : armed & ~(1u << s);
     ++issued;
@@ -349,8 +352,26 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   // ---- consumer
   const int gq = lane >> 2, tq = lane & 3;
+  // The 16 keys of a page go to the two 8-key tiles so that lane tq's four
+  // accumulator columns are keys 4 tq .. 4 tq + 3 (their exponents one word)
+  // and each tile's keys fall on eight different swizzle positions: columns
+  // 2i, 2i + 1 of tile t are keys 4 i + 2 (t ^ (i >> 1)) and the next.
+  auto tile_key = [](int t, int col) { return 4 * (col >> 1) + 2 * (t ^ (col >> 2)) + (col & 1); };
+  const int my_key[2] = {tile_key(0, 2 * tq), tile_key(1, 2 * tq)};
+  const uint32_t key_order = tq < 2 ? 0x3210u : 0x1032u;
+  // ldmatrix offsets within a plane (or half of one): lane 8 i + j addresses row
+  // j of matrix i. k_off: matrices (tile 0, chunk 2 c), (0, 2 c + 1), (1, ..);
+  // v_off: (tile 0, chunk 2 c), (1, 2 c), (0, 2 c + 1), (1, 2 c + 1).
+  uint32_t k_off[4], v_off[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int mi = lane >> 3, ri = lane & 7;
+    k_off[c] = swz(tile_key(mi >> 1, ri), 2 * c + (mi & 1));
+    v_off[c] = swz(tile_key(mi & 1, ri), 2 * c + (mi >> 1));
+  }
   uint4 qf[8];
-  float o[16][4], m_o[2], m_l[2], l[2], f_row[2];
+  float o[16][4], m_o[2], m_l[2], f_row[2];
+  float2 l[2];  // two partial sums
   int limit[2];  // keys that rows gq and gq + 8 of the tile see, counted from the item's first
   QueryRange qr{0, 0, 0, true};
   int g = 0, flat0 = 0, n_rows = 0;  // KV head, first row (within the sequence or the batch), rows
@@ -385,7 +406,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (cc.own && a.causal) limit[hr] -= qr.hi - qr.lo - 1 - flat / G;
       }
       m_o[hr] = m_l[hr] = -INFINITY;
-      l[hr] = 0.f;
+      l[hr] = make_float2(0.f, 0.f);
       f_row[hr] = a.scale_log2;
     }
 #pragma unroll
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     {
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
-        float sum = l[hr];
+        float sum = l[hr].x + l[hr].y;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = gq + 8 * hr;
@@ -446,7 +467,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G;
         if (whole) {
           // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
-          const float f = (m_o[hr] == m_l[hr] ? 1.f : exp2f(m_o[hr] - m_l[hr])) / sum;
+          const float f = (CODES ? exp2f(m_o[hr] - 127.f - m_l[hr]) : 1.f) / sum;
 #pragma unroll
           for (int n = 0; n < 16; n += 2) {
             __nv_bfloat16* d = a.out + row * 128;
@@ -483,7 +504,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                   make_float2(o[n + 1][2 * hr], o[n + 1][2 * hr + 1]);
             }
           }
-          if (tq == 0) *st = PartStat{m_o[hr], m_l[hr], sum, 0.f};
+          if (tq == 0) *st = PartStat{CODES ? m_o[hr] - 127.f : m_o[hr], m_l[hr], sum, 0.f};
         }
       }
     }
@@ -500,8 +521,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const uint32_t stage = smem_u32(ring + s * Cfg::kStage);
     const int key0 = cc.j * kKeys;
     const bool border = key0 + kKeys > safe;  // some row does not see some key of the unit
-    const uint32_t mi = lane >> 3, ri = lane & 7;
-    float sc[2 * kUnit][4];  // scores of the unit's key tiles (8 keys each)
+    float2 sc[2 * kUnit][2];  // scores: key tile (8 keys), row gq or gq + 8, two keys
     {
       constexpr int kChains = kUnit == 1 ? 2 : 1;  // accumulators per key tile, for independent products
       float acc[2 * kUnit][kChains][4] = {};
@@ -511,131 +531,138 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if constexpr (CODES) {
 #pragma unroll
           for (int k2 = 0; k2 < 4; ++k2) {  // 32 dims
-            uint32_t r[4];  // (keys 0-7, 8-15) of chunk 2 k2, then of the next
-            ldsm_x4(kb + swz((mi & 1) * 8 + ri, 2 * k2 + (mi >> 1)), r);
+            uint32_t r[4];  // key tiles 0 and 1 of chunk 2 k2, then of the next
+            ldsm_x4(kb + v_off[k2], r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
                 uint32_t lo, hi;
                 widen4(r[2 * h + nt], lo, hi);
-                  mma16816<true>(acc[2 * u + nt][h % kChains], qf[2 * k2 + h], lo, hi);
+                mma16816<true>(acc[2 * u + nt][h % kChains], qf[2 * k2 + h], lo, hi);
               }
             }
           }
         } else {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
-            uint32_t r[4];  // keys 0-7: dims 0-7, 8-15 of the 16; keys 8-15 likewise
-            ldsm_x4(kb + (ks >> 2) * 2048 + swz((mi >> 1) * 8 + ri, (ks & 3) * 2 + (mi & 1)), r);
-            {
-                mma16816<false>(acc[2 * u][ks % kChains], qf[ks], r[0], r[1]);
-              mma16816<false>(acc[2 * u + 1][ks % kChains], qf[ks], r[2], r[3]);
-            }
+            uint32_t r[4];  // key tile 0: dims 0-7, 8-15 of the 16; tile 1 likewise
+            ldsm_x4(kb + (ks >> 2) * 2048 + k_off[ks & 3], r);
+            mma16816<false>(acc[2 * u][ks % kChains], qf[ks], r[0], r[1]);
+            mma16816<false>(acc[2 * u + 1][ks % kChains], qf[ks], r[2], r[3]);
           }
         }
       }
 #pragma unroll
-        for (int nt = 0; nt < 2 * kUnit; ++nt)
+      for (int nt = 0; nt < 2 * kUnit; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            sc[nt][c] = kChains == 2 ? acc[nt][0][c] + acc[nt][kChains - 1][c] : acc[nt][0][c];
+        for (int hr = 0; hr < 2; ++hr) {
+          sc[nt][hr] = make_float2(acc[nt][0][2 * hr], acc[nt][0][2 * hr + 1]);
+          if constexpr (kChains == 2)
+            sc[nt][hr] = add2(sc[nt][hr], make_float2(acc[nt][1][2 * hr], acc[nt][1][2 * hr + 1]));
+        }
     }
-    float kf[2 * kUnit][2], ve[2 * kUnit][2];  // key factor, value exponent of this lane's keys
+    float2 ve[2 * kUnit];  // value exponents of this lane's keys, biased by 127
     if constexpr (CODES) {
 #pragma unroll
+      for (int u = 0; u < kUnit; ++u) {
+        const uint8_t* e = scales + (s * kUnit + u) * 32 + 4 * tq;
+        // this lane's four keys, tile 0's first
+        const uint32_t k4 = __byte_perm(*reinterpret_cast<const uint32_t*>(e), 0u, key_order);
+        const uint32_t v4 = __byte_perm(*reinterpret_cast<const uint32_t*>(e + 16), 0u, key_order);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 kf = make_float2(__uint_as_float((h ? k4 << 7 : k4 << 23) & 0x7f800000u),
+                                        __uint_as_float((h ? k4 >> 1 : k4 << 15) & 0x7f800000u));
+          // byte b as the float 2^23 + b, exactly
+          ve[2 * u + h] = add2(make_float2(__uint_as_float(__byte_perm(v4, 0x4b000000u, h ? 0x7442 : 0x7440)),
+                                           __uint_as_float(__byte_perm(v4, 0x4b000000u, h ? 0x7443 : 0x7441))),
+                               make_float2(-8388608.f, -8388608.f));
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr)
+            sc[2 * u + h][hr] = mul2(sc[2 * u + h][hr], mul2(kf, make_float2(f_row[hr], f_row[hr])));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < 2 * kUnit; ++nt)
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) sc[nt][hr] = mul2(sc[nt][hr], make_float2(f_row[hr], f_row[hr]));
+    }
+    if (border) {
+#pragma unroll
       for (int nt = 0; nt < 2 * kUnit; ++nt) {
-        const uint8_t* e = scales + (s * kUnit + (nt >> 1)) * 32 + (nt & 1) * 8 + 2 * tq;
-        const uint32_t k2 = *reinterpret_cast<const uint16_t*>(e), v2 = *reinterpret_cast<const uint16_t*>(e + 16);
-        kf[nt][0] = pow2_byte(k2 & 0xffu);
-        kf[nt][1] = pow2_byte(k2 >> 8);
-        ve[nt][0] = static_cast<float>(static_cast<int>(v2 & 0xffu) - 127);
-        ve[nt][1] = static_cast<float>(static_cast<int>(v2 >> 8) - 127);
+        const int key = key0 + (nt >> 1) * kPage + my_key[nt & 1];
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          if (key >= limit[hr]) sc[nt][hr].x = -INFINITY;
+          if (key + 1 >= limit[hr]) sc[nt][hr].y = -INFINITY;
+        }
+      }
+    }
+    float mo[2], ml[2];
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+      ml[hr] = fmaxf(sc[0][hr].x, sc[0][hr].y);
+#pragma unroll
+      for (int nt = 1; nt < 2 * kUnit; ++nt) ml[hr] = fmaxf(ml[hr], fmaxf(sc[nt][hr].x, sc[nt][hr].y));
+      ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 1));
+      ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 2));
+      if constexpr (CODES) {
+        float2 t = add2(sc[0][hr], ve[0]);
+        mo[hr] = fmaxf(t.x, t.y);
+#pragma unroll
+        for (int nt = 1; nt < 2 * kUnit; ++nt) {
+          t = add2(sc[nt][hr], ve[nt]);
+          mo[hr] = fmaxf(mo[hr], fmaxf(t.x, t.y));
+        }
+        mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 1));
+        mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 2));
+      } else {
+        mo[hr] = ml[hr];
+      }
+    }
+    // The reference maxima move only when a unit exceeds them by more than
+    // 2^8: weights stay below 256 and the rescale is skipped on most units.
+    if (__any_sync(0xffffffffu, mo[0] > m_o[0] + 8.f || mo[1] > m_o[1] + 8.f || ml[0] > m_l[0] + 8.f ||
+                                    ml[1] > m_l[1] + 8.f)) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const float no = fmaxf(m_o[hr], mo[hr]), nl = fmaxf(m_l[hr], ml[hr]);
+        const float fo = no == -INFINITY ? 1.f : exp2f(m_o[hr] - no);
+        const float fl = nl == -INFINITY ? 1.f : exp2f(m_l[hr] - nl);
+        l[hr] = mul2(l[hr], make_float2(fl, fl));
+        m_o[hr] = no;
+        m_l[hr] = nl;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          o[n][2 * hr] *= fo;
+          o[n][2 * hr + 1] *= fo;
+        }
       }
     }
     uint4 pa[kUnit];
     {
-      float mo[2] = {-INFINITY, -INFINITY}, ml[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int nt = 0; nt < 2 * kUnit; ++nt) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if constexpr (CODES)
-            sc[nt][c] *= f_row[c >> 1] * kf[nt][c & 1];
-          else
-            sc[nt][c] *= f_row[c >> 1];
-        }
-      }
-      if (border) {
-#pragma unroll
-        for (int nt = 0; nt < 2 * kUnit; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (key0 + nt * 8 + tq * 2 + (c & 1) >= limit[c >> 1]) sc[nt][c] = -INFINITY;
-      }
-#pragma unroll
-      for (int nt = 0; nt < 2 * kUnit; ++nt) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          ml[c >> 1] = fmaxf(ml[c >> 1], sc[nt][c]);
-          if constexpr (CODES) mo[c >> 1] = fmaxf(mo[c >> 1], sc[nt][c] + ve[nt][c & 1]);
-        }
-      }
+      uint32_t pr[kUnit][4];
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
-        ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 1));
-        ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 2));
-        if constexpr (CODES) {
-          mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 1));
-          mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 2));
-        } else {
-          mo[hr] = ml[hr];
-        }
-      }
-      // The reference maxima move only when a unit exceeds them by more than
-      // 2^8: weights stay below 256 and the rescale is skipped on most units.
-      if (__any_sync(0xffffffffu, mo[0] > m_o[0] + 8.f || mo[1] > m_o[1] + 8.f || ml[0] > m_l[0] + 8.f ||
-                                      ml[1] > m_l[1] + 8.f)) {
+        // no key seen yet: the reference is still -inf, and every weight is 0
+        const float rl = m_l[hr] == -INFINITY ? 0.f : -m_l[hr], ro = m_o[hr] == -INFINITY ? 0.f : -m_o[hr];
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          const float no = fmaxf(m_o[hr], mo[hr]), nl = fmaxf(m_l[hr], ml[hr]);
-          const float fo = no == -INFINITY ? 1.f : exp2f(m_o[hr] - no);
-          l[hr] *= nl == -INFINITY ? 1.f : exp2f(m_l[hr] - nl);
-          m_o[hr] = no;
-          m_l[hr] = nl;
-#pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            o[n][2 * hr] *= fo;
-            o[n][2 * hr + 1] *= fo;
+        for (int nt = 0; nt < 2 * kUnit; ++nt) {
+          const float2 x = add2(sc[nt][hr], make_float2(rl, rl));
+          const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          l[hr] = add2(l[hr], e);
+          if constexpr (CODES) {
+            const float2 t = add2(sc[nt][hr], add2(ve[nt], make_float2(ro, ro)));
+            pr[nt >> 1][(nt & 1) * 2 + hr] = pack_f16(fast_exp2(t.x), fast_exp2(t.y));
+          } else {
+            pr[nt >> 1][(nt & 1) * 2 + hr] = pack_bf16(e.x, e.y);
           }
         }
       }
-      // no key seen yet: the reference is still -inf, and every weight is 0
-      float rl[2], ro[2];
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        rl[hr] = m_l[hr] == -INFINITY ? 0.f : m_l[hr];
-        ro[hr] = m_o[hr] == -INFINITY ? 0.f : m_o[hr];
-      }
-#pragma unroll
-      for (int u = 0; u < kUnit; ++u) {
-        uint32_t pr[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int nt = 2 * u + h;
-#pragma unroll
-          for (int hr = 0; hr < 2; ++hr) {
-            const float x0 = sc[nt][2 * hr], x1 = sc[nt][2 * hr + 1];
-            const float e0 = fast_exp2(x0 - rl[hr]), e1 = fast_exp2(x1 - rl[hr]);
-            l[hr] += e0 + e1;
-            if constexpr (CODES)
-              pr[h * 2 + hr] = pack_f16(fast_exp2(x0 + (ve[nt][0] - ro[hr])), fast_exp2(x1 + (ve[nt][1] - ro[hr])));
-            else
-              pr[h * 2 + hr] = pack_bf16(e0, e1);
-          }
-        }
-        pa[u] = make_uint4(pr[0], pr[1], pr[2], pr[3]);
-      }
+      for (int u = 0; u < kUnit; ++u) pa[u] = make_uint4(pr[u][0], pr[u][1], pr[u][2], pr[u][3]);
     }
     // O += P V. Slots past the sequence's end may hold anything: their values
     // are zeroed in registers, since 0 * NaN would reach O.
@@ -645,47 +672,30 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const int valid = keys - key0 - u * kPage;
       uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
       if (valid < kPage) {
-        const int k0 = tq * 2, k1 = k0 + 8;
-        m0 = (k0 < valid ? 0x0000ffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
-        m1 = (k1 < valid ? 0x0000ffffu : 0u) | (k1 + 1 < valid ? 0xffff0000u : 0u);
+        m0 = (my_key[0] < valid ? 0x0000ffffu : 0u) | (my_key[0] + 1 < valid ? 0xffff0000u : 0u);
+        m1 = (my_key[1] < valid ? 0x0000ffffu : 0u) | (my_key[1] + 1 < valid ? 0xffff0000u : 0u);
       }
-      if constexpr (CODES) {
 #pragma unroll
-        for (int c2 = 0; c2 < 4; ++c2) {  // 32 dims: chunks 2 c2 and 2 c2 + 1
-          uint32_t r[4];  // (keys 0-7, 8-15) of the first chunk, then of the second
-          ldsm_x4_t(vb + swz((mi & 1) * 8 + ri, 2 * c2 + (mi >> 1)), r);
-          if (valid < kPage) {
-            r[0] &= m0;
-            r[1] &= m1;
-            r[2] &= m0;
-            r[3] &= m1;
-          }
+      for (int c = 0; c < (CODES ? 4 : 8); ++c) {
+        uint32_t r[4];  // key tiles 0 and 1 of one chunk, then of the next
+        ldsm_x4_t(vb + (CODES ? 0 : (c >> 2) * 2048) + v_off[c & 3], r);
+        if (valid < kPage) {
+          r[0] &= m0;
+          r[1] &= m1;
+          r[2] &= m0;
+          r[3] &= m1;
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (CODES) {
             // bytes (k0 d0, k0 d1, k1 d0, k1 d1) -> even dims (k0, k1), odd dims (k0, k1)
             uint32_t e0, d0, e1, d1;
             widen4(__byte_perm(r[2 * h], 0u, 0x3120), e0, d0);
             widen4(__byte_perm(r[2 * h + 1], 0u, 0x3120), e1, d1);
-            {
-              mma16816<true>(o[(2 * c2 + h) * 2], pa[u], e0, e1);
-              mma16816<true>(o[(2 * c2 + h) * 2 + 1], pa[u], d0, d1);
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int np = 0; np < 8; ++np) {
-          uint32_t r[4];
-          ldsm_x4_t(vb + (np >> 2) * 2048 + swz((mi & 1) * 8 + ri, (np & 3) * 2 + (mi >> 1)), r);
-          if (valid < kPage) {
-            r[0] &= m0;
-            r[1] &= m1;
-            r[2] &= m0;
-            r[3] &= m1;
-          }
-          {
-            mma16816<false>(o[np * 2], pa[u], r[0], r[1]);
-            mma16816<false>(o[np * 2 + 1], pa[u], r[2], r[3]);
+            mma16816<true>(o[(2 * c + h) * 2], pa[u], e0, e1);
+            mma16816<true>(o[(2 * c + h) * 2 + 1], pa[u], d0, d1);
+          } else {
+            mma16816<false>(o[2 * c + h], pa[u], r[2 * h], r[2 * h + 1]);
           }
         }
       }
