@@ -943,7 +943,8 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   const long seq_rows = static_cast<long>(std::min(max_q, total_q)) * G;  // query rows of a sequence per KV head
   const long all_rows = static_cast<long>(total_q) * G;
   const bool stream = t.streamed = seq_rows <= 32;
-  const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > 16 : seq_rows < 128 && c->num_seqs > 1);
+  t.item_rows = seq_rows <= 8 ? 8 : 16;
+  const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > t.item_rows : seq_rows < 128 && c->num_seqs > 1);
   if (tile_prefix)
     choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, &t.prefix_split,
                       &t.prefix_splits);
@@ -961,17 +962,17 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   t.wide_pages = codes && (tile_prefix || !stream);
   Carver k{base};
   if (stream) {
-    const size_t workers = stream_workers(sms);
+    const size_t workers = static_cast<size_t>(stream_warps(t.item_rows)) * sms;
     t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
     if (prefix_len > 0 && !tile_prefix) {
-      t.prefix_row_tiles = static_cast<int>((all_rows + kStreamRows - 1) / kStreamRows);
+      t.prefix_row_tiles = static_cast<int>((all_rows + t.item_rows - 1) / t.item_rows);
       t.prefix_o = k.take<float>(rows * 128);
       t.prefix_st = k.take<PartStat>(rows);
     }
     t.own_o = k.take<float>(rows * 128);
     t.own_st = k.take<PartStat>(rows);
-    t.cont_o = k.take<float>(workers * kStreamRows * 128);
-    t.cont_st = k.take<PartStat>(workers * kStreamRows);
+    t.cont_o = k.take<float>(workers * t.item_rows * 128);
+    t.cont_st = k.take<PartStat>(workers * t.item_rows);
   }
   if (t.dense_parts > 0) {
     t.dense_o = k.take<float>(t.dense_parts * rows * 128);

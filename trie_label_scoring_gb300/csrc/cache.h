@@ -73,6 +73,7 @@ struct SharedAttnArgs {
   // workers. plan: [0] units, [1] chunk, [2 + b]
   // first unit of sequence b, [2 + num_seqs] past the last.
   bool streamed;
+  int item_rows;  // query rows of an item, 8 or 16
   int prefix_row_tiles;
   long long* plan;
   // Parts, each [rows, 128] fp32 and a PartStat per row; rows are (token, head)
@@ -81,7 +82,7 @@ struct SharedAttnArgs {
   PartStat* prefix_st;
   float* own_o;          // pieces that begin a sequence's own keys
   PartStat* own_st;
-  float* cont_o;         // [workers, kStreamRows, 128]
+  float* cont_o;         // [workers, item_rows, 128]
   PartStat* cont_st;
 
   // The tensor-core tiles' work: the prefix for all rows in prefix_splits key
@@ -103,11 +104,10 @@ struct SharedAttnArgs {
 };
 
 constexpr int kTileRows = 256;  // query rows of a tensor-core CTA
-constexpr int kStreamWarps = 8;
-constexpr int kStreamRows = 16;  // query rows of a streamed item
+// Workers (warps) of an SM for items of 8 or 16 query rows.
+__host__ __device__ constexpr int stream_warps(int item_rows) { return item_rows == 8 ? 12 : 8; }
 // Pages that a streaming worker takes at a time.
 __host__ __device__ constexpr int stream_unit_pages(bool codes) { return codes ? 2 : 1; }
-int stream_workers(int num_sms);
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     int num_sms, cudaStream_t st);
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st);

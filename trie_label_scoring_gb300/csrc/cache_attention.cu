@@ -27,28 +27,34 @@ namespace {
 // share are joined by the second kernel.
 //
 // Per page of 16 keys (two e4m3 pages at a time, so that the bookkeeping and the
-// row reductions are shared by 32 keys): S = Q K^T and O += P V on mma.sync
-// m16n8k16 with 16 query rows as M. A sequence with more rows is several items
-// in a row, so its pages come from L2 after the first. Over bf16 pages q and P are bf16; over e4m3
-// pages the codes widen exactly to fp16, q is scaled by a power of two per row
-// (exact) and P is rounded to fp16. The key's power of two multiplies its score,
-// the value's is added to the exponent of its weight: o and l keep separate
-// maxima, so that value rows of any scale neither overflow P nor starve the sum.
-template <bool CODES>
+// row reductions are shared by 32 keys), on mma.sync m16n8k16 with the query
+// rows as N: S^T = K Q^T (M 16 keys, N 8 rows) and O^T += V^T P^T (M 16 dims, N 8
+// rows). Keys and values are the A operands, so a few query rows waste little:
+// with the rows as M, 12 of 16 rows of a 4-head group were padding, in O's
+// registers, the exponentials and the products alike. NT = 1 or 2 tiles of 8
+// rows; a sequence with more rows is several items in a row, so its pages come
+// from L2 after the first.
+// Over bf16 pages q and P are bf16; over e4m3 pages the codes widen exactly to
+// fp16, q is scaled by a power of two per row (exact) and P is rounded to fp16.
+// The key's power of two multiplies its score, the value's is added to the
+// exponent of its weight: o and l keep separate maxima, so that value rows of any
+// scale neither overflow P nor starve the sum.
+template <bool CODES, int NT>
 struct StreamCfg {
+  static constexpr int kWarps = stream_warps(8 * NT);
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kUnit = stream_unit_pages(CODES);   // pages a stage
   static constexpr uint32_t kPlane = CODES ? 2048 : 4096;  // K or V of one (page, head)
   static constexpr uint32_t kStage = 2 * kPlane * kUnit;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kScaleLanes = CODES ? 2 * kUnit : 0;  // lanes that copy 16 scale bytes each
-  static constexpr uint32_t kRing = kStreamWarps * kStages * kStage;
-  static constexpr uint32_t kScales = CODES ? kStreamWarps * kStages * kUnit * 32 : 0;  // key, value exponents
-  static constexpr uint32_t kBars = kStreamWarps * kStages * 8;
-  static constexpr uint32_t kScan = (kStreamWarps * 32 + 1) * 8;
+  static constexpr uint32_t kRing = kWarps * kStages * kStage;
+  static constexpr uint32_t kScales = CODES ? kWarps * kStages * kUnit * 32 : 0;  // key, value exponents
+  static constexpr uint32_t kBars = kWarps * kStages * 8;
+  static constexpr uint32_t kScan = (kThreads + 1) * 8;
   static constexpr size_t kSmem = 1024 + kRing + kScales + kBars + kScan + 16;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
-static_assert(StreamCfg<false>::kSmem <= 227 * 1024 && StreamCfg<true>::kSmem <= 227 * 1024, "shared memory");
-constexpr int kStreamThreads = 32 * kStreamWarps;
 constexpr int kMinChunk = 2;  // units a worker takes at least
 
 __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
@@ -66,17 +72,24 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, const uint2& b) {
   if constexpr (F16)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y));
+}
+// Transposes an 8x8 matrix of 16-bit elements: from (row lane / 4, columns
+// 2 (lane % 4) and the next) to (column lane / 4, rows 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 // Four e4m3 codes as two pairs of fp16.
 __device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
@@ -118,7 +131,7 @@ __device__ __forceinline__ int own_units(const SharedAttnArgs& a, int b) {
 // Items of sequence b: its row tiles for every KV head.
 __device__ __forceinline__ int own_items(const SharedAttnArgs& a, int b) {
   const int n = a.q_offsets ? a.q_offsets[b + 1] - a.q_offsets[b] : 1;
-  return (n * (a.hq / a.c.hkv) + kStreamRows - 1) / kStreamRows * a.c.hkv;
+  return (n * (a.hq / a.c.hkv) + a.item_rows - 1) / a.item_rows * a.c.hkv;
 }
 // All units of sequence b; b may lie past the last.
 template <int UNIT>
@@ -162,12 +175,12 @@ __device__ __forceinline__ int item_head(const SharedAttnArgs& a, const Cursor& 
   return c.own ? c.x / (c.X / a.c.hkv) : c.x;
 }
 
-template <bool CODES>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+template <bool CODES, int NT>
+__global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
     attention_stream_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV) {
-  using Cfg = StreamCfg<CODES>;
-  constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit;
+  using Cfg = StreamCfg<CODES, NT>;
+  constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit, kThreads = Cfg::kThreads, kRows = 8 * NT;
   constexpr int kKeys = kUnit * kPage;  // keys of a unit
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -188,7 +201,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   // ---- the plan: thread i counts the units of its own run of sequences
   const int B = a.c.num_seqs, G = a.hq / a.c.hkv;
-  const int per = (B + kStreamThreads - 1) / kStreamThreads;
+  const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
@@ -214,8 +227,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     scan[threadIdx.x + 1] = x + before;
     __syncthreads();
   }
-  const long long units = prefix_units + scan[kStreamThreads];
-  const long long workers = static_cast<long long>(gridDim.x) * kStreamWarps;
+  const long long units = prefix_units + scan[kThreads];
+  const long long workers = static_cast<long long>(gridDim.x) * Cfg::kWarps;
   const long long chunk = max(static_cast<long long>(kMinChunk), (units + workers - 1) / workers);
   if (blockIdx.x == 0) {
     long long at = prefix_units + scan[threadIdx.x];
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     cc.n = pu;
   } else {
     const long long v = u0 - prefix_units;
-    int lo = 0, hi = kStreamThreads;  // scan[lo] <= v < scan[hi]
+    int lo = 0, hi = kThreads;  // scan[lo] <= v < scan[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (scan[mid] <= v)
@@ -352,27 +365,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   // ---- consumer
   const int gq = lane >> 2, tq = lane & 3;
-  // The 16 keys of a page go to the two 8-key tiles so that lane tq's four
-  // accumulator columns are keys 4 tq .. 4 tq + 3 (their exponents one word)
-  // and each tile's keys fall on eight different swizzle positions: columns
-  // 2i, 2i + 1 of tile t are keys 4 i + 2 (t ^ (i >> 1)) and the next.
-  auto tile_key = [](int t, int col) { return 4 * (col >> 1) + 2 * (t ^ (col >> 2)) + (col & 1); };
-  const int my_key[2] = {tile_key(0, 2 * tq), tile_key(1, 2 * tq)};
-  const uint32_t key_order = tq < 2 ? 0x3210u : 0x1032u;
+  // The 16 keys of a page go to the two halves of M so that lane group gq's two
+  // accumulator rows are keys 2 gq and 2 gq + 1 (their exponents one half word)
+  // and the 8 keys of a half fall on eight different swizzle positions: row i
+  // of half t is key 2 i + (t ^ (i >> 2)).
+  auto half_key = [](int t, int i) { return 2 * i + (t ^ (i >> 2)); };
+  const int my_key[2] = {half_key(0, gq), half_key(1, gq)};
   // ldmatrix offsets within a plane (or half of one): lane 8 i + j addresses row
-  // j of matrix i. k_off: matrices (tile 0, chunk 2 c), (0, 2 c + 1), (1, ..);
-  // v_off: (tile 0, chunk 2 c), (1, 2 c), (0, 2 c + 1), (1, 2 c + 1).
-  uint32_t k_off[4], v_off[4];
+  // j of matrix i: (half 0, chunk 2 c), (1, 2 c), (0, 2 c + 1), (1, 2 c + 1).
+  uint32_t off[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int mi = lane >> 3, ri = lane & 7;
-    k_off[c] = swz(tile_key(mi >> 1, ri), 2 * c + (mi & 1));
-    v_off[c] = swz(tile_key(mi & 1, ri), 2 * c + (mi >> 1));
-  }
-  uint4 qf[8];
-  float o[16][4], m_o[2], m_l[2], f_row[2];
-  float2 l[2];  // two partial sums
-  int limit[2];  // keys that rows gq and gq + 8 of the tile see, counted from the item's first
+  for (int c = 0; c < 4; ++c) off[c] = swz(half_key((lane >> 3) & 1, lane & 7), 2 * c + (lane >> 4));
+
+  uint2 qf[NT][8];              // Q^T fragments
+  float o[8][NT][4];            // O^T: 16 dims x 8 rows
+  float2 m_o[NT], m_l[NT], l[NT], f_row[NT];  // of rows 2 tq, 2 tq + 1 of a tile; l: this lane's keys only
+  int limit[NT][2];             // keys that those rows see, counted from the item's first
   QueryRange qr{0, 0, 0, true};
   int g = 0, flat0 = 0, n_rows = 0;  // KV head, first row (within the sequence or the batch), rows
   int first_unit = 0;
@@ -384,54 +392,37 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     g = item_head(a, cc);
     if (cc.own) {
       qr = query_range(a, cc.b);
-      flat0 = cc.x % (cc.X / a.c.hkv) * kStreamRows;
-      n_rows = min(kStreamRows, (qr.hi - qr.lo) * G - flat0);
+      flat0 = cc.x % (cc.X / a.c.hkv) * kRows;
+      n_rows = min(kRows, (qr.hi - qr.lo) * G - flat0);
       keys = qr.len - a.prefix_len;
       safe = a.causal ? keys - (qr.hi - qr.lo - 1) + flat0 / G : keys;
     } else {
       qr.lo = 0;
-      flat0 = cc.b * kStreamRows;
-      n_rows = min(kStreamRows, a.total_q * G - flat0);
+      flat0 = cc.b * kRows;
+      n_rows = min(kRows, a.total_q * G - flat0);
       keys = safe = a.prefix_len;
     }
     first_unit = cc.j;
-    const __nv_bfloat16* src[2];
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const int r = gq + 8 * hr, flat = flat0 + r;
-      src[hr] = nullptr;
-      limit[hr] = keys;
+    for (int t = 0; t < NT; ++t) {
+      // fragment of 16 dims: row gq of the tile, the dims that lane tq's A registers hold
+      const int r = 8 * t + gq, flat = flat0 + r;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) qf[t][ks] = make_uint2(0u, 0u);
       if (r < n_rows) {
-        src[hr] = a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G) * 128;
-        if (cc.own && a.causal) limit[hr] -= qr.hi - qr.lo - 1 - flat / G;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(
+            a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G) * 128);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          qf[t][ks] = CODES ? *reinterpret_cast<const uint2*>(p + ks * 8 + 2 * tq)
+                            : make_uint2(p[ks * 8 + tq], p[ks * 8 + tq + 4]);
       }
-      m_o[hr] = m_l[hr] = -INFINITY;
-      l[hr] = make_float2(0.f, 0.f);
-      f_row[hr] = a.scale_log2;
-    }
-#pragma unroll
-    for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    // A fragment of 16 dims: registers 0 and 2 are row gq's first and second
-    // half of the dims that lane tq's B registers hold, 1 and 3 row gq + 8's.
-    uint2 w[2][8];
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        w[hr][ks] = make_uint2(0u, 0u);
-        if (src[hr] != nullptr) {
-          const uint32_t* p = reinterpret_cast<const uint32_t*>(src[hr] + ks * 16);
-          w[hr][ks] = CODES ? *reinterpret_cast<const uint2*>(p + 2 * tq) : make_uint2(p[tq], p[tq + 4]);
-        }
-      }
-    }
-    if constexpr (CODES) {
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
+      f_row[t] = make_float2(a.scale_log2, a.scale_log2);
+      if constexpr (CODES) {
         float am = 0.f;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
+          const float2 x = unpack_bf16(qf[t][ks].x), y = unpack_bf16(qf[t][ks].y);
           am = fmaxf(fmaxf(fmaxf(am, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
         }
         am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
@@ -439,72 +430,73 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         // 2^e <= max |q| < 2^(e+1), e in [-126, 126]: q / 2^e is exact in fp16
         // down to 2^-24 of the row's maximum
         const int e = am > 0.f ? min(126, max(-126, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 0;
-        const float down = pow2_byte(127 - e);
-        f_row[hr] = a.scale_log2 * pow2_byte(127 + e);
+        const float down = pow2_byte(127 - e), f = a.scale_log2 * pow2_byte(127 + e);
+        f_row[t] = make_float2(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const float2 x = unpack_bf16(w[hr][ks].x), y = unpack_bf16(w[hr][ks].y);
-          w[hr][ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
+          const float2 x = unpack_bf16(qf[t][ks].x), y = unpack_bf16(qf[t][ks].y);
+          qf[t][ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
         }
       }
-    }
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) qf[ks] = make_uint4(w[0][ks].x, w[1][ks].x, w[0][ks].y, w[1][ks].y);
+      for (int e = 0; e < 2; ++e) {
+        const int rc = 8 * t + 2 * tq + e;
+        limit[t][e] = cc.own && a.causal && rc < n_rows ? keys - (qr.hi - qr.lo - 1 - (flat0 + rc) / G) : keys;
+      }
+      m_o[t] = m_l[t] = make_float2(-INFINITY, -INFINITY);
+      l[t] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+    }
   };
 
   // the piece's rows: final when it is the whole of what they attend to, else parts
   auto close_item = [&]() {
     const bool whole = cc.own && a.prefix_len == 0 && first_unit == 0 && cc.j == cc.n - 1;
-    {
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        float sum = l[hr].x + l[hr].y;
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = gq + 8 * hr;
-        if (r >= n_rows) continue;
-        const int flat = flat0 + r;
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[t].x += __shfl_xor_sync(0xffffffffu, l[t].x, x);
+        l[t].y += __shfl_xor_sync(0xffffffffu, l[t].y, x);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * t + 2 * tq + e;
+        const float sum = e ? l[t].y : l[t].x, ml = e ? m_l[t].y : m_l[t].x;
+        const float mo = (e ? m_o[t].y : m_o[t].x) - (CODES ? 127.f : 0.f);
+        const int flat = flat0 + min(r, n_rows - 1);
         const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G;
-        if (whole) {
-          // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
-          const float f = (CODES ? exp2f(m_o[hr] - 127.f - m_l[hr]) : 1.f) / sum;
+        const bool rest = first_unit > 0;  // the piece continues an earlier worker's
+        const size_t at = rest ? static_cast<size_t>(worker) * kRows + r : row;
+        float* po = rest ? a.cont_o : cc.own ? a.own_o : a.prefix_o;
+        PartStat* ps = rest ? a.cont_st : cc.own ? a.own_st : a.prefix_st;
+        // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
+        const float f = whole ? (CODES ? exp2f(mo - ml) : 1.f) / sum : 1.f;
 #pragma unroll
-          for (int n = 0; n < 16; n += 2) {
-            __nv_bfloat16* d = a.out + row * 128;
-            if constexpr (CODES) {
-              *reinterpret_cast<uint2*>(d + n * 8 + 4 * tq) =
-                  make_uint2(pack_bf16(o[n][2 * hr] * f, o[n + 1][2 * hr] * f),
-                             pack_bf16(o[n][2 * hr + 1] * f, o[n + 1][2 * hr + 1] * f));
-            } else {
-              *reinterpret_cast<uint32_t*>(d + n * 8 + 2 * tq) = pack_bf16(o[n][2 * hr] * f, o[n][2 * hr + 1] * f);
-              *reinterpret_cast<uint32_t*>(d + n * 8 + 8 + 2 * tq) =
-                  pack_bf16(o[n + 1][2 * hr] * f, o[n + 1][2 * hr + 1] * f);
-            }
+        for (int n = 0; n < 8; ++n) {
+          // two neighbouring dims of the 16 per lane: e4m3 products leave them so, bf16
+          // ones trade with the neighbour (dims gq and gq + 8 -> a pair of one half)
+          float v0 = o[n][t][e], v1 = o[n][t][2 + e];
+          int dim = 16 * n + 2 * gq;
+          if constexpr (!CODES) {
+            const bool odd = gq & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 4);
+            (odd ? v0 : v1) = got;
+            dim = 16 * n + (odd ? 8 : 0) + (gq & ~1);
           }
-          if (tq == 0 && a.lse != nullptr) a.lse[row] = (m_l[hr] + log2f(sum)) * 0.6931471805599453f;
-        } else {
-          float* d;
-          PartStat* st;
-          if (first_unit > 0) {
-            const size_t at = static_cast<size_t>(worker) * kStreamRows + r;
-            d = a.cont_o + at * 128;
-            st = a.cont_st + at;
-          } else {
-            d = (cc.own ? a.own_o : a.prefix_o) + row * 128;
-            st = (cc.own ? a.own_st : a.prefix_st) + row;
+          if (r < n_rows) {
+            if (whole)
+              *reinterpret_cast<uint32_t*>(a.out + row * 128 + dim) = pack_bf16(v0 * f, v1 * f);
+            else
+              *reinterpret_cast<float2*>(po + at * 128 + dim) = make_float2(v0, v1);
           }
-#pragma unroll
-          for (int n = 0; n < 16; n += 2) {
-            if constexpr (CODES) {
-              *reinterpret_cast<float4*>(d + n * 8 + 4 * tq) =
-                  make_float4(o[n][2 * hr], o[n + 1][2 * hr], o[n][2 * hr + 1], o[n + 1][2 * hr + 1]);
-            } else {
-              *reinterpret_cast<float2*>(d + n * 8 + 2 * tq) = make_float2(o[n][2 * hr], o[n][2 * hr + 1]);
-              *reinterpret_cast<float2*>(d + n * 8 + 8 + 2 * tq) =
-                  make_float2(o[n + 1][2 * hr], o[n + 1][2 * hr + 1]);
-            }
-          }
-          if (tq == 0) *st = PartStat{CODES ? m_o[hr] - 127.f : m_o[hr], m_l[hr], sum, 0.f};
+        }
+        if (gq == 0 && r < n_rows) {
+          if (!whole)
+            ps[at] = PartStat{mo, ml, sum, 0.f};
+          else if (a.lse != nullptr)
+            a.lse[row] = (ml + log2f(sum)) * 0.6931471805599453f;
         }
       }
     }
@@ -521,182 +513,175 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const uint32_t stage = smem_u32(ring + s * Cfg::kStage);
     const int key0 = cc.j * kKeys;
     const bool border = key0 + kKeys > safe;  // some row does not see some key of the unit
-    float2 sc[2 * kUnit][2];  // scores: key tile (8 keys), row gq or gq + 8, two keys
+    float2 sc[2 * kUnit][NT];  // scores of this lane's keys (half 0, half 1 of each page), its two rows
     {
-      constexpr int kChains = kUnit == 1 ? 2 : 1;  // accumulators per key tile, for independent products
-      float acc[2 * kUnit][kChains][4] = {};
+      float acc[kUnit][NT][2][4] = {};  // two chains, for independent products
 #pragma unroll
       for (int u = 0; u < kUnit; ++u) {
         const uint32_t kb = stage + u * 2 * Cfg::kPlane;
-        if constexpr (CODES) {
 #pragma unroll
-          for (int k2 = 0; k2 < 4; ++k2) {  // 32 dims
-            uint32_t r[4];  // key tiles 0 and 1 of chunk 2 k2, then of the next
-            ldsm_x4(kb + v_off[k2], r);
+        for (int c = 0; c < (CODES ? 4 : 8); ++c) {
+          uint32_t r[4];  // halves 0 and 1 of one chunk, then of the next
+          ldsm_x4(kb + (CODES ? 0 : (c >> 2) * 2048) + off[c & 3], r);
+          if constexpr (CODES) {  // a chunk is 16 dims
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              uint4 A;
+              widen4(r[2 * h], A.x, A.z);
+              widen4(r[2 * h + 1], A.y, A.w);
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
-                uint32_t lo, hi;
-                widen4(r[2 * h + nt], lo, hi);
-                mma16816<true>(acc[2 * u + nt][h % kChains], qf[2 * k2 + h], lo, hi);
-              }
+              for (int t = 0; t < NT; ++t) mma16816<true>(acc[u][t][h], A, qf[t][2 * c + h]);
             }
-          }
-        } else {
+          } else {
+            const uint4 A = make_uint4(r[0], r[1], r[2], r[3]);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            uint32_t r[4];  // key tile 0: dims 0-7, 8-15 of the 16; tile 1 likewise
-            ldsm_x4(kb + (ks >> 2) * 2048 + k_off[ks & 3], r);
-            mma16816<false>(acc[2 * u][ks % kChains], qf[ks], r[0], r[1]);
-            mma16816<false>(acc[2 * u + 1][ks % kChains], qf[ks], r[2], r[3]);
+            for (int t = 0; t < NT; ++t) mma16816<false>(acc[u][t][c & 1], A, qf[t][c]);
           }
         }
       }
 #pragma unroll
-      for (int nt = 0; nt < 2 * kUnit; ++nt)
+      for (int u = 0; u < kUnit; ++u)
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          sc[nt][hr] = make_float2(acc[nt][0][2 * hr], acc[nt][0][2 * hr + 1]);
-          if constexpr (kChains == 2)
-            sc[nt][hr] = add2(sc[nt][hr], make_float2(acc[nt][1][2 * hr], acc[nt][1][2 * hr + 1]));
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            sc[2 * u + h][t] = add2(make_float2(acc[u][t][0][2 * h], acc[u][t][0][2 * h + 1]),
+                                    make_float2(acc[u][t][1][2 * h], acc[u][t][1][2 * h + 1]));
     }
-    float2 ve[2 * kUnit];  // value exponents of this lane's keys, biased by 127
-    if constexpr (CODES) {
+    float ve[2 * kUnit];  // value exponents of this lane's keys, biased by 127
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) {
-        const uint8_t* e = scales + (s * kUnit + u) * 32 + 4 * tq;
-        // this lane's four keys, tile 0's first
-        const uint32_t k4 = __byte_perm(*reinterpret_cast<const uint32_t*>(e), 0u, key_order);
-        const uint32_t v4 = __byte_perm(*reinterpret_cast<const uint32_t*>(e + 16), 0u, key_order);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 kf = make_float2(__uint_as_float((h ? k4 << 7 : k4 << 23) & 0x7f800000u),
-                                        __uint_as_float((h ? k4 >> 1 : k4 << 15) & 0x7f800000u));
-          // byte b as the float 2^23 + b, exactly
-          ve[2 * u + h] = add2(make_float2(__uint_as_float(__byte_perm(v4, 0x4b000000u, h ? 0x7442 : 0x7440)),
-                                           __uint_as_float(__byte_perm(v4, 0x4b000000u, h ? 0x7443 : 0x7441))),
-                               make_float2(-8388608.f, -8388608.f));
-#pragma unroll
-          for (int hr = 0; hr < 2; ++hr)
-            sc[2 * u + h][hr] = mul2(sc[2 * u + h][hr], mul2(kf, make_float2(f_row[hr], f_row[hr])));
-        }
+    for (int k = 0; k < 2 * kUnit; ++k) {
+      float kf = 1.f;
+      if constexpr (CODES) {
+        const uint8_t* e = scales + (s * kUnit + (k >> 1)) * 32 + my_key[k & 1];
+        kf = pow2_byte(e[0]);
+        // byte b as the float 2^23 + b, exactly
+        ve[k] = __uint_as_float(0x4b000000u | e[16]) - 8388608.f;
       }
-    } else {
 #pragma unroll
-      for (int nt = 0; nt < 2 * kUnit; ++nt)
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) sc[nt][hr] = mul2(sc[nt][hr], make_float2(f_row[hr], f_row[hr]));
+      for (int t = 0; t < NT; ++t)
+        sc[k][t] = mul2(sc[k][t], CODES ? mul2(f_row[t], make_float2(kf, kf)) : f_row[t]);
     }
     if (border) {
 #pragma unroll
-      for (int nt = 0; nt < 2 * kUnit; ++nt) {
-        const int key = key0 + (nt >> 1) * kPage + my_key[nt & 1];
+      for (int k = 0; k < 2 * kUnit; ++k) {
+        const int key = key0 + (k >> 1) * kPage + my_key[k & 1];
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          if (key >= limit[hr]) sc[nt][hr].x = -INFINITY;
-          if (key + 1 >= limit[hr]) sc[nt][hr].y = -INFINITY;
+        for (int t = 0; t < NT; ++t) {
+          if (key >= limit[t][0]) sc[k][t].x = -INFINITY;
+          if (key >= limit[t][1]) sc[k][t].y = -INFINITY;
         }
       }
     }
-    float mo[2], ml[2];
+    float2 mo[NT], ml[NT];
+    bool grows = false;
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      ml[hr] = fmaxf(sc[0][hr].x, sc[0][hr].y);
+    for (int t = 0; t < NT; ++t) {
+      ml[t] = sc[0][t];
 #pragma unroll
-      for (int nt = 1; nt < 2 * kUnit; ++nt) ml[hr] = fmaxf(ml[hr], fmaxf(sc[nt][hr].x, sc[nt][hr].y));
-      ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 1));
-      ml[hr] = fmaxf(ml[hr], __shfl_xor_sync(0xffffffffu, ml[hr], 2));
-      if constexpr (CODES) {
-        float2 t = add2(sc[0][hr], ve[0]);
-        mo[hr] = fmaxf(t.x, t.y);
+      for (int k = 1; k < 2 * kUnit; ++k) ml[t] = make_float2(fmaxf(ml[t].x, sc[k][t].x), fmaxf(ml[t].y, sc[k][t].y));
 #pragma unroll
-        for (int nt = 1; nt < 2 * kUnit; ++nt) {
-          t = add2(sc[nt][hr], ve[nt]);
-          mo[hr] = fmaxf(mo[hr], fmaxf(t.x, t.y));
-        }
-        mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 1));
-        mo[hr] = fmaxf(mo[hr], __shfl_xor_sync(0xffffffffu, mo[hr], 2));
-      } else {
-        mo[hr] = ml[hr];
+      for (int x = 4; x < 32; x <<= 1) {
+        ml[t].x = fmaxf(ml[t].x, __shfl_xor_sync(0xffffffffu, ml[t].x, x));
+        ml[t].y = fmaxf(ml[t].y, __shfl_xor_sync(0xffffffffu, ml[t].y, x));
       }
+      mo[t] = ml[t];
+      if constexpr (CODES) {
+        mo[t] = add2(sc[0][t], make_float2(ve[0], ve[0]));
+#pragma unroll
+        for (int k = 1; k < 2 * kUnit; ++k) {
+          const float2 v = add2(sc[k][t], make_float2(ve[k], ve[k]));
+          mo[t] = make_float2(fmaxf(mo[t].x, v.x), fmaxf(mo[t].y, v.y));
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          mo[t].x = fmaxf(mo[t].x, __shfl_xor_sync(0xffffffffu, mo[t].x, x));
+          mo[t].y = fmaxf(mo[t].y, __shfl_xor_sync(0xffffffffu, mo[t].y, x));
+        }
+      }
+      grows = grows || ml[t].x > m_l[t].x + 8.f || ml[t].y > m_l[t].y + 8.f || mo[t].x > m_o[t].x + 8.f ||
+              mo[t].y > m_o[t].y + 8.f;
     }
     // The reference maxima move only when a unit exceeds them by more than
     // 2^8: weights stay below 256 and the rescale is skipped on most units.
-    if (__any_sync(0xffffffffu, mo[0] > m_o[0] + 8.f || mo[1] > m_o[1] + 8.f || ml[0] > m_l[0] + 8.f ||
-                                    ml[1] > m_l[1] + 8.f)) {
+    if (__any_sync(0xffffffffu, grows)) {
+      auto step = [](float m, float n) { return n == -INFINITY ? 1.f : exp2f(m - n); };
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const float no = fmaxf(m_o[hr], mo[hr]), nl = fmaxf(m_l[hr], ml[hr]);
-        const float fo = no == -INFINITY ? 1.f : exp2f(m_o[hr] - no);
-        const float fl = nl == -INFINITY ? 1.f : exp2f(m_l[hr] - nl);
-        l[hr] = mul2(l[hr], make_float2(fl, fl));
-        m_o[hr] = no;
-        m_l[hr] = nl;
+      for (int t = 0; t < NT; ++t) {
+        const float2 no = make_float2(fmaxf(m_o[t].x, mo[t].x), fmaxf(m_o[t].y, mo[t].y));
+        const float2 nl = make_float2(fmaxf(m_l[t].x, ml[t].x), fmaxf(m_l[t].y, ml[t].y));
+        const float2 fo = make_float2(step(m_o[t].x, no.x), step(m_o[t].y, no.y));
+        l[t] = mul2(l[t], make_float2(step(m_l[t].x, nl.x), step(m_l[t].y, nl.y)));
+        m_o[t] = no;
+        m_l[t] = nl;
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          o[n][2 * hr] *= fo;
-          o[n][2 * hr + 1] *= fo;
-        }
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[n][t][c] *= (c & 1) ? fo.y : fo.x;
       }
     }
-    uint4 pa[kUnit];
-    {
-      uint32_t pr[kUnit][4];
+    uint2 pb[kUnit][NT];  // P^T fragments
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        // no key seen yet: the reference is still -inf, and every weight is 0
-        const float rl = m_l[hr] == -INFINITY ? 0.f : -m_l[hr], ro = m_o[hr] == -INFINITY ? 0.f : -m_o[hr];
+    for (int t = 0; t < NT; ++t) {
+      // no key seen yet: the reference is still -inf, and every weight is 0
+      auto neg = [](float m) { return m == -INFINITY ? 0.f : -m; };
+      const float2 rl = make_float2(neg(m_l[t].x), neg(m_l[t].y)), ro = make_float2(neg(m_o[t].x), neg(m_o[t].y));
 #pragma unroll
-        for (int nt = 0; nt < 2 * kUnit; ++nt) {
-          const float2 x = add2(sc[nt][hr], make_float2(rl, rl));
-          const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          l[hr] = add2(l[hr], e);
-          if constexpr (CODES) {
-            const float2 t = add2(sc[nt][hr], add2(ve[nt], make_float2(ro, ro)));
-            pr[nt >> 1][(nt & 1) * 2 + hr] = pack_f16(fast_exp2(t.x), fast_exp2(t.y));
-          } else {
-            pr[nt >> 1][(nt & 1) * 2 + hr] = pack_bf16(e.x, e.y);
-          }
+      for (int k = 0; k < 2 * kUnit; ++k) {
+        const float2 x = add2(sc[k][t], rl);
+        const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        l[t] = add2(l[t], e);
+        uint32_t p;
+        if constexpr (CODES) {
+          const float2 v = add2(sc[k][t], add2(ro, make_float2(ve[k], ve[k])));
+          p = pack_f16(fast_exp2(v.x), fast_exp2(v.y));
+        } else {
+          p = pack_bf16(e.x, e.y);
         }
+        p = transpose8x8(p);
+        if (k & 1)
+          pb[k >> 1][t].y = p;
+        else
+          pb[k >> 1][t].x = p;
       }
-#pragma unroll
-      for (int u = 0; u < kUnit; ++u) pa[u] = make_uint4(pr[u][0], pr[u][1], pr[u][2], pr[u][3]);
     }
-    // O += P V. Slots past the sequence's end may hold anything: their values
-    // are zeroed in registers, since 0 * NaN would reach O.
+    // O^T += V^T P^T. Slots past the sequence's end may hold anything: their
+    // values are zeroed in registers, since 0 * NaN would reach O.
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
       const uint32_t vb = stage + u * 2 * Cfg::kPlane + Cfg::kPlane;
       const int valid = keys - key0 - u * kPage;
-      uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
+      uint32_t mask[2] = {0xffffffffu, 0xffffffffu};
       if (valid < kPage) {
-        m0 = (my_key[0] < valid ? 0x0000ffffu : 0u) | (my_key[0] + 1 < valid ? 0xffff0000u : 0u);
-        m1 = (my_key[1] < valid ? 0x0000ffffu : 0u) | (my_key[1] + 1 < valid ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mask[h] = (half_key(h, 2 * tq) < valid ? 0x0000ffffu : 0u) |
+                    (half_key(h, 2 * tq + 1) < valid ? 0xffff0000u : 0u);
       }
 #pragma unroll
       for (int c = 0; c < (CODES ? 4 : 8); ++c) {
-        uint32_t r[4];  // key tiles 0 and 1 of one chunk, then of the next
-        ldsm_x4_t(vb + (CODES ? 0 : (c >> 2) * 2048) + v_off[c & 3], r);
+        uint32_t r[4];  // halves 0 and 1 of one chunk, then of the next
+        ldsm_x4_t(vb + (CODES ? 0 : (c >> 2) * 2048) + off[c & 3], r);
         if (valid < kPage) {
-          r[0] &= m0;
-          r[1] &= m1;
-          r[2] &= m0;
-          r[3] &= m1;
+          r[0] &= mask[0];
+          r[1] &= mask[1];
+          r[2] &= mask[0];
+          r[3] &= mask[1];
         }
+        if constexpr (CODES) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if constexpr (CODES) {
+          for (int h = 0; h < 2; ++h) {
             // bytes (k0 d0, k0 d1, k1 d0, k1 d1) -> even dims (k0, k1), odd dims (k0, k1)
-            uint32_t e0, d0, e1, d1;
-            widen4(__byte_perm(r[2 * h], 0u, 0x3120), e0, d0);
-            widen4(__byte_perm(r[2 * h + 1], 0u, 0x3120), e1, d1);
-            mma16816<true>(o[(2 * c + h) * 2], pa[u], e0, e1);
-            mma16816<true>(o[(2 * c + h) * 2 + 1], pa[u], d0, d1);
-          } else {
-            mma16816<false>(o[2 * c + h], pa[u], r[2 * h], r[2 * h + 1]);
+            uint4 A;
+            widen4(__byte_perm(r[2 * h], 0u, 0x3120), A.x, A.y);
+            widen4(__byte_perm(r[2 * h + 1], 0u, 0x3120), A.z, A.w);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816<true>(o[2 * c + h][t], A, pb[u][t]);
           }
+        } else {
+          const uint4 A = make_uint4(r[0], r[2], r[1], r[3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816<false>(o[c][t], A, pb[u][t]);
         }
       }
     }
@@ -775,18 +760,18 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) attention_join_kernel(Sh
       if (a.prefix_row_tiles > 0) {
         const int flat = t * G + h % G;
         const int pu = (a.prefix_len / kPage + unit - 1) / unit;
-        const long long u = (static_cast<long long>(flat / kStreamRows) * a.c.hkv + g) * pu;
+        const long long u = (static_cast<long long>(flat / a.item_rows) * a.c.hkv + g) * pu;
         p.prefix_w = static_cast<size_t>(u / chunk);
         p.prefix_n = static_cast<int>((u + pu - 1) / chunk - u / chunk) + 1;
-        p.prefix_r = flat % kStreamRows;
+        p.prefix_r = flat % a.item_rows;
       }
       const int n = (own_pages(a, b) + unit - 1) / unit;
       if (n > 0) {
         const int tiles = own_items(a, b) / a.c.hkv;
-        const long long u = a.plan[2 + b] + (static_cast<long long>(g) * tiles + r / kStreamRows) * n;
+        const long long u = a.plan[2 + b] + (static_cast<long long>(g) * tiles + r / a.item_rows) * n;
         p.own_w = static_cast<size_t>(u / chunk);
         p.own_n = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
-        p.own_r = r % kStreamRows;
+        p.own_r = r % a.item_rows;
       }
       if (a.prefix_len == 0 && p.own_n == 1) live = false;  // written by its only worker
     } else {
@@ -814,7 +799,7 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) attention_join_kernel(Sh
         po = pre ? a.prefix_o : a.own_o;
         ps = pre ? a.prefix_st : a.own_st;
         if (piece > 0) {
-          at = ((pre ? p.prefix_w : p.own_w) + piece) * kStreamRows + (pre ? p.prefix_r : p.own_r);
+          at = ((pre ? p.prefix_w : p.own_w) + piece) * a.item_rows + (pre ? p.prefix_r : p.own_r);
           po = a.cont_o;
           ps = a.cont_st;
         }
@@ -890,15 +875,13 @@ __global__ void __launch_bounds__(32 * join_warps(WPR)) attention_join_kernel(Sh
 
 }  // namespace
 
-int stream_workers(int num_sms) { return num_sms * kStreamWarps; }
-
 namespace {
 
-template <bool CODES>
+template <bool CODES, int NT>
 cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
                           cudaStream_t st) {
-  auto kern = attention_stream_kernel<CODES>;
-  constexpr size_t smem = StreamCfg<CODES>::kSmem;
+  auto kern = attention_stream_kernel<CODES, NT>;
+  constexpr size_t smem = StreamCfg<CODES, NT>::kSmem;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -910,14 +893,16 @@ cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const
     configured[dev].store(true, std::memory_order_release);
   }
   count_launch();
-  return launch_pdl(kern, dim3(num_sms), dim3(kStreamThreads), smem, st, a, tmK, tmV);
+  return launch_pdl(kern, dim3(num_sms), dim3(StreamCfg<CODES, NT>::kThreads), smem, st, a, tmK, tmV);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     int num_sms, cudaStream_t st) {
-  return a.c.codes ? launch_stream<true>(a, tmK, tmV, num_sms, st) : launch_stream<false>(a, tmK, tmV, num_sms, st);
+  if (a.item_rows == 8)
+    return a.c.codes ? launch_stream<true, 1>(a, tmK, tmV, num_sms, st) : launch_stream<false, 1>(a, tmK, tmV, num_sms, st);
+  return a.c.codes ? launch_stream<true, 2>(a, tmK, tmV, num_sms, st) : launch_stream<false, 2>(a, tmK, tmV, num_sms, st);
 }
 
 namespace {
