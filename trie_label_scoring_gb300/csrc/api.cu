@@ -943,7 +943,7 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   const long seq_rows = static_cast<long>(std::min(max_q, total_q)) * G;  // query rows of a sequence per KV head
   const long all_rows = static_cast<long>(total_q) * G;
   const bool stream = t.streamed = seq_rows <= 32;
-  t.item_rows = seq_rows <= 8 ? 8 : 16;
+  t.item_rows = 8;
   const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > t.item_rows : seq_rows < 128 && c->num_seqs > 1);
   if (tile_prefix)
     choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, &t.prefix_split,
@@ -1978,26 +1978,28 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool streamed = a.streamed;
   if (a.wide_pages) CUDA_TRY(launch_cache_widen(a, st));
-  if (a.prefix_splits > 0 || !streamed) {
-    CUtensorMap tK, tV;
-    const uint64_t pool_rows = static_cast<uint64_t>(a.pool_pages) * cache->n_kv_heads * 16;
-    s = encode_2d_bf16(&tK, a.wide_pages ? a.wide_k : cache->k_pool, pool_rows, 128, 128, 64, 16);
-    if (s != QUAIL_OK) return s;
-    s = encode_2d_bf16(&tV, a.wide_pages ? a.wide_v : cache->v_pool, pool_rows, 128, 128, 64, 16);
-    if (s != QUAIL_OK) return s;
-    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
-    if (!streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
-  }
   if (streamed) {
+    // before the tiles: these start on the SMs that it leaves first, and their
+    // parts, the larger ones, are still in L2 when the join reads them
     CUtensorMap tK, tV;
-    const uint64_t pool_rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
     for (int i = 0; i < 2; ++i) {
       const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
       CUtensorMap* m = i == 0 ? &tK : &tV;
-      s = a.c.codes ? encode_2d_codes(m, pool, pool_rows, 16) : encode_2d_bf16(m, pool, pool_rows, 128, 128, 64, 16);
+      s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
       if (s != QUAIL_OK) return s;
     }
     CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
+  }
+  if (a.prefix_splits > 0 || !streamed) {
+    CUtensorMap tK, tV;
+    const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * cache->n_kv_heads * 16;
+    s = encode_2d_bf16(&tK, a.wide_pages ? a.wide_k : cache->k_pool, rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+    s = encode_2d_bf16(&tV, a.wide_pages ? a.wide_v : cache->v_pool, rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
+    if (!streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
   }
   if (streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
   return QUAIL_OK;

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
   long long* scan = reinterpret_cast<long long*>(base + Cfg::kRing + Cfg::kScales + Cfg::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + Cfg::kRing + Cfg::kScales + Cfg::kBars +
                                                              Cfg::kScan);
+  const long long limit_clk = pipeline_wait_limit();
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1 + Cfg::kScaleLanes);
     fence_mbar_init();
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
     const int s = i % kStages;
     if (i == 0 || cc.j == 0) open_item();
     // warp-uniform wait: the collectives below need every lane
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], static_cast<uint32_t>((i / kStages) & 1), abort_flag))) {
+    if (!__all_sync(0xffffffffu, wait_bar(&bars[s], static_cast<uint32_t>((i / kStages) & 1), abort_flag, limit_clk))) {
       ok = false;
       break;
     }
@@ -705,172 +706,194 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// WPR warps share one (token, head) row (many where rows are few and parts many,
-// else each warp has its own): every warp folds its parts into (m, l, o), then
-// the first adds them up. Bound by the latency of three dependent reads
-// (lengths, plan, parts), so a warp reads up to kBatch parts at once.
-__host__ __device__ constexpr int join_warps(int wpr) { return wpr > 4 ? wpr : 4; }  // of a block
-
+// A row's parts, in this order: the prefix by key range (tiles), the prefix in
+// pieces (streamed), the own keys in pieces (streamed) or by key range (tiles).
+// Bound by latency: dependent reads (lengths, plan, parts), and the fetching of
+// its instructions after hundreds of megabytes of keys have passed through L2.
+// So it is short: lane i finds part i and reads its statistics, all at once, and
+// one small loop adds the parts up.
 __device__ __forceinline__ float pow2_or_0(float x, float ref) {  // 2^(x - ref); 0 where nothing was seen
   return x == -INFINITY ? 0.f : exp2f(x - ref);
 }
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+  return v;
+}
 
-// A row's parts, in this order: the prefix by key range (tiles), the prefix in
-// pieces (streamed), the own keys in pieces (streamed) or by key range (tiles).
+// The sum of up to 32 parts, one per lane (o: its 128 values; m_l = -inf: none):
+// on return acc holds dims 4 lane .. 4 lane + 3, st the whole's statistics. The
+// values of the first parts are read along with the statistics.
+__device__ __forceinline__ float4 add_parts(const float* o, const PartStat* from, PartStat& st, int count, int lane) {
+  auto value = [&](int i) {
+    const float* p = reinterpret_cast<const float*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), i));
+    return *reinterpret_cast<const float4*>(p + 4 * lane);
+  };
+  st = lane < count ? *from : PartStat{-INFINITY, -INFINITY, 0.f, 0.f};
+  constexpr int kFirst = 6;
+  float4 v[kFirst];
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) v[i] = value(min(i, count - 1));
+  const float ml = warp_max(st.m_l), mo = warp_max(st.m_o);
+  const float f = pow2_or_0(st.m_o, mo);  // 0 in lanes past the last part
+  float l = st.l != st.l ? st.l : st.l * pow2_or_0(st.m_l, ml);  // a NaN sum stays one, whatever its maximum
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& x, float w) {
+    acc.x = fmaf(x.x, w, acc.x);
+    acc.y = fmaf(x.y, w, acc.y);
+    acc.z = fmaf(x.z, w, acc.z);
+    acc.w = fmaf(x.w, w, acc.w);
+  };
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) {
+    const float w = __shfl_sync(0xffffffffu, f, i);
+    if (i < count) add(v[i], w);
+  }
+#pragma unroll 4
+  for (int i = kFirst; i < count; ++i) add(value(i), __shfl_sync(0xffffffffu, f, i));
+  st = PartStat{mo, ml, l, 0.f};
+  return acc;
+}
+
+// (st, acc) += (ps, v), two sums with their own maxima.
+__device__ __forceinline__ void add_to(PartStat& st, float4& acc, const PartStat& ps, const float4& v) {
+  const float ml = fmaxf(st.m_l, ps.m_l), mo = fmaxf(st.m_o, ps.m_o);
+  const float f0 = pow2_or_0(st.m_o, mo), f1 = pow2_or_0(ps.m_o, mo);
+  acc = make_float4(acc.x * f0 + v.x * f1, acc.y * f0 + v.y * f1, acc.z * f0 + v.z * f1, acc.w * f0 + v.w * f1);
+  st.l = (st.l != st.l ? st.l : st.l * pow2_or_0(st.m_l, ml)) + (ps.l != ps.l ? ps.l : ps.l * pow2_or_0(ps.m_l, ml));
+  st.m_l = ml;
+  st.m_o = mo;
+}
+
 struct Parts {
   int prefix_dense, prefix_n, own_n, own_dense;
-  size_t prefix_w, own_w;  // worker of the first piece
-  int prefix_r, own_r;     // row within the items' tiles
+  uint32_t prefix_w, own_w;  // worker of the first piece
+  int prefix_r, own_r;       // row within the items' tiles
 };
 
-template <int WPR>
-__global__ void __launch_bounds__(32 * join_warps(WPR)) attention_join_kernel(SharedAttnArgs a) {
-  constexpr int kJoinWarps = join_warps(WPR);
+// first and number of the workers of units [u, u + n)
+__device__ __forceinline__ void pieces(long long u, int n, long long chunk, uint32_t* first, int* count) {
+  if (u + n <= 0x7fffffffLL && chunk <= 0x7fffffffLL) {  // 32-bit division
+    const uint32_t c = static_cast<uint32_t>(chunk), lo = static_cast<uint32_t>(u) / c;
+    *first = lo;
+    *count = static_cast<int>((static_cast<uint32_t>(u) + n - 1) / c - lo) + 1;
+  } else {
+    *first = static_cast<uint32_t>(u / chunk);
+    *count = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
+  }
+}
+
+// PER_ROW: the block's WARPS warps share row blockIdx.x = token * hq + head, else
+// they share the heads of token blockIdx.x.
+template <bool PER_ROW, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnArgs a) {
   grid_dependency_wait();
-  __shared__ float so[kJoinWarps][128];
-  __shared__ PartStat ss[kJoinWarps];
+  __shared__ float so[PER_ROW ? WARPS : 1][128];
+  __shared__ PartStat ss[PER_ROW ? WARPS : 1];
+  __shared__ int s_b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
-  const int sub = warp % WPR;
   const int G = a.hq / a.c.hkv;
-  bool live = row < static_cast<long long>(a.total_q) * a.hq;
-  const int t = live ? static_cast<int>(row / a.hq) : 0, h = live ? static_cast<int>(row % a.hq) : 0, g = h / G;
+  const int t = PER_ROW ? blockIdx.x / a.hq : blockIdx.x;
   int b = t;
-  if (live && a.q_offsets != nullptr) {  // last sequence that begins at or before t
-    int lo = 0, hi = a.c.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.q_offsets[mid] <= t)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    b = lo;
-  }
-  QueryRange qr{0, 0, 0, false};
-  if (live) qr = query_range(a, b);
-  live = live && qr.ok && t >= qr.lo && t < qr.hi;
-  Parts p{};
-  if (live && qr.len > 0) {
-    const int r = (t - qr.lo) * G + h % G;
-    p.prefix_dense = a.prefix_splits;
-    if (a.streamed) {
-      const long long chunk = a.plan[1];
-      const int unit = stream_unit_pages(a.c.codes);
-      if (a.prefix_row_tiles > 0) {
-        const int flat = t * G + h % G;
-        const int pu = (a.prefix_len / kPage + unit - 1) / unit;
-        const long long u = (static_cast<long long>(flat / a.item_rows) * a.c.hkv + g) * pu;
-        p.prefix_w = static_cast<size_t>(u / chunk);
-        p.prefix_n = static_cast<int>((u + pu - 1) / chunk - u / chunk) + 1;
-        p.prefix_r = flat % a.item_rows;
-      }
-      const int n = (own_pages(a, b) + unit - 1) / unit;
-      if (n > 0) {
-        const int tiles = own_items(a, b) / a.c.hkv;
-        const long long u = a.plan[2 + b] + (static_cast<long long>(g) * tiles + r / a.item_rows) * n;
-        p.own_w = static_cast<size_t>(u / chunk);
-        p.own_n = static_cast<int>((u + n - 1) / chunk - u / chunk) + 1;
-        p.own_r = r % a.item_rows;
-      }
-      if (a.prefix_len == 0 && p.own_n == 1) live = false;  // written by its only worker
-    } else {
-      const int keys = tile_key_end(a, qr, r) - a.seq_begin;
-      p.own_dense = keys > 0 ? (keys + a.seq_split - 1) / a.seq_split : 0;
-    }
-  }
-  const int parts = p.prefix_dense + p.prefix_n + p.own_n + p.own_dense;
-  float m_l = -INFINITY, m_o = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live) {
-    auto locate = [&](int i, const float*& o, const PartStat*& st) {
-      const float* po;
-      const PartStat* ps;
-      size_t at = static_cast<size_t>(row);
-      const int k = i - p.prefix_dense;
-      if (k < 0 || k >= p.prefix_n + p.own_n) {
-        const int s = k < 0 ? i : a.prefix_splits + k - p.prefix_n - p.own_n;
-        po = a.dense_o;
-        ps = a.dense_st;
-        at += static_cast<size_t>(s) * a.total_q * a.hq;
-      } else {
-        const bool pre = k < p.prefix_n;
-        const int piece = pre ? k : k - p.prefix_n;
-        po = pre ? a.prefix_o : a.own_o;
-        ps = pre ? a.prefix_st : a.own_st;
-        if (piece > 0) {
-          at = ((pre ? p.prefix_w : p.own_w) + piece) * a.item_rows + (pre ? p.prefix_r : p.own_r);
-          po = a.cont_o;
-          ps = a.cont_st;
-        }
-      }
-      o = po + at * 128;
-      st = ps + at;
-    };
-    constexpr int kBatch = WPR == 1 ? 6 : 4;
-    for (int i0 = sub; i0 < parts; i0 += WPR * kBatch) {
-      PartStat st[kBatch];
-      float4 v[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        st[k] = PartStat{-INFINITY, -INFINITY, 0.f, 0.f};
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i0 + k * WPR < parts) {
-          const float* o;
-          const PartStat* sp;
-          locate(i0 + k * WPR, o, sp);
-          st[k] = *sp;
-          v[k] = *reinterpret_cast<const float4*>(o + 4 * lane);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float nl = fmaxf(m_l, st[k].m_l), no = fmaxf(m_o, st[k].m_o);
-        l = l * pow2_or_0(m_l, nl) + st[k].l * (st[k].l != st[k].l ? 1.f : pow2_or_0(st[k].m_l, nl));
-        const float fo = pow2_or_0(m_o, no), fk = pow2_or_0(st[k].m_o, no);
-        acc.x = acc.x * fo + v[k].x * fk;
-        acc.y = acc.y * fo + v[k].y * fk;
-        acc.z = acc.z * fo + v[k].z * fk;
-        acc.w = acc.w * fo + v[k].w * fk;
-        m_l = nl;
-        m_o = no;
-      }
-    }
-  }
-  if constexpr (WPR > 1) {
-    *reinterpret_cast<float4*>(&so[warp][4 * lane]) = acc;
-    if (lane == 0) ss[warp] = PartStat{m_o, m_l, l, 0.f};
+  if (a.q_offsets != nullptr) {  // the sequence that has row t
+    if (threadIdx.x == 0) s_b = -1;
     __syncthreads();
-    if (sub != 0) return;
-    float nl = -INFINITY, no = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      nl = fmaxf(nl, ss[warp + w].m_l);
-      no = fmaxf(no, ss[warp + w].m_o);
-    }
-    l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) {
-      const PartStat st = ss[warp + w];
-      l += st.l * (st.l != st.l ? 1.f : pow2_or_0(st.m_l, nl));
-      const float f = pow2_or_0(st.m_o, no);
-      const float4 v = *reinterpret_cast<const float4*>(&so[warp + w][4 * lane]);
-      acc.x += v.x * f;
-      acc.y += v.y * f;
-      acc.z += v.z * f;
-      acc.w += v.w * f;
-    }
-    m_l = nl;
-    m_o = no;
+    for (int i = threadIdx.x; i < a.c.num_seqs; i += 32 * WARPS)
+      if (a.q_offsets[i] <= t && t < a.q_offsets[i + 1]) s_b = i;
+    __syncthreads();
+    b = s_b;
+    if (b < 0) return;  // of no sequence: left as it was
   }
-  if (!live) return;
-  // no key at all: 0 and -inf. A NaN sum makes the row NaN, as the formula has it.
-  const bool none = qr.len == 0;
-  const float f = none ? 0.f : (l != l ? l : exp2f(m_o - m_l) / l);
-  const float4 r = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-  *reinterpret_cast<uint2*>(a.out + row * 128 + 4 * lane) = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : (m_l + log2f(l)) * 0.6931471805599453f;
+  const QueryRange qr = query_range(a, b);
+  if (!qr.ok) return;
+  const int unit = stream_unit_pages(a.c.codes);
+  long long chunk = 1, base = 0;
+  int n = 0, tiles = 0;
+  if (a.streamed) {
+    chunk = a.plan[1];
+    base = a.plan[2 + b];
+    n = qr.len > 0 ? (own_pages(a, b) + unit - 1) / unit : 0;
+    tiles = own_items(a, b) / a.c.hkv;
+  }
+  const int pu = (a.prefix_len / kPage + unit - 1) / unit;
+  for (int h = PER_ROW ? blockIdx.x % a.hq : warp; h < a.hq; h += PER_ROW ? a.hq : WARPS) {
+    const int g = h / G;
+    const size_t row = static_cast<size_t>(t) * a.hq + h;
+    Parts p{};
+    if (qr.len > 0) {
+      const int r = (t - qr.lo) * G + h % G;
+      p.prefix_dense = a.prefix_splits;
+      if (a.streamed) {
+        if (a.prefix_row_tiles > 0) {
+          const int flat = t * G + h % G;
+          pieces((static_cast<long long>(flat / a.item_rows) * a.c.hkv + g) * pu, pu, chunk, &p.prefix_w, &p.prefix_n);
+          p.prefix_r = flat % a.item_rows;
+        }
+        if (n > 0) {
+          pieces(base + (static_cast<long long>(g) * tiles + r / a.item_rows) * n, n, chunk, &p.own_w, &p.own_n);
+          p.own_r = r % a.item_rows;
+        }
+        if (a.prefix_len == 0 && p.own_n == 1) continue;  // written by its only worker
+      } else {
+        const int keys = tile_key_end(a, qr, r) - a.seq_begin;
+        p.own_dense = keys > 0 ? (keys + a.seq_split - 1) / a.seq_split : 0;
+      }
+    }
+    const int parts = p.prefix_dense + p.prefix_n + p.own_n + p.own_dense;
+    // this warp's parts, 32 at a time
+    constexpr int kStep = PER_ROW ? WARPS : 1;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    PartStat st{-INFINITY, -INFINITY, 0.f, 0.f};
+    const int mine = PER_ROW ? (parts - warp + WARPS - 1) / WARPS : parts;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      const float* o = nullptr;
+      const PartStat* from = nullptr;
+      const int i = i0 + lane;
+      if (i < mine) {
+        int k = i * kStep + (PER_ROW ? warp : 0);
+        size_t at = row;
+        const float* po = a.dense_o;
+        const PartStat* pst = a.dense_st;
+        const int streamed = p.prefix_n + p.own_n;
+        if (k < p.prefix_dense || k >= p.prefix_dense + streamed) {
+          const int s = k < p.prefix_dense ? k : a.prefix_splits + k - p.prefix_dense - streamed;
+          at += static_cast<size_t>(s) * a.total_q * a.hq;
+        } else {
+          k -= p.prefix_dense;
+          const bool pre = k < p.prefix_n;
+          const int piece = pre ? k : k - p.prefix_n;
+          po = pre ? a.prefix_o : a.own_o;
+          pst = pre ? a.prefix_st : a.own_st;
+          if (piece > 0) {
+            at = (static_cast<size_t>(pre ? p.prefix_w : p.own_w) + piece) * a.item_rows + (pre ? p.prefix_r : p.own_r);
+            po = a.cont_o;
+            pst = a.cont_st;
+          }
+        }
+        o = po + at * 128;
+        from = pst + at;
+      }
+      PartStat ps;
+      const float4 v = add_parts(o, from, ps, min(32, mine - i0), lane);
+      add_to(st, acc, ps, v);
+    }
+    if constexpr (PER_ROW) {
+      *reinterpret_cast<float4*>(&so[warp][4 * lane]) = acc;
+      if (lane == 0) ss[warp] = st;
+      __syncthreads();
+      if (warp != 0) return;
+      acc = add_parts(so[lane % WARPS], ss + lane % WARPS, st, WARPS, lane);
+    }
+    // no key at all: 0 and -inf. A NaN sum makes the row NaN, as the formula has it.
+    const bool none = qr.len == 0;
+    const float f = none ? 0.f : (st.l != st.l ? st.l : exp2f(st.m_o - st.m_l) / st.l);
+    *reinterpret_cast<uint2*>(a.out + row * 128 + 4 * lane) =
+        make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+    if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : (st.m_l + log2f(st.l)) * 0.6931471805599453f;
+  }
 }
 
 }  // namespace
@@ -905,23 +928,15 @@ cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& 
   return a.c.codes ? launch_stream<true, 2>(a, tmK, tmV, num_sms, st) : launch_stream<false, 2>(a, tmK, tmV, num_sms, st);
 }
 
-namespace {
-
-template <int WPR>
-cudaError_t launch_join(const SharedAttnArgs& a, long long rows, cudaStream_t st) {
-  constexpr int per_block = join_warps(WPR) / WPR;
-  return launch_pdl(attention_join_kernel<WPR>, dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)),
-                    dim3(32 * join_warps(WPR)), 0, st, a);
-}
-
-}  // namespace
-
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.total_q) * a.hq;
   count_launch();
-  if (rows <= num_sms) return launch_join<16>(a, rows, st);
-  if (rows <= 16LL * num_sms) return launch_join<4>(a, rows, st);
-  return launch_join<1>(a, rows, st);
+  // few rows have many parts: a streamed row up to all workers over the KV heads
+  if (rows <= num_sms)
+    return launch_pdl(attention_join_kernel<true, 16>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, a);
+  if (rows <= 16LL * num_sms)
+    return launch_pdl(attention_join_kernel<true, 4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
+  return launch_pdl(attention_join_kernel<false, 8>, dim3(a.total_q), dim3(256), 0, st, a);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.

@@ -13,10 +13,11 @@
 // softmax warpgroup of the other works: a product is 512 tensor cycles, so each
 // softmax has 1,024 cycles for its 128 x 128 block.
 //
-// Roles (384 threads): warp 0 loads pages into one ring K0 V0 K1 V1 .., warp 1
-// owns TMEM and issues the MMAs, warps 4-7 and 8-11 are the softmax of tile 0
-// and 1, one thread per row (no exchange between threads), which also load
-// their Q row and write their O row.
+// Roles (384 threads): warps 0 and 3 load K and V pages into one ring K0 V0 K1
+// V1 .., warp 1 owns TMEM and issues the MMAs (a second issuer, one for each
+// tile, let the tiles' MMAs interleave and was slower), warps 4-7 and 8-11 are the
+// softmax of tile 0 and 1, one thread per row (no exchange between threads),
+// which also load their Q rows and write their O rows.
 #include <atomic>
 
 #include "cache_attn.cuh"
@@ -42,7 +43,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
+  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, drain;  // p_full: tile, half of the block's keys
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -102,9 +103,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(base + kOffBar);
   volatile int* abort_flag = &bars->abort_flag;
+  const long long limit_clk = pipeline_wait_limit();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.hq / a.c.hkv;
-  grid_dependency_wait();
+  // Behind the streaming kernel (prefix tiles only, no early exit) nothing here
+  // depends on it: it lets this kernel launch after its own wait, so all that
+  // came before it is complete, and these CTAs start on the SMs that it leaves
+  // first, 20 to 30 us before its last. The wait then comes before the exit.
+  const bool behind_stream = PREFIX && a.streamed;
+  if (!behind_stream) grid_dependency_wait();
 
   Item it;
   QueryRange qr{0, 0, 0, true};
@@ -148,6 +155,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_pages = (it.k_hi - it.k_lo + kPage - 1) / kPage;
   const int n_blocks = (n_pages + kBlkPages - 1) / kBlkPages;
 
+  // Query rows of the softmax warps, on their way before the set-up and before the
+  // page copies, which would hold them up (6,000 to 8,000 cycles otherwise): warp's
+  // 32 rows, half a warp to a row of 256 bytes.
+  const int t = (warp - 4) >> 2, quarter = warp & 3;  // tile and 32-row quarter of a softmax warp
+  const int rr = it.row0 + t * 128 + quarter * 32 + lane;  // row of the item
+  const bool row_ok = warp >= 4 && rr < it.n_rows;
+  const size_t out_row =
+      row_ok ? static_cast<size_t>(qr.lo + rr / G) * a.hq + it.g * G + rr % G : 0;  // (token, head)
+  uint4 qx[16];
+  if (warp >= 4 && (t == 0 || two)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int row = 2 * i + (lane >> 4);
+      const size_t src = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(out_row), row);
+      const bool in = it.row0 + t * 128 + quarter * 32 + row < it.n_rows;
+      qx[i] = in ? reinterpret_cast<const uint4*>(a.q + src * 128)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 1);
@@ -155,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], 128);
+      mbar_init(&bars->p_full[t][0], 128);
+      mbar_init(&bars->p_full[t][1], 128);
       mbar_init(&bars->pv_done[t], 1);
     }
     mbar_init(&bars->q_full, 256);
@@ -174,61 +201,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 0) {
-      // ---------------------------------------------- loader: lane q takes page q of a block
-      const int p0 = it.k_lo / kPage;
-      uint32_t armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int blk = 0; blk < n_blocks && ok; ++blk) {
-        const int np = min(kBlkPages, n_pages - blk * kBlkPages);
-        int page = -1;
-        if (lane < np) {
-          const int p = p0 + blk * kBlkPages + lane, pp = a.prefix_len / kPage;
-          if (a.wide_pages) {  // pages widened to bf16 in list order: the prefix, then each sequence's own
-            page = p < pp ? p : pp + it.b * a.wide_own + (p - pp);
-          } else {
-            page = p < pp ? a.prefix_pages[p] : a.c.table[static_cast<size_t>(it.b) * a.c.max_pages + p];
-          }
-          if (page < 0 || page >= a.pool_pages) {
-            raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, PREFIX ? 0 : it.b);
-            page = -1;  // not copied: the stage's old contents are consumed, the rows are void
-          }
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------------------- loaders (K: warp 0, V: warp 3)
+      // Lane q takes page q of a block; the ids of the next block are read while
+      // this one waits for its stage.
+      const int kv = warp == 0 ? 0 : 1;
+      const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
+      const int p0 = it.k_lo / kPage, pp = a.prefix_len / kPage;
+      auto page_id = [&](int blk) {
+        const int p = p0 + blk * kBlkPages + lane;
+        if (lane >= kBlkPages || blk * kBlkPages + lane >= n_pages) return -1;
+        // pages widened to bf16 lie in list order: the prefix, then each sequence's own
+        if (a.wide_pages) return p < pp ? p : pp + it.b * a.wide_own + (p - pp);
+        return p < pp ? a.prefix_pages[p] : a.c.table[static_cast<size_t>(it.b) * a.c.max_pages + p];
+      };
+      int next = page_id(0), issued = 0;
+      for (int blk = 0; blk < n_blocks; ++blk) {
+        int page = next;
+        if (blk + 1 < n_blocks) next = page_id(blk + 1);
+        const bool mine = lane < min(kBlkPages, n_pages - blk * kBlkPages);
+        if (mine && (page < 0 || page >= a.pool_pages)) {
+          raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, PREFIX ? 0 : it.b);
+          page = -1;  // not copied: the stage's old contents are consumed, the rows are void
         }
         const uint32_t good = __popc(__ballot_sync(0xffffffffu, page >= 0));
-#pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int idx = 2 * blk + kv, s = idx % kStages, use = idx / kStages;
-          if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty[s], static_cast<uint32_t>((use - 1) & 1), abort_flag))) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            if (good > 0)
-              mbar_arrive_expect_tx(&bars->full[s], good * 2 * 2048);
-            else
-              mbar_arrive(&bars->full[s]);
-          }
-          __syncwarp();
-          if (page >= 0) {
-            uint8_t* dst = base + kOffRing + s * kStage + lane * 2048;
-            const int y = (page * a.c.hkv + it.g) * kPage;
-            const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
-            tma_load_2d(dst, tm, &bars->full[s], 0, y);
-            tma_load_2d(dst + kHalf, tm, &bars->full[s], 64, y);
-          }
-          armed = good > 0 ? armed | 1u << s : armed & ~(1u << s);
-          armed_parity = (use & 1) ? armed_parity | 1u << s : armed_parity & ~(1u << s);
+        const int idx = 2 * blk + kv, s = idx % kStages, use = idx / kStages;
+        if (use > 0 && !__all_sync(0xffffffffu, wait_bar(&bars->empty[s], static_cast<uint32_t>((use - 1) & 1), abort_flag, limit_clk)))
+          break;
+        if (lane == 0) {
+          if (good > 0)
+            mbar_arrive_expect_tx(&bars->full[s], good * 2 * 2048);
+          else
+            mbar_arrive(&bars->full[s]);
         }
+        __syncwarp();
+        if (page >= 0) {
+          uint8_t* dst = base + kOffRing + s * kStage + lane * 2048;
+          const int y = (page * a.c.hkv + it.g) * kPage;
+          tma_load_2d(dst, tm, &bars->full[s], 0, y);
+          tma_load_2d(dst + kHalf, tm, &bars->full[s], 64, y);
+        }
+        ++issued;
       }
-      if (lane == 0) {  // no copy may still be landing when the CTA exits
-        for (int s = 0; s < kStages; ++s) {
-          if (!(armed >> s & 1u)) continue;
-          const long long t0 = clock64();
-          while (!mbar_try_wait(smem_u32(&bars->full[s]), armed_parity >> s & 1u)) {
-            if (clock64() - t0 > kWaitLimitCycles) {
-              *abort_flag = 1;
-              break;
-            }
+      // No copy may still be landing when the CTA exits: wait for this loader's last
+      // uses of the stages, but not for one that a later use has followed (the other
+      // loader filled the stage again only once it was consumed).
+      for (int blk = max(0, issued - 3); lane == 0 && blk < issued; ++blk) {
+        const int idx = 2 * blk + kv;
+        if (issued == n_blocks && idx + kStages < 2 * n_blocks) continue;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&bars->full[idx % kStages]), static_cast<uint32_t>((idx / kStages) & 1))) {
+          if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            break;
           }
         }
       }
@@ -240,6 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk = smem_desc_sw128(smem_u32(base + kOffRing));
       const uint64_t dv = smem_desc_sw128_mn(smem_u32(base + kOffRing), kHalf, 1024);
       const uint32_t dv_lo = static_cast<uint32_t>(dv), dv_hi = static_cast<uint32_t>(dv >> 32);
+      auto wait_full = [&](int idx) {
+        return wait_bar(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag, limit_clk);
+      };
       auto issue_s = [&](int t, int j) {
         const uint64_t k = dk + (((2 * j) % kStages * kStage) >> 4), q = dq + ((t * kStage) >> 4);
 #pragma unroll
@@ -249,18 +277,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&bars->s_full[t]);
       };
+      // the first half of the keys as soon as its weights are there, under the
+      // exponentials of the second
       auto issue_pv = [&](int t, int j) {
         const uint32_t v = dv_lo + (((2 * j + 1) % kStages * kStage) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)  // 16 keys = one page per instruction
-          umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
-                  (j > 0 || kk > 0) ? 1u : 0u);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait_bar(&bars->p_full[t][half], static_cast<uint32_t>(j & 1), abort_flag, limit_clk)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys = one page per instruction
+            umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+        }
         umma_commit(&bars->pv_done[t]);
+        return true;
       };
-      auto wait_full = [&](int idx) {
-        return mbar_wait(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag);
-      };
-      bool ok = mbar_wait(&bars->q_full, 0u, abort_flag) && wait_full(0);
+      bool ok = wait_bar(&bars->q_full, 0u, abort_flag, limit_clk) && wait_full(0);
       if (ok) {
         tc_fence_after();
         issue_s(0, 0);
@@ -269,22 +302,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = 0; ok && j < n_blocks; ++j) {
         const bool more = j + 1 < n_blocks;
-        const uint32_t par = static_cast<uint32_t>(j & 1);
-        ok = mbar_wait(&bars->p_full[0], par, abort_flag) && wait_full(2 * j + 1);
+        // the pages first: they are there long before the weights
+        ok = wait_full(2 * j + 1) && (!more || wait_full(2 * j + 2)) && issue_pv(0, j);
         if (!ok) break;
-        tc_fence_after();
-        issue_pv(0, j);
-        if (more) {
-          ok = wait_full(2 * j + 2);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(0, j + 1);
-        }
+        if (more) issue_s(0, j + 1);
         if (two) {
-          ok = mbar_wait(&bars->p_full[1], par, abort_flag);
+          ok = issue_pv(1, j);
           if (!ok) break;
-          tc_fence_after();
-          issue_pv(1, j);
         }
         umma_commit(&bars->empty[(2 * j + 1) % kStages]);
         if (more) {
@@ -305,20 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------ softmax: thread <-> row of tile t
-    const int t = (warp - 4) >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane;           // row of the tile = TMEM lane
-    const int rr = it.row0 + t * 128 + r;        // row of the item
-    const bool row_ok = rr < it.n_rows;
+    const int r = quarter * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    const size_t out_row =
-        row_ok ? static_cast<size_t>(qr.lo + rr / G) * a.hq + it.g * G + rr % G : 0;  // (token, head)
     uint8_t* q_tile = base + kOffQ + t * kStage;
     if (t == 0 || two) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row * 128);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const uint4 x = row_ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(q_tile + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+      for (int i = 0; i < 16; ++i) {
+        const int row = quarter * 32 + 2 * i + (lane >> 4), c = lane & 15;
+        *reinterpret_cast<uint4*>(q_tile + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = qx[i];
       }
       fence_proxy_async_smem();
     }
@@ -332,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n_blocks; ++j) {
         const uint32_t par = static_cast<uint32_t>(j & 1);
         const int key0 = it.k_lo + j * kBlkKeys;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[t], par, abort_flag))) {
+        if (!__all_sync(0xffffffffu, wait_bar(&bars->s_full[t], par, abort_flag, limit_clk))) {
           ok = false;
           break;
         }
@@ -340,24 +358,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t su[4][32];
         const int valid = limit - key0;
         const bool border = __any_sync(0xffffffffu, valid < kBlkKeys);
-        // The maximum of one quarter runs under the load of the next, on eight
-        // chains: a single chain of 128 dependent maxima would take longer than
-        // the exponentials.
+        // eight chains: one of 128 dependent maxima would take longer than the
+        // exponentials
         float mq[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mq[i] = -INFINITY;
-        tmem_ld_32cols_nowait(lane_addr + t * 128, su[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait(su[c]);
-          if (c < 3) tmem_ld_32cols_nowait(lane_addr + t * 128 + (c + 1) * 32, su[c + 1]);
-          if (border) {
+        for (int c = 0; c < 4; ++c) tmem_ld_32cols_nowait(lane_addr + t * 128 + c * 32, su[c]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) su[c][i] = c * 32 + i < valid ? su[c][i] : 0xff800000u;  // -infinity
-          }
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(su[c]);
+        if (border) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mq[i & 7] = fmaxf(mq[i & 7], __uint_as_float(su[c][i]));
+          for (int i = 0; i < 128; ++i) su[i >> 5][i & 31] = i < valid ? su[i >> 5][i & 31] : 0xff800000u;  // -infinity
         }
+#pragma unroll
+        for (int i = 0; i < 128; ++i) mq[i & 7] = fmaxf(mq[i & 7], __uint_as_float(su[i >> 5][i & 31]));
         const float mx = scale * fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
                                        fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
         // the reference maximum moves only past +8 in base 2 (weights stay below 256)
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j >= 1 && __any_sync(0xffffffffu, need)) {
           // O holds every product up to block j - 1 before it is rescaled
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], par ^ 1u, abort_flag))) {
+          if (!__all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], par ^ 1u, abort_flag, limit_clk))) {
             ok = false;
             break;
           }
@@ -383,6 +398,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) o[i] *= alpha;
             tmem_st_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
           }
+        }
+        // Keys past the range (tail of the last page, pages not loaded): their V
+        // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
+        // Tile 0 does it for both: its product is issued first.
+        const int in_range = it.k_hi - key0;
+        if (t == 0 && in_range < kBlkKeys) {
+          const int idx = 2 * j + 1;
+          if (!__all_sync(0xffffffffu, wait_bar(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag, limit_clk))) {
+            ok = false;
+            break;
+          }
+          uint8_t* v = base + kOffRing + (idx % kStages) * kStage;
+          for (int i = r; i < (kBlkKeys - in_range) * 16; i += 128) {
+            const int row = in_range + i / 16, c = i % 16;
+            *reinterpret_cast<uint4*>(v + (c / 8) * kHalf + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
         }
         // no key seen yet: the reference is still -inf, and every weight is 0
         const float ref = m_ref == -INFINITY ? 0.f : m_ref;
@@ -400,78 +432,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[i] = pack_bf16(e.x, e.y);
           }
           tmem_st_32cols_nowait(lane_addr + t * 128 + c * 32, w);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[t][c]);
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
-        // Keys past the range (tail of the last page, pages not loaded): their V
-        // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
-        // Tile 0 does it for both: its product is issued first.
-        const int in_range = it.k_hi - key0;
-        if (t == 0 && in_range < kBlkKeys) {
-          const int idx = 2 * j + 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag))) {
-            ok = false;
-            break;
-          }
-          uint8_t* v = base + kOffRing + (idx % kStages) * kStage;
-          for (int i = r; i < (kBlkKeys - in_range) * 16; i += 128) {
-            const int row = in_range + i / 16, c = i % 16;
-            *reinterpret_cast<uint4*>(v + (c / 8) * kHalf + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[t]);
       }
       // ---- rows out, through this tile's Q buffer (no MMA reads it any more):
       // a warp's 32 rows as whole 256-byte lines
-      if (ok && __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag))) {
+      if (ok && __all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag, limit_clk))) {
         tc_fence_after();
         uint8_t* stage = q_tile + quarter * 8192;
         const bool final = a.dense_parts == 0;
         const float inv = 1.f / l;
         const size_t part = (PREFIX ? it.split : a.prefix_splits + it.split) * static_cast<size_t>(a.total_q) * a.hq;
-        const int passes = final ? 1 : 2;  // 128 bf16, or twice 64 fp32
-#pragma unroll 1
-        for (int ps = 0; ps < passes; ++ps) {
+        uint32_t o[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32cols_nowait(lane_addr + kTmemO + t * 128 + c * 32, o[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(o[c]);
+        // 256 bytes of every row at a time: the row as bf16, or twice 64 of its fp32 elements
+        auto copy_out = [&](int pass) {
           __syncwarp();
-          if (final) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
+          for (int i0 = 0; i0 < 16; i0 += 8) {  // 16 lanes a row, eight pairs of rows in flight
+            uint4 x[8];
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                const int chunk = c * 4 + i / 8;
-                *reinterpret_cast<uint4*>(stage + lane * 256 + ((chunk ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                               pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
-              }
+            for (int i = 0; i < 8; ++i) {
+              const int row = 2 * (i0 + i) + (lane >> 4);
+              x[i] = *reinterpret_cast<const uint4*>(stage + row * 256 + (((lane & 15) ^ (row & 7)) << 4));
             }
-          } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float o[32];
-              tmem_ld_32cols(lane_addr + kTmemO + t * 128 + ps * 64 + c * 32, o);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const int chunk = c * 8 + i / 4;
-                *reinterpret_cast<float4*>(stage + lane * 256 + ((chunk ^ (lane & 7)) << 4)) =
-                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 8; ++i) {
+              const int row = 2 * (i0 + i) + (lane >> 4);
+              const size_t dst = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(out_row), row);
+              if (it.row0 + t * 128 + quarter * 32 + row < it.n_rows) {
+                if (final)
+                  reinterpret_cast<uint4*>(a.out + dst * 128)[lane & 15] = x[i];
+                else
+                  reinterpret_cast<uint4*>(a.dense_o + (part + dst) * 128 + pass * 64)[lane & 15] = x[i];
               }
             }
           }
           __syncwarp();
-          for (int i = 0; i < 32; i += 2) {  // 16 lanes a row
-            const int row = i + (lane >> 4), c = lane & 15;
-            const size_t dst = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(out_row), row);
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 256 + ((c ^ (row & 7)) << 4));
-            if (it.row0 + t * 128 + quarter * 32 + row >= it.n_rows) continue;
-            if (final)
-              reinterpret_cast<uint4*>(a.out + dst * 128)[c] = x;
-            else
-              reinterpret_cast<uint4*>(a.dense_o + (part + dst) * 128 + ps * 64)[c] = x;
+        };
+        auto put = [&](int chunk, uint4 v) {  // 16 bytes of this lane's row
+          *reinterpret_cast<uint4*>(stage + lane * 256 + ((chunk ^ (lane & 7)) << 4)) = v;
+        };
+        if (final) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t* v = &o[k >> 2][8 * k & 31];
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+            put(k, make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          copy_out(0);
+        } else {
+#pragma unroll
+          for (int ps = 0; ps < 2; ++ps) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const uint32_t* v = &o[2 * ps + (k >> 3)][4 * k & 31];
+              put(k, make_uint4(v[0], v[1], v[2], v[3]));
+            }
+            copy_out(ps);
           }
         }
         if (row_ok) {
@@ -491,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem_base, 512);
   }
   if (threadIdx.x == 0 && *abort_flag) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 5000);
+  if (behind_stream) grid_dependency_wait();
 }
 
 template <bool PREFIX>

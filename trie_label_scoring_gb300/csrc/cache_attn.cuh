@@ -26,6 +26,25 @@ __device__ __forceinline__ QueryRange query_range(const SharedAttnArgs& a, int b
   return r;
 }
 
+// mbar_wait for waits that are often not over at once: the limit comes in a
+// register instead of a load between two tries.
+__device__ __forceinline__ long long pipeline_wait_limit() {
+  return *const_cast<const volatile long long*>(&g_pipeline_wait_limit);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
 // Pages of sequence b's own keys that its queries read (0: none, or a bad sequence).
 __device__ __forceinline__ int own_pages(const SharedAttnArgs& a, int b) {
   const QueryRange r = query_range(a, b);
