@@ -944,7 +944,10 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   const long all_rows = static_cast<long>(total_q) * G;
   const bool stream = t.streamed = seq_rows <= 32;
   t.item_rows = 8;
-  const bool tile_prefix = prefix_len > 0 && (stream ? all_rows > t.item_rows : seq_rows < 128 && c->num_seqs > 1);
+  // pages that streaming the prefix would read, again for every eight rows of the batch
+  const long prefix_pages = (all_rows + t.item_rows - 1) / t.item_rows * hkv * (prefix_len / 16);
+  const bool tile_prefix =
+      prefix_len > 0 && (stream ? all_rows > t.item_rows && prefix_pages > 4096 : seq_rows < 128 && c->num_seqs > 1);
   if (tile_prefix)
     choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, &t.prefix_split,
                       &t.prefix_splits);

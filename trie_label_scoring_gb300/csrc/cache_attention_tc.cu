@@ -88,6 +88,33 @@ __device__ __forceinline__ void tmem_st_32cols_nowait(uint32_t taddr, const uint
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// 16 columns, waited for.
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])),
+      "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
+      "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+
 struct Item {
   int row0, n_rows;  // this CTA's first row and the rows there are, per KV head
   int k_lo, k_hi;    // keys
@@ -358,46 +385,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t su[4][32];
         const int valid = limit - key0;
         const bool border = __any_sync(0xffffffffu, valid < kBlkKeys);
-        // eight chains: one of 128 dependent maxima would take longer than the
-        // exponentials
-        float mq[8];
+        // The weights of the first half are computed against the reference
+        // maximum as it stands, while the second half and the block's own maximum
+        // are still on their way; the rare block that moves the reference (past +8
+        // in base 2, so weights stay below 256) computes them again.
+        float2 sum[4] = {};
+        uint32_t w[32];
+        auto weights = [&](int c) {  // of keys 64 c .. 64 c + 63: 32 columns of bf16 pairs
+          // no key seen yet: the reference is still -inf, and every weight is 0
+          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 sc2 = make_float2(scale, scale), nr2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mq[i] = -INFINITY;
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t* s = &su[2 * c + (i >> 4)][2 * i & 31];
+            const float2 x = fma2(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2, nr2);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum[i & 3] = add2(sum[i & 3], e);
+            w[i] = pack_bf16(e.x, e.y);
+          }
+        };
+        auto hide = [&](int c) {  // keys past this row's limit in quarter c
+          if (border) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32cols_nowait(lane_addr + t * 128 + c * 32, su[c]);
+            for (int i = 0; i < 32; ++i) su[c][i] = c * 32 + i < valid ? su[c][i] : 0xff800000u;  // -infinity
+          }
+        };
+        float mq[8];  // eight chains
+        auto raise = [&](int c) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(su[c]);
-        if (border) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) su[i >> 5][i & 31] = i < valid ? su[i >> 5][i & 31] : 0xff800000u;  // -infinity
-        }
-#pragma unroll
-        for (int i = 0; i < 128; ++i) mq[i & 7] = fmaxf(mq[i & 7], __uint_as_float(su[i >> 5][i & 31]));
+          for (int i = 0; i < 32; ++i) {
+            const float x = __uint_as_float(su[c][i]);
+            mq[i & 7] = c == 0 && i < 8 ? x : fmaxf(mq[i & 7], x);
+          }
+        };
+        tmem_ld_32cols_nowait(lane_addr + t * 128, su[0]);
+        tmem_ld_32cols_nowait(lane_addr + t * 128 + 32, su[1]);
+        tmem_ld_wait(su[0]);
+        tmem_ld_wait(su[1]);
+        tmem_ld_32cols_nowait(lane_addr + t * 128 + 64, su[2]);
+        tmem_ld_32cols_nowait(lane_addr + t * 128 + 96, su[3]);
+        hide(0);
+        hide(1);
+        if (j > 0) weights(0);
+        raise(0);
+        raise(1);
+        tmem_ld_wait(su[2]);
+        tmem_ld_wait(su[3]);
+        hide(2);
+        hide(3);
+        raise(2);
+        raise(3);
         const float mx = scale * fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
                                        fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
-        // the reference maximum moves only past +8 in base 2 (weights stay below 256)
         const bool need = mx > m_ref + 8.f;
-        float alpha = 1.f;
-        if (need) {
-          alpha = exp2f(m_ref - mx);
-          m_ref = mx;
-          l *= alpha;
-        }
-        if (j >= 1 && __any_sync(0xffffffffu, need)) {
-          // O holds every product up to block j - 1 before it is rescaled
-          if (!__all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], par ^ 1u, abort_flag, limit_clk))) {
-            ok = false;
-            break;
+        if (j == 0 || __any_sync(0xffffffffu, need)) {
+          float alpha = 1.f;
+          if (need) {
+            alpha = exp2f(m_ref - mx);
+            m_ref = mx;
+            l *= alpha;
           }
-          tc_fence_after();
+          if (j > 0) {
+            // O holds every product up to block j - 1 before it is rescaled
+            if (!__all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], par ^ 1u, abort_flag, limit_clk))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
+            for (int c = 0; c < 8; ++c) {
+              float o[16];
+              tmem_ld_16cols(lane_addr + kTmemO + t * 128 + c * 16, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st_32cols(lane_addr + kTmemO + t * 128 + c * 32, o);
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tmem_st_16cols(lane_addr + kTmemO + t * 128 + c * 16, o);
+            }
           }
+          sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
+          weights(0);
         }
         // Keys past the range (tail of the last page, pages not loaded): their V
         // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
@@ -416,21 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        // no key seen yet: the reference is still -inf, and every weight is 0
-        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-        const float2 sc2 = make_float2(scale, scale), nr2 = make_float2(-ref, -ref);
-        float2 sum[4] = {};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // 64 keys: 32 columns of bf16 pairs
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t* s = &su[2 * c + (i >> 4)][2 * i & 31];
-            const float2 x = fma2(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2, nr2);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            sum[i & 3] = add2(sum[i & 3], e);
-            w[i] = pack_bf16(e.x, e.y);
-          }
+        for (int c = 0; c < 2; ++c) {
+          if (c == 1) weights(1);
           tmem_st_32cols_nowait(lane_addr + t * 128 + c * 32, w);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
