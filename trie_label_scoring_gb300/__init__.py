@@ -554,6 +554,7 @@ def classify_trie_tree_ml(model: ModelML, kv: KVML, trie: Trie, num_docs: int, w
 
 # ------------------------------------------------------------------ document cache
 DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
+_torch = None  # set with the first KVCache: the calls below run once per token and layer, and are kept short
 
 
 def _need(ok: bool, message: str) -> None:
@@ -561,8 +562,12 @@ def _need(ok: bool, message: str) -> None:
         raise QuailError(-1, message)
 
 
-def _is(t, dtype, shape=None) -> bool:
-    return t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)
+def _at(cache, t, dtype, numel: int, what: str) -> int:
+    """Address of a contiguous tensor of numel elements on the cache's device."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != cache.index or not t.is_contiguous():
+        raise QuailError(-1, f"{what}: need {numel} contiguous {dtype} elements on {cache.device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 class KVCache:
@@ -572,26 +577,35 @@ class KVCache:
     calls as KV(k_pool, v_pool, page_table, seq_len, max_len)."""
 
     def __init__(self, k_pool, v_pool, page_table, k_scale=None, v_scale=None):
+        global _torch
         import torch
+        _torch = torch
+        _need(k_pool.is_cuda, "the pools must be device tensors")
+        self.device, self.index = k_pool.device, k_pool.get_device()
         shape = k_pool.shape
         _need(len(shape) == 4 and shape[2] == 16 and shape[3] == 128, "pools must be [pages, kv heads, 16, 128]")
         codes = k_pool.dtype in (torch.uint8, torch.float8_e4m3fn)
         _need(codes or k_pool.dtype is torch.bfloat16, "pools must be bfloat16, float8_e4m3fn or uint8")
-        _need(_is(k_pool, k_pool.dtype) and _is(v_pool, k_pool.dtype, shape), "pools must be contiguous and alike")
+        _need(v_pool.shape == shape, "the pools must have one shape")
         _need((k_scale is not None and v_scale is not None) if codes else (k_scale is None and v_scale is None),
               "an e4m3 cache has two scale tensors, a bf16 cache none")
-        for t in (k_scale, v_scale):
-            _need(t is None or _is(t, torch.uint8, shape[:3]), "scales must be contiguous uint8 [pages, kv heads, 16]")
-        _need(page_table.dim() == 2 and _is(page_table, torch.int32), "page_table must be contiguous int32 [seqs, pages]")
-        for t in (v_pool, k_scale, v_scale, page_table):
-            _need(t is None or t.device == k_pool.device, "the cache's tensors must share one device")
+        _need(page_table.dim() == 2, "page_table must be [num_seqs, max_pages]")
         self.tensors = (k_pool, v_pool, page_table, k_scale, v_scale)
-        self.n_kv_heads = int(shape[1])
-        self.num_seqs = int(page_table.shape[0])
-        self.device = k_pool.device
-        self.desc = CacheDesc(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                              DTYPE_E4M3 if codes else DTYPE_BF16, self.n_kv_heads, 128, int(shape[0]), 16,
-                              _ptr(page_table), self.num_seqs, int(page_table.shape[1]))
+        self.n_kv_heads, self.num_seqs = int(shape[1]), int(page_table.shape[0])
+        n = k_pool.numel()
+        scales = [None if t is None else _at(self, t, torch.uint8, n // 128, "scales") for t in (k_scale, v_scale)]
+        self.desc = CacheDesc(_at(self, k_pool, k_pool.dtype, n, "k_pool"), _at(self, v_pool, k_pool.dtype, n, "v_pool"),
+                              *scales, DTYPE_E4M3 if codes else DTYPE_BF16, self.n_kv_heads, 128, int(shape[0]), 16,
+                              _at(self, page_table, torch.int32, page_table.numel(), "page_table"), self.num_seqs,
+                              int(page_table.shape[1]))
+        self.ref = ctypes.byref(self.desc)
+
+
+def _cache_stream(cache: KVCache, stream) -> int:
+    """The given stream, or the current one of the cache's device."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(cache.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def cache_append(cache: KVCache, qkv, n_q_heads: int, token_seq, token_pos, q_out=None, q_norm=None, k_norm=None,
@@ -599,40 +613,38 @@ def cache_append(cache: KVCache, qkv, n_q_heads: int, token_seq, token_pos, q_ou
     """qkv [T, >= (n_q_heads + 2 H_kv) * 128] bf16 or fp32 (rows contiguous, any row stride that is a
     multiple of 8): the normed, rotated K and the V of token t go to position token_pos[t] of sequence
     token_seq[t] (negative: padding), its q to q_out [T, n_q_heads, 128] bf16."""
-    import torch
-    n = qkv.shape[0]
-    _need(qkv.dim() == 2 and qkv.stride(1) == 1 and
-          qkv.shape[1] >= (n_q_heads + 2 * cache.n_kv_heads) * 128, "qkv must be rows of (hq + 2 hkv) * 128 elements")
-    _need(qkv.dtype is torch.bfloat16 or qkv.dtype is torch.float32, "qkv must be bfloat16 or float32")
-    _need(_is(token_seq, torch.int32, (n,)) and _is(token_pos, torch.int32, (n,)), "token_seq, token_pos: int32 [tokens]")
-    _need(q_out is None or _is(q_out, torch.bfloat16, (n, n_q_heads, 128)), "q_out must be bfloat16 [tokens, hq, 128]")
-    for g in (q_norm, k_norm):
-        _need(g is None or _is(g, torch.bfloat16, (128,)), "gains must be bfloat16 [128]")
-    for t in (qkv, token_seq, token_pos, q_out, q_norm, k_norm):
-        _need(t is None or t.device == cache.device, "every tensor must be on the cache's device")
-    _check(lib().quail_cache_append(
-        ctypes.byref(cache.desc), _ptr(qkv), DTYPE_F32 if qkv.dtype is torch.float32 else DTYPE_BF16,
-        qkv.stride(0) if n > 1 else max(qkv.stride(0), qkv.shape[1]), n, n_q_heads, _ptr(token_seq), _ptr(token_pos),
-        _ptr(q_norm), _ptr(k_norm), rms_eps, rope_theta, _ptr(q_out), _stream(stream)))
+    n, width = qkv.shape
+    ld = qkv.stride(0) if n > 1 else width
+    dtype = qkv.dtype
+    if (qkv.stride(1) != 1 or width < (n_q_heads + 2 * cache.n_kv_heads) * 128 or qkv.get_device() != cache.index or
+            (dtype is not _torch.bfloat16 and dtype is not _torch.float32)):
+        raise QuailError(-1, "qkv must be bfloat16 or float32 rows of (hq + 2 hkv) * 128 elements on the cache's device")
+    bf16, i32 = _torch.bfloat16, _torch.int32
+    status = lib().quail_cache_append(
+        cache.ref, qkv.data_ptr(), DTYPE_BF16 if dtype is bf16 else DTYPE_F32, ld, n, n_q_heads,
+        _at(cache, token_seq, i32, n, "token_seq"), _at(cache, token_pos, i32, n, "token_pos"),
+        None if q_norm is None else _at(cache, q_norm, bf16, 128, "q_norm"),
+        None if k_norm is None else _at(cache, k_norm, bf16, 128, "k_norm"), rms_eps, rope_theta,
+        None if q_out is None else _at(cache, q_out, bf16, n * n_q_heads * 128, "q_out"), _cache_stream(cache, stream))
+    if status:
+        _check(status)
 
 
 def cache_read(cache: KVCache, token_seq, token_pos, k_out, v_out, stream=None) -> None:
     """k_out, v_out [T, H_kv, 128] bf16 (either may be None): the cached rows of (token_seq[t], token_pos[t])."""
-    import torch
     n = token_seq.shape[0]
-    _need(_is(token_seq, torch.int32, (n,)) and _is(token_pos, torch.int32, (n,)), "token_seq, token_pos: int32 [tokens]")
-    for t in (k_out, v_out):
-        _need(t is None or _is(t, torch.bfloat16, (n, cache.n_kv_heads, 128)),
-              "outputs must be bfloat16 [tokens, kv heads, 128]")
-    for t in (token_seq, token_pos, k_out, v_out):
-        _need(t is None or t.device == cache.device, "every tensor must be on the cache's device")
-    _check(lib().quail_cache_read(ctypes.byref(cache.desc), _ptr(token_seq), _ptr(token_pos), n, _ptr(k_out),
-                                  _ptr(v_out), _stream(stream)))
+    bf16, i32, size = _torch.bfloat16, _torch.int32, n * cache.n_kv_heads * 128
+    status = lib().quail_cache_read(
+        cache.ref, _at(cache, token_seq, i32, n, "token_seq"), _at(cache, token_pos, i32, n, "token_pos"), n,
+        None if k_out is None else _at(cache, k_out, bf16, size, "k_out"),
+        None if v_out is None else _at(cache, v_out, bf16, size, "v_out"), _cache_stream(cache, stream))
+    if status:
+        _check(status)
 
 
 def workspace_size_attention(cache: KVCache, n_q_heads: int, total_q: int, max_q_len: int, max_seq_len: int,
                              prefix_len: int = 0) -> int:
-    n = lib().quail_workspace_size_attention(ctypes.byref(cache.desc), int(n_q_heads), int(total_q), int(max_q_len),
+    n = lib().quail_workspace_size_attention(cache.ref, int(n_q_heads), int(total_q), int(max_q_len),
                                              int(max_seq_len), int(prefix_len))
     if n == 0:
         _check(-1)
@@ -643,21 +655,19 @@ def attention_shared(cache: KVCache, q, q_offsets, seq_len, max_q_len: int, max_
                      workspace, lse=None, causal: bool = True, scale: float | None = None, stream=None) -> None:
     """q, out [total_q, hq, 128] bf16; q_offsets int32 [num_seqs + 1] or None (one query per sequence);
     seq_len int32 [num_seqs], the shared keys included; prefix_pages int32 [prefix_len / 16] or None;
-    lse fp32 [total_q, hq] or None."""
-    import torch
-    n, hq, B = q.shape[0], q.shape[1], cache.num_seqs
-    _need(_is(q, torch.bfloat16, (n, hq, 128)) and _is(out, torch.bfloat16, (n, hq, 128)),
-          "q and out must be contiguous bfloat16 [total_q, hq, 128]")
-    _need(q_offsets is None or _is(q_offsets, torch.int32, (B + 1,)), "q_offsets must be int32 [num_seqs + 1]")
-    _need(_is(seq_len, torch.int32, (B,)), "seq_len must be int32 [num_seqs]")
-    _need(prefix_pages is None or (prefix_pages.dim() == 1 and _is(prefix_pages, torch.int32)),
-          "prefix_pages must be int32 [prefix_len / 16]")
-    _need(lse is None or _is(lse, torch.float32, (n, hq)), "lse must be float32 [total_q, hq]")
-    _need(workspace.is_contiguous(), "workspace must be contiguous")
-    for t in (q, out, q_offsets, seq_len, prefix_pages, lse, workspace):
-        _need(t is None or t.device == cache.device, "every tensor must be on the cache's device")
-    _check(lib().quail_attention_shared(
-        ctypes.byref(cache.desc), _ptr(prefix_pages), 0 if prefix_pages is None else prefix_pages.shape[0] * 16,
-        _ptr(seq_len), int(max_seq_len), _ptr(q), _ptr(q_offsets), n, int(max_q_len), hq, 1 if causal else 0,
-        0.0 if scale is None else float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(out), _ptr(lse), _stream(stream)))
+    lse fp32 [total_q, hq] or None; workspace uint8, workspace_size_attention bytes."""
+    n, hq, d = q.shape
+    if d != 128:
+        raise QuailError(-1, "q must be [total_q, hq, 128]")
+    B, bf16, i32 = cache.num_seqs, _torch.bfloat16, _torch.int32
+    pages = 0 if prefix_pages is None else prefix_pages.numel()
+    size = workspace.numel()
+    status = lib().quail_attention_shared(
+        cache.ref, _at(cache, prefix_pages, i32, pages, "prefix_pages") if pages else None, pages * 16,
+        _at(cache, seq_len, i32, B, "seq_len"), max_seq_len, _at(cache, q, bf16, n * hq * 128, "q"),
+        None if q_offsets is None else _at(cache, q_offsets, i32, B + 1, "q_offsets"), n, max_q_len, hq,
+        1 if causal else 0, 0.0 if scale is None else scale, _at(cache, workspace, _torch.uint8, size, "workspace"), size,
+        _at(cache, out, bf16, n * hq * 128, "out"), None if lse is None else _at(cache, lse, _torch.float32, n * hq, "lse"),
+        _cache_stream(cache, stream))
+    if status:
+        _check(status)

@@ -43,7 +43,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2][2], pv_done[2], q_full, drain;  // p_full: tile, half of the block's keys
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -208,8 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t][0], 128);
-      mbar_init(&bars->p_full[t][1], 128);
+      mbar_init(&bars->p_full[t], 128);
       mbar_init(&bars->pv_done[t], 1);
     }
     mbar_init(&bars->q_full, 256);
@@ -304,19 +303,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&bars->s_full[t]);
       };
-      // the first half of the keys as soon as its weights are there, under the
-      // exponentials of the second
       auto issue_pv = [&](int t, int j) {
         const uint32_t v = dv_lo + (((2 * j + 1) % kStages * kStage) >> 4);
+        if (!wait_bar(&bars->p_full[t], static_cast<uint32_t>(j & 1), abort_flag, limit_clk)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait_bar(&bars->p_full[t][half], static_cast<uint32_t>(j & 1), abort_flag, limit_clk)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys = one page per instruction
-            umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
-                    (j > 0 || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 8; ++kk)  // 16 keys = one page per instruction
+          umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
+                  (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&bars->pv_done[t]);
         return true;
       };
@@ -485,10 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
           if (c == 1) weights(1);
           tmem_st_32cols_nowait(lane_addr + t * 128 + c * 32, w);
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          tc_fence_before();
-          mbar_arrive(&bars->p_full[t][c]);
         }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
       }
