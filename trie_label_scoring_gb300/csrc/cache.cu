@@ -118,15 +118,18 @@ __device__ __forceinline__ int page_of(const CacheView& c, int seq, int pos, int
 // Block = TOK tokens: thread i first computes angle i % 64 of token i / 64 and
 // looks up its page while the first rows are on their way, then 32 row groups
 // of eight lanes walk the tokens' hq + 2 hkv heads, each one row ahead with its
-// loads. (One angle per thread and block: with the angles of a position
-// computed by every group, the kernel was bound by its instructions.)
+// loads. The gains go into the token's rotation once,
+//   y_j = r (x_j A_j + x_j+64 B_j),  y_j+64 = r (x_j+64 C_j + x_j D_j),  r = 1 / rms,
+//   A = g_j cos, B = -g_j+64 sin, C = g_j+64 cos, D = g_j sin,
+// so a row costs four products a pair and one by r: with angles and gains
+// applied row by row the kernel was bound by its instructions, not by memory.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendGroups = kAppendThreads / kRowLanes;
 
 template <typename T, int TOK>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs a, RopeTable rt) {
-  __shared__ __align__(16) float s_cos[TOK][64], s_sin[TOK][64];
-  __shared__ int s_page[TOK], s_slot[TOK];  // page -1: nothing of the token is written
+  __shared__ __align__(16) float s_turn[TOK][2][4][64];  // queries, keys; A, B, C, D
+  __shared__ int s_page[TOK], s_slot[TOK];               // page -1: nothing of the token is written
   grid_dependency_wait();
   grid_launch_dependents();
   const int t0 = blockIdx.x * TOK;
@@ -146,17 +149,15 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
     }
     float c = 1.f, sn = 0.f;
     if (a.theta > 0.f) rope_cs(pos, rt.w[j], c, sn);
-    s_cos[i][j] = c;
-    s_sin[i][j] = sn;
-  }
-  uint4 gain[2][2];  // of queries, keys
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bf16* g = i == 0 ? a.gq : a.gk;
-    gain[i][0] = gain[i][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (g != nullptr) {
-      gain[i][0] = *reinterpret_cast<const uint4*>(g + 8 * l);
-      gain[i][1] = *reinterpret_cast<const uint4*>(g + 64 + 8 * l);
+    for (int k = 0; k < 2; ++k) {
+      const bf16* g = k == 0 ? a.gq : a.gk;
+      const float g1 = g != nullptr ? __bfloat162float(g[j]) : 1.f;
+      const float g2 = g != nullptr ? __bfloat162float(g[j + 64]) : 1.f;
+      s_turn[i][k][0][j] = g1 * c;
+      s_turn[i][k][1][j] = -g2 * sn;
+      s_turn[i][k][2][j] = g2 * c;
+      s_turn[i][k][3][j] = g1 * sn;
     }
   }
   __syncthreads();
@@ -175,31 +176,34 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
     if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, l);
     const int page = in ? s_page[ct] : -1;
     const bool live = page >= 0;
-    const bool is_q = ch < a.hq, is_k = !is_q && ch < a.hq + a.c.hkv, is_v = !is_q && !is_k;
+    const bool is_q = ch < a.hq, is_k = !is_q && ch < a.hq + a.c.hkv;
+    const bool norm = is_q ? a.gq != nullptr : is_k && a.gk != nullptr;
+    const bool turn = (is_q || is_k) && (norm || a.theta > 0.f);
     float2 x[8];
     raw.pairs(x);
-    if (__any_sync(0xffffffffu, live && !is_v)) {
-      const bool norm = is_q ? a.gq != nullptr : a.gk != nullptr;
+    if (__any_sync(0xffffffffu, live && turn)) {
       float2 ss = mul2(x[0], x[0]);
 #pragma unroll
       for (int i = 1; i < 8; ++i) ss = fma2(x[i], x[i], ss);
       const float f = row_sum(ss.x + ss.y);
-      if (norm && !is_v) {
-        const float rs = rsqrtf(f * (1.f / 128.f) + a.eps);
-        const float2 r2 = make_float2(rs, rs);
-        const uint4 g0 = is_q ? gain[0][0] : gain[1][0], g1 = is_q ? gain[0][1] : gain[1][1];
-        const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      if (turn) {
+        const float4* tab = reinterpret_cast<const float4*>(&s_turn[ct][is_q ? 0 : 1][0][8 * l]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = mul2(mul2(x[i], r2), unpack_bf16(gw[i]));
-      }
-      if (a.theta > 0.f && !is_v) {
-        const float2* c2 = reinterpret_cast<const float2*>(&s_cos[ct][8 * l]);
-        const float2* s2 = reinterpret_cast<const float2*>(&s_sin[ct][8 * l]);
+        for (int i = 0; i < 2; ++i) {
+          const float4 A = tab[i], B = tab[16 + i], C = tab[32 + i], D = tab[48 + i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x1 = x[i], x2 = x[i + 4], c = c2[i], sn = s2[i];
-          x[i] = fma2(x1, c, mul2(make_float2(-x2.x, -x2.y), sn));
-          x[i + 4] = fma2(x2, c, mul2(x1, sn));
+          for (int k = 0; k < 2; ++k) {
+            const float2 x1 = x[2 * i + k], x2 = x[2 * i + k + 4];
+            x[2 * i + k] = fma2(x1, k ? make_float2(A.z, A.w) : make_float2(A.x, A.y),
+                                mul2(x2, k ? make_float2(B.z, B.w) : make_float2(B.x, B.y)));
+            x[2 * i + k + 4] = fma2(x2, k ? make_float2(C.z, C.w) : make_float2(C.x, C.y),
+                                    mul2(x1, k ? make_float2(D.z, D.w) : make_float2(D.x, D.y)));
+          }
+        }
+        if (norm) {
+          const float rs = rsqrtf(f * (1.f / 128.f) + a.eps);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(rs, rs));
         }
       }
     }
@@ -236,7 +240,13 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t two, float scale) {
   return pack_bf16(f.x * scale, f.y * scale);
 }
 
-// Elements 16 l .. 16 l + 15 of a row: sixteen codes w times sc.
+// A lane's sixteen codes of a row (elements 8 l .. and 64 + 8 l ..), and the same
+// times sc as bf16: every store of the eight lanes is a whole 128-byte line.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p, int l) {
+  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p + 8 * l));
+  const uint2 b = __ldcs(reinterpret_cast<const uint2*>(p + 64 + 8 * l));
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
 __device__ __forceinline__ void store_codes_bf16(bf16* out, int l, const uint4& w, float sc) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
   uint32_t o[8];
@@ -245,8 +255,8 @@ __device__ __forceinline__ void store_codes_bf16(bf16* out, int l, const uint4& 
     o[2 * i] = codes_to_bf16x2(in[i], sc);
     o[2 * i + 1] = codes_to_bf16x2(in[i] >> 16, sc);
   }
-  *reinterpret_cast<uint4*>(out + 16 * l) = make_uint4(o[0], o[1], o[2], o[3]);
-  *reinterpret_cast<uint4*>(out + 16 * l + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+  __stcs(reinterpret_cast<uint4*>(out + 8 * l), make_uint4(o[0], o[1], o[2], o[3]));
+  __stcs(reinterpret_cast<uint4*>(out + 64 + 8 * l), make_uint4(o[4], o[5], o[6], o[7]));
 }
 
 // Block = a few consecutive tokens: their pages are looked up once, then every
@@ -260,7 +270,7 @@ inline __host__ __device__ int read_tokens(int hkv) {  // tokens of a block: abo
 }
 
 template <bool CODES>
-__global__ void __launch_bounds__(kReadThreads)
+__global__ void __launch_bounds__(kReadThreads, 5)
     cache_read_kernel(CacheView c, const int* seq, const int* pos, int num_tokens, bf16* k_out, bf16* v_out) {
   __shared__ long long first_row[kReadTokens];  // row of the token's slot for head 0; -1: nothing to read
   grid_dependency_wait();
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(kReadThreads)
       out[k] += (static_cast<size_t>(t0 + t) * c.hkv + h) * 128;
       const size_t at = static_cast<size_t>(first_row[t]) + static_cast<size_t>(h) * kPage;
       if constexpr (CODES) {
-        x[k][0] = ldg_stream(static_cast<const uint8_t*>(is_k ? c.k : c.v) + at * 128 + 16 * l);
+        x[k][0] = load_codes(static_cast<const uint8_t*>(is_k ? c.k : c.v) + at * 128, l);
         sc[k] = __uint_as_float(static_cast<uint32_t>((is_k ? c.k_scale : c.v_scale)[at]) << 23);
       } else {
         const bf16* in = static_cast<const bf16*>(is_k ? c.k : c.v) + at * 128;
@@ -309,8 +319,8 @@ __global__ void __launch_bounds__(kReadThreads)
       if constexpr (CODES) {
         store_codes_bf16(out[k], l, x[k][0], sc[k]);
       } else {
-        *reinterpret_cast<uint4*>(out[k] + 8 * l) = x[k][0];
-        *reinterpret_cast<uint4*>(out[k] + 64 + 8 * l) = x[k][1];
+        __stcs(reinterpret_cast<uint4*>(out[k] + 8 * l), x[k][0]);
+        __stcs(reinterpret_cast<uint4*>(out[k] + 64 + 8 * l), x[k][1]);
       }
     }
   }
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_widen_kernel(SharedAttnArg
     const bool is_k = u < kPage;
     const int r = blockIdx.y * kPage + (is_k ? u : u - kPage);
     const size_t at = static_cast<size_t>(page) * rows + r;
-    const uint4 w = ldg_stream(static_cast<const uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128 + 16 * l);
+    const uint4 w = load_codes(static_cast<const uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128, l);
     const float sc = __uint_as_float(static_cast<uint32_t>((is_k ? a.c.k_scale : a.c.v_scale)[at]) << 23);
     store_codes_bf16((is_k ? a.wide_k : a.wide_v) + (static_cast<size_t>(p) * rows + r) * 128, l, w, sc);
   }
