@@ -519,6 +519,25 @@ quail_status quail_classify_trie_tree_shortlist(const quail_model_desc* model, c
                                                 float* label_logscore, float* label_prob, int32_t* label_argmax,
                                                 int32_t* group_selected, quail_stream_t stream);
 
+/* letters (sec. 3.3) over a document cache of either type, whose documents may
+ * share their first prefix_len tokens: the answer token's query attends to the
+ * document as in quail_attention_shared and to its own key and value, which stay
+ * fp32 and are not cached; the M letter rows score the result as in
+ * quail_classify_letters. The query and the document's part are bf16 here where
+ * quail_classify_letters keeps two-term splits; the cache is only read.
+ *   doc_len: device int32 [num_seqs], the tokens of each of the cache's sequences,
+ *            the shared ones included: 0 (an empty document), or prefix_len to
+ *            max_doc_len
+ * Other arguments, outputs and errors as the two calls named. */
+size_t quail_workspace_size_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,
+                                           int32_t num_letters, int32_t max_doc_len, int32_t prefix_len);
+quail_status quail_classify_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,
+                                           const int32_t* prefix_pages, int32_t prefix_len, const int32_t* doc_len,
+                                           int32_t max_doc_len, const int32_t* letter_tokens, int32_t num_letters,
+                                           int32_t root_token, void* workspace, size_t workspace_bytes,
+                                           float* letter_logprob, float* letter_prob, int32_t* letter_argmax,
+                                           quail_stream_t stream);
+
 /* ------------------------------------------------------------ cost model
  * Speed-of-light estimates of the three ways to classify and the choice
  * among them ("To Classify, Try a Trie Tree", sec. 4): for each method the

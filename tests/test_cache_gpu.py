@@ -661,3 +661,106 @@ def test_appended_cache_feeds_classification():
         r = OS.trie_tree(layer, dk, dv, t)
         C.check_scores(lsc[i].cpu().numpy(), prob[i].cpu().numpy(), int(am[i]), r["logscore"], r["prob"], r["argmax"],
                        f"doc {i}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("prefix", [0, 64])
+def test_letters_over_a_cache(kind, prefix):
+    """classify_letters_cached against the oracle on the rows that the cache holds, which it leaves as they are; over a
+    bf16 cache classify_letters gives the same."""
+    import synthetic as S
+    import trie_label_scoring_gb300 as Q
+    from oracle import scoring as OS
+    from tests import gpu_cases as C
+    sh = S.TINY
+    model, layer = C.device_model(sh), C.oracle_layer(sh)
+    letters, root = [7, 4000, 12, 900, 55, 8191, 0], 321
+    lens = [prefix + n for n in (128, 15, 16, 300, 97)]
+    N, M = len(lens), len(letters)
+    pool = Pool(kind, sh.n_kv_heads, [n + 1 for n in lens], prefix)
+    pool.fill(lens, k_scale=0.02, v_scale=0.02)
+    if kind == "e4m3":  # codes of unit size times 2^-6 or so: rows like the bf16 ones
+        pool.ks.copy_((pool.ks.int() - 6).to(torch.uint8))
+        pool.vs.copy_((pool.vs.int() - 6).to(torch.uint8))
+    keep = (pool.k.clone(), pool.v.clone())
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(Q.workspace_size_letters_cached(model, pool.cache, M, max(lens), prefix), dtype=torch.uint8,
+                     device="cuda")
+    lp, pr = torch.empty((N, M), device="cuda"), torch.empty((N, M), device="cuda")
+    am = torch.empty((N,), dtype=torch.int32, device="cuda")
+    Q.classify_letters_cached(model, pool.cache, pool.prefix_pages, L, max(lens), letters, root, ws, lp, pr, am)
+    status()
+    for i, n in enumerate(lens):
+        at = torch.arange(n, device="cuda", dtype=torch.int32)
+        which = torch.full_like(at, i)
+        dk, dv = (pool.rows(which, at, x).cpu().numpy() for x in ("k", "v"))
+        r = OS.letters(layer, dk, dv, letters, root)
+        C.check_scores(lp[i].cpu().numpy(), pr[i].cpu().numpy(), int(am[i]), r["logprob"], r["prob"], r["argmax"], f"doc {i}")
+    assert torch.equal(keep[0].view(torch.uint8), pool.k.view(torch.uint8))
+    assert torch.equal(keep[1].view(torch.uint8), pool.v.view(torch.uint8))
+    if kind == "bf16":
+        kv = Q.KV(pool.k, pool.v, pool.table, L, max(lens))
+        ws2 = torch.empty(Q.workspace_size(model, None, M, N, max(lens), Q.MODE_LETTERS), dtype=torch.uint8, device="cuda")
+        lp2, pr2, am2 = torch.empty_like(lp), torch.empty_like(pr), torch.empty_like(am)
+        Q.classify_letters(model, kv, letters, root, N, ws2, lp2, pr2, am2)
+        status()
+        assert float((lp - lp2).abs().max()) <= C.TOL_LOGSCORE
+
+
+def test_letters_over_a_cache_refusals():
+    import synthetic as S
+    import trie_label_scoring_gb300 as Q
+    from tests import gpu_cases as C
+    sh = S.TINY
+    model = C.device_model(sh)
+    pool = Pool("bf16", sh.n_kv_heads, [32, 20])
+    pool.fill([31, 19])
+    L = torch.tensor([31, 19], dtype=torch.int32, device="cuda")
+    ws = torch.empty(Q.workspace_size_letters_cached(model, pool.cache, 2, 31), dtype=torch.uint8, device="cuda")
+    lp, pr = torch.empty((2, 2), device="cuda"), torch.empty((2, 2), device="cuda")
+    am = torch.empty((2,), dtype=torch.int32, device="cuda")
+
+    def call(cache=pool.cache, lens=L, max_len=31, letters=(1, 2), root=3, w=ws):
+        Q.classify_letters_cached(model, cache, None, lens, max_len, letters, root, w, lp, pr, am)
+
+    call()
+    status()
+    for kw, name in ((dict(letters=(1, 1)), "QUAIL_ERR_DUPLICATE_LABEL"), (dict(letters=(1, 9000)), "QUAIL_ERR_TOKEN_RANGE"),
+                     (dict(root=-1), "QUAIL_ERR_TOKEN_RANGE"), (dict(w=ws[:256]), "QUAIL_ERR_WORKSPACE"),
+                     (dict(max_len=33), "QUAIL_ERR_INVALID_ARG")):  # no page for position 32
+        with pytest.raises(Q.QuailError) as e:
+            call(**kw)
+        assert e.value.name == name, (kw, e.value)
+    other = Pool("bf16", 3, [32, 20])
+    with pytest.raises(Q.QuailError):
+        call(cache=other.cache)
+    call(lens=torch.tensor([31, 32], dtype=torch.int32, device="cuda"))  # past max_doc_len
+    with pytest.raises(Q.QuailError) as e:
+        status()
+    assert e.value.name == "QUAIL_ERR_DEVICE_BOUNDS"
+    call()
+    status()
+
+
+def test_letters_over_a_cache_of_empty_documents():
+    """No document token at all: the answer token attends to itself alone, o = v."""
+    import synthetic as S
+    import trie_label_scoring_gb300 as Q
+    from oracle import scoring as OS
+    from tests import gpu_cases as C
+    sh = S.TINY
+    model, layer = C.device_model(sh), C.oracle_layer(sh)
+    pool = Pool("bf16", sh.n_kv_heads, [16, 16, 16])
+    pool.fill([16, 16, 16])
+    lens = [0, 5, 0]
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(Q.workspace_size_letters_cached(model, pool.cache, 3, 16), dtype=torch.uint8, device="cuda")
+    lp, pr = torch.empty((3, 3), device="cuda"), torch.empty((3, 3), device="cuda")
+    am = torch.empty((3,), dtype=torch.int32, device="cuda")
+    Q.classify_letters_cached(model, pool.cache, None, L, 16, [3, 5, 8000], 9, ws, lp, pr, am)
+    status()
+    for i, n in enumerate(lens):
+        at = torch.arange(n, device="cuda", dtype=torch.int32)
+        dk, dv = (pool.rows(torch.full_like(at, i), at, x).cpu().numpy().reshape(n, sh.n_kv_heads, 128) for x in ("k", "v"))
+        r = OS.letters(layer, dk, dv, [3, 5, 8000], 9)
+        C.check_scores(lp[i].cpu().numpy(), pr[i].cpu().numpy(), int(am[i]), r["logprob"], r["prob"], r["argmax"], f"doc {i}")

@@ -28,6 +28,8 @@ Entry points (same names as the C ABI, without the quail_ prefix):
                                  -> quail_cache_append / quail_cache_read
   workspace_size_attention(...), attention_shared(...)
                                  -> quail_workspace_size_attention / quail_attention_shared
+  workspace_size_letters_cached(...), classify_letters_cached(...)
+                                 -> quail_workspace_size_letters_cached / quail_classify_letters_cached
 """
 from __future__ import annotations
 
@@ -196,6 +198,13 @@ _SIGNATURES = {
                                               ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                               ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                               ctypes.c_void_p, ctypes.c_void_p]),
+    "quail_workspace_size_letters_cached": (ctypes.c_size_t, [ctypes.POINTER(ModelDesc), ctypes.POINTER(CacheDesc),
+                                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "quail_classify_letters_cached": (ctypes.c_int, [ctypes.POINTER(ModelDesc), ctypes.POINTER(CacheDesc),
+                                                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                                     ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p,
+                                                     ctypes.c_void_p, ctypes.c_void_p]),
     "quail_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "quail_set_stage_events": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
     "quail_launch_count": (ctypes.c_int32, []),
@@ -671,3 +680,27 @@ def attention_shared(cache: KVCache, q, q_offsets, seq_len, max_q_len: int, max_
         _cache_stream(cache, stream))
     if status:
         _check(status)
+
+
+def workspace_size_letters_cached(model: Model, cache: KVCache, num_letters: int, max_doc_len: int,
+                                  prefix_len: int = 0) -> int:
+    n = lib().quail_workspace_size_letters_cached(ctypes.byref(model.desc), cache.ref, int(num_letters),
+                                                  int(max_doc_len), int(prefix_len))
+    if n == 0:
+        raise QuailError(-1, "workspace_size_letters_cached: invalid arguments")
+    return int(n)
+
+
+def classify_letters_cached(model: Model, cache: KVCache, prefix_pages, doc_len, max_doc_len: int, letter_tokens,
+                            root_token: int, workspace, letter_logprob, letter_prob, letter_argmax, stream=None) -> None:
+    """letters over a document cache (bf16 or e4m3), which is only read; prefix_pages int32
+    [prefix_len / 16]: first pages that all documents share, or None."""
+    lt = np.ascontiguousarray(np.asarray(letter_tokens, dtype=np.int32))
+    N, M, f32, i32 = cache.num_seqs, len(lt), _torch.float32, _torch.int32
+    pages = 0 if prefix_pages is None else prefix_pages.numel()
+    _check(lib().quail_classify_letters_cached(
+        ctypes.byref(model.desc), cache.ref, _at(cache, prefix_pages, i32, pages, "prefix_pages") if pages else None,
+        pages * 16, _at(cache, doc_len, i32, N, "doc_len"), int(max_doc_len), lt.ctypes.data, M, int(root_token),
+        _at(cache, workspace, _torch.uint8, workspace.numel(), "workspace"), workspace.numel(),
+        _at(cache, letter_logprob, f32, N * M, "letter_logprob"), _at(cache, letter_prob, f32, N * M, "letter_prob"),
+        _at(cache, letter_argmax, i32, N, "letter_argmax"), _cache_stream(cache, stream)))

@@ -929,6 +929,40 @@ void choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
   }
 }
 
+// The letter list of a letters call.
+quail_status check_letters(const quail_model_desc* model, const int32_t* letter_tokens, int num_letters,
+                           int root_token) {
+  if (letter_tokens == nullptr || num_letters < 2) return fail(QUAIL_ERR_INVALID_ARG, "need at least 2 letters");
+  if (num_letters > 8192) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most 8192 letters");
+  if (root_token < 0 || root_token >= model->vocab) return fail(QUAIL_ERR_TOKEN_RANGE, "root token out of range");
+  for (int i = 0; i < num_letters; ++i) {
+    if (letter_tokens[i] < 0 || letter_tokens[i] >= model->vocab)
+      return fail(QUAIL_ERR_TOKEN_RANGE, "letter %d has token %d outside [0, vocab)", i, letter_tokens[i]);
+  }
+  {
+    std::vector<int32_t> sorted(letter_tokens, letter_tokens + num_letters);
+    std::sort(sorted.begin(), sorted.end());
+    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
+      return fail(QUAIL_ERR_DUPLICATE_LABEL, "letter tokens must be distinct");
+  }
+  return QUAIL_OK;
+}
+
+// The node table of the answer position and the letters, into b.small.
+quail_status copy_letters(const Buffers& b, const int32_t* letter_tokens, int num_letters, int root_token,
+                          cudaStream_t st, NodeTables* nt) {
+  // small ints: [0] root token, [1] depth 0, [2] parent -1, [4..] letters
+  std::vector<int32_t> host(num_letters + 4);
+  host[0] = root_token;
+  host[1] = 0;
+  host[2] = -1;
+  host[3] = 0;
+  std::memcpy(host.data() + 4, letter_tokens, num_letters * sizeof(int32_t));
+  CUDA_TRY(cudaMemcpyAsync(b.small, host.data(), host.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
+  *nt = NodeTables{b.small, b.small + 1, b.small + 2, 1};
+  return QUAIL_OK;
+}
+
 // How one attention call is carried out, and its workspace.
 //   up to 32 query rows per sequence and KV head: streamed (memory bound); the
 //       prefix too while the whole batch has no more rows than that, else on tiles
@@ -992,6 +1026,64 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   }
   if (a != nullptr) *a = t;
   return k.off + 256;
+}
+
+// The launches of one attention call: a filled in, its plan included.
+quail_status run_attention_shared(const quail_cache_desc* cache, const SharedAttnArgs& a, DeviceState* ds,
+                                  cudaStream_t st) {
+  quail_status s = QUAIL_OK;
+  const bool streamed = a.streamed;
+  if (a.wide_pages) CUDA_TRY(launch_cache_widen(a, st));
+  if (streamed) {
+    // before the tiles: these start on the SMs that it leaves first, and their
+    // parts, the larger ones, are still in L2 when the join reads them
+    CUtensorMap tK, tV;
+    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+    for (int i = 0; i < 2; ++i) {
+      const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
+      CUtensorMap* m = i == 0 ? &tK : &tV;
+      s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
+      if (s != QUAIL_OK) return s;
+    }
+    CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
+  }
+  if (a.prefix_splits > 0 || !streamed) {
+    CUtensorMap tK, tV;
+    const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * cache->n_kv_heads * 16;
+    s = encode_2d_bf16(&tK, a.wide_pages ? a.wide_k : cache->k_pool, rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+    s = encode_2d_bf16(&tV, a.wide_pages ? a.wide_v : cache->v_pool, rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
+    if (!streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
+  }
+  if (streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
+  return QUAIL_OK;
+}
+
+// Workspace of quail_classify_letters_cached: that of letters with one document's
+// attention (not used), the documents' q, o and lse, the cache attention's.
+struct LettersCachedBuffers {
+  Buffers b;
+  bf16 *q, *o;
+  float* lse;
+  SharedAttnArgs attn;
+};
+
+size_t plan_letters_cached(uint8_t* base, const quail_model_desc* m, const quail_cache_desc* c, int num_letters,
+                           int max_doc_len, int prefix_len, LettersCachedBuffers* out) {
+  const int N = c->num_seqs, hq = m->n_q_heads;
+  LettersCachedBuffers x{};
+  size_t off = round_up(plan(base, m, 1, N, 1, 16, false, 0, true, num_letters + 4, base ? &x.b : nullptr), 256);
+  Carver k{base ? base + off : nullptr};
+  x.q = k.take<bf16>(static_cast<size_t>(N) * hq * 128);
+  x.o = k.take<bf16>(static_cast<size_t>(N) * hq * 128);
+  x.lse = k.take<float>(static_cast<size_t>(N) * hq);
+  off += round_up(k.off, 256);
+  const size_t attn = plan_attention(base ? base + off : nullptr, c, hq, N, 1, max_doc_len, prefix_len, &x.attn);
+  if (attn == 0) return 0;
+  if (out) *out = x;
+  return off + attn;
 }
 
 }  // namespace
@@ -1172,19 +1264,8 @@ quail_status quail_classify_letters(const quail_model_desc* model, const quail_p
   if (s != QUAIL_OK) return s;
   s = check_kv(kv, model);
   if (s != QUAIL_OK) return s;
-  if (letter_tokens == nullptr || num_letters < 2) return fail(QUAIL_ERR_INVALID_ARG, "need at least 2 letters");
-  if (num_letters > 8192) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most 8192 letters");
-  if (root_token < 0 || root_token >= model->vocab) return fail(QUAIL_ERR_TOKEN_RANGE, "root token out of range");
-  for (int i = 0; i < num_letters; ++i) {
-    if (letter_tokens[i] < 0 || letter_tokens[i] >= model->vocab)
-      return fail(QUAIL_ERR_TOKEN_RANGE, "letter %d has token %d outside [0, vocab)", i, letter_tokens[i]);
-  }
-  {
-    std::vector<int32_t> sorted(letter_tokens, letter_tokens + num_letters);
-    std::sort(sorted.begin(), sorted.end());
-    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
-      return fail(QUAIL_ERR_DUPLICATE_LABEL, "letter tokens must be distinct");
-  }
+  s = check_letters(model, letter_tokens, num_letters, root_token);
+  if (s != QUAIL_OK) return s;
   if (num_docs < 0) return fail(QUAIL_ERR_INVALID_ARG, "num_docs < 0");
   if (num_docs == 0) return QUAIL_OK;
   if (num_docs > 65535) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most 65535 documents per call");
@@ -1199,15 +1280,9 @@ quail_status quail_classify_letters(const quail_model_desc* model, const quail_p
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Buffers b;
   plan(static_cast<uint8_t*>(workspace), model, 1, num_docs, 1, kv->max_doc_len, false, 0, true, num_letters + 4, &b);
-  // small ints: [0] root token, [1] depth 0, [2] parent -1, [4..] letters
-  std::vector<int32_t> host(num_letters + 4);
-  host[0] = root_token;
-  host[1] = 0;
-  host[2] = -1;
-  host[3] = 0;
-  std::memcpy(host.data() + 4, letter_tokens, num_letters * sizeof(int32_t));
-  CUDA_TRY(cudaMemcpyAsync(b.small, host.data(), host.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
-  const NodeTables nt{b.small, b.small + 1, b.small + 2, 1};
+  NodeTables nt;
+  s = copy_letters(b, letter_tokens, num_letters, root_token, st, &nt);
+  if (s != QUAIL_OK) return s;
   const RowMap map{1, nullptr, nullptr, nullptr};
 
   stage_mark(QUAIL_STAGE_PROLOGUE, false, st);
@@ -1979,32 +2054,92 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
   a.out = static_cast<bf16*>(out);
   a.lse = lse;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool streamed = a.streamed;
-  if (a.wide_pages) CUDA_TRY(launch_cache_widen(a, st));
-  if (streamed) {
-    // before the tiles: these start on the SMs that it leaves first, and their
-    // parts, the larger ones, are still in L2 when the join reads them
-    CUtensorMap tK, tV;
-    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
-    for (int i = 0; i < 2; ++i) {
-      const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
-      CUtensorMap* m = i == 0 ? &tK : &tV;
-      s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
-      if (s != QUAIL_OK) return s;
-    }
-    CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
-  }
-  if (a.prefix_splits > 0 || !streamed) {
-    CUtensorMap tK, tV;
-    const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * cache->n_kv_heads * 16;
-    s = encode_2d_bf16(&tK, a.wide_pages ? a.wide_k : cache->k_pool, rows, 128, 128, 64, 16);
-    if (s != QUAIL_OK) return s;
-    s = encode_2d_bf16(&tV, a.wide_pages ? a.wide_v : cache->v_pool, rows, 128, 128, 64, 16);
-    if (s != QUAIL_OK) return s;
-    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
-    if (!streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
-  }
-  if (streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
+  return run_attention_shared(cache, a, ds, st);
+}
+
+size_t quail_workspace_size_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,
+                                           int32_t num_letters, int32_t max_doc_len, int32_t prefix_len) {
+  if (model == nullptr || num_letters < 2 || max_doc_len <= 0 || model->hidden <= 0 ||
+      model->n_q_heads <= 0 || model->n_kv_heads <= 0 || model->vocab <= 0)
+    return 0;
+  if (cache == nullptr || cache->num_seqs <= 0 ||
+      check_attention_shape(cache, model->n_q_heads, cache->num_seqs, 1, max_doc_len, prefix_len) != QUAIL_OK)
+    return 0;
+  return plan_letters_cached(nullptr, model, cache, num_letters, max_doc_len, prefix_len, nullptr);
+}
+
+quail_status quail_classify_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,
+                                           const int32_t* prefix_pages, int32_t prefix_len, const int32_t* doc_len,
+                                           int32_t max_doc_len, const int32_t* letter_tokens, int32_t num_letters,
+                                           int32_t root_token, void* workspace, size_t workspace_bytes,
+                                           float* letter_logprob, float* letter_prob, int32_t* letter_argmax,
+                                           quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_model(model);
+  if (s != QUAIL_OK) return s;
+  s = check_cache_shape(cache);
+  if (s != QUAIL_OK) return s;
+  if (cache->n_kv_heads != model->n_kv_heads)
+    return fail(QUAIL_ERR_INVALID_ARG, "cache has %d KV heads, the model %d", cache->n_kv_heads, model->n_kv_heads);
+  s = check_letters(model, letter_tokens, num_letters, root_token);
+  if (s != QUAIL_OK) return s;
+  const int N = cache->num_seqs;
+  if (max_doc_len <= 0) return fail(QUAIL_ERR_INVALID_ARG, "bad max_doc_len");
+  if (N == 0) return QUAIL_OK;
+  s = check_attention_shape(cache, model->n_q_heads, N, 1, max_doc_len, prefix_len);
+  if (s != QUAIL_OK) return s;
+  if (doc_len == nullptr || (prefix_len > 0 && prefix_pages == nullptr))
+    return fail(QUAIL_ERR_INVALID_ARG, "doc_len or prefix_pages is null");
+  if (letter_logprob == nullptr || letter_prob == nullptr || letter_argmax == nullptr)
+    return fail(QUAIL_ERR_INVALID_ARG, "an output pointer is null");
+  const size_t need = plan_letters_cached(nullptr, model, cache, num_letters, max_doc_len, prefix_len, nullptr);
+  if (need == 0) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "num_seqs x max_doc_len is too large for an e4m3 cache");
+  s = check_workspace(workspace, workspace_bytes, need);
+  if (s != QUAIL_OK) return s;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  CacheView view;
+  s = open_cache(cache, &ds, &dev, &view);
+  if (s != QUAIL_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  LettersCachedBuffers x;
+  plan_letters_cached(static_cast<uint8_t*>(workspace), model, cache, num_letters, max_doc_len, prefix_len, &x);
+  NodeTables nt;
+  s = copy_letters(x.b, letter_tokens, num_letters, root_token, st, &nt);
+  if (s != QUAIL_OK) return s;
+  const RowMap map{1, nullptr, nullptr, nullptr};
+
+  stage_mark(QUAIL_STAGE_PROLOGUE, false, st);
+  s = run_prologue(model, nt, x.b, ds, st);
+  if (s != QUAIL_OK) return s;
+  stage_mark(QUAIL_STAGE_PROLOGUE, true, st);
+  stage_mark(QUAIL_STAGE_ATTENTION, false, st);
+  CUDA_TRY(launch_answer_query(x.b.qkv, doc_len, N, model->n_q_heads, model->rope_theta, x.q, st));
+  SharedAttnArgs a = x.attn;
+  a.c = view;
+  a.hq = model->n_q_heads;
+  a.q = x.q;
+  a.total_q = N;
+  a.max_q = 1;
+  a.seq_len = doc_len;
+  a.max_seq_len = max_doc_len;
+  a.prefix_pages = prefix_pages;
+  a.prefix_len = prefix_len;
+  a.scale_log2 = 0.08838834764831845f * 1.4426950408889634f;
+  a.out = x.o;
+  a.lse = x.lse;
+  s = run_attention_shared(cache, a, ds, st);
+  if (s != QUAIL_OK) return s;
+  CUDA_TRY(launch_answer_join(x.b.qkv, x.o, x.lse, N, model->n_q_heads, model->n_kv_heads, x.b.attn_out, st));
+  stage_mark(QUAIL_STAGE_ATTENTION, true, st);
+  stage_mark(QUAIL_STAGE_WO_NORM, false, st);
+  s = run_wo_norm(model, nt, map, N, x.b, ds, st);
+  if (s != QUAIL_OK) return s;
+  stage_mark(QUAIL_STAGE_WO_NORM, true, st);
+  stage_mark(QUAIL_STAGE_HEAD, false, st);
+  CUDA_TRY(launch_letters_head(x.b.z_f32, static_cast<const bf16*>(model->lm_head), x.b.small + 4, num_letters, N,
+                               model->hidden, letter_logprob, letter_prob, letter_argmax, st));
+  stage_mark(QUAIL_STAGE_HEAD, true, st);
   return QUAIL_OK;
 }
 

@@ -359,7 +359,71 @@ __global__ void __launch_bounds__(kReadThreads) cache_widen_kernel(SharedAttnArg
   }
 }
 
+// ------------------------------------------------------------------ answer token
+// The answer token of a letters call: one normed row q | k | v for all documents.
+// answer_query_kernel turns its q by each document's length; answer_join_kernel
+// adds its own key and value to what the document gave. Score and value of the
+// own key stay fp32 and never pass through the cache: q and k are turned by the
+// same angle, so q . k is the unturned rows' product, and with the document's
+// (o, lse),  o' = (o e^lse + v e^s) / (e^lse + e^s),  s = q . k / sqrt(128).
+// A few MB at most for thousands of documents: latency is what they cost.
+__global__ void __launch_bounds__(256) answer_query_kernel(const float* qkv, const int* len, int hq, bf16* q,
+                                                           RopeTable rt) {
+  __shared__ float2 s_cs[64];
+  grid_dependency_wait();
+  if (threadIdx.x < 64) rope_cs(len[blockIdx.x], rt.w[threadIdx.x], s_cs[threadIdx.x].x, s_cs[threadIdx.x].y);
+  __syncthreads();
+  bf16* out = q + static_cast<size_t>(blockIdx.x) * hq * 128;
+  for (int i = threadIdx.x; i < hq * 32; i += 256) {  // two neighbouring pairs (j, j + 64)
+    const int h = i / 32, j = i % 32 * 2;
+    const float2 x = *reinterpret_cast<const float2*>(qkv + h * 128 + j);
+    const float2 y = *reinterpret_cast<const float2*>(qkv + h * 128 + 64 + j);
+    const float2 t0 = s_cs[j], t1 = s_cs[j + 1];
+    uint32_t* o = reinterpret_cast<uint32_t*>(out + h * 128 + j);
+    o[0] = pack_bf16(x.x * t0.x - y.x * t0.y, x.y * t1.x - y.y * t1.y);
+    o[32] = pack_bf16(y.x * t0.x + x.x * t0.y, y.y * t1.x + x.y * t1.y);
+  }
+}
+
+// A warp per (document, head); out rows are the two-term splits that W_o reads.
+__global__ void __launch_bounds__(256) answer_join_kernel(const float* qkv, const bf16* o, const float* lse, int rows,
+                                                          int hq, int group, bf16* out) {
+  grid_dependency_wait();
+  const int r = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (r >= rows) return;
+  const int doc = r / hq, h = r % hq, kv = h / group;
+  const float4 x = *reinterpret_cast<const float4*>(qkv + h * 128 + 4 * lane);
+  const float4 k = *reinterpret_cast<const float4*>(qkv + (hq + kv) * 128 + 4 * lane);
+  const float4 v = *reinterpret_cast<const float4*>(qkv + (hq + hq / group + kv) * 128 + 4 * lane);
+  float s = x.x * k.x + x.y * k.y + x.z * k.z + x.w * k.w;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  s *= 0.08838834764831845f;
+  const float le = lse[r], m = fmaxf(le, s);
+  const float wd = __expf(le - m), ws = __expf(s - m);  // an empty document: lse = -inf, weight 0
+  const float inv = 1.f / (wd + ws), a = wd * inv, b = ws * inv;
+  const uint2 od = *reinterpret_cast<const uint2*>(o + static_cast<size_t>(r) * 128 + 4 * lane);
+  const float2 d0 = unpack_bf16(od.x), d1 = unpack_bf16(od.y);
+  uint2 hi, lo;
+  split_bf16(a * d0.x + b * v.x, a * d0.y + b * v.y, hi.x, lo.x);
+  split_bf16(a * d1.x + b * v.z, a * d1.y + b * v.w, hi.y, lo.y);
+  bf16* row = out + static_cast<size_t>(doc) * 2 * hq * 128 + h * 128 + 4 * lane;
+  *reinterpret_cast<uint2*>(row) = hi;
+  *reinterpret_cast<uint2*>(row + hq * 128) = lo;
+}
+
 }  // namespace
+
+cudaError_t launch_answer_query(const float* qkv, const int* len, int n, int hq, float theta, bf16* q, cudaStream_t st) {
+  count_launch();
+  return launch_pdl(answer_query_kernel, dim3(n), dim3(256), 0, st, qkv, len, hq, q, make_rope_table(theta));
+}
+
+cudaError_t launch_answer_join(const float* qkv, const bf16* o, const float* lse, int n, int hq, int hkv, bf16* out,
+                               cudaStream_t st) {
+  count_launch();
+  return launch_pdl(answer_join_kernel, dim3((n * hq + 7) / 8), dim3(256), 0, st, qkv, o, lse, n * hq, hq, hq / hkv, out);
+}
 
 cudaError_t launch_cache_widen(const SharedAttnArgs& a, cudaStream_t st) {
   const long long pages = a.prefix_len / kPage + static_cast<long long>(a.c.num_seqs) * a.wide_own;

@@ -45,6 +45,15 @@ cudaError_t launch_cache_append(const AppendArgs& a, bool f32, int num_sms, cuda
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens,
                               __nv_bfloat16* k_out, __nv_bfloat16* v_out, cudaStream_t st);
 
+// The answer token of a letters call, its normed row q | k | v (fp32) the same for
+// all n documents: q turned by the documents' lengths (bf16 [n, hq, 128]); and
+// attention over the document (o, lse) joined with the token's own key, as rows
+// [n, 2 hq 128] of two-term splits.
+cudaError_t launch_answer_query(const float* qkv, const int* len, int n, int hq, float theta, __nv_bfloat16* q,
+                                cudaStream_t st);
+cudaError_t launch_answer_join(const float* qkv, const __nv_bfloat16* o, const float* lse, int n, int hq, int hkv,
+                               __nv_bfloat16* out, cudaStream_t st);
+
 // One softmax part of a query row: o = sum 2^(t_j - m_o) v_j and
 // l = sum 2^(s_j - m_l), with s the scores in base 2 and t = s, or s plus the
 // power of two of key j's value row where v_j are bare codes.
