@@ -346,17 +346,33 @@ def attend(pool, q, offs, lens, prefix, causal, scale=None, slack=0, max_q=None,
     return out[:T], None if ls is None else ls[:T]
 
 
+@pytest.fixture(params=[0, 1, 2, 3])
+def way(request):
+    """Every way that an attention call can be carried out."""
+    import trie_label_scoring_gb300 as Q
+    Q._test_set_attention_way(request.param)
+    yield request.param
+    Q._test_set_attention_way(-1)
+
+
 def check_attention(pool, q, offs, lens, prefix, causal, scale=None, **kw):
-    out, lse = attend(pool, q, offs, lens, prefix, causal, scale, **kw)
-    offs = list(range(len(lens) + 1)) if offs is None else offs
-    o, z, tol_o, tol_l = attention_64(pool, q, offs, lens, prefix, causal, scale or D ** -0.5)
-    err = (out.double() - o).abs()
-    assert bool((err <= tol_o).all()), f"o: off by {float((err - tol_o).max()):.3g} more than allowed"
-    if lse is not None:
-        assert torch.equal(z == float("-inf"), lse == float("-inf"))
-        live = z > float("-inf")
-        err = (lse.double() - z)[live].abs()
-        assert bool((err <= tol_l[live]).all()), f"lse: off by {float((err - tol_l[live]).max()):.3g} too much"
+    """Every way, and the one that the call takes by itself, against 64 bits."""
+    import trie_label_scoring_gb300 as Q
+    at = list(range(len(lens) + 1)) if offs is None else offs
+    o, z, tol_o, tol_l = attention_64(pool, q, at, lens, prefix, causal, scale or D ** -0.5)
+    live = z > float("-inf")
+    for way in [0, 1, 2, 3, -1] if prefix else [0, 3, -1]:
+        Q._test_set_attention_way(way)
+        try:
+            out, lse = attend(pool, q, offs, lens, prefix, causal, scale, **kw)
+        finally:
+            Q._test_set_attention_way(-1)
+        err = (out.double() - o).abs()
+        assert bool((err <= tol_o).all()), f"way {way}: o off by {float((err - tol_o).max()):.3g} more than allowed"
+        if lse is not None:
+            assert torch.equal(z == float("-inf"), lse == float("-inf")), f"way {way}"
+            err = (lse.double() - z)[live].abs()
+            assert bool((err <= tol_l[live]).all()), f"way {way}: lse off by {float((err - tol_l[live]).max()):.3g} too much"
     return out, lse
 
 
@@ -432,7 +448,7 @@ def test_attention_score_ranges(kind, nq, q_scale, scale):
 
 
 @pytest.mark.parametrize("nq", [1, 20])
-def test_attention_e4m3_value_scales_far_apart(nq):
+def test_attention_e4m3_value_scales_far_apart(nq, way):
     """V rows whose powers of two differ by 2^100: the sums keep what counts."""
     lens = [90, 333]
     pool = Pool("e4m3", 2, lens, 64)
@@ -449,7 +465,7 @@ def test_attention_e4m3_value_scales_far_apart(nq):
     assert bool(((lse.double() - z).abs() <= tol_l).all())
 
 
-def test_attention_nan_and_infinity_stay_in_their_rows():
+def test_attention_nan_and_infinity_stay_in_their_rows(way):
     """A NaN query row gives NaN in its own rows only; an infinite score takes the whole weight or gives NaN, as the formula."""
     lens = [40, 70, 33]
     pool = Pool("bf16", 2, lens, 16)
@@ -480,7 +496,7 @@ def test_attention_large_pool_offsets():
 
 @pytest.mark.parametrize("nq", [1, 20])
 @pytest.mark.parametrize("what", ["page", "prefix page", "length", "short", "offsets"])
-def test_attention_reports_bad_indices(nq, what):
+def test_attention_reports_bad_indices(nq, what, way):
     """Out-of-range ids and lengths set the error word; the other sequences' rows stay right."""
     import trie_label_scoring_gb300 as Q
     lens, prefix = [90, 64, 333], 32
@@ -517,6 +533,30 @@ def test_attention_reports_bad_indices(nq, what):
     status()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_attention_wait_timeout_is_reported(kind, way):
+    """With the limit of every pipeline wait cut to a few hundred cycles (a test hook) the waits run out before their
+    copies arrive: the kernels drain what is in flight, free their tensor memory and return, the error word says so,
+    and the next call is right."""
+    import trie_label_scoring_gb300 as Q
+    lens, prefix = [3000, 2222] * 40, 1024  # enough pages under way for some to wait in line
+    pool = Pool(kind, 8, lens, prefix)
+    pool.fill(lens)
+    q = torch.randn((80, 32, D), device="cuda").bfloat16()
+    good, _ = attend(pool, q, None, lens, prefix, True)
+    Q._test_set_pipeline_wait_limit(200)
+    try:
+        short, _ = attend(pool, q, None, lens, prefix, True)
+    except Q.QuailError as e:
+        assert e.name == "QUAIL_ERR_DEVICE_TIMEOUT"
+    else:  # streamed pages: a wait may be over within its first try, which has no limit of its own
+        assert way == 0 and torch.equal(good, short)
+    finally:
+        Q._test_set_pipeline_wait_limit(0)
+    again, _ = attend(pool, q, None, lens, prefix, True)
+    assert torch.equal(good, again)
+
+
 def test_python_checks_of_tensors():
     import trie_label_scoring_gb300 as Q
     pool = Pool("bf16", 2, [64, 64])
@@ -542,7 +582,7 @@ def test_python_checks_of_tensors():
 
 # ------------------------------------------------------------------ streams, graphs, the operators together
 @pytest.mark.parametrize("nq", [1, 24])
-def test_capture_and_replay_on_a_side_stream(nq):
+def test_capture_and_replay_on_a_side_stream(nq, way):
     """append + attention captured into two graphs with a workspace each, replayed with new inputs, against eager calls."""
     import trie_label_scoring_gb300 as Q
     lens, prefix, hq, hkv = [100, 77, 200], 48, 8, 2
@@ -594,7 +634,7 @@ def test_capture_and_replay_on_a_side_stream(nq):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-def test_prefill_then_tokens(kind):
+def test_prefill_then_tokens(kind, way):
     """The operators as a document engine uses them: the instructions written once, documents prefilled behind them in
     two chunks, then single tokens; every step's attention against 64 bits on what the cache holds."""
     import trie_label_scoring_gb300 as Q
@@ -665,7 +705,7 @@ def test_appended_cache_feeds_classification():
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("prefix", [0, 64])
-def test_letters_over_a_cache(kind, prefix):
+def test_letters_over_a_cache(kind, prefix, way):
     """classify_letters_cached against the oracle on the rows that the cache holds, which it leaves as they are; over a
     bf16 cache classify_letters gives the same."""
     import synthetic as S

@@ -216,6 +216,7 @@ _SIGNATURES = {
 # Exported for the tests only; not declared in include/quail.h.
 _TEST_SIGNATURES = {
     "quail_test_set_pipeline_wait_limit": (ctypes.c_int, [ctypes.c_longlong]),
+    "quail_test_set_attention_way": (ctypes.c_int, [ctypes.c_int]),
 }
 
 _lib = None
@@ -492,6 +493,12 @@ def _test_set_pipeline_wait_limit(cycles: int) -> None:
     """Test hook (not in the public header): every pipeline wait gives up
     after `cycles` cycles; cycles <= 0 restores the default limit."""
     _check(lib().quail_test_set_pipeline_wait_limit(int(cycles)))
+
+
+def _test_set_attention_way(way: int) -> None:
+    """Test hook (not in the public header): attention over the cache goes way 0 (streamed), 1 (streamed behind
+    a prefix on tiles), 2 (prefix and sequences on tiles apart) or 3 (tiles in one pass) where it can; -1: the cheapest."""
+    _check(lib().quail_test_set_attention_way(int(way)))
 
 
 def set_stage_events(events) -> None:

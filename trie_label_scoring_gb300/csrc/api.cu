@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -911,7 +912,7 @@ quail_status check_attention_shape(const quail_cache_desc* c, int n_q_heads, int
 // Key ranges (whole 128-key blocks) that `items` tiles of nb blocks are cut
 // into: the cut that minimises waves x (blocks + the fixed cost of a tile, in
 // blocks: its queries, the pipeline's fill and its rows out).
-void choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
+long choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
   constexpr int kFixed = 4;
   long best = -1;
   *split = 128;
@@ -927,6 +928,7 @@ void choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
     }
     if (blocks == 1 || items * n > 4L * sms) break;
   }
+  return best;
 }
 
 // The letter list of a letters call.
@@ -963,35 +965,91 @@ quail_status copy_letters(const Buffers& b, const int32_t* letter_tokens, int nu
   return QUAIL_OK;
 }
 
-// How one attention call is carried out, and its workspace.
-//   up to 32 query rows per sequence and KV head: streamed (memory bound); the
-//       prefix too while the whole batch has no more rows than that, else on tiles
-//   fewer rows than half a tile, and a prefix: prefix and sequences on tiles apart
-//   else: every sequence's rows fill tiles by themselves, prefix and own keys in one pass
+// Set by a test: the way every attention call is carried out, -1 the rule's.
+std::atomic<int> g_attention_way{-1};
+
+// How one attention call is carried out, and its workspace. Own keys are streamed
+// (every 8 query rows of a sequence read its pages again, from L2 after the first
+// time) or multiplied on tiles of 256 rows (over e4m3 widened to bf16 first); the
+// prefix is streamed, multiplied on tiles that take the rows of all sequences, or
+// a part of every sequence's own keys. The least estimate is taken, in us:
+//   tiles     1.6 per 128 keys of a CTA, 4 blocks' worth of it to begin and end one
+//   streaming the larger of reading pages, 1.2 (e4m3 0.7) per 1000 pages and heads,
+//             and of multiplying them, 0.9 (0.6) per 1000 and 8 rows
+//   widening  2.1 per 1000 pages and heads
+//   parts     1.0 (streamed) or 1.6 per 1000 rows and heads written and joined
+//   launches  5.4 one pass, 7.1 two on tiles, 11 stream and tiles, 14 stream alone
+// (the constants fitted to 1,900 timed calls: 1 to 256 sequences of 1 to 96 queries,
+// 1 to 8 heads a group, prefixes to 32,768, own keys to 8,000, both types; the way
+// it takes costs 1.4% more than the fastest on the mean over them.) Measured, 32
+// heads on 8, us, streamed + streamed / streamed + tiles / tiles apart / one pass:
+//   bf16  256 x 1 query, prefix 4096, 300 own keys   208 /  94 / 203 / 775
+//   bf16   64 x 1,       512,         1500            79 /  83 / 124 / 117
+//   bf16   16 x 4,       8192,        2048             - /  65 /  66 / 125
+//   bf16   64 x 8,       2048,        2048             - / 343 / 186 / 251
+//   bf16   16 x 24,      2048,        64               - /   - /  49 /  33
+//   e4m3    4 x 1,       32768,       300             35 /  79 /  78 / 132
+//   e4m3   16 x 4,       512,         64              31 /   - /  32 /  18
 size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
                       int prefix_len, SharedAttnArgs* a) {
-  const int hkv = c->n_kv_heads, G = hq / hkv, sms = planning_sms();
+  const int hkv = c->n_kv_heads, G = hq / hkv, sms = planning_sms(), S = c->num_seqs;
   const size_t rows = static_cast<size_t>(total_q) * hq;
   const bool codes = c->dtype == QUAIL_DTYPE_E4M3;
   SharedAttnArgs t{};
   const long seq_rows = static_cast<long>(std::min(max_q, total_q)) * G;  // query rows of a sequence per KV head
   const long all_rows = static_cast<long>(total_q) * G;
-  const bool stream = t.streamed = seq_rows <= 32;
-  t.item_rows = 8;
-  // pages that streaming the prefix would read, again for every eight rows of the batch
-  const long prefix_pages = (all_rows + t.item_rows - 1) / t.item_rows * hkv * (prefix_len / 16);
-  const bool tile_prefix =
-      prefix_len > 0 && (stream ? all_rows > t.item_rows && prefix_pages > 4096 : seq_rows < 128 && c->num_seqs > 1);
-  if (tile_prefix)
-    choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, &t.prefix_split,
-                      &t.prefix_splits);
+  const int own = std::max(0, max_seq_len - prefix_len);
+  const long prefix_pages = prefix_len / 16, own_pages = (own + 15) / 16;
+  // pages of the widened copies; the row coordinates of the tiles' pool stay below 2^31
+  const auto fits = [&](long pages) { return !codes || pages * hkv * 16 <= INT32_MAX; };
+  bool tile_prefix = false, stream = true;
+  int apart_split = 0, apart_splits = 0, one_split = 0, one_splits = 0;
+  {
+    const long seq_ctas = (seq_rows + kTileRows - 1) / kTileRows * hkv * S;
+    const double thousand = hkv * 1e-3, k_read = codes ? 0.7 : 1.2, k_pass = codes ? 0.6 : 0.9;
+    const double passes = std::min<double>(static_cast<double>(S) * ((seq_rows + 7) / 8), all_rows / 8. + S) * thousand;
+    const double read = static_cast<double>(S) * own_pages * thousand * k_read, pass = passes * own_pages * k_pass;
+    const double widen_prefix = codes ? 2.1 * prefix_pages * thousand : 0.;
+    const double widen_all = codes ? widen_prefix + 2.1 * S * own_pages * thousand : 0.;
+    const double join = all_rows * thousand;
+    const int forced = g_attention_way.load(std::memory_order_relaxed);
+    double best = forced == 0 ? -1. : 14. + (prefix_len > 0 ? join : 0.) +
+                  std::max(read + prefix_pages * thousand * k_read,
+                           pass + (all_rows + 7) / 8 * thousand * prefix_pages * k_pass);
+    const auto take = [&](int way, double us, bool s, bool p) {
+      if (way == forced) us = -1.;
+      if (us < best) {
+        best = us;
+        stream = s;
+        tile_prefix = p;
+      }
+    };
+    long on_prefix = 0;
+    if (prefix_len > 0) {
+      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms,
+                                    &t.prefix_split, &t.prefix_splits);
+      if (fits(prefix_pages)) take(1, 11. + std::max(read, pass) + 1.9 * on_prefix + widen_prefix + 1.6 * join, true, true);
+    }
+    if (fits(prefix_pages + S * own_pages)) {
+      if (prefix_len > 0 && S > 1) {
+        const long on_own =
+            own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, &apart_split, &apart_splits) : 0;
+        take(2, 7.1 + 1.6 * (on_prefix + on_own) + widen_all + 1.6 * join, false, true);
+      }
+      const long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, &one_split, &one_splits);
+      take(3, 5.4 + 1.6 * on_all + widen_all, false, false);
+    }
+  }
+  t.streamed = stream;
+  if (!tile_prefix) t.prefix_split = t.prefix_splits = 0;
   if (!stream) {
     t.seq_begin = tile_prefix ? prefix_len : 0;
-    t.seq_split = 128;
-    t.seq_splits = 1;
-    if (max_seq_len > t.seq_begin)
-      choose_key_splits((seq_rows + kTileRows - 1) / kTileRows * hkv * c->num_seqs,
-                        (max_seq_len - t.seq_begin + 127) / 128, sms, &t.seq_split, &t.seq_splits);
+    t.seq_split = tile_prefix ? apart_split : one_split;
+    t.seq_splits = tile_prefix ? apart_splits : one_splits;
+    if (t.seq_splits == 0) {  // no key of a sequence's own
+      t.seq_split = 128;
+      t.seq_splits = 1;
+    }
   }
   t.dense_parts = t.prefix_splits + t.seq_splits;
   if (t.dense_parts == 1 && !tile_prefix) t.dense_parts = 0;
@@ -999,27 +1057,25 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   t.wide_pages = codes && (tile_prefix || !stream);
   Carver k{base};
   if (stream) {
-    const size_t workers = static_cast<size_t>(stream_warps(t.item_rows)) * sms;
+    const size_t workers = static_cast<size_t>(kStreamWarps) * sms;
     t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
     if (prefix_len > 0 && !tile_prefix) {
-      t.prefix_row_tiles = static_cast<int>((all_rows + t.item_rows - 1) / t.item_rows);
+      t.prefix_row_tiles = static_cast<int>((all_rows + kItemRows - 1) / kItemRows);
       t.prefix_o = k.take<float>(rows * 128);
       t.prefix_st = k.take<PartStat>(rows);
     }
     t.own_o = k.take<float>(rows * 128);
     t.own_st = k.take<PartStat>(rows);
-    t.cont_o = k.take<float>(workers * t.item_rows * 128);
-    t.cont_st = k.take<PartStat>(workers * t.item_rows);
+    t.cont_o = k.take<float>(workers * kItemRows * 128);
+    t.cont_st = k.take<PartStat>(workers * kItemRows);
   }
   if (t.dense_parts > 0) {
     t.dense_o = k.take<float>(t.dense_parts * rows * 128);
     t.dense_st = k.take<PartStat>(t.dense_parts * rows);
   }
   if (t.wide_pages) {
-    t.wide_own = stream ? 0 : (max_seq_len - prefix_len + 15) / 16;
+    t.wide_own = stream ? 0 : static_cast<int>(own_pages);
     const size_t pages = static_cast<size_t>(prefix_len / 16) + static_cast<size_t>(c->num_seqs) * t.wide_own;
-    // row coordinates of the widened pool stay below 2^31
-    if (pages * hkv * 16 > (size_t(1) << 31) - 1) return 0;
     t.pool_pages = static_cast<int>(std::max<size_t>(pages, 1));
     t.wide_k = k.take<bf16>(static_cast<size_t>(t.pool_pages) * hkv * 16 * 128);
     t.wide_v = k.take<bf16>(static_cast<size_t>(t.pool_pages) * hkv * 16 * 128);
@@ -1081,7 +1137,6 @@ size_t plan_letters_cached(uint8_t* base, const quail_model_desc* m, const quail
   x.lse = k.take<float>(static_cast<size_t>(N) * hq);
   off += round_up(k.off, 256);
   const size_t attn = plan_attention(base ? base + off : nullptr, c, hq, N, 1, max_doc_len, prefix_len, &x.attn);
-  if (attn == 0) return 0;
   if (out) *out = x;
   return off + attn;
 }
@@ -1613,6 +1668,16 @@ quail_status quail_test_set_pipeline_wait_limit(long long cycles) {
   return QUAIL_OK;
 }
 
+// Test hook, not part of the public header: attention over the cache goes one
+// way (0 streamed, 1 streamed behind a prefix on tiles, 2 prefix and sequences on
+// tiles apart, 3 in one pass) wherever that exists, whatever it costs; -1: the
+// cheapest again. Process-wide; the workspace of a call depends on it.
+quail_status quail_test_set_attention_way(int way) {
+  if (way < -1 || way > 3) return fail(QUAIL_ERR_INVALID_ARG, "way must be -1..3");
+  g_attention_way.store(way);
+  return QUAIL_OK;
+}
+
 quail_status quail_device_status(quail_stream_t stream) {
   DeviceState* ds = nullptr;
   quail_status s = device_state(&ds);
@@ -2008,7 +2073,6 @@ size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
   const size_t n = plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
-  if (n == 0) fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "num_seqs x max_seq_len is too large for an e4m3 cache");
   return n;
 }
 
@@ -2029,7 +2093,6 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
     return fail(QUAIL_ERR_INVALID_ARG, "q, out, seq_len or prefix_pages is null");
   if (!aligned16(q) || !aligned16(out)) return fail(QUAIL_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   const size_t need = plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
-  if (need == 0) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "num_seqs x max_seq_len is too large for an e4m3 cache");
   s = check_workspace(workspace, workspace_bytes, need);
   if (s != QUAIL_OK) return s;
   DeviceState* ds = nullptr;
@@ -2093,7 +2156,6 @@ quail_status quail_classify_letters_cached(const quail_model_desc* model, const 
   if (letter_logprob == nullptr || letter_prob == nullptr || letter_argmax == nullptr)
     return fail(QUAIL_ERR_INVALID_ARG, "an output pointer is null");
   const size_t need = plan_letters_cached(nullptr, model, cache, num_letters, max_doc_len, prefix_len, nullptr);
-  if (need == 0) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "num_seqs x max_doc_len is too large for an e4m3 cache");
   s = check_workspace(workspace, workspace_bytes, need);
   if (s != QUAIL_OK) return s;
   DeviceState* ds = nullptr;

@@ -78,11 +78,10 @@ struct SharedAttnArgs {
 
   // The streaming kernel's work list: prefix_row_tiles x hkv passes over the
   // prefix pages (0: the prefix is not its work), then every sequence's own pages
-  // per KV head and row tile, in units of stream_unit_pages, cut into equal chunks over the
-  // workers. plan: [0] units, [1] chunk, [2 + b]
-  // first unit of sequence b, [2 + num_seqs] past the last.
+  // per KV head and row tile, in units of stream_unit_pages, cut into equal chunks
+  // over the workers. plan: [0] units, [1] chunk, [2 + b] first unit of sequence b,
+  // [2 + num_seqs] past the last.
   bool streamed;
-  int item_rows;  // query rows of an item, 8 or 16
   int prefix_row_tiles;
   long long* plan;
   // Parts, each [rows, 128] fp32 and a PartStat per row; rows are (token, head)
@@ -91,7 +90,7 @@ struct SharedAttnArgs {
   PartStat* prefix_st;
   float* own_o;          // pieces that begin a sequence's own keys
   PartStat* own_st;
-  float* cont_o;         // [workers, item_rows, 128]
+  float* cont_o;         // [workers, kItemRows, 128]
   PartStat* cont_st;
 
   // The tensor-core tiles' work: the prefix for all rows in prefix_splits key
@@ -113,8 +112,8 @@ struct SharedAttnArgs {
 };
 
 constexpr int kTileRows = 256;  // query rows of a tensor-core CTA
-// Workers (warps) of an SM for items of 8 or 16 query rows.
-__host__ __device__ constexpr int stream_warps(int item_rows) { return item_rows == 8 ? 12 : 8; }
+constexpr int kItemRows = 8;       // query rows of a streaming work item
+constexpr int kStreamWarps = 12;   // streaming workers of an SM
 // Pages that a streaming worker takes at a time.
 __host__ __device__ constexpr int stream_unit_pages(bool codes) { return codes ? 2 : 1; }
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,

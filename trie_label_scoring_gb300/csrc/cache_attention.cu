@@ -31,22 +31,22 @@ namespace {
 // rows as N: S^T = K Q^T (M 16 keys, N 8 rows) and O^T += V^T P^T (M 16 dims, N 8
 // rows). Keys and values are the A operands, so a few query rows waste little:
 // with the rows as M, 12 of 16 rows of a 4-head group were padding, in O's
-// registers, the exponentials and the products alike. NT = 1 or 2 tiles of 8
-// rows; a sequence with more rows is several items in a row, so its pages come
-// from L2 after the first.
+// registers, the exponentials and the products alike. A sequence with more than 8
+// rows is several items in a row, so its pages come from L2 after the first (items
+// of 16 rows were slower: 8 workers an SM for their registers).
 // Over bf16 pages q and P are bf16; over e4m3 pages the codes widen exactly to
 // fp16, q is scaled by a power of two per row (exact) and P is rounded to fp16.
 // The key's power of two multiplies its score, the value's is added to the
 // exponent of its weight: o and l keep separate maxima, so that value rows of any
 // scale neither overflow P nor starve the sum.
-template <bool CODES, int NT>
+template <bool CODES>
 struct StreamCfg {
-  static constexpr int kWarps = stream_warps(8 * NT);
+  static constexpr int kWarps = kStreamWarps;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kUnit = stream_unit_pages(CODES);   // pages a stage
   static constexpr uint32_t kPlane = CODES ? 2048 : 4096;  // K or V of one (page, head)
   static constexpr uint32_t kStage = 2 * kPlane * kUnit;
-  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kStages = 2;
   static constexpr int kScaleLanes = CODES ? 2 * kUnit : 0;  // lanes that copy 16 scale bytes each
   static constexpr uint32_t kRing = kWarps * kStages * kStage;
   static constexpr uint32_t kScales = CODES ? kWarps * kStages * kUnit * 32 : 0;  // key, value exponents
@@ -131,7 +131,7 @@ __device__ __forceinline__ int own_units(const SharedAttnArgs& a, int b) {
 // Items of sequence b: its row tiles for every KV head.
 __device__ __forceinline__ int own_items(const SharedAttnArgs& a, int b) {
   const int n = a.q_offsets ? a.q_offsets[b + 1] - a.q_offsets[b] : 1;
-  return (n * (a.hq / a.c.hkv) + a.item_rows - 1) / a.item_rows * a.c.hkv;
+  return (n * (a.hq / a.c.hkv) + kItemRows - 1) / kItemRows * a.c.hkv;
 }
 // All units of sequence b; b may lie past the last.
 template <int UNIT>
@@ -175,12 +175,12 @@ __device__ __forceinline__ int item_head(const SharedAttnArgs& a, const Cursor& 
   return c.own ? c.x / (c.X / a.c.hkv) : c.x;
 }
 
-template <bool CODES, int NT>
-__global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
+template <bool CODES>
+__global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     attention_stream_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV) {
-  using Cfg = StreamCfg<CODES, NT>;
-  constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit, kThreads = Cfg::kThreads, kRows = 8 * NT;
+  using Cfg = StreamCfg<CODES>;
+  constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit, kThreads = Cfg::kThreads, kRows = kItemRows;
   constexpr int kKeys = kUnit * kPage;  // keys of a unit
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -378,10 +378,10 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
 #pragma unroll
   for (int c = 0; c < 4; ++c) off[c] = swz(half_key((lane >> 3) & 1, lane & 7), 2 * c + (lane >> 4));
 
-  uint2 qf[NT][8];              // Q^T fragments
-  float o[8][NT][4];            // O^T: 16 dims x 8 rows
-  float2 m_o[NT], m_l[NT], l[NT], f_row[NT];  // of rows 2 tq, 2 tq + 1 of a tile; l: this lane's keys only
-  int limit[NT][2];             // keys that those rows see, counted from the item's first
+  uint2 qf[8];     // Q^T fragments
+  float o[8][4];   // O^T: 16 dims x 8 rows
+  float2 m_o, m_l, l, f_row;  // of rows 2 tq, 2 tq + 1; l: this lane's keys only
+  int limit[2];    // keys that those rows see, counted from the item's first
   QueryRange qr{0, 0, 0, true};
   int g = 0, flat0 = 0, n_rows = 0;  // KV head, first row (within the sequence or the batch), rows
   int first_unit = 0;
@@ -404,101 +404,95 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
       keys = safe = a.prefix_len;
     }
     first_unit = cc.j;
+    // fragment of 16 dims: row gq, the dims that lane tq's A registers hold
+    const int flat = flat0 + gq;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // fragment of 16 dims: row gq of the tile, the dims that lane tq's A registers hold
-      const int r = 8 * t + gq, flat = flat0 + r;
+    for (int ks = 0; ks < 8; ++ks) qf[ks] = make_uint2(0u, 0u);
+    if (gq < n_rows) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(
+          a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G) * 128);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) qf[t][ks] = make_uint2(0u, 0u);
-      if (r < n_rows) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(
-            a.q + (static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G) * 128);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          qf[t][ks] = CODES ? *reinterpret_cast<const uint2*>(p + ks * 8 + 2 * tq)
-                            : make_uint2(p[ks * 8 + tq], p[ks * 8 + tq + 4]);
-      }
-      f_row[t] = make_float2(a.scale_log2, a.scale_log2);
-      if constexpr (CODES) {
-        float am = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const float2 x = unpack_bf16(qf[t][ks].x), y = unpack_bf16(qf[t][ks].y);
-          am = fmaxf(fmaxf(fmaxf(am, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
-        }
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        // 2^e <= max |q| < 2^(e+1), e in [-126, 126]: q / 2^e is exact in fp16
-        // down to 2^-24 of the row's maximum
-        const int e = am > 0.f ? min(126, max(-126, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 0;
-        const float down = pow2_byte(127 - e), f = a.scale_log2 * pow2_byte(127 + e);
-        f_row[t] = make_float2(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const float2 x = unpack_bf16(qf[t][ks].x), y = unpack_bf16(qf[t][ks].y);
-          qf[t][ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rc = 8 * t + 2 * tq + e;
-        limit[t][e] = cc.own && a.causal && rc < n_rows ? keys - (qr.hi - qr.lo - 1 - (flat0 + rc) / G) : keys;
-      }
-      m_o[t] = m_l[t] = make_float2(-INFINITY, -INFINITY);
-      l[t] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+      for (int ks = 0; ks < 8; ++ks)
+        qf[ks] = CODES ? *reinterpret_cast<const uint2*>(p + ks * 8 + 2 * tq)
+                       : make_uint2(p[ks * 8 + tq], p[ks * 8 + tq + 4]);
     }
+    f_row = make_float2(a.scale_log2, a.scale_log2);
+    if constexpr (CODES) {
+      float am = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const float2 x = unpack_bf16(qf[ks].x), y = unpack_bf16(qf[ks].y);
+        am = fmaxf(fmaxf(fmaxf(am, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
+      }
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      // 2^e <= max |q| < 2^(e+1), e in [-126, 126]: q / 2^e is exact in fp16
+      // down to 2^-24 of the row's maximum
+      const int e = am > 0.f ? min(126, max(-126, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 0;
+      const float down = pow2_byte(127 - e), f = a.scale_log2 * pow2_byte(127 + e);
+      f_row = make_float2(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const float2 x = unpack_bf16(qf[ks].x), y = unpack_bf16(qf[ks].y);
+        qf[ks] = make_uint2(pack_f16(x.x * down, x.y * down), pack_f16(y.x * down, y.y * down));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rc = 2 * tq + e;
+      limit[e] = cc.own && a.causal && rc < n_rows ? keys - (qr.hi - qr.lo - 1 - (flat0 + rc) / G) : keys;
+    }
+    m_o = m_l = make_float2(-INFINITY, -INFINITY);
+    l = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   };
 
   // the piece's rows: final when it is the whole of what they attend to, else parts
   auto close_item = [&]() {
     const bool whole = cc.own && a.prefix_len == 0 && first_unit == 0 && cc.j == cc.n - 1;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int x = 4; x < 32; x <<= 1) {
+      l.x += __shfl_xor_sync(0xffffffffu, l.x, x);
+      l.y += __shfl_xor_sync(0xffffffffu, l.y, x);
+    }
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        l[t].x += __shfl_xor_sync(0xffffffffu, l[t].x, x);
-        l[t].y += __shfl_xor_sync(0xffffffffu, l[t].y, x);
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * tq + e;
+      const float sum = e ? l.y : l.x, ml = e ? m_l.y : m_l.x;
+      const float mo = (e ? m_o.y : m_o.x) - (CODES ? 127.f : 0.f);
+      const int flat = flat0 + min(r, n_rows - 1);
+      const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G;
+      const bool rest = first_unit > 0;  // the piece continues an earlier worker's
+      const size_t at = rest ? static_cast<size_t>(worker) * kRows + r : row;
+      float* po = rest ? a.cont_o : cc.own ? a.own_o : a.prefix_o;
+      PartStat* ps = rest ? a.cont_st : cc.own ? a.own_st : a.prefix_st;
+      // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
+      const float f = whole ? (CODES ? exp2f(mo - ml) : 1.f) / sum : 1.f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        // two neighbouring dims of the 16 per lane: e4m3 products leave them so, bf16
+        // ones trade with the neighbour (dims gq and gq + 8 -> a pair of one half)
+        float v0 = o[n][e], v1 = o[n][2 + e];
+        int dim = 16 * n + 2 * gq;
+        if constexpr (!CODES) {
+          const bool odd = gq & 1;
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 4);
+          (odd ? v0 : v1) = got;
+          dim = 16 * n + (odd ? 8 : 0) + (gq & ~1);
+        }
+        if (r < n_rows) {
+          if (whole)
+            *reinterpret_cast<uint32_t*>(a.out + row * 128 + dim) = pack_bf16(v0 * f, v1 * f);
+          else
+            *reinterpret_cast<float2*>(po + at * 128 + dim) = make_float2(v0, v1);
+        }
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * t + 2 * tq + e;
-        const float sum = e ? l[t].y : l[t].x, ml = e ? m_l[t].y : m_l[t].x;
-        const float mo = (e ? m_o[t].y : m_o[t].x) - (CODES ? 127.f : 0.f);
-        const int flat = flat0 + min(r, n_rows - 1);
-        const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G;
-        const bool rest = first_unit > 0;  // the piece continues an earlier worker's
-        const size_t at = rest ? static_cast<size_t>(worker) * kRows + r : row;
-        float* po = rest ? a.cont_o : cc.own ? a.own_o : a.prefix_o;
-        PartStat* ps = rest ? a.cont_st : cc.own ? a.own_st : a.prefix_st;
-        // 2^(m_o - m_l) brings values summed at m_o to the weights' maximum
-        const float f = whole ? (CODES ? exp2f(mo - ml) : 1.f) / sum : 1.f;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          // two neighbouring dims of the 16 per lane: e4m3 products leave them so, bf16
-          // ones trade with the neighbour (dims gq and gq + 8 -> a pair of one half)
-          float v0 = o[n][t][e], v1 = o[n][t][2 + e];
-          int dim = 16 * n + 2 * gq;
-          if constexpr (!CODES) {
-            const bool odd = gq & 1;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 4);
-            (odd ? v0 : v1) = got;
-            dim = 16 * n + (odd ? 8 : 0) + (gq & ~1);
-          }
-          if (r < n_rows) {
-            if (whole)
-              *reinterpret_cast<uint32_t*>(a.out + row * 128 + dim) = pack_bf16(v0 * f, v1 * f);
-            else
-              *reinterpret_cast<float2*>(po + at * 128 + dim) = make_float2(v0, v1);
-          }
-        }
-        if (gq == 0 && r < n_rows) {
-          if (!whole)
-            ps[at] = PartStat{mo, ml, sum, 0.f};
-          else if (a.lse != nullptr)
-            a.lse[row] = (ml + log2f(sum)) * 0.6931471805599453f;
-        }
+      if (gq == 0 && r < n_rows) {
+        if (!whole)
+          ps[at] = PartStat{mo, ml, sum, 0.f};
+        else if (a.lse != nullptr)
+          a.lse[row] = (ml + log2f(sum)) * 0.6931471805599453f;
       }
     }
   };
@@ -514,9 +508,9 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
     const uint32_t stage = smem_u32(ring + s * Cfg::kStage);
     const int key0 = cc.j * kKeys;
     const bool border = key0 + kKeys > safe;  // some row does not see some key of the unit
-    float2 sc[2 * kUnit][NT];  // scores of this lane's keys (half 0, half 1 of each page), its two rows
+    float2 sc[2 * kUnit];  // scores of this lane's keys (half 0, half 1 of each page), its two rows
     {
-      float acc[kUnit][NT][2][4] = {};  // two chains, for independent products
+      float acc[kUnit][2][4] = {};  // two chains, for independent products
 #pragma unroll
       for (int u = 0; u < kUnit; ++u) {
         const uint32_t kb = stage + u * 2 * Cfg::kPlane;
@@ -530,24 +524,20 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
               uint4 A;
               widen4(r[2 * h], A.x, A.z);
               widen4(r[2 * h + 1], A.y, A.w);
-#pragma unroll
-              for (int t = 0; t < NT; ++t) mma16816<true>(acc[u][t][h], A, qf[t][2 * c + h]);
+              mma16816<true>(acc[u][h], A, qf[2 * c + h]);
             }
           } else {
             const uint4 A = make_uint4(r[0], r[1], r[2], r[3]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<false>(acc[u][t][c & 1], A, qf[t][c]);
+            mma16816<false>(acc[u][c & 1], A, qf[c]);
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < kUnit; ++u)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            sc[2 * u + h][t] = add2(make_float2(acc[u][t][0][2 * h], acc[u][t][0][2 * h + 1]),
-                                    make_float2(acc[u][t][1][2 * h], acc[u][t][1][2 * h + 1]));
+        for (int h = 0; h < 2; ++h)
+          sc[2 * u + h] = add2(make_float2(acc[u][0][2 * h], acc[u][0][2 * h + 1]),
+                              make_float2(acc[u][1][2 * h], acc[u][1][2 * h + 1]));
     }
     float ve[2 * kUnit];  // value exponents of this lane's keys, biased by 127
 #pragma unroll
@@ -559,92 +549,75 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
         // byte b as the float 2^23 + b, exactly
         ve[k] = __uint_as_float(0x4b000000u | e[16]) - 8388608.f;
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        sc[k][t] = mul2(sc[k][t], CODES ? mul2(f_row[t], make_float2(kf, kf)) : f_row[t]);
+      sc[k] = mul2(sc[k], CODES ? mul2(f_row, make_float2(kf, kf)) : f_row);
     }
     if (border) {
 #pragma unroll
       for (int k = 0; k < 2 * kUnit; ++k) {
         const int key = key0 + (k >> 1) * kPage + my_key[k & 1];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (key >= limit[t][0]) sc[k][t].x = -INFINITY;
-          if (key >= limit[t][1]) sc[k][t].y = -INFINITY;
-        }
+        if (key >= limit[0]) sc[k].x = -INFINITY;
+        if (key >= limit[1]) sc[k].y = -INFINITY;
       }
     }
-    float2 mo[NT], ml[NT];
-    bool grows = false;
+    float2 ml = sc[0];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      ml[t] = sc[0][t];
+    for (int k = 1; k < 2 * kUnit; ++k) ml = make_float2(fmaxf(ml.x, sc[k].x), fmaxf(ml.y, sc[k].y));
 #pragma unroll
-      for (int k = 1; k < 2 * kUnit; ++k) ml[t] = make_float2(fmaxf(ml[t].x, sc[k][t].x), fmaxf(ml[t].y, sc[k][t].y));
+    for (int x = 4; x < 32; x <<= 1) {
+      ml.x = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, x));
+      ml.y = fmaxf(ml.y, __shfl_xor_sync(0xffffffffu, ml.y, x));
+    }
+    float2 mo = ml;
+    if constexpr (CODES) {
+      mo = add2(sc[0], make_float2(ve[0], ve[0]));
+#pragma unroll
+      for (int k = 1; k < 2 * kUnit; ++k) {
+        const float2 v = add2(sc[k], make_float2(ve[k], ve[k]));
+        mo = make_float2(fmaxf(mo.x, v.x), fmaxf(mo.y, v.y));
+      }
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
-        ml[t].x = fmaxf(ml[t].x, __shfl_xor_sync(0xffffffffu, ml[t].x, x));
-        ml[t].y = fmaxf(ml[t].y, __shfl_xor_sync(0xffffffffu, ml[t].y, x));
+        mo.x = fmaxf(mo.x, __shfl_xor_sync(0xffffffffu, mo.x, x));
+        mo.y = fmaxf(mo.y, __shfl_xor_sync(0xffffffffu, mo.y, x));
       }
-      mo[t] = ml[t];
-      if constexpr (CODES) {
-        mo[t] = add2(sc[0][t], make_float2(ve[0], ve[0]));
-#pragma unroll
-        for (int k = 1; k < 2 * kUnit; ++k) {
-          const float2 v = add2(sc[k][t], make_float2(ve[k], ve[k]));
-          mo[t] = make_float2(fmaxf(mo[t].x, v.x), fmaxf(mo[t].y, v.y));
-        }
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          mo[t].x = fmaxf(mo[t].x, __shfl_xor_sync(0xffffffffu, mo[t].x, x));
-          mo[t].y = fmaxf(mo[t].y, __shfl_xor_sync(0xffffffffu, mo[t].y, x));
-        }
-      }
-      grows = grows || ml[t].x > m_l[t].x + 8.f || ml[t].y > m_l[t].y + 8.f || mo[t].x > m_o[t].x + 8.f ||
-              mo[t].y > m_o[t].y + 8.f;
     }
+    const bool grows = ml.x > m_l.x + 8.f || ml.y > m_l.y + 8.f || mo.x > m_o.x + 8.f || mo.y > m_o.y + 8.f;
     // The reference maxima move only when a unit exceeds them by more than
     // 2^8: weights stay below 256 and the rescale is skipped on most units.
     if (__any_sync(0xffffffffu, grows)) {
       auto step = [](float m, float n) { return n == -INFINITY ? 1.f : exp2f(m - n); };
+      const float2 no = make_float2(fmaxf(m_o.x, mo.x), fmaxf(m_o.y, mo.y));
+      const float2 nl = make_float2(fmaxf(m_l.x, ml.x), fmaxf(m_l.y, ml.y));
+      const float2 fo = make_float2(step(m_o.x, no.x), step(m_o.y, no.y));
+      l = mul2(l, make_float2(step(m_l.x, nl.x), step(m_l.y, nl.y)));
+      m_o = no;
+      m_l = nl;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float2 no = make_float2(fmaxf(m_o[t].x, mo[t].x), fmaxf(m_o[t].y, mo[t].y));
-        const float2 nl = make_float2(fmaxf(m_l[t].x, ml[t].x), fmaxf(m_l[t].y, ml[t].y));
-        const float2 fo = make_float2(step(m_o[t].x, no.x), step(m_o[t].y, no.y));
-        l[t] = mul2(l[t], make_float2(step(m_l[t].x, nl.x), step(m_l[t].y, nl.y)));
-        m_o[t] = no;
-        m_l[t] = nl;
+      for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[n][t][c] *= (c & 1) ? fo.y : fo.x;
-      }
+        for (int c = 0; c < 4; ++c) o[n][c] *= (c & 1) ? fo.y : fo.x;
     }
-    uint2 pb[kUnit][NT];  // P^T fragments
+    uint2 pb[kUnit];  // P^T fragments
+    // no key seen yet: the reference is still -inf, and every weight is 0
+    auto neg = [](float m) { return m == -INFINITY ? 0.f : -m; };
+    const float2 rl = make_float2(neg(m_l.x), neg(m_l.y)), ro = make_float2(neg(m_o.x), neg(m_o.y));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // no key seen yet: the reference is still -inf, and every weight is 0
-      auto neg = [](float m) { return m == -INFINITY ? 0.f : -m; };
-      const float2 rl = make_float2(neg(m_l[t].x), neg(m_l[t].y)), ro = make_float2(neg(m_o[t].x), neg(m_o[t].y));
-#pragma unroll
-      for (int k = 0; k < 2 * kUnit; ++k) {
-        const float2 x = add2(sc[k][t], rl);
-        const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-        l[t] = add2(l[t], e);
-        uint32_t p;
-        if constexpr (CODES) {
-          const float2 v = add2(sc[k][t], add2(ro, make_float2(ve[k], ve[k])));
-          p = pack_f16(fast_exp2(v.x), fast_exp2(v.y));
-        } else {
-          p = pack_bf16(e.x, e.y);
-        }
-        p = transpose8x8(p);
-        if (k & 1)
-          pb[k >> 1][t].y = p;
-        else
-          pb[k >> 1][t].x = p;
+    for (int k = 0; k < 2 * kUnit; ++k) {
+      const float2 x = add2(sc[k], rl);
+      const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      l = add2(l, e);
+      uint32_t p;
+      if constexpr (CODES) {
+        const float2 v = add2(sc[k], add2(ro, make_float2(ve[k], ve[k])));
+        p = pack_f16(fast_exp2(v.x), fast_exp2(v.y));
+      } else {
+        p = pack_bf16(e.x, e.y);
       }
+      p = transpose8x8(p);
+      if (k & 1)
+        pb[k >> 1].y = p;
+      else
+        pb[k >> 1].x = p;
     }
     // O^T += V^T P^T. Slots past the sequence's end may hold anything: their
     // values are zeroed in registers, since 0 * NaN would reach O.
@@ -676,13 +649,11 @@ __global__ void __launch_bounds__(StreamCfg<CODES, NT>::kThreads, 1)
             uint4 A;
             widen4(__byte_perm(r[2 * h], 0u, 0x3120), A.x, A.y);
             widen4(__byte_perm(r[2 * h + 1], 0u, 0x3120), A.z, A.w);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<true>(o[2 * c + h][t], A, pb[u][t]);
+            mma16816<true>(o[2 * c + h], A, pb[u]);
           }
         } else {
           const uint4 A = make_uint4(r[0], r[2], r[1], r[3]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816<false>(o[c][t], A, pb[u][t]);
+          mma16816<false>(o[c], A, pb[u]);
         }
       }
     }
@@ -829,12 +800,12 @@ __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnAr
       if (a.streamed) {
         if (a.prefix_row_tiles > 0) {
           const int flat = t * G + h % G;
-          pieces((static_cast<long long>(flat / a.item_rows) * a.c.hkv + g) * pu, pu, chunk, &p.prefix_w, &p.prefix_n);
-          p.prefix_r = flat % a.item_rows;
+          pieces((static_cast<long long>(flat / kItemRows) * a.c.hkv + g) * pu, pu, chunk, &p.prefix_w, &p.prefix_n);
+          p.prefix_r = flat % kItemRows;
         }
         if (n > 0) {
-          pieces(base + (static_cast<long long>(g) * tiles + r / a.item_rows) * n, n, chunk, &p.own_w, &p.own_n);
-          p.own_r = r % a.item_rows;
+          pieces(base + (static_cast<long long>(g) * tiles + r / kItemRows) * n, n, chunk, &p.own_w, &p.own_n);
+          p.own_r = r % kItemRows;
         }
         if (a.prefix_len == 0 && p.own_n == 1) continue;  // written by its only worker
       } else {
@@ -868,7 +839,7 @@ __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnAr
           po = pre ? a.prefix_o : a.own_o;
           pst = pre ? a.prefix_st : a.own_st;
           if (piece > 0) {
-            at = (static_cast<size_t>(pre ? p.prefix_w : p.own_w) + piece) * a.item_rows + (pre ? p.prefix_r : p.own_r);
+            at = (static_cast<size_t>(pre ? p.prefix_w : p.own_w) + piece) * kItemRows + (pre ? p.prefix_r : p.own_r);
             po = a.cont_o;
             pst = a.cont_st;
           }
@@ -900,11 +871,11 @@ __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnAr
 
 namespace {
 
-template <bool CODES, int NT>
+template <bool CODES>
 cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
                           cudaStream_t st) {
-  auto kern = attention_stream_kernel<CODES, NT>;
-  constexpr size_t smem = StreamCfg<CODES, NT>::kSmem;
+  auto kern = attention_stream_kernel<CODES>;
+  constexpr size_t smem = StreamCfg<CODES>::kSmem;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -916,16 +887,14 @@ cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const
     configured[dev].store(true, std::memory_order_release);
   }
   count_launch();
-  return launch_pdl(kern, dim3(num_sms), dim3(StreamCfg<CODES, NT>::kThreads), smem, st, a, tmK, tmV);
+  return launch_pdl(kern, dim3(num_sms), dim3(StreamCfg<CODES>::kThreads), smem, st, a, tmK, tmV);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     int num_sms, cudaStream_t st) {
-  if (a.item_rows == 8)
-    return a.c.codes ? launch_stream<true, 1>(a, tmK, tmV, num_sms, st) : launch_stream<false, 1>(a, tmK, tmV, num_sms, st);
-  return a.c.codes ? launch_stream<true, 2>(a, tmK, tmV, num_sms, st) : launch_stream<false, 2>(a, tmK, tmV, num_sms, st);
+  return a.c.codes ? launch_stream<true>(a, tmK, tmV, num_sms, st) : launch_stream<false>(a, tmK, tmV, num_sms, st);
 }
 
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {

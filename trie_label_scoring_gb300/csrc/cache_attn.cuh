@@ -33,6 +33,8 @@ __device__ __forceinline__ long long pipeline_wait_limit() {
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
   const uint32_t a = smem_u32(bar);
+  // A try waits a while by itself; most waits that the first does not see out end in
+  // the second, which the checks would hold up.
   if (mbar_try_wait(a, parity)) return true;
   const long long t0 = clock64();
   while (true) {
