@@ -970,13 +970,12 @@ std::atomic<int> g_attention_way{-1};
 
 // How one attention call is carried out, and its workspace. Own keys are streamed
 // (every 8 query rows of a sequence read its pages again, from L2 after the first
-// time) or multiplied on tiles of 256 rows (over e4m3 widened to bf16 first); the
+// time) or multiplied on tiles of 256 rows; the
 // prefix is streamed, multiplied on tiles that take the rows of all sequences, or
 // a part of every sequence's own keys. The least estimate is taken, in us:
 //   tiles     1.6 per 128 keys of a CTA, 4 blocks' worth of it to begin and end one
 //   streaming the larger of reading pages, 1.2 (e4m3 0.7) per 1000 pages and heads,
 //             and of multiplying them, 0.9 (0.6) per 1000 and 8 rows
-//   widening  2.1 per 1000 pages and heads
 //   parts     1.0 (streamed) or 1.6 per 1000 rows and heads written and joined
 //   launches  5.4 one pass, 7.1 two on tiles, 11 stream and tiles, 14 stream alone
 // (the constants fitted to 1,900 timed calls: 1 to 256 sequences of 1 to 96 queries,
@@ -1000,8 +999,6 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   const long all_rows = static_cast<long>(total_q) * G;
   const int own = std::max(0, max_seq_len - prefix_len);
   const long prefix_pages = prefix_len / 16, own_pages = (own + 15) / 16;
-  // pages of the widened copies; the row coordinates of the tiles' pool stay below 2^31
-  const auto fits = [&](long pages) { return !codes || pages * hkv * 16 <= INT32_MAX; };
   bool tile_prefix = false, stream = true;
   int apart_split = 0, apart_splits = 0, one_split = 0, one_splits = 0;
   {
@@ -1009,8 +1006,6 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     const double thousand = hkv * 1e-3, k_read = codes ? 0.7 : 1.2, k_pass = codes ? 0.6 : 0.9;
     const double passes = std::min<double>(static_cast<double>(S) * ((seq_rows + 7) / 8), all_rows / 8. + S) * thousand;
     const double read = static_cast<double>(S) * own_pages * thousand * k_read, pass = passes * own_pages * k_pass;
-    const double widen_prefix = codes ? 2.1 * prefix_pages * thousand : 0.;
-    const double widen_all = codes ? widen_prefix + 2.1 * S * own_pages * thousand : 0.;
     const double join = all_rows * thousand;
     const int forced = g_attention_way.load(std::memory_order_relaxed);
     double best = forced == 0 ? -1. : 14. + (prefix_len > 0 ? join : 0.) +
@@ -1028,17 +1023,15 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     if (prefix_len > 0) {
       on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms,
                                     &t.prefix_split, &t.prefix_splits);
-      if (fits(prefix_pages)) take(1, 11. + std::max(read, pass) + 1.9 * on_prefix + widen_prefix + 1.6 * join, true, true);
+      take(1, 11. + std::max(read, pass) + 1.9 * on_prefix + 1.6 * join, true, true);
     }
-    if (fits(prefix_pages + S * own_pages)) {
-      if (prefix_len > 0 && S > 1) {
-        const long on_own =
-            own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, &apart_split, &apart_splits) : 0;
-        take(2, 7.1 + 1.6 * (on_prefix + on_own) + widen_all + 1.6 * join, false, true);
-      }
-      const long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, &one_split, &one_splits);
-      take(3, 5.4 + 1.6 * on_all + widen_all, false, false);
+    if (prefix_len > 0 && S > 1) {
+      const long on_own =
+          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, &apart_split, &apart_splits) : 0;
+      take(2, 7.1 + 1.6 * (on_prefix + on_own) + 1.6 * join, false, true);
     }
+    const long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, &one_split, &one_splits);
+    take(3, 5.4 + 1.6 * on_all, false, false);
   }
   t.streamed = stream;
   if (!tile_prefix) t.prefix_split = t.prefix_splits = 0;
@@ -1053,8 +1046,6 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   }
   t.dense_parts = t.prefix_splits + t.seq_splits;
   if (t.dense_parts == 1 && !tile_prefix) t.dense_parts = 0;
-  t.pool_pages = c->num_pages;
-  t.wide_pages = codes && (tile_prefix || !stream);
   Carver k{base};
   if (stream) {
     const size_t workers = static_cast<size_t>(kStreamWarps) * sms;
@@ -1073,13 +1064,6 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     t.dense_o = k.take<float>(t.dense_parts * rows * 128);
     t.dense_st = k.take<PartStat>(t.dense_parts * rows);
   }
-  if (t.wide_pages) {
-    t.wide_own = stream ? 0 : static_cast<int>(own_pages);
-    const size_t pages = static_cast<size_t>(prefix_len / 16) + static_cast<size_t>(c->num_seqs) * t.wide_own;
-    t.pool_pages = static_cast<int>(std::max<size_t>(pages, 1));
-    t.wide_k = k.take<bf16>(static_cast<size_t>(t.pool_pages) * hkv * 16 * 128);
-    t.wide_v = k.take<bf16>(static_cast<size_t>(t.pool_pages) * hkv * 16 * 128);
-  }
   if (a != nullptr) *a = t;
   return k.off + 256;
 }
@@ -1088,32 +1072,20 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
 quail_status run_attention_shared(const quail_cache_desc* cache, const SharedAttnArgs& a, DeviceState* ds,
                                   cudaStream_t st) {
   quail_status s = QUAIL_OK;
-  const bool streamed = a.streamed;
-  if (a.wide_pages) CUDA_TRY(launch_cache_widen(a, st));
-  if (streamed) {
-    // before the tiles: these start on the SMs that it leaves first, and their
-    // parts, the larger ones, are still in L2 when the join reads them
-    CUtensorMap tK, tV;
-    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
-    for (int i = 0; i < 2; ++i) {
-      const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
-      CUtensorMap* m = i == 0 ? &tK : &tV;
-      s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
-      if (s != QUAIL_OK) return s;
-    }
-    CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
-  }
-  if (a.prefix_splits > 0 || !streamed) {
-    CUtensorMap tK, tV;
-    const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * cache->n_kv_heads * 16;
-    s = encode_2d_bf16(&tK, a.wide_pages ? a.wide_k : cache->k_pool, rows, 128, 128, 64, 16);
+  CUtensorMap tK, tV;
+  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+  for (int i = 0; i < 2; ++i) {
+    const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
+    CUtensorMap* m = i == 0 ? &tK : &tV;
+    s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
     if (s != QUAIL_OK) return s;
-    s = encode_2d_bf16(&tV, a.wide_pages ? a.wide_v : cache->v_pool, rows, 128, 128, 64, 16);
-    if (s != QUAIL_OK) return s;
-    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
-    if (!streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
   }
-  if (streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
+  // the streaming first: the prefix's tiles start on the SMs that it leaves first, and
+  // their parts, the larger ones, are still in L2 when the join reads them
+  if (a.streamed) CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
+  if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
+  if (!a.streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
+  if (a.streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
   return QUAIL_OK;
 }
 

@@ -326,39 +326,6 @@ __global__ void __launch_bounds__(kReadThreads, 5)
   }
 }
 
-// ------------------------------------------------------------------ widen
-// Block = one head of a page of the list (the prefix, then wide_own pages per
-// sequence): its K and V rows as bf16 for the tensor-core tiles. Exact, and small next to
-// their work: the tiles have 256 rows to multiply with every key.
-__global__ void __launch_bounds__(kReadThreads) cache_widen_kernel(SharedAttnArgs a) {
-  grid_dependency_wait();
-  const int pp = a.prefix_len / kPage, p = blockIdx.x;
-  int page;
-  if (p < pp) {
-    page = a.prefix_pages[p];
-  } else {
-    const int b = (p - pp) / a.wide_own, j = (p - pp) % a.wide_own;
-    const int len = a.seq_len[b];
-    if (len > a.max_seq_len || (pp + j) * kPage >= len) return;
-    page = a.c.table[static_cast<size_t>(b) * a.c.max_pages + pp + j];
-  }
-  if (page < 0 || page >= a.c.num_pages) {
-    if (threadIdx.x == 0) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, p);
-    return;  // the rows that read this page are void
-  }
-  // y: 32 rows of the page, K and V of one head (16 slots each)
-  const int l = threadIdx.x % kRowLanes, u = threadIdx.x / kRowLanes;
-  const int rows = a.c.hkv * kPage;
-  {
-    const bool is_k = u < kPage;
-    const int r = blockIdx.y * kPage + (is_k ? u : u - kPage);
-    const size_t at = static_cast<size_t>(page) * rows + r;
-    const uint4 w = load_codes(static_cast<const uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128, l);
-    const float sc = __uint_as_float(static_cast<uint32_t>((is_k ? a.c.k_scale : a.c.v_scale)[at]) << 23);
-    store_codes_bf16((is_k ? a.wide_k : a.wide_v) + (static_cast<size_t>(p) * rows + r) * 128, l, w, sc);
-  }
-}
-
 // ------------------------------------------------------------------ answer token
 // The answer token of a letters call: one normed row q | k | v for all documents.
 // answer_query_kernel turns its q by each document's length; answer_join_kernel
@@ -423,13 +390,6 @@ cudaError_t launch_answer_join(const float* qkv, const bf16* o, const float* lse
                                cudaStream_t st) {
   count_launch();
   return launch_pdl(answer_join_kernel, dim3((n * hq + 7) / 8), dim3(256), 0, st, qkv, o, lse, n * hq, hq, hq / hkv, out);
-}
-
-cudaError_t launch_cache_widen(const SharedAttnArgs& a, cudaStream_t st) {
-  const long long pages = a.prefix_len / kPage + static_cast<long long>(a.c.num_seqs) * a.wide_own;
-  if (pages <= 0) return cudaSuccess;
-  count_launch();
-  return launch_pdl(cache_widen_kernel, dim3(static_cast<unsigned>(pages), a.c.hkv), dim3(kReadThreads), 0, st, a);
 }
 
 namespace {

@@ -103,12 +103,6 @@ struct SharedAttnArgs {
   int dense_parts;
   float* dense_o;  // [dense_parts, total_q * hq, 128]
   PartStat* dense_st;
-  // The pool that the tiles read: the cache, or (codes) its pages widened to
-  // bf16 in list order, the prefix and then wide_own pages for every sequence.
-  bool wide_pages;
-  int wide_own, pool_pages;
-  __nv_bfloat16* wide_k;
-  __nv_bfloat16* wide_v;
 };
 
 constexpr int kTileRows = 256;  // query rows of a tensor-core CTA
@@ -123,8 +117,6 @@ cudaError_t launch_attention_prefix(const SharedAttnArgs& a, const CUtensorMap& 
                                     cudaStream_t st);
 cudaError_t launch_attention_sequences(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                        cudaStream_t st);
-// wide_k / wide_v from the prefix pages and, when wide_own > 0, every sequence's own.
-cudaError_t launch_cache_widen(const SharedAttnArgs& a, cudaStream_t st);
 cudaError_t set_pipeline_wait_limit_cache_attention(long long cycles);
 cudaError_t set_pipeline_wait_limit_cache_attention_tc(long long cycles);
 

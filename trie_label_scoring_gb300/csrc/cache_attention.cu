@@ -91,29 +91,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// Four e4m3 codes as two pairs of fp16.
-__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(v));
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 16 bytes to shared memory, and this thread's arrival on `bar` once its copies
-// have landed (counted in the barrier's expected arrivals).
-__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ float pow2_byte(uint32_t e) { return __uint_as_float(e << 23); }
-
 // A unit of the work list (a stage: UNIT pages, fewer at an item's end): unit j
 // of the n of an item. Items: (row tile, head) over the prefix, then (sequence,
 // head) over own pages.
@@ -183,7 +164,8 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
   constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit, kThreads = Cfg::kThreads, kRows = kItemRows;
   constexpr int kKeys = kUnit * kPage;  // keys of a unit
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // by an offset: from an address rounded up, the compiler could not tell shared memory
+  uint8_t* base = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = base + warp * kStages * Cfg::kStage;
   uint8_t* scales = base + Cfg::kRing + warp * kStages * kUnit * 32;

@@ -18,11 +18,14 @@
 // behind 2,048 (32 heads on 8): 380 us, 970 TFLOP/s. Few rows a sequence: bound
 // by the page copies, 1.6 us for 64 KB a CTA, 6.2 TB/s out of L2.
 //
-// Roles (384 threads): warps 0 and 3 load K and V pages into one ring K0 V0 K1
-// V1 .., warp 1 owns TMEM and issues the MMAs (a second issuer, one for each
+// Roles (384 threads, over codes 512): warps 0 and 3 load K and V pages into one ring
+// K0 V0 K1 V1 .., warp 1 owns TMEM and issues the MMAs (a second issuer, one for each
 // tile, let the tiles' MMAs interleave and was slower), warps 4-7 and 8-11 are the
 // softmax of tile 0 and 1, one thread per row (no exchange between threads),
-// which also load their Q rows and write their O rows.
+// which also load their Q rows and write their O rows. Over an e4m3 cache the loaders
+// fill a ring of codes (half the bytes) and warps 12-15 (with an empty second tile
+// 8-11 too) widen each block, times its rows' powers of two, into the ring of bf16
+// that the MMAs read: exact, so a code takes part as the bf16 value that it stands for.
 #include <atomic>
 
 #include "cache_attn.cuh"
@@ -32,28 +35,43 @@ namespace quail {
 
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kBlkKeys = 128;
 constexpr int kBlkPages = kBlkKeys / kPage;
-constexpr int kStages = 5;
 constexpr uint32_t kHalf = kBlkKeys * 128;  // 128 rows x 64 bf16, 128-byte rows, swizzled
 constexpr uint32_t kStage = 2 * kHalf;
 constexpr uint32_t kOffQ = 0;  // two tiles
 constexpr uint32_t kOffRing = 2 * kStage;
-constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
 constexpr uint32_t kTmemO = 256;
-// A block starts with 384 x 168 registers; the softmax keeps a whole row of S.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "the split draws on the launch's registers");
+constexpr int kSoftmaxRegs = 200;  // the softmax keeps a whole row of S
+
+template <bool CODES>
+struct TileCfg {
+  static constexpr int kThreads = CODES ? 512 : 384;
+  static constexpr int kStages = CODES ? 3 : 5;      // blocks of K or V that the MMAs read
+  static constexpr int kCodeStages = CODES ? 4 : 0;  // blocks of codes on their way
+  static constexpr uint32_t kCodeStage = kBlkKeys * 128;
+  static constexpr uint32_t kOffCodes = kOffRing + kStages * kStage;
+  static constexpr uint32_t kOffScales = kOffCodes + kCodeStages * kCodeStage;
+  static constexpr uint32_t kOffBar = kOffScales + kCodeStages * kBlkKeys;
+  // registers a thread: at launch, and of the warps beside the softmax's 256 threads
+  static constexpr int kLaunchRegs = CODES ? 128 : 168, kOtherRegs = CODES ? 56 : 104;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
+                "the split draws on the launch's registers");
+};
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[5], empty[5];
+  uint64_t code_full[4], code_empty[4];
   uint64_t s_full[2], p_full[2], pv_done[2], q_full, drain;
   uint32_t tmem_slot;
   int abort_flag;
 };
-constexpr size_t kSmem = 1024 + kOffBar + sizeof(Bars);
-static_assert(kSmem <= 227 * 1024, "shared memory");
+template <bool CODES>
+constexpr size_t tile_smem() {
+  constexpr size_t n = 1024 + TileCfg<CODES>::kOffBar + sizeof(Bars);
+  static_assert(n <= 227 * 1024, "shared memory");
+  return n;
+}
 
 // Starts the load of 32 columns; the registers hold them after tmem_ld_wait,
 // which names them so that no use can move ahead of it.
@@ -127,13 +145,99 @@ struct Item {
   int g, split;
 };
 
-template <bool PREFIX>
-__global__ void __launch_bounds__(kThreads, 1)
+// 16 codes times 2^(e - 127), as 16 bf16. A code's magnitude bits, moved to bits 4-10
+// of a bf16, are its value times 2^-120 (its subnormals too), so one product
+// with 2^(e - 7) finishes a pair: a byte permute that extends the signs, a product
+// by 16, a mask and a bf16 product, where the conversions fp16 -> fp32 -> bf16 took
+// three times as long. NaN codes and scales from 2^8 on go the long way.
+__device__ __forceinline__ void widen16(const uint4& x, uint32_t e, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[8], odd = 0;
+  const uint32_t m = (e + 120) << 7, m2 = m | m << 16;  // 2^(e - 7) as a bf16 pair
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    odd |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t y;  // bytes 2k and 2k + 1 as signed 16-bit numbers
+      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w[i]), "r"(k == 0 ? 0x9180 : 0xb3a2));
+      y = y * 16u & 0x87f087f0u;
+      const __nv_bfloat162 v =
+          __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&m2));
+      r[2 * i + k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  if ((odd & 0x80808080u) != 0 || e > 134) {
+    const float f = pow2_byte(e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[2];
+      widen4(w[i], h[0], h[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+        r[2 * i + k] = pack_bf16(v.x * f, v.y * f);
+      }
+    }
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// Blocks first, first + step, .. of the code ring (K0 V0 K1 V1 ..) into the ring that
+// the MMAs read; warp w of four takes 32 rows of each. Eight lanes to a row of 128
+// codes, 16 each: two 16-byte chunks of bf16. Lanes of a row's second half store
+// theirs in the other order, so that eight lanes always hit eight different chunks
+// of a row's 128 bytes.
+__device__ __forceinline__ void widen_blocks(uint8_t* base, Bars* bars, int w, int lane, int first, int step,
+                                             int n_blocks, int n_keys, long long limit_clk) {
+  using Cfg = TileCfg<true>;
+  volatile int* abort_flag = &bars->abort_flag;
+  const int c = lane & 7, half = c >> 2, ch = 2 * (c & 3) + half;
+  for (int idx = first; idx < 2 * n_blocks; idx += step) {
+    const int cs = idx % Cfg::kCodeStages, s = idx % Cfg::kStages, use = idx / Cfg::kStages;
+    const bool here =
+        wait_bar(&bars->code_full[cs], static_cast<uint32_t>((idx / Cfg::kCodeStages) & 1), abort_flag, limit_clk) &&
+        (use == 0 || wait_bar(&bars->empty[s], static_cast<uint32_t>((use - 1) & 1), abort_flag, limit_clk));
+    if (!__all_sync(0xffffffffu, here)) break;
+    const uint8_t* code = base + Cfg::kOffCodes + cs * Cfg::kCodeStage;
+    const uint8_t* exps = base + Cfg::kOffScales + cs * kBlkKeys;
+    uint8_t* dst = base + kOffRing + s * kStage + half * kHalf;
+    // value rows past the range are zeros, whatever their slots hold
+    const int rows = (idx & 1) ? n_keys - (idx >> 1) * kBlkKeys : kBlkKeys;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int row = 32 * w + 4 * i + (lane >> 3), sw = row & 7;
+      uint4 x = *reinterpret_cast<const uint4*>(code + row * 128 + ((c ^ sw) << 4));
+      uint32_t e = exps[row];
+      if (row >= rows) {
+        x = make_uint4(0u, 0u, 0u, 0u);
+        e = 127;
+      }
+      uint4 lo, hi;
+      widen16(x, e, lo, hi);
+      *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ sw) << 4)) = half ? hi : lo;
+      *reinterpret_cast<uint4*>(dst + row * 128 + (((ch ^ 1) ^ sw) << 4)) = half ? lo : hi;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&bars->code_empty[cs]);
+      mbar_arrive(&bars->full[s]);
+    }
+  }
+}
+
+template <bool PREFIX, bool CODES>
+__global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
     attention_tile_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV) {
+  using Cfg = TileCfg<CODES>;
+  constexpr int kThreads = Cfg::kThreads, kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Bars* bars = reinterpret_cast<Bars*>(base + kOffBar);
+  // by an offset: from an address rounded up, the compiler could not tell shared memory
+  uint8_t* base = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  Bars* bars = reinterpret_cast<Bars*>(base + Cfg::kOffBar);
   volatile int* abort_flag = &bars->abort_flag;
   const long long limit_clk = pipeline_wait_limit();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -191,11 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // copies: a warp's 32 rows, half a warp to a row of 256 bytes.
   const int t = (warp - 4) >> 2, quarter = warp & 3;  // tile and 32-row quarter of a softmax warp
   const int rr = it.row0 + t * 128 + quarter * 32 + lane;  // row of the item
-  const bool row_ok = warp >= 4 && rr < it.n_rows;
+  const bool softmax_warp = warp >= 4 && warp < 12;
+  const bool row_ok = softmax_warp && rr < it.n_rows;
   const size_t out_row =
       row_ok ? static_cast<size_t>(qr.lo + rr / G) * a.hq + it.g * G + rr % G : 0;  // (token, head)
   uint4 qx[16];
-  if (warp >= 4 && (t == 0 || two)) {
+  if (softmax_warp && (t == 0 || two)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = 2 * i + (lane >> 4);
@@ -207,8 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->full[s], CODES ? 4 : 1);  // the warps that widen, or the loader
       mbar_init(&bars->empty[s], 1);
+    }
+    for (int s = 0; s < Cfg::kCodeStages; ++s) {
+      mbar_init(&bars->code_full[s], 1 + kBlkPages);  // the loader, and its lanes' copies of exponents
+      mbar_init(&bars->code_empty[s], 4);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
@@ -230,19 +339,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = bars->tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kOtherRegs));
     if (warp == 0 || warp == 3) {
       // ---------------------------------------------- loaders (K: warp 0, V: warp 3)
       // Lane q takes page q of a block; the ids of the next block are read while
       // this one waits for its stage.
       const int kv = warp == 0 ? 0 : 1;
       const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
+      constexpr int kIn = CODES ? Cfg::kCodeStages : kStages;
+      uint64_t* full = CODES ? bars->code_full : bars->full;
+      uint64_t* empty = CODES ? bars->code_empty : bars->empty;
       const int p0 = it.k_lo / kPage, pp = a.prefix_len / kPage;
       auto page_id = [&](int blk) {
         const int p = p0 + blk * kBlkPages + lane;
         if (lane >= kBlkPages || blk * kBlkPages + lane >= n_pages) return -1;
-        // pages widened to bf16 lie in list order: the prefix, then each sequence's own
-        if (a.wide_pages) return p < pp ? p : pp + it.b * a.wide_own + (p - pp);
         return p < pp ? a.prefix_pages[p] : a.c.table[static_cast<size_t>(it.b) * a.c.max_pages + p];
       };
       int next = page_id(0), issued = 0;
@@ -250,37 +360,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         int page = next;
         if (blk + 1 < n_blocks) next = page_id(blk + 1);
         const bool mine = lane < min(kBlkPages, n_pages - blk * kBlkPages);
-        if (mine && (page < 0 || page >= a.pool_pages)) {
+        if (mine && (page < 0 || page >= a.c.num_pages)) {
           raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, PREFIX ? 0 : it.b);
           page = -1;  // not copied: the stage's old contents are consumed, the rows are void
         }
         const uint32_t good = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        const int idx = 2 * blk + kv, s = idx % kStages, use = idx / kStages;
-        if (use > 0 && !__all_sync(0xffffffffu, wait_bar(&bars->empty[s], static_cast<uint32_t>((use - 1) & 1), abort_flag, limit_clk)))
+        const int idx = 2 * blk + kv, s = idx % kIn, use = idx / kIn;
+        if (use > 0 && !__all_sync(0xffffffffu, wait_bar(&empty[s], static_cast<uint32_t>((use - 1) & 1), abort_flag, limit_clk)))
           break;
         if (lane == 0) {
           if (good > 0)
-            mbar_arrive_expect_tx(&bars->full[s], good * 2 * 2048);
+            mbar_arrive_expect_tx(&full[s], good * (CODES ? 2048 : 4096));
           else
-            mbar_arrive(&bars->full[s]);
+            mbar_arrive(&full[s]);
         }
         __syncwarp();
+        const int y = (page * a.c.hkv + it.g) * kPage;
         if (page >= 0) {
-          uint8_t* dst = base + kOffRing + s * kStage + lane * 2048;
-          const int y = (page * a.c.hkv + it.g) * kPage;
-          tma_load_2d(dst, tm, &bars->full[s], 0, y);
-          tma_load_2d(dst + kHalf, tm, &bars->full[s], 64, y);
+          if constexpr (CODES) {
+            tma_load_2d(base + Cfg::kOffCodes + s * Cfg::kCodeStage + lane * 2048, tm, &full[s], 0, y);
+            copy16_async(base + Cfg::kOffScales + s * kBlkKeys + lane * kPage,
+                         (kv == 0 ? a.c.k_scale : a.c.v_scale) + static_cast<size_t>(y));
+          } else {
+            uint8_t* dst = base + kOffRing + s * kStage + lane * 2048;
+            tma_load_2d(dst, tm, &full[s], 0, y);
+            tma_load_2d(dst + kHalf, tm, &full[s], 64, y);
+          }
         }
+        if (CODES && lane < kBlkPages) arrive_after_copies(&full[s]);
         ++issued;
       }
       // No copy may still be landing when the CTA exits: wait for this loader's last
-      // uses of the stages, but not for one that a later use has followed (the other
-      // loader filled the stage again only once it was consumed).
-      for (int blk = max(0, issued - 3); lane == 0 && blk < issued; ++blk) {
+      // uses of the stages, but not for one that a later use has followed (a stage is
+      // filled again only once it was consumed).
+      for (int blk = max(0, issued - (CODES ? 2 : 3)); lane == 0 && blk < issued; ++blk) {
         const int idx = 2 * blk + kv;
-        if (issued == n_blocks && idx + kStages < 2 * n_blocks) continue;
+        if (issued == n_blocks && idx + kIn < 2 * n_blocks) continue;
         const long long t0 = clock64();
-        while (!mbar_try_wait(smem_u32(&bars->full[idx % kStages]), static_cast<uint32_t>((idx / kStages) & 1))) {
+        while (!mbar_try_wait(smem_u32(&full[idx % kIn]), static_cast<uint32_t>((idx / kIn) & 1))) {
           if (clock64() - t0 > kWaitLimitCycles) {
             *abort_flag = 1;
             break;
@@ -351,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else {
+  } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------ softmax: thread <-> row of tile t
     const int r = quarter * 32 + lane;  // row of the tile = TMEM lane
@@ -368,9 +485,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_arrive(&bars->q_full);
     if (t == 0 || two) {
       const int limit = PREFIX || !row_ok ? it.k_hi : min(it.k_hi, row_limit(a, qr, rr));
+      // a warp without a row takes part in the waits and leaves its weights as they are
+      const bool live = it.row0 + t * 128 + quarter * 32 < it.n_rows;
       const float scale = a.scale_log2;
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
+      // Keys past the range (tail of the last page, pages not loaded): their V
+      // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
+      // Tile 0 does it for both: its product is issued first. (Codes are zeroed as
+      // they are widened.)
+      auto clear_tail = [&](int j, int key0) {
+        const int in_range = it.k_hi - key0;
+        if (CODES || t != 0 || in_range >= kBlkKeys) return true;
+        const int idx = 2 * j + 1;
+        if (!__all_sync(0xffffffffu, wait_bar(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag, limit_clk)))
+          return false;
+        uint8_t* v = base + kOffRing + (idx % kStages) * kStage;
+        for (int i = r; i < (kBlkKeys - in_range) * 16; i += 128) {
+          const int row = in_range + i / 16, c = i % 16;
+          *reinterpret_cast<uint4*>(v + (c / 8) * kHalf + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        return true;
+      };
 #pragma unroll 1
       for (int j = 0; j < n_blocks; ++j) {
         const uint32_t par = static_cast<uint32_t>(j & 1);
@@ -380,6 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
+        if (!live) {
+          if (!clear_tail(j, key0)) break;
+          mbar_arrive(&bars->p_full[t]);
+          continue;
+        }
         uint32_t su[4][32];
         const int valid = limit - key0;
         const bool border = __any_sync(0xffffffffu, valid < kBlkKeys);
@@ -462,22 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
           weights(0);
         }
-        // Keys past the range (tail of the last page, pages not loaded): their V
-        // rows are zeroed, so that what the slots hold cannot reach O as 0 * NaN.
-        // Tile 0 does it for both: its product is issued first.
-        const int in_range = it.k_hi - key0;
-        if (t == 0 && in_range < kBlkKeys) {
-          const int idx = 2 * j + 1;
-          if (!__all_sync(0xffffffffu, wait_bar(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag, limit_clk))) {
-            ok = false;
-            break;
-          }
-          uint8_t* v = base + kOffRing + (idx % kStages) * kStage;
-          for (int i = r; i < (kBlkKeys - in_range) * 16; i += 128) {
-            const int row = in_range + i / 16, c = i % 16;
-            *reinterpret_cast<uint4*>(v + (c / 8) * kHalf + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
+        if (!clear_tail(j, key0)) {
+          ok = false;
+          break;
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -492,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- rows out, through this tile's Q buffer (no MMA reads it any more):
       // a warp's 32 rows as whole 256-byte lines
-      if (ok && __all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag, limit_clk))) {
+      if (live && ok && __all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag, limit_clk))) {
         tc_fence_after();
         uint8_t* stage = q_tile + quarter * 8192;
         const bool final = a.dense_parts == 0;
@@ -560,6 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[out_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
         }
       }
+    } else if constexpr (CODES) {  // no rows: these warps take the values off the others
+      widen_blocks(base, bars, quarter, lane, 1, 2, n_blocks, it.k_hi - it.k_lo, limit_clk);
+    }
+  }
+
+  if constexpr (CODES) {
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kOtherRegs));
+      widen_blocks(base, bars, warp & 3, lane, 0, two ? 1 : 2, n_blocks, it.k_hi - it.k_lo, limit_clk);
     }
   }
 
@@ -573,10 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (behind_stream) grid_dependency_wait();
 }
 
-template <bool PREFIX>
+template <bool PREFIX, bool CODES>
 cudaError_t launch_tile(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, dim3 grid,
                         cudaStream_t st) {
-  auto kern = attention_tile_kernel<PREFIX>;
+  auto kern = attention_tile_kernel<PREFIX, CODES>;
+  using Cfg = TileCfg<CODES>;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -586,13 +725,13 @@ cudaError_t launch_tile(const SharedAttnArgs& a, const CUtensorMap& tmK, const C
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;  // the register split would not add up
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (attr.numRegs != Cfg::kLaunchRegs) return cudaErrorLaunchOutOfResources;  // the register split would not add up
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tile_smem<CODES>()));
     if (e != cudaSuccess) return e;
     configured[dev].store(true, std::memory_order_release);
   }
   count_launch();
-  return launch_pdl(kern, grid, dim3(kThreads), kSmem, st, a, tmK, tmV);
+  return launch_pdl(kern, grid, dim3(Cfg::kThreads), tile_smem<CODES>(), st, a, tmK, tmV);
 }
 
 }  // namespace
@@ -600,14 +739,15 @@ cudaError_t launch_tile(const SharedAttnArgs& a, const CUtensorMap& tmK, const C
 cudaError_t launch_attention_prefix(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     cudaStream_t st) {
   const long rows = static_cast<long>(a.total_q) * (a.hq / a.c.hkv);
-  return launch_tile<true>(a, tmK, tmV, dim3((rows + kTileRows - 1) / kTileRows, a.c.hkv, a.prefix_splits), st);
+  const dim3 grid((rows + kTileRows - 1) / kTileRows, a.c.hkv, a.prefix_splits);
+  return a.c.codes ? launch_tile<true, true>(a, tmK, tmV, grid, st) : launch_tile<true, false>(a, tmK, tmV, grid, st);
 }
 
 cudaError_t launch_attention_sequences(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                        cudaStream_t st) {
   const long rows = static_cast<long>(a.max_q) * (a.hq / a.c.hkv);
-  return launch_tile<false>(a, tmK, tmV,
-                            dim3((rows + kTileRows - 1) / kTileRows * a.seq_splits, a.c.hkv, a.c.num_seqs), st);
+  const dim3 grid((rows + kTileRows - 1) / kTileRows * a.seq_splits, a.c.hkv, a.c.num_seqs);
+  return a.c.codes ? launch_tile<false, true>(a, tmK, tmV, grid, st) : launch_tile<false, false>(a, tmK, tmV, grid, st);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.

@@ -47,6 +47,25 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
+// Four e4m3 codes as two pairs of fp16.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+// 16 bytes to shared memory, and this thread's arrival on `bar` once its copies
+// have landed (counted in the barrier's expected arrivals).
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float pow2_byte(uint32_t e) { return __uint_as_float(e << 23); }
+
 // Pages of sequence b's own keys that its queries read (0: none, or a bad sequence).
 __device__ __forceinline__ int own_pages(const SharedAttnArgs& a, int b) {
   const QueryRange r = query_range(a, b);
