@@ -145,50 +145,45 @@ struct Item {
   int g, split;
 };
 
-// 16 codes times 2^(e - 127), as 16 bf16. A code's magnitude bits, moved to bits 4-10
-// of a bf16, are its value times 2^-120 (its subnormals too), so one product
-// with 2^(e - 7) finishes a pair: a byte permute that extends the signs, a product
-// by 16, a mask and a bf16 product, where the conversions fp16 -> fp32 -> bf16 took
-// three times as long. NaN codes and scales from 2^8 on go the long way.
-__device__ __forceinline__ void widen16(const uint4& x, uint32_t e, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r[8], odd = 0;
-  const uint32_t m = (e + 120) << 7, m2 = m | m << 16;  // 2^(e - 7) as a bf16 pair
+// Eight codes times 2^(e - 127) as bf16. A code's magnitude bits, moved to bits 4-10
+// of a bf16, are its value times 2^-120 (its subnormals too), so one product with
+// m2 = (2^(e - 7), 2^(e - 7)) finishes a pair: a byte permute that extends the signs,
+// a product by 16, a mask and a bf16 product.
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t m2) {
+  const uint32_t w[2] = {a, b};
+  uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    odd |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t y;  // bytes 2k and 2k + 1 as signed 16-bit numbers
-      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w[i]), "r"(k == 0 ? 0x9180 : 0xb3a2));
-      y = y * 16u & 0x87f087f0u;
-      const __nv_bfloat162 v =
-          __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&m2));
-      r[2 * i + k] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+    uint32_t y;  // two bytes as signed 16-bit numbers
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(w[i >> 1]), "r"((i & 1) == 0 ? 0x9180 : 0xb3a2));
+    y = y * 16u & 0x87f087f0u;
+    const __nv_bfloat162 v =
+        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&m2));
+    r[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  if ((odd & 0x80808080u) != 0 || e > 134) {
-    const float f = pow2_byte(e);
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// The same for any code and e, NaN and scales from 2^8 on included, by conversions.
+__device__ __forceinline__ uint4 widen8_any(uint32_t a, uint32_t b, float f) {
+  uint32_t h[4], r[4];
+  widen4(a, h[0], h[1]);
+  widen4(b, h[2], h[3]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h[2];
-      widen4(w[i], h[0], h[1]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-        r[2 * i + k] = pack_bf16(v.x * f, v.y * f);
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    r[i] = pack_bf16(v.x * f, v.y * f);
   }
-  lo = make_uint4(r[0], r[1], r[2], r[3]);
-  hi = make_uint4(r[4], r[5], r[6], r[7]);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Blocks first, first + step, .. of the code ring (K0 V0 K1 V1 ..) into the ring that
 // the MMAs read; warp w of four takes 32 rows of each. Eight lanes to a row of 128
 // codes, 16 each: two 16-byte chunks of bf16. Lanes of a row's second half store
 // theirs in the other order, so that eight lanes always hit eight different chunks
-// of a row's 128 bytes.
+// of a row's 128 bytes. A warp whose rows hold a NaN or a large scale, or rows past
+// the range, does them again the long way: the loop that all others take has 60
+// instructions a row and no branch (2,400 clocks a block and warp with one, 1,750
+// without).
 __device__ __forceinline__ void widen_blocks(uint8_t* base, Bars* bars, int w, int lane, int first, int step,
                                              int n_blocks, int n_keys, long long limit_clk) {
   using Cfg = TileCfg<true>;
@@ -203,21 +198,32 @@ __device__ __forceinline__ void widen_blocks(uint8_t* base, Bars* bars, int w, i
     const uint8_t* code = base + Cfg::kOffCodes + cs * Cfg::kCodeStage;
     const uint8_t* exps = base + Cfg::kOffScales + cs * kBlkKeys;
     uint8_t* dst = base + kOffRing + s * kStage + half * kHalf;
-    // value rows past the range are zeros, whatever their slots hold
-    const int rows = (idx & 1) ? n_keys - (idx >> 1) * kBlkKeys : kBlkKeys;
+    uint32_t odd = 0;
+    auto row_of = [&](int i) { return 32 * w + 4 * i + (lane >> 3); };
 #pragma unroll 2
     for (int i = 0; i < 8; ++i) {
-      const int row = 32 * w + 4 * i + (lane >> 3), sw = row & 7;
-      uint4 x = *reinterpret_cast<const uint4*>(code + row * 128 + ((c ^ sw) << 4));
-      uint32_t e = exps[row];
-      if (row >= rows) {
-        x = make_uint4(0u, 0u, 0u, 0u);
-        e = 127;
+      const int row = row_of(i), sw = row & 7;
+      const uint4 x = *reinterpret_cast<const uint4*>(code + row * 128 + ((c ^ sw) << 4));
+      const uint32_t e = exps[row], m = (e + 120) << 7;
+      odd |= ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u);
+      odd |= ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
+      odd |= (e + 121) >> 1 & 0x80u;  // e > 134: 2^(e - 7) is no bf16
+      const uint32_t m2 = m | m << 16;
+      *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ sw) << 4)) = widen8(half ? x.z : x.x, half ? x.w : x.y, m2);
+      *reinterpret_cast<uint4*>(dst + row * 128 + (((ch ^ 1) ^ sw) << 4)) = widen8(half ? x.x : x.z, half ? x.y : x.w, m2);
+    }
+    // value rows past the range are zeros, whatever their slots hold
+    const int rows = (idx & 1) ? n_keys - (idx >> 1) * kBlkKeys : kBlkKeys;
+    if (__any_sync(0xffffffffu, (odd & 0x80808080u) != 0) || rows < 32 * (w + 1)) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const int row = row_of(i), sw = row & 7;
+        uint4 x = *reinterpret_cast<const uint4*>(code + row * 128 + ((c ^ sw) << 4));
+        const float f = row < rows ? pow2_byte(exps[row]) : 0.f;
+        if (row >= rows) x = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ sw) << 4)) = widen8_any(half ? x.z : x.x, half ? x.w : x.y, f);
+        *reinterpret_cast<uint4*>(dst + row * 128 + (((ch ^ 1) ^ sw) << 4)) = widen8_any(half ? x.x : x.z, half ? x.y : x.w, f);
       }
-      uint4 lo, hi;
-      widen16(x, e, lo, hi);
-      *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ sw) << 4)) = half ? hi : lo;
-      *reinterpret_cast<uint4*>(dst + row * 128 + (((ch ^ 1) ^ sw) << 4)) = half ? lo : hi;
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -444,9 +450,12 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
       }
       for (int j = 0; ok && j < n_blocks; ++j) {
         const bool more = j + 1 < n_blocks;
-        // the pages first: they are there long before the weights
-        ok = wait_full(2 * j + 1) && (!more || wait_full(2 * j + 2)) && issue_pv(0, j);
+        // the pages first: they are there long before the weights (widened ones may
+        // not be, and the next keys wait for this product to free their stage)
+        ok = wait_full(2 * j + 1) && (CODES || !more || wait_full(2 * j + 2)) && issue_pv(0, j) &&
+             (!CODES || !more || wait_full(2 * j + 2));
         if (!ok) break;
+        if (CODES) tc_fence_after();
         if (more) issue_s(0, j + 1);
         if (two) {
           ok = issue_pv(1, j);
