@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
   const int n_blocks = (n_pages + kBlkPages - 1) / kBlkPages;
 
   // Query rows of the softmax warps, on their way before the set-up and the page
-  // copies: a warp's 32 rows, half a warp to a row of 256 bytes.
+  // copies: a warp's 32 rows, half a warp to a row of 256 bytes. Rows past the last
+  // read the first one, and nothing reads theirs; asking for each row made the loads
+  // wait for one another, 7,000 clocks a CTA.
   const int t = (warp - 4) >> 2, quarter = warp & 3;  // tile and 32-row quarter of a softmax warp
   const int rr = it.row0 + t * 128 + quarter * 32 + lane;  // row of the item
   const bool softmax_warp = warp >= 4 && warp < 12;
@@ -311,8 +313,7 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
     for (int i = 0; i < 16; ++i) {
       const int row = 2 * i + (lane >> 4);
       const size_t src = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(out_row), row);
-      const bool in = it.row0 + t * 128 + quarter * 32 + row < it.n_rows;
-      qx[i] = in ? reinterpret_cast<const uint4*>(a.q + src * 128)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+      qx[i] = reinterpret_cast<const uint4*>(a.q + src * 128)[lane & 15];
     }
   }
 
