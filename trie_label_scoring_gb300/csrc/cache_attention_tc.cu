@@ -138,6 +138,14 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const float (&v)[
       : "memory");
 }
 
+// The tensor memory that warp 1 has taken, for it and the softmax warps.
+__device__ __forceinline__ uint32_t tmem_ready(const Bars* bars) {
+  tc_fence_before();
+  asm volatile("bar.sync 1, 288;" ::: "memory");
+  tc_fence_after();
+  return bars->tmem_slot;
+}
+
 struct Item {
   int row0, n_rows;  // this CTA's first row and the rows there are, per KV head
   int k_lo, k_hi;    // keys
@@ -254,9 +262,32 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
   // first, 20 to 30 us before its last. The wait then comes before the exit.
   const bool behind_stream = PREFIX && a.streamed;
   if (!behind_stream) grid_dependency_wait();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->full[s], CODES ? 4 : 1);  // the warps that widen, or the loader
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int s = 0; s < Cfg::kCodeStages; ++s) {
+      mbar_init(&bars->code_full[s], 1 + kBlkPages);  // the loader, and its lanes' copies of exponents
+      mbar_init(&bars->code_empty[s], 4);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 128);
+      mbar_init(&bars->pv_done[t], 1);
+    }
+    mbar_init(&bars->q_full, 256);
+    mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
 
   Item it;
   QueryRange qr{0, 0, 0, true};
+  int first_page = -1;  // of a loader's lane, asked for along with the lengths that say whether it is in range
   it.g = blockIdx.y;
   if constexpr (PREFIX) {
     it.b = -1;
@@ -265,11 +296,20 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
     it.split = blockIdx.z;
     it.k_lo = it.split * a.prefix_split;
     it.k_hi = min(a.prefix_len, it.k_lo + a.prefix_split);
+    if (warp < 4 && it.k_lo / kPage + lane < a.prefix_len / kPage) first_page = a.prefix_pages[it.k_lo / kPage + lane];
   } else {
     // the rows that see the most keys first
     it.b = blockIdx.z;
     it.split = blockIdx.x % a.seq_splits;
     it.row0 = (gridDim.x / a.seq_splits - 1 - blockIdx.x / a.seq_splits) * kTileRows;
+    it.k_lo = a.seq_begin + it.split * a.seq_split;
+    if (warp < 4) {
+      const int p = it.k_lo / kPage + lane;
+      if (p < a.prefix_len / kPage)
+        first_page = a.prefix_pages[p];
+      else if (p < a.c.max_pages)
+        first_page = a.c.table[static_cast<size_t>(it.b) * a.c.max_pages + p];
+    }
     qr = query_range(a, it.b);
     if (!qr.ok) {
       if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
@@ -289,7 +329,6 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
       }
       return;
     }
-    it.k_lo = a.seq_begin + it.split * a.seq_split;
     it.k_hi = min(tile_key_end(a, qr, it.row0), it.k_lo + a.seq_split);
     if (it.k_hi <= it.k_lo) return;
   }
@@ -297,8 +336,7 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
   const int n_pages = (it.k_hi - it.k_lo + kPage - 1) / kPage;
   const int n_blocks = (n_pages + kBlkPages - 1) / kBlkPages;
 
-  // Query rows of the softmax warps, on their way before the set-up and the page
-  // copies: a warp's 32 rows, half a warp to a row of 256 bytes. Rows past the last
+  // Query rows of the softmax warps: a warp's 32 rows, half a warp to a row of 256 bytes. Rows past the last
   // read the first one, and nothing reads theirs; asking for each row made the loads
   // wait for one another, 7,000 clocks a CTA.
   const int t = (warp - 4) >> 2, quarter = warp & 3;  // tile and 32-row quarter of a softmax warp
@@ -317,34 +355,6 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
     }
   }
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->full[s], CODES ? 4 : 1);  // the warps that widen, or the loader
-      mbar_init(&bars->empty[s], 1);
-    }
-    for (int s = 0; s < Cfg::kCodeStages; ++s) {
-      mbar_init(&bars->code_full[s], 1 + kBlkPages);  // the loader, and its lanes' copies of exponents
-      mbar_init(&bars->code_empty[s], 4);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], 128);
-      mbar_init(&bars->pv_done[t], 1);
-    }
-    mbar_init(&bars->q_full, 256);
-    mbar_init(&bars->drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(&bars->tmem_slot, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = bars->tmem_slot;
-
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kOtherRegs));
     if (warp == 0 || warp == 3) {
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
         if (lane >= kBlkPages || blk * kBlkPages + lane >= n_pages) return -1;
         return p < pp ? a.prefix_pages[p] : a.c.table[static_cast<size_t>(it.b) * a.c.max_pages + p];
       };
-      int next = page_id(0), issued = 0;
+      int next = lane < min(kBlkPages, n_pages) ? first_page : -1, issued = 0;
       for (int blk = 0; blk < n_blocks; ++blk) {
         int page = next;
         if (blk + 1 < n_blocks) next = page_id(blk + 1);
@@ -411,70 +421,75 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
           }
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------- MMA issuer
-      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, kBlkKeys);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16_f32_bmn(128, 128);
-      const uint64_t dq = smem_desc_sw128(smem_u32(base + kOffQ));
-      const uint64_t dk = smem_desc_sw128(smem_u32(base + kOffRing));
-      const uint64_t dv = smem_desc_sw128_mn(smem_u32(base + kOffRing), kHalf, 1024);
-      const uint32_t dv_lo = static_cast<uint32_t>(dv), dv_hi = static_cast<uint32_t>(dv >> 32);
-      auto wait_full = [&](int idx) {
-        return wait_bar(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag, limit_clk);
-      };
-      auto issue_s = [&](int t, int j) {
-        const uint64_t k = dk + (((2 * j) % kStages * kStage) >> 4), q = dq + ((t * kStage) >> 4);
+      tmem_alloc(&bars->tmem_slot, 512);
+      tmem_relinquish();
+      const uint32_t tmem_base = tmem_ready(bars);
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, kBlkKeys);
+        constexpr uint32_t idesc_pv = umma_idesc_bf16_f32_bmn(128, 128);
+        const uint64_t dq = smem_desc_sw128(smem_u32(base + kOffQ));
+        const uint64_t dk = smem_desc_sw128(smem_u32(base + kOffRing));
+        const uint64_t dv = smem_desc_sw128_mn(smem_u32(base + kOffRing), kHalf, 1024);
+        const uint32_t dv_lo = static_cast<uint32_t>(dv), dv_hi = static_cast<uint32_t>(dv >> 32);
+        auto wait_full = [&](int idx) {
+          return wait_bar(&bars->full[idx % kStages], static_cast<uint32_t>((idx / kStages) & 1), abort_flag, limit_clk);
+        };
+        auto issue_s = [&](int t, int j) {
+          const uint64_t k = dk + (((2 * j) % kStages * kStage) >> 4), q = dq + ((t * kStage) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-          umma_bf16(tmem_base + t * 128, q + off, k + off, idesc_s, ks != 0 ? 1u : 0u);
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+            umma_bf16(tmem_base + t * 128, q + off, k + off, idesc_s, ks != 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->s_full[t]);
+        };
+        auto issue_pv = [&](int t, int j) {
+          const uint32_t v = dv_lo + (((2 * j + 1) % kStages * kStage) >> 4);
+          if (!wait_bar(&bars->p_full[t], static_cast<uint32_t>(j & 1), abort_flag, limit_clk)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // 16 keys = one page per instruction
+            umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->pv_done[t]);
+          return true;
+        };
+        bool ok = wait_bar(&bars->q_full, 0u, abort_flag, limit_clk) && wait_full(0);
+        if (ok) {
+          tc_fence_after();
+          issue_s(0, 0);
+          if (two) issue_s(1, 0);
+          umma_commit(&bars->empty[0]);
         }
-        umma_commit(&bars->s_full[t]);
-      };
-      auto issue_pv = [&](int t, int j) {
-        const uint32_t v = dv_lo + (((2 * j + 1) % kStages * kStage) >> 4);
-        if (!wait_bar(&bars->p_full[t], static_cast<uint32_t>(j & 1), abort_flag, limit_clk)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)  // 16 keys = one page per instruction
-          umma_ts(tmem_base + kTmemO + t * 128, tmem_base + t * 128 + kk * 8, v + ((kk * 2048) >> 4), dv_hi, idesc_pv,
-                  (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&bars->pv_done[t]);
-        return true;
-      };
-      bool ok = wait_bar(&bars->q_full, 0u, abort_flag, limit_clk) && wait_full(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0, 0);
-        if (two) issue_s(1, 0);
-        umma_commit(&bars->empty[0]);
-      }
-      for (int j = 0; ok && j < n_blocks; ++j) {
-        const bool more = j + 1 < n_blocks;
-        // the pages first: they are there long before the weights (widened ones may
-        // not be, and the next keys wait for this product to free their stage)
-        ok = wait_full(2 * j + 1) && (CODES || !more || wait_full(2 * j + 2)) && issue_pv(0, j) &&
-             (!CODES || !more || wait_full(2 * j + 2));
-        if (!ok) break;
-        if (CODES) tc_fence_after();
-        if (more) issue_s(0, j + 1);
-        if (two) {
-          ok = issue_pv(1, j);
+        for (int j = 0; ok && j < n_blocks; ++j) {
+          const bool more = j + 1 < n_blocks;
+          // the pages first: they are there long before the weights (widened ones may
+          // not be, and the next keys wait for this product to free their stage)
+          ok = wait_full(2 * j + 1) && (CODES || !more || wait_full(2 * j + 2)) && issue_pv(0, j) &&
+               (!CODES || !more || wait_full(2 * j + 2));
           if (!ok) break;
+          if (CODES) tc_fence_after();
+          if (more) issue_s(0, j + 1);
+          if (two) {
+            ok = issue_pv(1, j);
+            if (!ok) break;
+          }
+          umma_commit(&bars->empty[(2 * j + 1) % kStages]);
+          if (more) {
+            if (two) issue_s(1, j + 1);
+            umma_commit(&bars->empty[(2 * j + 2) % kStages]);
+          }
         }
-        umma_commit(&bars->empty[(2 * j + 1) % kStages]);
-        if (more) {
-          if (two) issue_s(1, j + 1);
-          umma_commit(&bars->empty[(2 * j + 2) % kStages]);
-        }
-      }
-      // every MMA of this thread completes before TMEM is released
-      umma_commit(&bars->drain);
-      const long long t0 = clock64();
-      while (!mbar_try_wait(smem_u32(&bars->drain), 0u)) {
-        if (clock64() - t0 > kWaitLimitCycles) {
-          *abort_flag = 1;
-          break;
+        // every MMA of this thread completes before TMEM is released
+        umma_commit(&bars->drain);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(smem_u32(&bars->drain), 0u)) {
+          if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            break;
+          }
         }
       }
     }
@@ -482,7 +497,6 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------ softmax: thread <-> row of tile t
     const int r = quarter * 32 + lane;  // row of the tile = TMEM lane
-    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     uint8_t* q_tile = base + kOffQ + t * kStage;
     if (t == 0 || two) {
 #pragma unroll
@@ -493,6 +507,8 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
       fence_proxy_async_smem();
     }
     mbar_arrive(&bars->q_full);
+    const uint32_t tmem_base = tmem_ready(bars);
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     if (t == 0 || two) {
       const int limit = PREFIX || !row_ok ? it.k_hi : min(it.k_hi, row_limit(a, qr, rr));
       // a warp without a row takes part in the waits and leaves its weights as they are
@@ -715,7 +731,7 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(bars->tmem_slot, 512);
   }
   if (threadIdx.x == 0 && *abort_flag) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 5000);
   if (behind_stream) grid_dependency_wait();
