@@ -973,26 +973,26 @@ std::atomic<int> g_attention_way{-1};
 // time) or multiplied on tiles of 256 rows; the
 // prefix is streamed, multiplied on tiles that take the rows of all sequences, or
 // a part of every sequence's own keys. The least estimate is taken, in us:
-//   tiles     1.5 per 128 keys of a CTA with up to 128 rows, 1.9 with more (e4m3 1.9,
-//             2.3), 10% more behind the streaming, and 4 blocks' worth to begin and end
-//   streaming the larger of reading pages, 1.3 (e4m3 0.73) per 1000 pages and heads,
-//             and of multiplying them, 0.86 (0.57) per 1000 and 8 rows
-//   parts     0.95 (streamed) or 1.1 per 1000 rows and heads written and joined
-//   launches  5 one pass, 9.4 two on tiles, 12 stream and tiles, 15 stream alone
+//   tiles     1.4 per 128 keys of a CTA with up to 128 rows, 1.75 with more (e4m3 1.8,
+//             2.15), 18% more behind the streaming, and 4 blocks' worth to begin and end
+//   streaming the larger of reading pages, 1.29 (e4m3 0.72) per 1000 pages and heads,
+//             and of multiplying them, 0.85 (0.57) per 1000 and 8 rows
+//   parts     0.95 per 1000 rows and heads written and joined
+//   launches  6.2 one pass, 7.7 two on tiles, 11.8 stream and tiles, 15.2 stream alone
 // (the constants fitted to 3,200 sizes, each timed in every way: 1 to 256 sequences
 // of 1 to 100 queries, 1 to 8 heads a group, prefixes to 32,768, own keys to 6,000,
-// both types; the way it takes costs 0.9% more than the fastest on the mean over
+// both types; the way it takes costs 1% more than the fastest on the mean over
 // them.) Measured, 32 heads on 8, us, streamed / streamed + prefix on tiles / tiles
 // apart / one pass:
-//   bf16 256 x 1 query  prefix  2048,  300 own keys  127 /  89 / 179 / 441
-//   bf16  64 x 1        prefix   512, 1500 own keys   79 /  87 / 120 / 114
-//   bf16  16 x 4        prefix  8192, 1500 own keys  110 /  63 /  59 / 122
-//   bf16  64 x 8        prefix  2048, 6000 own keys    - / 943 / 351 / 388
-//   bf16  16 x 16       prefix  2048,   48 own keys    - /  40 /  40 /  32
-//   e4m3   4 x 1        prefix 32768,  300 own keys   34 /  52 /  54 / 132
-//   e4m3  64 x 6        prefix  2048, 1500 own keys  187 / 129 / 177 / 271
-//   e4m3  64 x 6        prefix  8192, 6000 own keys  665 / 448 / 469 / 839
-//   e4m3  16 x 4        prefix   512,   48 own keys   25 /  30 /  32 /  18
+//   bf16 256 x 1 query  prefix  2048,  300 own keys  127 /  86 / 164 / 431
+//   bf16  64 x 1        prefix   512, 1500 own keys   80 /  83 / 113 / 111
+//   bf16  16 x 4        prefix  8192, 1500 own keys  110 /  60 /  55 / 115
+//   bf16  64 x 8        prefix  2048, 6000 own keys    - / 940 / 330 / 371
+//   bf16  16 x 16       prefix  2048,   48 own keys    - /  38 /  35 /  31
+//   e4m3   4 x 1        prefix 32768,  300 own keys   35 /  50 /  50 / 130
+//   e4m3  64 x 6        prefix  2048, 1500 own keys  187 / 125 / 160 / 242
+//   e4m3  64 x 6        prefix  8192, 6000 own keys  666 / 443 / 439 / 812
+//   e4m3  16 x 4        prefix   512,   48 own keys   25 /  30 /  30 /  17
 size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
                       int prefix_len, SharedAttnArgs* a) {
   const int hkv = c->n_kv_heads, G = hq / hkv, sms = planning_sms(), S = c->num_seqs;
@@ -1007,14 +1007,14 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   int apart_split = 0, apart_splits = 0, one_split = 0, one_splits = 0;
   {
     const long seq_ctas = (seq_rows + kTileRows - 1) / kTileRows * hkv * S;
-    const double thousand = hkv * 1e-3, k_read = codes ? 0.73 : 1.3, k_pass = codes ? 0.57 : 0.86;
-    const double k_tile = (codes ? 1.9 : 1.5) + (seq_rows > 128 ? 0.4 : 0.);
-    const double k_tile_all = (codes ? 1.9 : 1.5) + (all_rows > 128 ? 0.4 : 0.);
+    const double thousand = hkv * 1e-3, k_read = codes ? 0.72 : 1.29, k_pass = codes ? 0.57 : 0.85;
+    const double k_tile = (codes ? 1.8 : 1.4) + (seq_rows > 128 ? 0.35 : 0.);
+    const double k_tile_all = (codes ? 1.8 : 1.4) + (all_rows > 128 ? 0.35 : 0.);
     const double passes = std::min<double>(static_cast<double>(S) * ((seq_rows + 7) / 8), all_rows / 8. + S) * thousand;
     const double read = static_cast<double>(S) * own_pages * thousand * k_read, pass = passes * own_pages * k_pass;
-    const double join = all_rows * thousand;
+    const double join = 0.95 * all_rows * thousand;
     const int forced = g_attention_way.load(std::memory_order_relaxed);
-    double best = forced == 0 ? -1. : 15. + (prefix_len > 0 ? 0.95 * join : 0.) +
+    double best = forced == 0 ? -1. : 15.2 + (prefix_len > 0 ? join : 0.) +
                   std::max(read + prefix_pages * thousand * k_read,
                            pass + (all_rows + 7) / 8 * thousand * prefix_pages * k_pass);
     const auto take = [&](int way, double us, bool s, bool p) {
@@ -1029,15 +1029,15 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     if (prefix_len > 0) {
       on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms,
                                     &t.prefix_split, &t.prefix_splits);
-      take(1, 12. + std::max(read, pass) + 1.1 * k_tile_all * on_prefix + 1.1 * join, true, true);
+      take(1, 11.8 + std::max(read, pass) + 1.18 * k_tile_all * on_prefix + join, true, true);
     }
     if (prefix_len > 0 && S > 1) {
       const long on_own =
           own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, &apart_split, &apart_splits) : 0;
-      take(2, 9.4 + k_tile_all * on_prefix + k_tile * on_own + 1.1 * join, false, true);
+      take(2, 7.7 + k_tile_all * on_prefix + k_tile * on_own + join, false, true);
     }
     const long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, &one_split, &one_splits);
-    take(3, 5. + k_tile * on_all, false, false);
+    take(3, 6.2 + k_tile * on_all, false, false);
   }
   t.streamed = stream;
   if (!tile_prefix) t.prefix_split = t.prefix_splits = 0;
