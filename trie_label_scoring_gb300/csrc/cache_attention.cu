@@ -22,7 +22,7 @@ namespace {
 // with a private ring of pages, and the work list (all pages of all sequences
 // and KV heads, in order) is cut into equal contiguous chunks, one per worker,
 // whatever the lengths are. A worker's lane 0 issues the TMA copies of a page
-// STAGES pages ahead, across the borders of work items, so the stream of loads
+// two stages ahead, across the borders of work items, so the stream of loads
 // never drains; no barrier joins warps. Pieces of an item that several workers
 // share are joined by the second kernel.
 //
@@ -39,6 +39,12 @@ namespace {
 // The key's power of two multiplies its score, the value's is added to the
 // exponent of its weight: o and l keep separate maxima, so that value rows of any
 // scale neither overflow P nor starve the sum.
+//
+// Bound, with up to 8 rows, by HBM: 64 sequences of 2,048 own keys (8 KV heads, bf16)
+// take 90 us, 6.0 TB/s; e4m3, 4,096 keys, 97 us, 5.7 TB/s. With more rows by the page
+// copies out of L2: a box of 2 KB costs an SM 74 clocks, and a pass of 8 rows over an
+// e4m3 page (two boxes) 166. Taking the units' maxima only when some weight would
+// pass 2^8, without their shuffles, changed nothing.
 template <bool CODES>
 struct StreamCfg {
   static constexpr int kWarps = kStreamWarps;
@@ -664,7 +670,8 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
 // Bound by latency: dependent reads (lengths, plan, parts), and the fetching of
 // its instructions after hundreds of megabytes of keys have passed through L2.
 // So it is short: lane i finds part i and reads its statistics, all at once, and
-// one small loop adds the parts up.
+// one small loop adds the parts up. 8,192 rows of five parts: 10 us (12.4 with four
+// rows to a warp, one after the other).
 __device__ __forceinline__ float pow2_or_0(float x, float ref) {  // 2^(x - ref); 0 where nothing was seen
   return x == -INFINITY ? 0.f : exp2f(x - ref);
 }
@@ -740,7 +747,7 @@ __device__ __forceinline__ void pieces(long long u, int n, long long chunk, uint
 }
 
 // PER_ROW: the block's WARPS warps share row blockIdx.x = token * hq + head, else
-// they share the heads of token blockIdx.x.
+// each has a row, heads 8 blockIdx.y .. of token blockIdx.x.
 template <bool PER_ROW, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnArgs a) {
   grid_dependency_wait();
@@ -772,7 +779,7 @@ __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnAr
     tiles = own_items(a, b) / a.c.hkv;
   }
   const int pu = (a.prefix_len / kPage + unit - 1) / unit;
-  for (int h = PER_ROW ? blockIdx.x % a.hq : warp; h < a.hq; h += PER_ROW ? a.hq : WARPS) {
+  for (int h = PER_ROW ? blockIdx.x % a.hq : blockIdx.y * WARPS + warp; h < a.hq; h += a.hq) {
     const int g = h / G;
     const size_t row = static_cast<size_t>(t) * a.hq + h;
     Parts p{};
@@ -882,12 +889,15 @@ cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& 
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.total_q) * a.hq;
   count_launch();
-  // few rows have many parts: a streamed row up to all workers over the KV heads
+  // Few rows have many parts (a streamed row up to all workers over the KV heads) and
+  // leave SMs idle. Warps a row 16 / 4 / 1, us: 32 rows 13 / 23 / 46, 512 rows
+  // 20 / 15 / 16, 1,024 rows 18 / 6.6 / 7.1, 2,048 rows 33 / 10 / 7.7, 8,192 rows
+  // 103 / 30 / 10.
   if (rows <= num_sms)
     return launch_pdl(attention_join_kernel<true, 16>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, a);
-  if (rows <= 16LL * num_sms)
+  if (rows <= 8LL * num_sms)
     return launch_pdl(attention_join_kernel<true, 4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
-  return launch_pdl(attention_join_kernel<false, 8>, dim3(a.total_q), dim3(256), 0, st, a);
+  return launch_pdl(attention_join_kernel<false, 8>, dim3(a.total_q, (a.hq + 7) / 8), dim3(256), 0, st, a);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.
