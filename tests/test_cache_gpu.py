@@ -480,6 +480,70 @@ def test_attention_nan_and_infinity_stay_in_their_rows(way):
     assert torch.equal(out[~bad], ref[~bad])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("prefix", [0, 64])
+def test_attention_nan_in_the_cache_stays_in_its_rows(kind, nq, prefix, way):
+    """A NaN value reaches its own dimension of its sequence's rows, a NaN key all of them; nothing else changes."""
+    lens = [prefix + 90, prefix + 300, prefix + 49]
+    pool = Pool(kind, 2, lens, prefix)
+    pool.fill(lens)
+    q = torch.randn((3 * nq, 8, D), device="cuda").bfloat16()
+    offs = None if nq == 1 else [0, nq, 2 * nq, 3 * nq]
+    good, lse = attend(pool, q, offs, lens, prefix, False)
+    at = prefix + 137
+    nan = float("nan") if kind == "bf16" else 0xFF
+    page = int(pool.table[1, at // PAGE])
+    mine = torch.zeros(good.shape, dtype=torch.bool, device="cuda")
+    keep = pool.v[page, 1, at % PAGE, 71].clone()
+    pool.v[page, 1, at % PAGE, 71] = nan
+    out, z = attend(pool, q, offs, lens, prefix, False)
+    mine[nq:2 * nq, 4:, 71] = True
+    assert bool(out[mine].isnan().all()) and torch.equal(out[~mine], good[~mine]) and torch.equal(z, lse)
+    pool.v[page, 1, at % PAGE, 71] = keep
+    pool.k[page, 1, at % PAGE, 3] = nan
+    out, z = attend(pool, q, offs, lens, prefix, False)
+    mine[nq:2 * nq, 4:] = True
+    assert bool(out[mine].isnan().all()) and torch.equal(out[~mine], good[~mine])
+    assert bool(z[mine[..., 0]].isnan().all()) and torch.equal(z[~mine[..., 0]], lse[~mine[..., 0]])
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_takes_every_e4m3_code(nq, way):
+    """All 254 finite codes among keys and values, keys' scales from 2^-30 to 2^-9, values' from 2^-60 to 2^60. Streamed
+    weights times the values' scales are fp16: below 2^-14 they round by at most 2^-25 of the largest one's step to 1."""
+    lens = [254, 254]
+    pool = Pool("e4m3", 2, lens)
+    pool.fill(lens)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    codes = torch.tensor([c for c in range(256) if c & 127 != 127], dtype=torch.uint8, device="cuda")
+    for i in range(2):
+        for j in range(254):
+            page = int(pool.table[i, j // PAGE])
+            pool.v[page, :, j % PAGE] = codes[(torch.arange(D, device="cuda") + j) % 254]
+            pool.k[page, :, j % PAGE] = codes[(torch.arange(D, device="cuda") * 3 + j) % 254]
+    pool.ks.copy_(torch.randint(97, 119, pool.ks.shape, generator=g, device="cuda").to(torch.uint8))
+    pool.vs.copy_(torch.randint(67, 188, pool.vs.shape, generator=g, device="cuda").to(torch.uint8))
+    q = torch.randn((2 * nq, 8, D), generator=g, device="cuda").bfloat16()
+    offs = [0, nq, 2 * nq]
+    out, lse = attend(pool, q, None if nq == 1 else offs, lens, 0, True)
+    o, z, tol_o, tol_l = attention_64(pool, q, offs, lens, 0, True, D ** -0.5)
+    pos = torch.arange(254, device="cuda", dtype=torch.int32)
+    for b in range(2):
+        seq = torch.full_like(pos, b)
+        k, v = pool.rows(seq, pos, "k"), pool.rows(seq, pos, "v")
+        ve = torch.exp2(pool.vs[pool.table[b, pos.long() // PAGE].long(), :, pos.long() % PAGE].double() - 127)  # [n, hkv]
+        x = q[b * nq:(b + 1) * nq].double().reshape(nq, 2, 4, D)
+        sc = torch.einsum("qhgd,khd->qhgk", x, k) * D ** -0.5
+        i = torch.arange(nq, device="cuda")[:, None]
+        sc = sc.masked_fill((pos[None, :] > 254 - nq + i)[:, None, None, :], float("-inf"))
+        top = (torch.softmax(sc, -1) * ve.T[None, :, None, :]).amax(-1)  # [q, hkv, G]
+        size = (v.abs() / ve[..., None]).sum(0)  # sum of |code| [hkv, D]
+        tol_o[b * nq:(b + 1) * nq] += (2.0 ** -25 * top[..., None] * size[None, :, None, :]).reshape(nq, 8, D)
+    assert bool(((out.double() - o).abs() <= tol_o).all())
+    assert bool(((lse.double() - z).abs() <= tol_l).all())
+
+
 def test_attention_large_pool_offsets():
     """Page ids whose byte and element offsets pass 32 bits."""
     for kind in ("bf16", "e4m3"):

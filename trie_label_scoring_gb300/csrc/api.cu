@@ -2050,8 +2050,7 @@ quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* toke
 size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
-  const size_t n = plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
-  return n;
+  return plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
 }
 
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
@@ -2126,6 +2125,8 @@ quail_status quail_classify_letters_cached(const quail_model_desc* model, const 
   if (s != QUAIL_OK) return s;
   const int N = cache->num_seqs;
   if (max_doc_len <= 0) return fail(QUAIL_ERR_INVALID_ARG, "bad max_doc_len");
+  if (max_doc_len >= (1 << 24))
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "rotation is exact for positions below 2^24 only");
   if (N == 0) return QUAIL_OK;
   s = check_attention_shape(cache, model->n_q_heads, N, 1, max_doc_len, prefix_len);
   if (s != QUAIL_OK) return s;

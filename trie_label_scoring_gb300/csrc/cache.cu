@@ -406,7 +406,7 @@ cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t st) {
   // (48 heads, bf16; e4m3 9.8 / 10.1 at 608, 12.7 / 11.7 at 800).
   if (a.num_tokens <= 4 * num_sms)
     return launch_pdl(cache_append_kernel<T, 1>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt);
-  return launch_pdl(cache_append_kernel<T, 4>, dim3((a.num_tokens + 3) / 4), dim3(kAppendThreads), 0, st, a, rt);
+  return launch_pdl(cache_append_kernel<T, 4>, dim3((a.num_tokens - 1) / 4 + 1), dim3(kAppendThreads), 0, st, a, rt);
 }
 
 }  // namespace
