@@ -383,11 +383,26 @@ __global__ void __launch_bounds__(256) answer_join_kernel(const float* qkv, cons
   *reinterpret_cast<uint2*>(row + hq * 128) = lo;
 }
 
+// theta^(-2j/128) for all j from one power: in 64 bits the products are off by at
+// most j 2^-53, less than the two floats hold, and 64 powers a call took the host
+// longer than the launch.
+RopeTable angle_table(float theta) {
+  RopeTable t;
+  const double step = std::pow(static_cast<double>(theta), -1.0 / 64.0);
+  double w = 1.0;
+  for (float2& x : t.w) {
+    x.x = static_cast<float>(w);
+    x.y = static_cast<float>(w - static_cast<double>(x.x));
+    w *= step;
+  }
+  return t;
+}
+
 }  // namespace
 
 cudaError_t launch_answer_query(const float* qkv, const int* len, int n, int hq, float theta, bf16* q, cudaStream_t st) {
   count_launch();
-  return launch_pdl(answer_query_kernel, dim3(n), dim3(256), 0, st, qkv, len, hq, q, make_rope_table(theta));
+  return launch_pdl(answer_query_kernel, dim3(n), dim3(256), 0, st, qkv, len, hq, q, angle_table(theta));
 }
 
 cudaError_t launch_answer_join(const float* qkv, const bf16* o, const float* lse, int n, int hq, int hkv, bf16* out,
@@ -400,7 +415,7 @@ namespace {
 
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const RopeTable rt = a.theta > 0.f ? make_rope_table(a.theta) : RopeTable{};
+  const RopeTable rt = a.theta > 0.f ? angle_table(a.theta) : RopeTable{};
   // Few tokens: a block each, so that they spread over the SMs. One / four a block, us:
   // 4 tokens 3.2 / 5.5, 256 3.9 / 5.7, 608 5.0 / 5.8, 800 7.7 / 7.4, 1,216 8.7 / 7.6
   // (48 heads, bf16; e4m3 9.8 / 10.1 at 608, 12.7 / 11.7 at 800).
