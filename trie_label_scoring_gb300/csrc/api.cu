@@ -1077,20 +1077,21 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
 // The launches of one attention call: a filled in, its plan included.
 quail_status run_attention_shared(const quail_cache_desc* cache, const SharedAttnArgs& a, DeviceState* ds,
                                   cudaStream_t st) {
-  quail_status s = QUAIL_OK;
-  CUtensorMap tK, tV;
-  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
-  for (int i = 0; i < 2; ++i) {
-    const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
-    CUtensorMap* m = i == 0 ? &tK : &tV;
-    s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
-    if (s != QUAIL_OK) return s;
-  }
   // the streaming first: the prefix's tiles start on the SMs that it leaves first, and
   // their parts, the larger ones, are still in L2 when the join reads them
-  if (a.streamed) CUDA_TRY(launch_attention_stream(a, tK, tV, ds->num_sms, st));
-  if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
-  if (!a.streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
+  if (a.streamed) CUDA_TRY(launch_attention_stream(a, ds->num_sms, st));
+  if (a.prefix_splits > 0 || !a.streamed) {
+    CUtensorMap tK, tV;
+    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+    for (int i = 0; i < 2; ++i) {
+      const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
+      CUtensorMap* m = i == 0 ? &tK : &tV;
+      const quail_status s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
+      if (s != QUAIL_OK) return s;
+    }
+    if (a.prefix_splits > 0) CUDA_TRY(launch_attention_prefix(a, tK, tV, st));
+    if (!a.streamed) CUDA_TRY(launch_attention_sequences(a, tK, tV, st));
+  }
   if (a.streamed || a.dense_parts > 0) CUDA_TRY(launch_attention_join(a, ds->num_sms, st));
   return QUAIL_OK;
 }

@@ -110,8 +110,7 @@ constexpr int kItemRows = 8;       // query rows of a streaming work item
 constexpr int kStreamWarps = 12;   // streaming workers of an SM
 // Pages that a streaming worker takes at a time.
 __host__ __device__ constexpr int stream_unit_pages(bool codes) { return codes ? 2 : 1; }
-cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                    int num_sms, cudaStream_t st);
+cudaError_t launch_attention_stream(const SharedAttnArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_attention_prefix(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     cudaStream_t st);

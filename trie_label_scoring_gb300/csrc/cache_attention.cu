@@ -21,9 +21,10 @@ namespace {
 // reading keys and values once: every warp of the grid is a worker of its own
 // with a private ring of pages, and the work list (all pages of all sequences
 // and KV heads, in order) is cut into equal contiguous chunks, one per worker,
-// whatever the lengths are. A worker's lane 0 issues the TMA copies of a page
-// two stages ahead, across the borders of work items, so the stream of loads
-// never drains; no barrier joins warps. Pieces of an item that several workers
+// whatever the lengths are. A worker's lanes copy a page two stages ahead, across
+// the borders of work items, so the stream of loads never drains; no barrier joins
+// warps. (16-byte copies by the lanes, whose arrivals complete a stage, take 0.3 to
+// 1.6% less time than bulk copies of 2 KB.) Pieces of an item that several workers
 // share are joined by the second kernel.
 //
 // Per page of 16 keys (two e4m3 pages at a time, so that the bookkeeping and the
@@ -41,10 +42,10 @@ namespace {
 // scale neither overflow P nor starve the sum.
 //
 // Bound, with up to 8 rows, by HBM: 64 sequences of 2,048 own keys (8 KV heads, bf16)
-// take 90 us, 6.0 TB/s; e4m3, 4,096 keys, 97 us, 5.7 TB/s. With more rows by the page
-// copies out of L2: a box of 2 KB costs an SM 74 clocks, and a pass of 8 rows over an
-// e4m3 page (two boxes) 166. Taking the units' maxima only when some weight would
-// pass 2^8, without their shuffles, changed nothing.
+// take 90 us, 6.0 TB/s; e4m3, 4,096 keys, 97 us, 5.7 TB/s. With more rows by the
+// latency of its products and softmax, three workers to a scheduler: 160 clocks of an
+// SM for a pass of 8 rows over an e4m3 page. Taking the units' maxima only when some
+// weight would pass 2^8, without their shuffles, was 2% slower.
 template <bool CODES>
 struct StreamCfg {
   static constexpr int kWarps = kStreamWarps;
@@ -164,8 +165,7 @@ __device__ __forceinline__ int item_head(const SharedAttnArgs& a, const Cursor& 
 
 template <bool CODES>
 __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
-    attention_stream_kernel(SharedAttnArgs a, const __grid_constant__ CUtensorMap tmK,
-                            const __grid_constant__ CUtensorMap tmV) {
+    attention_stream_kernel(SharedAttnArgs a) {
   using Cfg = StreamCfg<CODES>;
   constexpr int kStages = Cfg::kStages, kUnit = Cfg::kUnit, kThreads = Cfg::kThreads, kRows = kItemRows;
   constexpr int kKeys = kUnit * kPage;  // keys of a unit
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
                                                              Cfg::kScan);
   const long long limit_clk = pipeline_wait_limit();
   if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1 + Cfg::kScaleLanes);
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 32);
     fence_mbar_init();
     if (warp == 0) *abort_flag = 0;
   }
@@ -290,7 +290,6 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
   Cursor pc = cc;
   int issued = 0, win = 0, ids = 0, pages = 0, head = 0;  // ids: pages win .. win + 31 of the item's `pages`
   const int* list = nullptr;
-  uint32_t armed = 0;  // stages whose latest phase carries copies
   auto open_list = [&]() {
     list = pc.own ? a.c.table + static_cast<size_t>(pc.b) * a.c.max_pages + pp : a.prefix_pages;
     pages = pc.own ? own_pages(a, pc.b) : pp;
@@ -299,46 +298,44 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     ids = win + lane < pages ? list[win + lane] : -1;
   };
   if (pc.n > 0) open_list();
+  // the lane's 16-byte chunk of rows lane / 8 + 4 k of a plane (or half of one)
+  const uint32_t from = (lane >> 3) * (CODES ? 128 : 256) + (lane & 7) * 16;
+  const uint32_t to[2] = {swz(lane >> 3, lane & 7), swz(4 + (lane >> 3), lane & 7) - 512};
   auto produce = [&]() {
     const int j0 = pc.j * kUnit;
     const int s = issued % kStages;
     int page[kUnit];
-    bool any = false, bad = false;
-    uint32_t bytes = 0;
+    bool bad = false;
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
       page[u] = __shfl_sync(0xffffffffu, ids, j0 - win + u);
       const bool ok = page[u] >= 0 && page[u] < a.c.num_pages;
       bad = bad || (!ok && j0 + u < pages);
       if (!ok) page[u] = -1;
-      any = any || ok;
-      bytes += ok ? 2 * Cfg::kPlane : 0;
     }
-    if (lane == 0) {
-      if (bad) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, pc.own ? pc.b : 0);
-      if (any)
-        mbar_arrive_expect_tx(&bars[s], bytes);
-      else
-        mbar_arrive(&bars[s]);  // the stage's old contents are consumed; the rows are void
+    if (bad && lane == 0) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, pc.own ? pc.b : 0);
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) {
-        if (page[u] < 0) continue;
-        uint8_t* dst = ring + s * Cfg::kStage + u * 2 * Cfg::kPlane;
-        const int row = (page[u] * a.c.hkv + head) * kPage;
-        tma_load_2d(dst, &tmK, &bars[s], 0, row);
-        if (!CODES) tma_load_2d(dst + 2048, &tmK, &bars[s], 64, row);
-        tma_load_2d(dst + Cfg::kPlane, &tmV, &bars[s], 0, row);
-        if (!CODES) tma_load_2d(dst + Cfg::kPlane + 2048, &tmV, &bars[s], 64, row);
+    for (int u = 0; u < kUnit; ++u) {
+      if (page[u] < 0) continue;  // the stage's old contents are consumed; the rows are void
+      const size_t row = static_cast<size_t>(page[u] * a.c.hkv + head) * kPage;
+      const uint32_t dst = smem_u32(ring + s * Cfg::kStage + u * 2 * Cfg::kPlane);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* src = static_cast<const uint8_t*>(kv == 0 ? a.c.k : a.c.v) + row * (CODES ? 128 : 256) + from;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int h = 0; h < (CODES ? 1 : 2); ++h)
+            copy16_async(dst + kv * Cfg::kPlane + h * 2048 + k * 512 + to[k & 1], src + k * (CODES ? 512 : 1024) + h * 128);
       }
     }
     if (CODES && lane < Cfg::kScaleLanes) {  // lane 2u: the keys' exponents of page u, 2u + 1: the values'
       const int p = lane < 2 ? page[0] : page[kUnit - 1];
       if (p >= 0)
-        copy16_async(scales + s * kUnit * 32 + lane * 16,
+        copy16_async(smem_u32(scales + s * kUnit * 32 + lane * 16),
                      ((lane & 1) ? a.c.v_scale : a.c.k_scale) + static_cast<size_t>(p * a.c.hkv + head) * kPage);
-      arrive_after_copies(&bars[s]);
     }
-    armed = any ? armed | 1u << s : armed & ~(1u << s);
+    arrive_after_copies(&bars[s]);
     ++issued;
     if (issued == count) return;
     const int j = pc.j;
@@ -651,15 +648,8 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     if (i < count - 1) next_unit<kUnit>(a, cc, lane);
   }
 
+  if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");  // gave up: copies may still be landing
   if (!ok && lane == 0) {
-    // gave up: wait for the copies in flight, which may still land in this block's memory
-    for (int s = 0; s < kStages; ++s) {
-      if (!(armed >> s & 1u)) continue;
-      const int last = (issued - 1 - s) / kStages;  // index of the stage's latest phase
-      const long long t0 = clock64();
-      while (!mbar_try_wait(smem_u32(&bars[s]), static_cast<uint32_t>(last & 1)) && clock64() - t0 < kWaitLimitCycles) {
-      }
-    }
     raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 4000);
   }
 }
@@ -861,8 +851,7 @@ __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnAr
 namespace {
 
 template <bool CODES>
-cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
-                          cudaStream_t st) {
+cudaError_t launch_stream(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {
   auto kern = attention_stream_kernel<CODES>;
   constexpr size_t smem = StreamCfg<CODES>::kSmem;
   static std::atomic<bool> configured[64];
@@ -876,14 +865,13 @@ cudaError_t launch_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const
     configured[dev].store(true, std::memory_order_release);
   }
   count_launch();
-  return launch_pdl(kern, dim3(num_sms), dim3(StreamCfg<CODES>::kThreads), smem, st, a, tmK, tmV);
+  return launch_pdl(kern, dim3(num_sms), dim3(StreamCfg<CODES>::kThreads), smem, st, a);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_stream(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                    int num_sms, cudaStream_t st) {
-  return a.c.codes ? launch_stream<true>(a, tmK, tmV, num_sms, st) : launch_stream<false>(a, tmK, tmV, num_sms, st);
+cudaError_t launch_attention_stream(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {
+  return a.c.codes ? launch_stream<true>(a, num_sms, st) : launch_stream<false>(a, num_sms, st);
 }
 
 cudaError_t launch_attention_join(const SharedAttnArgs& a, int num_sms, cudaStream_t st) {

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
         if (page >= 0) {
           if constexpr (CODES) {
             tma_load_2d(base + Cfg::kOffCodes + s * Cfg::kCodeStage + lane * 2048, tm, &full[s], 0, y);
-            copy16_async(base + Cfg::kOffScales + s * kBlkKeys + lane * kPage,
+            copy16_async(smem_u32(base + Cfg::kOffScales + s * kBlkKeys + lane * kPage),
                          (kv == 0 ? a.c.k_scale : a.c.v_scale) + static_cast<size_t>(y));
           } else {
             uint8_t* dst = base + kOffRing + s * kStage + lane * 2048;
