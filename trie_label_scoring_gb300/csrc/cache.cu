@@ -114,6 +114,40 @@ __device__ __forceinline__ int page_of(const CacheView& c, int seq, int pos, int
   return page;
 }
 
+// cos and sin of pos * (w.x + w.y) to 1e-7, for pos < 2^24: what an e4m3 or
+// bf16 rounding makes of a rotated element then differs from exact arithmetic's as
+// rarely as fp32 allows. The product is held in two floats; multiples of pi/2
+// (two floats) come off it in two steps, the first exactly (k * C1 is a multiple of
+// 2^-23, like the product's leading float); what is left, at most pi/4, goes into the
+// Taylor series, whose next terms are below 3e-8, and the trailing float into one
+// step of the angle sum.
+__device__ __forceinline__ void cos_sin(int pos, float2 w, float& c, float& s) {
+  constexpr float kC1 = 1.57079637050628662f, kC2 = -4.37113900018624283e-8f, kInv = 0.636619772367581343f;
+  const float p = static_cast<float>(pos);
+  const float a = p * w.x;
+  const float k = rintf(a * kInv);
+  const float r = fmaf(-k, kC1, a), lo = fmaf(-k, kC2, fmaf(p, w.x, -a) + p * w.y);
+  float t = r + lo;
+  const float d = t - r;
+  float tl = (r - (t - d)) + (lo - d);
+  const float k2 = rintf(t * kInv);
+  t = fmaf(-k2, kC1, t);
+  tl = fmaf(-k2, kC2, tl);
+  const float u = t + tl, ul = tl - (u - t), z = u * u;
+  const float sp = fmaf(u * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), u);
+  const float cp = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float su = fmaf(cp, ul, sp), cu = fmaf(-sp, ul, cp);
+  const int q = static_cast<int>(k) + static_cast<int>(k2);
+  const float x = (q & 1) ? su : cu, y = (q & 1) ? cu : su;
+  c = ((q + 1) & 2) ? -x : x;
+  s = (q & 2) ? -y : y;
+}
+// 1 / sqrt(v): the hardware's value and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return r > 0.f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;  // 0: the squares overflowed
+}
+
 // ------------------------------------------------------------------ append
 // Block = TOK tokens: thread i first computes angle i % 64 of token i / 64 and
 // looks up its page while the first rows are on their way, then 32 row groups
@@ -151,7 +185,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       s_slot[i] = pos % kPage;
     }
     float c = 1.f, sn = 0.f;
-    if (a.theta > 0.f) rope_cs(pos, rt.w[j], c, sn);
+    if (a.theta > 0.f) cos_sin(pos, rt.w[j], c, sn);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const bf16* g = k == 0 ? a.gq : a.gk;
@@ -204,7 +238,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
           }
         }
         if (norm) {
-          const float rs = rsqrtf(f * (1.f / 128.f) + a.eps);
+          const float rs = inv_sqrt(f * (1.f / 128.f) + a.eps);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(rs, rs));
         }
@@ -342,7 +376,7 @@ __global__ void __launch_bounds__(256) answer_query_kernel(const float* qkv, con
                                                            RopeTable rt) {
   __shared__ float2 s_cs[64];
   grid_dependency_wait();
-  if (threadIdx.x < 64) rope_cs(len[blockIdx.x], rt.w[threadIdx.x], s_cs[threadIdx.x].x, s_cs[threadIdx.x].y);
+  if (threadIdx.x < 64) cos_sin(len[blockIdx.x], rt.w[threadIdx.x], s_cs[threadIdx.x].x, s_cs[threadIdx.x].y);
   __syncthreads();
   bf16* out = q + static_cast<size_t>(blockIdx.x) * hq * 128;
   for (int i = threadIdx.x; i < hq * 32; i += 256) {  // two neighbouring pairs (j, j + 64)
