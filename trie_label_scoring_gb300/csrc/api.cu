@@ -909,10 +909,16 @@ quail_status check_attention_shape(const quail_cache_desc* c, int n_q_heads, int
   return QUAIL_OK;
 }
 
+// Clusters of n CTAs that run at once when each takes an SM (152 SMs, by the
+// occupancy query): processors of fewer than n free SMs are left over.
+constexpr int kClusterCtas = 8;
+constexpr int kClustersAtOnce[kClusterCtas + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+
 // Key ranges (whole 128-key blocks) that `items` tiles of nb blocks are cut
 // into: the cut that minimises waves x (blocks + the fixed cost of a tile, in
-// blocks: its queries, the pipeline's fill and its rows out).
-long choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
+// blocks: its queries, the pipeline's fill and its rows out). clustered: up to
+// kClusterCtas ranges, each tile's in one cluster.
+long choose_key_splits(long items, int nb, int sms, bool clustered, int* split, int* splits) {
   constexpr int kFixed = 4;
   long best = -1;
   *split = 128;
@@ -920,7 +926,9 @@ long choose_key_splits(long items, int nb, int sms, int* split, int* splits) {
   for (int p = 1; p <= nb; ++p) {
     const int blocks = (nb + p - 1) / p;
     const int n = (nb + blocks - 1) / blocks;
-    const long cost = (items * n + sms - 1) / sms * (blocks + kFixed);
+    if (clustered && n > kClusterCtas) break;
+    const long at_once = clustered ? std::max(1, kClustersAtOnce[n] * sms / 152) : sms;
+    const long cost = ((clustered ? items : items * n) + at_once - 1) / at_once * (blocks + kFixed);
     if (best < 0 || cost < best) {
       best = cost;
       *split = blocks * 128;
@@ -973,26 +981,26 @@ std::atomic<int> g_attention_way{-1};
 // time) or multiplied on tiles of 256 rows; the
 // prefix is streamed, multiplied on tiles that take the rows of all sequences, or
 // a part of every sequence's own keys. The least estimate is taken, in us:
-//   tiles     1.4 per 128 keys of a CTA with up to 128 rows, 1.75 with more (e4m3 1.8,
-//             2.15), 18% more behind the streaming, and 4 blocks' worth to begin and end
-//   streaming the larger of reading pages, 1.29 (e4m3 0.72) per 1000 pages and heads,
-//             and of multiplying them, 0.85 (0.57) per 1000 and 8 rows
-//   parts     0.95 per 1000 rows and heads written and joined
-//   launches  6.2 one pass, 7.7 two on tiles, 11.8 stream and tiles, 15.2 stream alone
+//   tiles     1.4 per 128 keys of a CTA with up to 128 rows, 1.7 with more (e4m3 1.9,
+//             2.1), 10% more behind the streaming, and 4 blocks' worth to begin and end
+//   streaming the larger of reading pages, 1.3 (e4m3 0.7) per 1000 pages and heads,
+//             and of multiplying them, 0.83 (0.55) per 1000 and 8 rows
+//   parts     0.56 (streamed) or 0.91 per 1000 rows and heads written and joined
+//   launches  3.5 one pass, 6.2 two on tiles, 11 stream and tiles, 15 stream alone
 // (the constants fitted to 3,200 sizes, each timed in every way: 1 to 256 sequences
 // of 1 to 100 queries, 1 to 8 heads a group, prefixes to 32,768, own keys to 6,000,
-// both types; the way it takes costs 1% more than the fastest on the mean over
+// both types; the way it takes costs 0.7% more than the fastest on the mean over
 // them.) Measured, 32 heads on 8, us, streamed / streamed + prefix on tiles / tiles
 // apart / one pass:
-//   bf16 256 x 1 query  prefix  2048,  300 own keys  127 /  86 / 164 / 431
-//   bf16  64 x 1        prefix   512, 1500 own keys   80 /  83 / 113 / 111
-//   bf16  16 x 4        prefix  8192, 1500 own keys  110 /  60 /  55 / 115
-//   bf16  64 x 8        prefix  2048, 6000 own keys    - / 940 / 330 / 371
-//   bf16  16 x 16       prefix  2048,   48 own keys    - /  38 /  35 /  31
-//   e4m3   4 x 1        prefix 32768,  300 own keys   35 /  50 /  50 / 130
-//   e4m3  64 x 6        prefix  2048, 1500 own keys  187 / 125 / 160 / 242
-//   e4m3  64 x 6        prefix  8192, 6000 own keys  666 / 443 / 439 / 812
-//   e4m3  16 x 4        prefix   512,   48 own keys   25 /  30 /  30 /  17
+//   bf16 256 x 1 query  prefix  2048,  300 own keys  120 /  82 / 165 / 446
+//   bf16  64 x 1        prefix   512, 1500 own keys   76 /  78 / 111 / 112
+//   bf16  16 x 4        prefix  8192, 1500 own keys  102 /  56 /  53 / 117
+//   bf16  64 x 8        prefix  2048, 6000 own keys    - / 928 / 324 / 373
+//   bf16  16 x 16       prefix  2048,   48 own keys    - /  36 /  33 /  31
+//   e4m3   4 x 1        prefix 32768,  300 own keys   34 /  49 /  50 / 138
+//   e4m3  64 x 6        prefix  2048, 1500 own keys  182 / 123 / 161 / 246
+//   e4m3  64 x 6        prefix  8192, 6000 own keys  646 / 441 / 445 / 824
+//   e4m3  16 x 4        prefix   512,   48 own keys   22 /  24 /  26 /  17
 size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
                       int prefix_len, SharedAttnArgs* a) {
   const int hkv = c->n_kv_heads, G = hq / hkv, sms = planning_sms(), S = c->num_seqs;
@@ -1007,14 +1015,15 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   int apart_split = 0, apart_splits = 0, one_split = 0, one_splits = 0;
   {
     const long seq_ctas = (seq_rows + kTileRows - 1) / kTileRows * hkv * S;
-    const double thousand = hkv * 1e-3, k_read = codes ? 0.72 : 1.29, k_pass = codes ? 0.57 : 0.85;
-    const double k_tile = (codes ? 1.8 : 1.4) + (seq_rows > 128 ? 0.35 : 0.);
-    const double k_tile_all = (codes ? 1.8 : 1.4) + (all_rows > 128 ? 0.35 : 0.);
+    const double thousand = hkv * 1e-3, k_read = codes ? 0.7 : 1.3, k_pass = codes ? 0.55 : 0.83;
+    const double k_tile = codes ? (seq_rows > 128 ? 2.1 : 1.9) : (seq_rows > 128 ? 1.7 : 1.4);
+    const double k_tile_all = codes ? (all_rows > 128 ? 2.1 : 1.9) : (all_rows > 128 ? 1.7 : 1.4);
     const double passes = std::min<double>(static_cast<double>(S) * ((seq_rows + 7) / 8), all_rows / 8. + S) * thousand;
     const double read = static_cast<double>(S) * own_pages * thousand * k_read, pass = passes * own_pages * k_pass;
-    const double join = 0.95 * all_rows * thousand;
+    const double rows_heads = all_rows * thousand;
+    constexpr long kJoinBlocks = 3;  // what a join costs, in blocks
     const int forced = g_attention_way.load(std::memory_order_relaxed);
-    double best = forced == 0 ? -1. : 15.2 + (prefix_len > 0 ? join : 0.) +
+    double best = forced == 0 ? -1. : 15. + (prefix_len > 0 ? 0.56 * rows_heads : 0.) +
                   std::max(read + prefix_pages * thousand * k_read,
                            pass + (all_rows + 7) / 8 * thousand * prefix_pages * k_pass);
     const auto take = [&](int way, double us, bool s, bool p) {
@@ -1027,19 +1036,30 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     };
     long on_prefix = 0;
     if (prefix_len > 0) {
-      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms,
+      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, false,
                                     &t.prefix_split, &t.prefix_splits);
-      take(1, 11.8 + std::max(read, pass) + 1.18 * k_tile_all * on_prefix + join, true, true);
+      take(1, 11. + std::max(read, pass) + 1.1 * k_tile_all * on_prefix + 0.91 * rows_heads, true, true);
     }
     if (prefix_len > 0 && S > 1) {
       const long on_own =
-          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, &apart_split, &apart_splits) : 0;
-      take(2, 7.7 + k_tile_all * on_prefix + k_tile * on_own + join, false, true);
+          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, false, &apart_split, &apart_splits) : 0;
+      take(2, 6.2 + k_tile_all * on_prefix + k_tile * on_own + 0.91 * rows_heads, false, true);
     }
-    const long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, &one_split, &one_splits);
-    take(3, 6.2 + k_tile * on_all, false, false);
+    // Up to eight key ranges join in a cluster's shared memory, more in another kernel
+    // (4 sequences of up to 640 keys, 8 heads on 2: 9.0 us, by another kernel 10.8).
+    long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, false, &one_split, &one_splits);
+    int split = 0, splits = 0;
+    const long clustered = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, true, &split, &splits);
+    t.clustered = splits > 1 && clustered <= on_all + (one_splits > 1 ? kJoinBlocks : 0);
+    if (t.clustered) {
+      on_all = clustered;
+      one_split = split;
+      one_splits = splits;
+    }
+    take(3, 3.5 + k_tile * on_all, false, false);
   }
   t.streamed = stream;
+  t.clustered = t.clustered && !stream && !tile_prefix;
   if (!tile_prefix) t.prefix_split = t.prefix_splits = 0;
   if (!stream) {
     t.seq_begin = tile_prefix ? prefix_len : 0;
@@ -1051,7 +1071,7 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     }
   }
   t.dense_parts = t.prefix_splits + t.seq_splits;
-  if (t.dense_parts == 1 && !tile_prefix) t.dense_parts = 0;
+  if ((t.dense_parts == 1 && !tile_prefix) || t.clustered) t.dense_parts = 0;
   Carver k{base};
   if (stream) {
     const size_t workers = static_cast<size_t>(kStreamWarps) * sms;

@@ -97,10 +97,12 @@ struct SharedAttnArgs {
   // ranges of prefix_split (0: not its work), then every sequence's keys from
   // seq_begin on in seq_splits ranges of seq_split (0: streamed instead).
   // Part s of a row is dense_o[s], the prefix's first; dense_parts 0: a single
-  // part, written to out directly.
+  // part, written to out directly, or (clustered) up to eight parts that a cluster of
+  // CTAs joins in its shared memory.
   int prefix_split, prefix_splits;
   int seq_begin, seq_split, seq_splits;
   int dense_parts;
+  bool clustered;
   float* dense_o;  // [dense_parts, total_q * hq, 128]
   PartStat* dense_st;
 };

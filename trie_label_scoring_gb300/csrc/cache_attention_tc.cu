@@ -15,10 +15,14 @@
 // S -> maximum -> weights -> P of a tile (1,630) and its own two products (1,024) are
 // one chain: the tensor memory has no room for a second S. A CTA takes another 3,000
 // to 5,000 to its first S and 3,000 to write its rows.
-// 16 prefills of 128 to 1,024 tokens behind 2,048 (32 heads on 8): 330 us,
-// 1,110 TFLOP/s. A CTA with one tile's rows is bound by that
+// 16 prefills of 128 to 1,024 tokens behind 2,048 (32 heads on 8): 318 us,
+// 1,160 TFLOP/s. A CTA with one tile's rows is bound by that
 // tile's chain, 1.45 us a block; e4m3 1.9 us, the widening warps competing with it
 // for shared memory.
+//
+// Few CTAs' worth of rows: their keys are cut into up to eight ranges, a CTA each in one
+// cluster, which leave their parts in shared memory and join them there row by row
+// (more ranges, and parts of other kernels, go through memory and the join kernel).
 //
 // Roles (384 threads, over codes 512): warps 0 and 3 load K and V pages into one ring
 // K0 V0 K1 V1 .., warp 1 owns TMEM and issues the MMAs (a second issuer, one for each
@@ -147,6 +151,29 @@ __device__ __forceinline__ uint32_t tmem_ready(const Bars* bars) {
   tc_fence_after();
   return bars->tmem_slot;
 }
+
+// 16 bytes, or two floats, at this CTA's shared address `at` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t at, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+// A clustered CTA's part: 256 rows of 128 fp32, chunk c of row r at (c ^ (r & 7)),
+// then their (maximum, sum). It lies over the queries and the rings.
+__device__ __forceinline__ uint32_t part_at(int row, int chunk) { return row * 512u + ((chunk ^ (row & 7)) << 4); }
+constexpr uint32_t kPartStats = kTileRows * 512;
+static_assert(kPartStats + kTileRows * 8 <= TileCfg<false>::kOffBar && kPartStats + kTileRows * 8 <= TileCfg<true>::kOffBar,
+              "a part fits over the queries and the rings");
 
 struct Item {
   int row0, n_rows;  // this CTA's first row and the rows there are, per KV head
@@ -331,7 +358,13 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
       return;
     }
     it.k_hi = min(tile_key_end(a, qr, it.row0), it.k_lo + a.seq_split);
-    if (it.k_hi <= it.k_lo) return;
+    if (it.k_hi <= it.k_lo) {  // no key of these rows' in this range
+      if (a.clustered) {
+        cluster_sync();
+        cluster_sync();
+      }
+      return;
+    }
   }
   const bool two = it.n_rows - it.row0 > 128;
   const int n_pages = (it.k_hi - it.k_lo + kPage - 1) / kPage;
@@ -646,6 +679,26 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
       }
+      // ---- clustered: the rows' part into this CTA's shared memory, once no product
+      // of either tile reads it any more
+      if (!PREFIX && a.clustered) {
+        const bool done = ok && (!live || __all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag, limit_clk)));
+        asm volatile("bar.sync 2, %0;" ::"r"(two ? 256 : 128) : "memory");
+        if (live && done) {
+          tc_fence_after();
+          const int pr = t * 128 + r;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld_32cols_nowait(lane_addr + kTmemO + t * 128 + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(base + part_at(pr, 8 * c + k)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+          *reinterpret_cast<float2*>(base + kPartStats + pr * 8) = make_float2(m_ref, l);
+        }
+      } else
       // ---- rows out, through this tile's Q buffer (no MMA reads it any more):
       // a warp's 32 rows as whole 256-byte lines
       if (live && ok && __all_sync(0xffffffffu, wait_bar(&bars->pv_done[t], static_cast<uint32_t>((n_blocks - 1) & 1), abort_flag, limit_clk))) {
@@ -735,12 +788,49 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
     tmem_dealloc(bars->tmem_slot, 512);
   }
   if (threadIdx.x == 0 && *abort_flag) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 5000);
+  if constexpr (!PREFIX) {
+    if (a.clustered) {  // the key ranges of these rows, each in a CTA of the cluster, meet here
+      __syncwarp();
+      cluster_sync();
+      if (softmax_warp) {
+        const int parts = (tile_key_end(a, qr, it.row0) - a.seq_begin + a.seq_split - 1) / a.seq_split;
+        const int rows = min(kTileRows, it.n_rows - it.row0);
+        const uint32_t at = smem_u32(base);
+        for (int row = it.split * 8 + warp - 4; row < rows; row += 8 * parts) {
+          float2 st = make_float2(-INFINITY, 0.f);
+          if (lane < parts) st = ld_cluster2(in_cta(at + kPartStats + row * 8, lane));
+          float m = st.x;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const float f = st.x == -INFINITY ? 0.f : exp2f(st.x - m);
+          float sum = st.y != st.y ? st.y : f * st.y;  // a NaN sum stays one
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+          for (int p = 0; p < parts; ++p) {
+            const float w = __shfl_sync(0xffffffffu, f, p);
+            const float4 v = ld_cluster4(in_cta(at + part_at(row, lane), p));
+            acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+          }
+          const float inv = 1.f / sum;
+          const int fr = it.row0 + row;
+          const size_t to = static_cast<size_t>(qr.lo + fr / G) * a.hq + it.g * G + fr % G;
+          *reinterpret_cast<uint2*>(a.out + to * 128 + 4 * lane) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+          if (lane == 0 && a.lse != nullptr) a.lse[to] = (m + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another reads its part
+    }
+  }
   if (behind_stream) grid_dependency_wait();
 }
 
 template <bool PREFIX, bool CODES>
 cudaError_t launch_tile(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV, dim3 grid,
-                        cudaStream_t st) {
+                        int cluster, cudaStream_t st) {
   auto kern = attention_tile_kernel<PREFIX, CODES>;
   using Cfg = TileCfg<CODES>;
   static std::atomic<bool> configured[64];
@@ -758,7 +848,22 @@ cudaError_t launch_tile(const SharedAttnArgs& a, const CUtensorMap& tmK, const C
     configured[dev].store(true, std::memory_order_release);
   }
   count_launch();
-  return launch_pdl(kern, grid, dim3(Cfg::kThreads), tile_smem<CODES>(), st, a, tmK, tmV);
+  if (cluster == 1) return launch_pdl(kern, grid, dim3(Cfg::kThreads), tile_smem<CODES>(), st, a, tmK, tmV);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = tile_smem<CODES>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, tmK, tmV);
 }
 
 }  // namespace
@@ -767,14 +872,16 @@ cudaError_t launch_attention_prefix(const SharedAttnArgs& a, const CUtensorMap& 
                                     cudaStream_t st) {
   const long rows = static_cast<long>(a.total_q) * (a.hq / a.c.hkv);
   const dim3 grid((rows + kTileRows - 1) / kTileRows, a.c.hkv, a.prefix_splits);
-  return a.c.codes ? launch_tile<true, true>(a, tmK, tmV, grid, st) : launch_tile<true, false>(a, tmK, tmV, grid, st);
+  return a.c.codes ? launch_tile<true, true>(a, tmK, tmV, grid, 1, st) : launch_tile<true, false>(a, tmK, tmV, grid, 1, st);
 }
 
 cudaError_t launch_attention_sequences(const SharedAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                        cudaStream_t st) {
   const long rows = static_cast<long>(a.max_q) * (a.hq / a.c.hkv);
   const dim3 grid((rows + kTileRows - 1) / kTileRows * a.seq_splits, a.c.hkv, a.c.num_seqs);
-  return a.c.codes ? launch_tile<false, true>(a, tmK, tmV, grid, st) : launch_tile<false, false>(a, tmK, tmV, grid, st);
+  const int cluster = a.clustered ? a.seq_splits : 1;
+  return a.c.codes ? launch_tile<false, true>(a, tmK, tmV, grid, cluster, st)
+                   : launch_tile<false, false>(a, tmK, tmV, grid, cluster, st);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.
