@@ -215,9 +215,9 @@ size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q
  *                 shared (NULL then). Positions from prefix_len on come from
  *                 page_table; its first prefix_len / 16 columns are not read.
  *   seq_len:      device int32 [num_seqs], keys of each sequence, the shared ones
- *                 included, at most max_seq_len; 0: no keys at all (its rows get
- *                 o = 0, lse = -inf), else at least prefix_len (+ the sequence's
- *                 queries when causal).
+ *                 included, at most max_seq_len (which is at most 2^30); 0: no
+ *                 keys at all (its rows get o = 0, lse = -inf), else at least
+ *                 prefix_len (+ the sequence's queries when causal).
  *   q, out:       device bf16 [total_q, n_q_heads, 128]; q as quail_cache_append
  *                 writes it. Query head h reads KV head h / (n_q_heads / n_kv_heads).
  *   q_offsets:    device int32 [num_seqs + 1]: sequence b's queries are rows

@@ -150,3 +150,17 @@ def test_attention_workspace_size():
                                                       a["prefix"])
     assert size() >= 256
     assert size(max_len=4097) == 0 and size(prefix=8) == 0 and size(hq=12) == 0
+
+
+@pytest.mark.parametrize("max_len", [(1 << 30) + 1, (1 << 31) - 128, (1 << 31) - 127, (1 << 31) - 1])
+def test_attention_refuses_lengths_whose_sums_pass_32_bits(max_len):
+    """The page table may hold 2^31 positions; a call's longest sequence may not."""
+    d = desc(n_kv_heads=1, num_seqs=1, max_pages=1 << 27)
+    refused(attend(d, total=1, max_len=max_len), "QUAIL_ERR_UNSUPPORTED_SHAPE")
+    assert Q.lib().quail_workspace_size_attention(ctypes.byref(d), 4, 1, 1, max_len, 16) == 0
+
+
+def test_attention_workspace_of_the_longest_sequence():
+    d = desc(n_kv_heads=1, num_seqs=1, max_pages=1 << 27)
+    short = Q.lib().quail_workspace_size_attention(ctypes.byref(d), 4, 1, 1, 1 << 20, 16)
+    assert 256 < short <= Q.lib().quail_workspace_size_attention(ctypes.byref(d), 4, 1, 1, 1 << 30, 16) < 1 << 30

@@ -906,6 +906,8 @@ quail_status check_attention_shape(const quail_cache_desc* c, int n_q_heads, int
   if (max_seq_len < 1 || max_seq_len < prefix_len ||
       static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(c->max_pages) * 16)
     return fail(QUAIL_ERR_INVALID_ARG, "max_seq_len must cover prefix_len and fit max_pages");
+  // a key range's first key plus its length is a 32-bit sum, in the plan and in the kernels
+  if (max_seq_len > (1 << 30)) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "max_seq_len must be at most 2^30");
   return QUAIL_OK;
 }
 
