@@ -26,6 +26,10 @@
  *    is the legacy default stream). The caller owns every device buffer passed
  *    in (weights, KV pool, outputs, workspace). The library owns quail_trie
  *    objects, including their device image.
+ *  - Calls may be captured into a CUDA graph once the same call has run before
+ *    (the first one on a device uploads tries and sets kernel attributes). Host
+ *    arrays that a call takes (letters, answer tokens) are kept by value; a
+ *    replay uses the device buffers and the trie of the captured call.
  *  - All device pointers must be 16-byte aligned; bf16 tensors are row-major
  *    with the innermost dimension contiguous.
  */

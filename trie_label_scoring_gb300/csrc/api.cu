@@ -117,6 +117,19 @@ quail_status encode_2d_codes(CUtensorMap* m, const void* ptr, uint64_t rows, uin
   return QUAIL_OK;
 }
 
+// A call's own integers to the device. A copy that is captured into a graph would
+// read `host` again at every replay, after the call has freed it: there they travel
+// as kernel arguments, which the graph keeps.
+quail_status copy_ints(int* dst, const std::vector<int32_t>& host, cudaStream_t st) {
+  cudaStreamCaptureStatus capture;
+  CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+  if (capture == cudaStreamCaptureStatusNone)
+    CUDA_TRY(cudaMemcpyAsync(dst, host.data(), host.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
+  else
+    CUDA_TRY(launch_store_ints(dst, host.data(), host.size(), st));
+  return QUAIL_OK;
+}
+
 // ------------------------------------------------------------------ profiling hook
 std::mutex g_ev_mu;
 std::vector<cudaEvent_t> g_events;
@@ -970,7 +983,8 @@ quail_status copy_letters(const Buffers& b, const int32_t* letter_tokens, int nu
   host[2] = -1;
   host[3] = 0;
   std::memcpy(host.data() + 4, letter_tokens, num_letters * sizeof(int32_t));
-  CUDA_TRY(cudaMemcpyAsync(b.small, host.data(), host.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
+  const quail_status s = copy_ints(b.small, host, st);
+  if (s != QUAIL_OK) return s;
   *nt = NodeTables{b.small, b.small + 1, b.small + 2, 1};
   return QUAIL_OK;
 }
@@ -1417,7 +1431,8 @@ quail_status quail_classify_trie_tree_ml(const quail_model_ml_desc* model, const
       host[2 * static_cast<size_t>(rows) + r] = trie->eval_parent[e] < 0 ? -1 : i * a + trie->eval_parent[e];
     }
   }
-  CUDA_TRY(cudaMemcpyAsync(b.small, host.data(), host.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
+  s = copy_ints(b.small, host, st);
+  if (s != QUAIL_OK) return s;
   const NodeTables nt{b.small, b.small + rows, b.small + 2 * static_cast<size_t>(rows), rows};
   const RowMap map{a, nullptr, nullptr, nullptr, nullptr, a};
   const int d = model->hidden, I = model->intermediate;
@@ -1561,7 +1576,8 @@ quail_status quail_join_if(const quail_model_desc* model, const quail_paged_kv* 
   std::vector<int32_t> host(M + R);
   for (int m = 0; m < M; ++m) host[m] = partners->eval_index_of_node[partners->label_end_node[m]];
   std::memcpy(host.data() + M, answer_tokens, R * sizeof(int32_t));
-  CUDA_TRY(cudaMemcpyAsync(b.small, host.data(), host.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st));
+  s = copy_ints(b.small, host, st);
+  if (s != QUAIL_OK) return s;
   const NodeTables nt{img->eval_token, img->eval_depth, img->eval_parent, nodes};
   const RowMap map{M, nullptr, nullptr, nullptr, b.small};
   const int rows = num_anchors * M;

@@ -139,6 +139,9 @@ cudaError_t launch_silu_mul_split(const float* part, int ks, size_t slab, int ro
 cudaError_t launch_norm_out(const float* h, int rows, int d, const bf16* gain, float eps, bf16* z, float* z_f32,
                             cudaStream_t st);
 
+// dst[0, n) = host[0, n), carried as kernel arguments: nothing reads host after the call.
+cudaError_t launch_store_ints(int* dst, const int* host, size_t n, cudaStream_t st);
+
 // AI.IF on joined pairs: for every row of z_f32 [rows, d] (anchor * M +
 // partner), the softmax over the R answer-spelling rows of W_lm (tokens[0,
 // n_true) spell TRUE) and p_true[row] = the TRUE rows' share.

@@ -2,7 +2,9 @@
 // RMSNorms, log-sum-exp reduction, label path sums and softmax
 // ("To Classify, Try a Trie Tree", sec. 3.2), the letters head (sec. 3.3) and
 // the trie_decode step bookkeeping (sec. 3.1).
+#include <algorithm>
 #include <cfloat>
+#include <cstring>
 
 #include "kernels.h"
 #include "launch.cuh"
@@ -577,7 +579,30 @@ __global__ void decode_select_kernel(DecodeTrie t, const float* __restrict__ z, 
   }
 }
 
+// ------------------------------------------------------------------ host integers
+struct IntBlock {
+  int v[960];  // with the other arguments below 4 KB
+};
+
+__global__ void store_ints_kernel(int* __restrict__ dst, int n, IntBlock b) {
+  grid_dependency_wait();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = b.v[i];
+}
+
 }  // namespace
+
+cudaError_t launch_store_ints(int* dst, const int* host, size_t n, cudaStream_t st) {
+  IntBlock b;
+  constexpr size_t kBlock = sizeof(b.v) / sizeof(int);
+  for (size_t at = 0; at < n; at += kBlock) {
+    const int m = static_cast<int>(std::min(kBlock, n - at));
+    std::memcpy(b.v, host + at, m * sizeof(int));
+    count_launch();
+    const cudaError_t e = launch_pdl(store_ints_kernel, dim3(1), dim3(256), 0, st, dst + at, m, b);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 cudaError_t launch_embed_rmsnorm(const bf16* embed, const int* tokens, int n, int d, const bf16* gain, float eps,
                                  bf16* out, cudaStream_t st, const int* live) {
