@@ -203,8 +203,10 @@ quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, 
 quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* token_seq, const int32_t* token_pos,
                               int32_t num_tokens, void* k_out, void* v_out, quail_stream_t stream);
 
-/* Bytes of device workspace quail_attention_shared needs for these bounds
- * (256-byte aligned base required); 0 on invalid arguments. */
+/* Bytes of device workspace that quail_attention_shared needs at most for these
+ * bounds and any smaller ones (total_q, max_q_len, max_seq_len, prefix_len, and
+ * fewer sequences in the cache), so that one allocation for the largest serves
+ * them all (256-byte aligned base required); 0 on invalid arguments. */
 size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len);
 
@@ -240,8 +242,7 @@ size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q
  * in the formula. Bounds that only the device can see set
  * QUAIL_ERR_DEVICE_BOUNDS and void that sequence's rows (all rows, for a prefix
  * page). Nothing in the workspace needs to start at zero; calls that may run at
- * the same time need one each. How the work is cut, and so the size of the
- * workspace, follows from the bounds, and smaller ones may need more of it. */
+ * the same time need one each. How the work is cut follows from the bounds. */
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
                                     const int32_t* seq_len, int32_t max_seq_len, const void* q,
                                     const int32_t* q_offsets, int32_t total_q, int32_t max_q_len, int32_t n_q_heads,
@@ -535,7 +536,8 @@ quail_status quail_classify_trie_tree_shortlist(const quail_model_desc* model, c
  *   doc_len: device int32 [num_seqs], the tokens of each of the cache's sequences,
  *            the shared ones included: 0 (an empty document), or prefix_len to
  *            max_doc_len
- * Other arguments, outputs and errors as the two calls named. */
+ * Other arguments, outputs and errors as the two calls named. The workspace size
+ * serves these bounds and any smaller ones (num_letters, max_doc_len, prefix_len). */
 size_t quail_workspace_size_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,
                                            int32_t num_letters, int32_t max_doc_len, int32_t prefix_len);
 quail_status quail_classify_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,

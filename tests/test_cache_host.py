@@ -6,6 +6,12 @@ import pytest
 
 import trie_label_scoring_gb300 as Q
 
+try:
+    import torch
+    HAS_GPU = torch.cuda.is_available()
+except ImportError:
+    HAS_GPU = False
+
 
 @pytest.fixture(scope="module", autouse=True)
 def built():
@@ -164,3 +170,73 @@ def test_attention_workspace_of_the_longest_sequence():
     d = desc(n_kv_heads=1, num_seqs=1, max_pages=1 << 27)
     short = Q.lib().quail_workspace_size_attention(ctypes.byref(d), 4, 1, 1, 1 << 20, 16)
     assert 256 < short <= Q.lib().quail_workspace_size_attention(ctypes.byref(d), 4, 1, 1, 1 << 30, 16) < 1 << 30
+
+
+def _attention_bounds(rng):
+    """Random bounds of an attention call, log-uniform: (kv heads, q heads, sequences, total_q, max_q, max_len, prefix)."""
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    hkv, group = rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 4, 8, 16])
+    seqs, max_q = log(1, 512), log(1, 2048)
+    total = rng.choice([seqs * max_q, max(1, seqs * max_q // 3), log(1, 1 << 20)])  # batches may carry spare rows
+    total = min(total, (1 << 30) // (hkv * group))
+    max_len = log(1, 1 << 18)
+    return [hkv, hkv * group, seqs, total, max_q, max_len, rng.choice([0, log(1, max_len) // 16 * 16])]
+
+
+def _need(dtype, b, ws_bytes):
+    """The status of an attention call with that much workspace (other refusals come before or after it)."""
+    d = desc(dtype=dtype, n_kv_heads=b[0], num_seqs=b[2], max_pages=1 << 18, num_pages=4096, k_scale=0x4000 if dtype else None,
+             v_scale=0x5000 if dtype else None)
+    code = attend(d, prefix=b[6], max_len=b[5], offs=0x100, total=b[3], max_q=b[4], hq=b[1], ws_bytes=ws_bytes)
+    with pytest.raises(Q.QuailError) as e:
+        Q._check(code)
+    return e.value.name
+
+
+def _size(dtype, b):
+    d = desc(dtype=dtype, n_kv_heads=b[0], num_seqs=b[2], max_pages=1 << 18, num_pages=4096)
+    return Q.lib().quail_workspace_size_attention(ctypes.byref(d), b[1], b[3], b[4], b[5], b[6])
+
+
+@pytest.mark.skipif(HAS_GPU, reason="the calls would go past the workspace check with addresses that are none")
+@pytest.mark.parametrize("dtype", [Q.DTYPE_BF16, Q.DTYPE_E4M3])
+def test_attention_workspace_serves_all_smaller_bounds(dtype):
+    """One allocation for the largest bounds: smaller ones ask for no more, and no call within them is refused it,
+    whatever the way it takes."""
+    import random
+    rng = random.Random(dtype)
+    for _ in range(400):
+        big = _attention_bounds(rng)
+        small = list(big)
+        for i in rng.sample([2, 3, 4, 5, 6], rng.randint(0, 5)):
+            small[i] = rng.randint(1, big[i]) if i != 6 else rng.randint(0, big[6] // 16) * 16
+        small[6] = min(small[6], small[5] // 16 * 16)
+        size = _size(dtype, big)
+        assert 0 < _size(dtype, small) <= size, (big, small)
+        for way in (-1, 0, 1, 2, 3):
+            Q._test_set_attention_way(way)
+            try:
+                assert _need(dtype, small, size) != "QUAIL_ERR_WORKSPACE", (big, small, way)
+            finally:
+                Q._test_set_attention_way(-1)
+
+
+def test_attention_workspace_grows_with_the_length():
+    """64 sequences of one query behind 512 shared keys, 32 heads on 8; and 16 sequences of one."""
+    for seqs, prefix in ((64, 512), (16, 0)):
+        sizes = [_size(Q.DTYPE_BF16, [8, 32, seqs, seqs, 1, n, prefix]) for n in (512, 1024, 2048, 3072, 8192, 16384)]
+        assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("seqs", [1, 16, 64, 256])
+def test_letters_workspace_grows_with_its_bounds(seqs):
+    """Letters over a cache: more letters, longer documents or more shared tokens ask for no less."""
+    m = Q.ModelDesc(2560, 32, 8, 128, 151936, 1e-6, 1e6)
+    d = desc(n_kv_heads=8, num_seqs=seqs, max_pages=1 << 16, num_pages=4096)
+
+    def size(letters, n, prefix):
+        return Q.lib().quail_workspace_size_letters_cached(ctypes.byref(m), ctypes.byref(d), letters, n, prefix)
+
+    for sizes in ([size(26, n, 512) for n in (512, 1024, 3072, 8192, 16384, 100000)],
+                  [size(26, 8192, p) for p in (0, 16, 512, 2048, 8192)], [size(k, 8192, 0) for k in (2, 26, 300, 8192)]):
+        assert sizes[0] > 0 and sizes == sorted(sizes)

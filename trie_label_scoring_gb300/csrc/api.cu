@@ -932,8 +932,12 @@ constexpr int kClustersAtOnce[kClusterCtas + 1] = {0, 152, 76, 46, 36, 28, 23, 1
 // Key ranges (whole 128-key blocks) that `items` tiles of nb blocks are cut
 // into: the cut that minimises waves x (blocks + the fixed cost of a tile, in
 // blocks: its queries, the pipeline's fill and its rows out). clustered: up to
-// kClusterCtas ranges, each tile's in one cluster.
-long choose_key_splits(long items, int nb, int sms, bool clustered, int* split, int* splits) {
+// kClusterCtas ranges, each tile's in one cluster. Else more than one range leaves a
+// part of each of the call's `rows` in memory, at most part_rows(sms) in all. Where
+// the rows belong to the tiles that bound holds by itself: the count before the last
+// one looked at keeps items * n within 4 sms, and it at most doubles from one to the next.
+size_t part_rows(int sms) { return static_cast<size_t>(8) * kTileRows * sms; }
+long choose_key_splits(long items, int nb, int sms, size_t rows, bool clustered, int* split, int* splits) {
   constexpr int kFixed = 4;
   long best = -1;
   *split = 128;
@@ -941,7 +945,7 @@ long choose_key_splits(long items, int nb, int sms, bool clustered, int* split, 
   for (int p = 1; p <= nb; ++p) {
     const int blocks = (nb + p - 1) / p;
     const int n = (nb + blocks - 1) / blocks;
-    if (clustered && n > kClusterCtas) break;
+    if (clustered ? n > kClusterCtas : n > 1 && n * rows > part_rows(sms)) break;
     const long at_once = clustered ? std::max(1, kClustersAtOnce[n] * sms / 152) : sms;
     const long cost = ((clustered ? items : items * n) + at_once - 1) / at_once * (blocks + kFixed);
     if (best < 0 || cost < best) {
@@ -1052,20 +1056,20 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     };
     long on_prefix = 0;
     if (prefix_len > 0) {
-      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, false,
+      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, rows, false,
                                     &t.prefix_split, &t.prefix_splits);
       take(1, 11. + std::max(read, pass) + 1.1 * k_tile_all * on_prefix + 0.91 * rows_heads, true, true);
     }
     if (prefix_len > 0 && S > 1) {
       const long on_own =
-          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, false, &apart_split, &apart_splits) : 0;
+          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, rows, false, &apart_split, &apart_splits) : 0;
       take(2, 6.2 + k_tile_all * on_prefix + k_tile * on_own + 0.91 * rows_heads, false, true);
     }
     // Up to eight key ranges join in a cluster's shared memory, more in another kernel
     // (4 sequences of up to 640 keys, 8 heads on 2: 9.0 us, by another kernel 10.8).
-    long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, false, &one_split, &one_splits);
+    long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, rows, false, &one_split, &one_splits);
     int split = 0, splits = 0;
-    const long clustered = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, true, &split, &splits);
+    const long clustered = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, rows, true, &split, &splits);
     t.clustered = splits > 1 && clustered <= on_all + (one_splits > 1 ? kJoinBlocks : 0);
     if (t.clustered) {
       on_all = clustered;
@@ -1110,6 +1114,31 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
   return k.off + 256;
 }
 
+// What plan_attention needs at most, in any way, for these bounds and all smaller ones
+// (fewer sequences, queries, keys or shared keys): how the work is cut changes with the
+// bounds, and a smaller call may take more than a larger one.
+size_t attention_workspace(const quail_cache_desc* c, int hq, int total_q, int max_seq_len, int prefix_len) {
+  const int sms = planning_sms();
+  const size_t rows = static_cast<size_t>(total_q) * hq, workers = static_cast<size_t>(kStreamWarps) * sms;
+  const auto parts = [&](int keys) {  // rows written by the tiles of so many keys
+    return std::min((keys + 127) / 128 * rows, std::max(rows, part_rows(sms)));
+  };
+  size_t dense = parts(max_seq_len);
+  if (prefix_len > 0)
+    dense += parts(prefix_len);
+  else if (max_seq_len <= 128)
+    dense = 0;  // a single range, written to the output
+  else
+    dense = std::min(dense, part_rows(sms));  // the same, or several ranges
+  Carver k{nullptr};
+  k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
+  for (const size_t n : {prefix_len > 0 ? rows : 0, rows, workers * kItemRows, dense}) {
+    k.take<float>(n * 128);
+    k.take<PartStat>(n);
+  }
+  return k.off + 256;
+}
+
 // The launches of one attention call: a filled in, its plan included.
 quail_status run_attention_shared(const quail_cache_desc* cache, const SharedAttnArgs& a, DeviceState* ds,
                                   cudaStream_t st) {
@@ -1141,8 +1170,9 @@ struct LettersCachedBuffers {
   SharedAttnArgs attn;
 };
 
+// any_smaller: of these bounds and all smaller ones.
 size_t plan_letters_cached(uint8_t* base, const quail_model_desc* m, const quail_cache_desc* c, int num_letters,
-                           int max_doc_len, int prefix_len, LettersCachedBuffers* out) {
+                           int max_doc_len, int prefix_len, LettersCachedBuffers* out, bool any_smaller = false) {
   const int N = c->num_seqs, hq = m->n_q_heads;
   LettersCachedBuffers x{};
   size_t off = round_up(plan(base, m, 1, N, 1, 16, false, 0, true, num_letters + 4, base ? &x.b : nullptr), 256);
@@ -1151,6 +1181,7 @@ size_t plan_letters_cached(uint8_t* base, const quail_model_desc* m, const quail
   x.o = k.take<bf16>(static_cast<size_t>(N) * hq * 128);
   x.lse = k.take<float>(static_cast<size_t>(N) * hq);
   off += round_up(k.off, 256);
+  if (any_smaller) return off + attention_workspace(c, hq, N, max_doc_len, prefix_len);
   const size_t attn = plan_attention(base ? base + off : nullptr, c, hq, N, 1, max_doc_len, prefix_len, &x.attn);
   if (out) *out = x;
   return off + attn;
@@ -1688,7 +1719,7 @@ quail_status quail_test_set_pipeline_wait_limit(long long cycles) {
 // Test hook, not part of the public header: attention over the cache goes one
 // way (0 streamed, 1 streamed behind a prefix on tiles, 2 prefix and sequences on
 // tiles apart, 3 in one pass) wherever that exists, whatever it costs; -1: the
-// cheapest again. Process-wide; the workspace of a call depends on it.
+// cheapest again. Process-wide.
 quail_status quail_test_set_attention_way(int way) {
   if (way < -1 || way > 3) return fail(QUAIL_ERR_INVALID_ARG, "way must be -1..3");
   g_attention_way.store(way);
@@ -2089,7 +2120,7 @@ quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* toke
 size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
-  return plan_attention(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len, nullptr);
+  return attention_workspace(cache, n_q_heads, total_q, max_seq_len, prefix_len);
 }
 
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
@@ -2144,7 +2175,7 @@ size_t quail_workspace_size_letters_cached(const quail_model_desc* model, const 
   if (cache == nullptr || cache->num_seqs <= 0 ||
       check_attention_shape(cache, model->n_q_heads, cache->num_seqs, 1, max_doc_len, prefix_len) != QUAIL_OK)
     return 0;
-  return plan_letters_cached(nullptr, model, cache, num_letters, max_doc_len, prefix_len, nullptr);
+  return plan_letters_cached(nullptr, model, cache, num_letters, max_doc_len, prefix_len, nullptr, true);
 }
 
 quail_status quail_classify_letters_cached(const quail_model_desc* model, const quail_cache_desc* cache,
