@@ -933,11 +933,13 @@ constexpr int kClustersAtOnce[kClusterCtas + 1] = {0, 152, 76, 46, 36, 28, 23, 1
 // into: the cut that minimises waves x (blocks + the fixed cost of a tile, in
 // blocks: its queries, the pipeline's fill and its rows out). clustered: up to
 // kClusterCtas ranges, each tile's in one cluster. Else more than one range leaves a
-// part of each of the call's `rows` in memory, at most part_rows(sms) in all. Where
-// the rows belong to the tiles that bound holds by itself: the count before the last
-// one looked at keeps items * n within 4 sms, and it at most doubles from one to the next.
-size_t part_rows(int sms) { return static_cast<size_t>(8) * kTileRows * sms; }
-long choose_key_splits(long items, int nb, int sms, size_t rows, bool clustered, int* split, int* splits) {
+// part of each of the call's `rows` in memory, at most part_rows in all, where a tile
+// has up to tile_rows of them. If every row belongs to a tile that holds by itself: the
+// count before the last one looked at keeps items * n within 4 sms, and it at most
+// doubles from one to the next.
+size_t part_rows(int sms, long tile_rows) { return static_cast<size_t>(8 * sms) * std::min<long>(kTileRows, tile_rows); }
+long choose_key_splits(long items, int nb, int sms, size_t rows, long tile_rows, bool clustered, int* split,
+                       int* splits) {
   constexpr int kFixed = 4;
   long best = -1;
   *split = 128;
@@ -945,7 +947,7 @@ long choose_key_splits(long items, int nb, int sms, size_t rows, bool clustered,
   for (int p = 1; p <= nb; ++p) {
     const int blocks = (nb + p - 1) / p;
     const int n = (nb + blocks - 1) / blocks;
-    if (clustered ? n > kClusterCtas : n > 1 && n * rows > part_rows(sms)) break;
+    if (clustered ? n > kClusterCtas : n > 1 && n * rows > part_rows(sms, tile_rows)) break;
     const long at_once = clustered ? std::max(1, kClustersAtOnce[n] * sms / 152) : sms;
     const long cost = ((clustered ? items : items * n) + at_once - 1) / at_once * (blocks + kFixed);
     if (best < 0 || cost < best) {
@@ -1056,20 +1058,22 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
     };
     long on_prefix = 0;
     if (prefix_len > 0) {
-      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, rows, false,
-                                    &t.prefix_split, &t.prefix_splits);
+      on_prefix = choose_key_splits((all_rows + kTileRows - 1) / kTileRows * hkv, (prefix_len + 127) / 128, sms, rows, all_rows,
+                                    false, &t.prefix_split, &t.prefix_splits);
       take(1, 11. + std::max(read, pass) + 1.1 * k_tile_all * on_prefix + 0.91 * rows_heads, true, true);
     }
     if (prefix_len > 0 && S > 1) {
       const long on_own =
-          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, rows, false, &apart_split, &apart_splits) : 0;
+          own > 0 ? choose_key_splits(seq_ctas, (own + 127) / 128, sms, rows, seq_rows, false, &apart_split, &apart_splits)
+                  : 0;
       take(2, 6.2 + k_tile_all * on_prefix + k_tile * on_own + 0.91 * rows_heads, false, true);
     }
     // Up to eight key ranges join in a cluster's shared memory, more in another kernel
     // (4 sequences of up to 640 keys, 8 heads on 2: 9.0 us, by another kernel 10.8).
-    long on_all = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, rows, false, &one_split, &one_splits);
+    const int nb = (max_seq_len + 127) / 128;
+    long on_all = choose_key_splits(seq_ctas, nb, sms, rows, seq_rows, false, &one_split, &one_splits);
     int split = 0, splits = 0;
-    const long clustered = choose_key_splits(seq_ctas, (max_seq_len + 127) / 128, sms, rows, true, &split, &splits);
+    const long clustered = choose_key_splits(seq_ctas, nb, sms, rows, seq_rows, true, &split, &splits);
     t.clustered = splits > 1 && clustered <= on_all + (one_splits > 1 ? kJoinBlocks : 0);
     if (t.clustered) {
       on_all = clustered;
@@ -1117,22 +1121,20 @@ size_t plan_attention(uint8_t* base, const quail_cache_desc* c, int hq, int tota
 // What plan_attention needs at most, in any way, for these bounds and all smaller ones
 // (fewer sequences, queries, keys or shared keys): how the work is cut changes with the
 // bounds, and a smaller call may take more than a larger one.
-size_t attention_workspace(const quail_cache_desc* c, int hq, int total_q, int max_seq_len, int prefix_len) {
+size_t attention_workspace(const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
+                           int prefix_len) {
   const int sms = planning_sms();
+  const long G = hq / c->n_kv_heads, seq_rows = std::min(max_q, total_q) * G, all_rows = total_q * G;
   const size_t rows = static_cast<size_t>(total_q) * hq, workers = static_cast<size_t>(kStreamWarps) * sms;
-  const auto parts = [&](int keys) {  // rows written by the tiles of so many keys
-    return std::min((keys + 127) / 128 * rows, std::max(rows, part_rows(sms)));
+  const size_t one_part = prefix_len > 0 ? rows : 0;  // without a prefix a single range is written to the output
+  const auto parts = [&](int keys, long tile_rows) {  // rows written by tiles over so many keys
+    const size_t nb = (keys + 127) / 128;
+    return nb > 1 ? std::max(one_part, std::min(nb * rows, part_rows(sms, tile_rows))) : one_part;
   };
-  size_t dense = parts(max_seq_len);
-  if (prefix_len > 0)
-    dense += parts(prefix_len);
-  else if (max_seq_len <= 128)
-    dense = 0;  // a single range, written to the output
-  else
-    dense = std::min(dense, part_rows(sms));  // the same, or several ranges
+  const size_t dense = parts(max_seq_len, seq_rows) + (prefix_len > 0 ? parts(prefix_len, all_rows) : 0);
   Carver k{nullptr};
   k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
-  for (const size_t n : {prefix_len > 0 ? rows : 0, rows, workers * kItemRows, dense}) {
+  for (const size_t n : {one_part, rows, workers * kItemRows, dense}) {
     k.take<float>(n * 128);
     k.take<PartStat>(n);
   }
@@ -1181,7 +1183,7 @@ size_t plan_letters_cached(uint8_t* base, const quail_model_desc* m, const quail
   x.o = k.take<bf16>(static_cast<size_t>(N) * hq * 128);
   x.lse = k.take<float>(static_cast<size_t>(N) * hq);
   off += round_up(k.off, 256);
-  if (any_smaller) return off + attention_workspace(c, hq, N, max_doc_len, prefix_len);
+  if (any_smaller) return off + attention_workspace(c, hq, N, 1, max_doc_len, prefix_len);
   const size_t attn = plan_attention(base ? base + off : nullptr, c, hq, N, 1, max_doc_len, prefix_len, &x.attn);
   if (out) *out = x;
   return off + attn;
@@ -2120,7 +2122,7 @@ quail_status quail_cache_read(const quail_cache_desc* cache, const int32_t* toke
 size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                       int32_t max_q_len, int32_t max_seq_len, int32_t prefix_len) {
   if (check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len) != QUAIL_OK) return 0;
-  return attention_workspace(cache, n_q_heads, total_q, max_seq_len, prefix_len);
+  return attention_workspace(cache, n_q_heads, total_q, max_q_len, max_seq_len, prefix_len);
 }
 
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
