@@ -648,9 +648,16 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     if (i < count - 1) next_unit<kUnit>(a, cc, lane);
   }
 
-  if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");  // gave up: copies may still be landing
-  if (!ok && lane == 0) {
-    raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 4000);
+  if (!ok) {
+    // Gave up: no copy, and no arrival that follows one, may land after the CTA's end.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int k = max(0, issued - kStages); k < issued; ++k) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(smem_u32(&bars[k % kStages]), static_cast<uint32_t>((k / kStages) & 1)) &&
+             clock64() - t0 <= kWaitLimitCycles) {
+      }
+    }
+    if (lane == 0) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_TIMEOUT, 4000);
   }
 }
 

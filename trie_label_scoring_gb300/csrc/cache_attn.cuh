@@ -27,7 +27,8 @@ __device__ __forceinline__ QueryRange query_range(const SharedAttnArgs& a, int b
 }
 
 // mbar_wait for waits that are often not over at once: the limit comes in a
-// register instead of a load between two tries.
+// register instead of a load between two tries. A negative limit (a test's) makes
+// every wait give up without a try.
 __device__ __forceinline__ long long pipeline_wait_limit() {
   return *const_cast<const volatile long long*>(&g_pipeline_wait_limit);
 }
@@ -35,10 +36,10 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   const uint32_t a = smem_u32(bar);
   // A try waits a while by itself; most waits that the first does not see out end in
   // the second, which the checks would hold up.
-  if (mbar_try_wait(a, parity)) return true;
+  if (limit >= 0 && mbar_try_wait(a, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(a, parity)) return true;
+    if (limit >= 0 && mbar_try_wait(a, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > limit) {
       *abort_flag = 1;
