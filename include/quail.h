@@ -239,7 +239,7 @@ size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q
  * over e4m3 keys read directly) for the product with V. Keys past a sequence's
  * end are never used, whatever their slots hold; a key that causal hides from a
  * query has weight 0, which leaves a NaN or an infinity among its values a NaN, as
- * in the formula. Bounds that only the device can see set
+ * in the formula. A score of +infinity makes o and lse of its row NaN. Bounds that only the device can see set
  * QUAIL_ERR_DEVICE_BOUNDS and void that sequence's rows (all rows, for a prefix
  * page). Nothing in the workspace needs to start at zero; calls that may run at
  * the same time need one each. How the work is cut follows from the bounds. */
