@@ -101,3 +101,101 @@ def _without_key(pool, page, slot, q, offs, lens, prefix):
     r = attention_64(pool, q, offs, lens, prefix, False, D ** -0.5)
     pool.k[page, 0, slot, 3], pool.v[page, 1, slot, 71] = keep
     return r
+
+
+# ------------------------------------------------------------------ appends of many tokens
+def _append_case(kind, src, hq, hkv, extra, norm=True, seed=0):
+    """Tokens of ragged sequences in any order: 4 an SM and `extra` more, past which a block takes four of them."""
+    n = 4 * torch.cuda.get_device_properties(0).multi_processor_count + extra
+    rng = np.random.RandomState(seed)
+    lens = [int(x) for x in rng.randint(1, 200, size=n // 60)]
+    while sum(lens) < n:
+        lens.append(97)
+    pool = Pool(kind, hkv, lens)
+    seq, pos = tokens(lens)
+    pick = torch.from_numpy(rng.permutation(seq.numel())[:n]).cuda()
+    seq, pos = seq[pick].contiguous(), pos[pick].contiguous()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    qkv = torch.randn((n, (hq + 2 * hkv) * D), generator=g, device="cuda").to(src)
+    gq = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16() if norm else None
+    gk = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16() if norm else None
+    return pool, seq, pos, qkv, gq, gk
+
+
+def _check_append(pool, seq, pos, live, qkv, hq, gq, gk, q, before, theta):
+    hkv = pool.hkv
+    s, p = seq[live], pos[live]
+    (wq, sq), (wk, sk), (wv, sv) = expected_rows(qkv[live], p, hq, hkv, gq, gk, 1e-6, theta)
+    check_stored(q[live].double(), wq, sq)
+    assert bool((q[~live] == 7).all())
+    page, slot = pool.table[s.long(), p.long() // PAGE].long(), p.long() % PAGE
+    for name, want, slack, sc in (("k", wk, sk, pool.ks), ("v", wv, sv, pool.vs)):
+        check_stored(pool.rows(s, p, name), want, slack, None if sc is None else sc[page, :, slot])
+    touched = torch.zeros(pool.k.shape[:3], dtype=torch.bool, device="cuda")
+    touched[page, :, slot] = True
+    for old, new in zip(before, (pool.k, pool.v)):
+        as_int = torch.uint8 if pool.kind == "e4m3" else torch.int16
+        assert torch.equal(old.view(as_int)[~touched], new.view(as_int)[~touched])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("src", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hq,hkv,extra,norm,theta", [(5, 3, 0, True, 1e6), (5, 3, 1, True, 1e6), (8, 2, 2, False, 1e4),
+                                                     (1, 1, 3, True, 0.0), (32, 8, 2401, True, 1e6), (0, 1, 4, False, 0.0)])
+def test_append_of_many_tokens(kind, src, hq, hkv, extra, norm, theta):
+    """Both block forms at their border, with padding tokens at the ends and between the others."""
+    import trie_label_scoring_gb300 as Q
+    pool, seq, pos, qkv, gq, gk = _append_case(kind, src, hq, hkv, extra, norm, seed=extra)
+    n = seq.numel()
+    pad = torch.tensor([0, 5, 6, 7, 8, 17, n // 2, n - 3, n - 1], device="cuda")
+    seq[pad] = -1
+    pos[pad[::2]] = -9
+    q = torch.full((n, hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = (pool.k.clone(), pool.v.clone())
+    Q.cache_append(pool.cache, qkv, hq, seq, pos, q_out=q, q_norm=gq, k_norm=gk, rms_eps=1e-6, rope_theta=theta)
+    status()
+    _check_append(pool, seq, pos, seq >= 0, qkv, hq, gq, gk, q, before, theta)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("extra", [0, 3])
+def test_append_of_many_tokens_drops_bad_indices_only(kind, extra):
+    """Bad sequences, positions and pages inside and at the end of a block: reported, and their tokens alone dropped."""
+    import trie_label_scoring_gb300 as Q
+    pool, seq, pos, qkv, gq, gk = _append_case(kind, torch.float32, 5, 3, extra, seed=7)
+    n = seq.numel()
+    bad = torch.tensor([2, 4, 7, 9, n - 2, n - 1], device="cuda")
+    seq[2], seq[7] = pool.table.shape[0], 1 << 30
+    pos[4], pos[9], pos[n - 2] = -1, (1 << 24) - 1, pool.table.shape[1] * PAGE
+    pool.table[seq[n - 1].long(), pos[n - 1].long() // PAGE] = pool.pages  # and of whoever shares that page
+    live = torch.ones(n, dtype=torch.bool, device="cuda")
+    live[bad] = False
+    live &= ~((seq == seq[n - 1]) & (pos // PAGE == pos[n - 1] // PAGE))
+    q = torch.full((n, 5, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = (pool.k.clone(), pool.v.clone())
+    Q.cache_append(pool.cache, qkv, 5, seq, pos, q_out=q, q_norm=gq, k_norm=gk, rms_eps=1e-6, rope_theta=1e6)
+    with pytest.raises(Q.QuailError) as e:
+        Q.device_status()
+    assert e.value.name == "QUAIL_ERR_DEVICE_BOUNDS"
+    _check_append(pool, seq, pos, live, qkv, 5, gq, gk, q, before, 1e6)
+    status()
+
+
+# ------------------------------------------------------------------ hundreds of sequences
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("seqs,max_q", [(385, 1), (770, 3), (1537, 1), (1200, 2)])
+def test_attention_of_hundreds_of_sequences(kind, seqs, max_q):
+    """More sequences than the streaming kernel has threads, so that one of them plans several: ragged lengths, some of them
+    0, some sequences without queries."""
+    rng = np.random.RandomState(seqs)
+    own = rng.randint(0, 70, size=seqs)
+    own[rng.rand(seqs) < 0.1] = 0
+    own[seqs // 2] = 3000
+    nq = np.ones(seqs, dtype=int) if max_q == 1 else rng.randint(0, max_q + 1, size=seqs)
+    for prefix in (0, 32):
+        lens = [int(x) + prefix if x else 0 for x in own]
+        pool = Pool(kind, 2, lens, prefix, seed=seqs)
+        pool.fill(lens)
+        offs = [0] + [int(x) for x in np.cumsum(nq)]
+        q = torch.randn((offs[-1], 8, D), generator=torch.Generator(device="cuda").manual_seed(seqs), device="cuda").bfloat16()
+        check_attention(pool, q, None if max_q == 1 else offs, lens, prefix, False, max_q=max_q)
