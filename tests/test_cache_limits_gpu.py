@@ -181,6 +181,77 @@ def test_append_of_many_tokens_drops_bad_indices_only(kind, extra):
     status()
 
 
+# ------------------------------------------------------------------ far positions
+def _round_bf16(x):
+    """Nearest bf16 of 64-bit values in its normal range, ties to even."""
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -120))) - 7)
+    return torch.round(x / step) * step
+
+
+@pytest.mark.parametrize("theta", [1e6, 1e4, 1.5])
+def test_append_rotates_to_the_last_position(theta):
+    """Unit rows at positions up to 2^24 - 1 come out as cosines and sines. The kernel's are within 1.7e-7 of the exact ones
+    (emulated over every position: 1.6e-7), so what it rounds to bf16 lies between the roundings of exact -+ 1.7e-7."""
+    import trie_label_scoring_gb300 as Q
+    rng = np.random.RandomState(int(theta))
+    pos = np.unique(np.concatenate([
+        np.array([0, 1, 2, 4095, 65535, 65536, (1 << 20) + 1, (1 << 24) - 2, (1 << 24) - 1]),
+        rng.randint(0, 1 << 24, size=12000), rng.randint((1 << 24) - 4096, 1 << 24, size=3000)])).astype(np.int32)
+    pages = np.unique(pos // PAGE)
+    table = np.full((1, 1 << 20), -1, dtype=np.int32)
+    table[0, pages] = rng.permutation(pages.size)
+    k, v = (torch.zeros((pages.size, 1, PAGE, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache = Q.KVCache(k, v, torch.from_numpy(table).cuda())
+    n = pos.size
+    qkv = torch.zeros((n, 3 * D), device="cuda")
+    qkv[:, :64] = 1            # q: (cos, sin)
+    qkv[:, D + 64:2 * D] = 1   # k: (-sin, cos)
+    p = torch.from_numpy(pos).cuda()
+    q = torch.empty((n, 1, D), dtype=torch.bfloat16, device="cuda")
+    Q.cache_append(cache, qkv, 1, torch.zeros_like(p), p, q_out=q, rope_theta=theta)
+    status()
+    ang = p.double()[:, None] * theta ** (-torch.arange(64, device="cuda").double() / 64)
+    c, s = torch.cos(ang), torch.sin(ang)
+    at = torch.from_numpy(table).cuda()[0, p.long() // PAGE].long()
+    for got, want in ((q[:, 0], torch.cat([c, s], -1)), (k[at, 0, p.long() % PAGE], torch.cat([-s, c], -1))):
+        got = got.double()
+        assert bool((got >= _round_bf16(want - 1.7e-7)).all()) and bool((got <= _round_bf16(want + 1.7e-7)).all())
+
+
+@pytest.mark.parametrize("n", [65537, (1 << 20) + 1, (1 << 24) - 1])
+def test_letters_over_a_cache_of_far_documents(n):
+    """The answer token at positions up to 2^24 - 1: classify_letters_cached beside classify_letters, whose own rotation is
+    another one, on a document whose pages repeat."""
+    import synthetic as S
+    import trie_label_scoring_gb300 as Q
+    from tests import gpu_cases as C
+    sh = S.TINY
+    model = C.device_model(sh)
+    pages = 64
+    g = torch.Generator(device="cuda").manual_seed(n % 1000)
+    k, v = (0.02 * torch.randn((pages, sh.n_kv_heads, PAGE, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = (torch.arange(-(-n // PAGE), device="cuda", dtype=torch.int32) * 37 % pages).view(1, -1).contiguous()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    letters = [7, 4000, 12, 900, 55]
+    cache = Q.KVCache(k, v, table)
+    kv = Q.KV(k, v, table, lens, n)
+    got = []
+    for cached in (True, False):
+        outs = [torch.empty((1, 5), device="cuda"), torch.empty((1, 5), device="cuda"),
+                torch.empty((1,), dtype=torch.int32, device="cuda")]
+        size = (Q.workspace_size_letters_cached(model, cache, 5, n) if cached else
+                Q.workspace_size(model, None, 5, 1, n, Q.MODE_LETTERS))
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        if cached:
+            Q.classify_letters_cached(model, cache, None, lens, n, letters, 321, ws, *outs)
+        else:
+            Q.classify_letters(model, kv, letters, 321, 1, ws, *outs)
+        status()
+        got.append(outs)
+    assert float((got[0][0] - got[1][0]).abs().max()) <= C.TOL_LOGSCORE
+    assert int(got[0][2]) == int(got[1][2])
+
+
 # ------------------------------------------------------------------ hundreds of sequences
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("seqs,max_q", [(385, 1), (770, 3), (1537, 1), (1200, 2)])
