@@ -235,14 +235,16 @@ size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q
  *                 sees every key.
  *   scale:        0: 1/sqrt(128)
  *   lse:          device fp32 [total_q, n_q_heads] (natural logarithm), or NULL.
- * Sums and softmax statistics are fp32; the weights are rounded to bf16 (fp16
- * over e4m3 keys read directly) for the product with V. Keys past a sequence's
- * end are never used, whatever their slots hold; a key that causal hides from a
- * query has weight 0, which leaves a NaN or an infinity among its values a NaN, as
- * in the formula. A score of +infinity makes o and lse of its row NaN. Bounds that only the device can see set
- * QUAIL_ERR_DEVICE_BOUNDS and void that sequence's rows (all rows, for a prefix
- * page). Nothing in the workspace needs to start at zero; calls that may run at
- * the same time need one each. How the work is cut follows from the bounds. */
+ * Sums and softmax statistics are fp32. For the product with V the weights are
+ * two bf16 terms where bf16 keys are streamed, fp16 where e4m3 keys are, and one
+ * bf16 term in the tiles that many queries take. Keys past a sequence's end are
+ * never used, whatever their slots hold; a key that causal hides from a query has
+ * weight 0, which leaves a NaN or an infinity among its values a NaN, as in the
+ * formula. A score of +infinity makes o and lse of its row NaN. Bounds that only
+ * the device can see set QUAIL_ERR_DEVICE_BOUNDS and void that sequence's rows (all
+ * rows, for a prefix page). Nothing in the workspace needs to start at zero; calls
+ * that may run at the same time need one each. How the work is cut follows from the
+ * bounds. */
 quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
                                     const int32_t* seq_len, int32_t max_seq_len, const void* q,
                                     const int32_t* q_offsets, int32_t total_q, int32_t max_q_len, int32_t n_q_heads,

@@ -270,3 +270,32 @@ def test_attention_of_hundreds_of_sequences(kind, seqs, max_q):
         offs = [0] + [int(x) for x in np.cumsum(nq)]
         q = torch.randn((offs[-1], 8, D), generator=torch.Generator(device="cuda").manual_seed(seqs), device="cuda").bfloat16()
         check_attention(pool, q, None if max_q == 1 else offs, lens, prefix, False, max_q=max_q)
+
+
+# ------------------------------------------------------------------ bits of the streamed weights
+@pytest.fixture
+def streamed():
+    import trie_label_scoring_gb300 as Q
+    Q._test_set_attention_way(0)
+    yield
+    Q._test_set_attention_way(-1)
+
+
+@pytest.mark.parametrize("lens,prefix,nq", [([17] * 200, 0, 1), ([90, 400, 333], 64, 1), ([300] * 40, 0, 3), ([700], 0, 1)])
+def test_streamed_bf16_weights_are_two_terms(lens, prefix, nq, streamed):
+    """Queries and keys of -1, 0 and 1, so that the scores' sums are exact. A weight's two bf16 terms leave 2^-15 of it (a
+    step of the first, 2^-7, times half a step of the second); its exponent, up to 16, is rounded three times in fp32, 2^-18 of the weight at most, twice (numerator
+    and sum) with exp2 2^-17; fewer than 512 additions and joins in fp32 2^-15; the result is rounded once, 2^-8."""
+    pool = Pool("bf16", 2, lens, prefix)
+    pool.fill(lens)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    pool.k.copy_(torch.randint(-1, 2, pool.k.shape, generator=g, device="cuda"))
+    offs = [nq * i for i in range(len(lens) + 1)]
+    q = torch.randint(-1, 2, (offs[-1], 8, D), generator=g, device="cuda").bfloat16()
+    out, _ = attend(pool, q, None if nq == 1 else offs, lens, prefix, True)
+    o = attention_64(pool, q, offs, lens, prefix, True, D ** -0.5)[0]
+    pool.v.abs_()
+    size = attention_64(pool, q, offs, lens, prefix, True, D ** -0.5)[0]  # sum p|v|
+    allowed = (2.0 ** -15 + 2.0 ** -17 + 2.0 ** -15) * size + 2.0 ** -8 * o.abs()
+    err = (out.double() - o).abs()
+    assert bool((err <= allowed).all()), f"{int((err > allowed).sum())} of {err.numel()}"
