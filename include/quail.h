@@ -236,8 +236,9 @@ size_t quail_workspace_size_attention(const quail_cache_desc* cache, int32_t n_q
  *   scale:        0: 1/sqrt(128)
  *   lse:          device fp32 [total_q, n_q_heads] (natural logarithm), or NULL.
  * Sums and softmax statistics are fp32. For the product with V the weights are
- * two bf16 terms where bf16 keys are streamed, fp16 where e4m3 keys are, and one
- * bf16 term in the tiles that many queries take. Keys past a sequence's end are
+ * two bf16 terms where bf16 keys are streamed, fp16 where e4m3 keys are (times
+ * their value rows' powers of two; lost below 2^-32 of the largest), and one bf16
+ * term in the tiles that many queries take. Keys past a sequence's end are
  * never used, whatever their slots hold; a key that causal hides from a query has
  * weight 0, which leaves a NaN or an infinity among its values a NaN, as in the
  * formula. A score of +infinity makes o and lse of its row NaN. Bounds that only

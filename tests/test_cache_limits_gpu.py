@@ -299,3 +299,28 @@ def test_streamed_bf16_weights_are_two_terms(lens, prefix, nq, streamed):
     allowed = (2.0 ** -15 + 2.0 ** -17 + 2.0 ** -15) * size + 2.0 ** -8 * o.abs()
     err = (out.double() - o).abs()
     assert bool((err <= allowed).all()), f"{int((err > allowed).sum())} of {err.numel()}"
+
+
+def test_streamed_e4m3_weights_keep_small_ones(streamed):
+    """One key takes nearly all the weight but has no value; 511 others have weights of 2^-26 and values of 1. So many
+    sequences that a worker streams all keys of one: o is the others' sum, not 0."""
+    n, seqs = 512, 2000
+    pool = Pool("e4m3", 1, [n] * seqs)
+    pool.k.zero_()
+    pool.k[..., 0] = torch.tensor(-26.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    pool.v.fill_(torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8))
+    pool.ks.fill_(127)
+    pool.vs.fill_(127)
+    first = pool.table[:, 0].long()
+    pool.k[first, 0, 0] = 0
+    pool.v[first, 0, 0] = 0
+    q = torch.zeros((seqs, 4, D), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    out, lse = attend(pool, q, None, [n] * seqs, 0, True, scale=float(np.log(2)))
+    rest = (n - 1) * 2.0 ** -26
+    want = rest / (1 + rest)
+    # the weights are powers of two but for the score factor's rounding, 2^-24 * 26; the result is rounded to bf16
+    assert bool(((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -15) * want).all()), float(out.float().min())
+    # a lane adds the weights of 64 keys of the 512 in fp32; beside the first key's 1, whose half step is 2^-24, each of
+    # the other 63 adds nothing: 63 2^-26 at most are missing from the sum
+    assert bool(((lse.double() - np.log1p(rest)).abs() <= 63 * 2.0 ** -26 + 2.0 ** -23).all())

@@ -66,6 +66,10 @@ struct StreamCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 constexpr int kMinChunk = 2;  // units a worker takes at least
+// fp16 weights are taken times 2^7: at most 2^15 with the 2^8 that a score may pass the
+// reference maximum by. They keep their 11 bits down to 2^-21 of the largest, and are
+// lost below 2^-32 (2^-14 and 2^-25 as they are, which a sum over 100,000 keys would show).
+constexpr float kLift = 7.f;
 
 __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
 
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     for (int e = 0; e < 2; ++e) {
       const int r = 2 * tq + e;
       const float sum = e ? l.y : l.x, ml = e ? m_l.y : m_l.x;
-      const float mo = (e ? m_o.y : m_o.x) - (CODES ? 127.f : 0.f);
+      const float mo = (e ? m_o.y : m_o.x) - (CODES ? 127.f + kLift : 0.f);
       const int flat = flat0 + min(r, n_rows - 1);
       const size_t row = static_cast<size_t>(qr.lo + flat / G) * a.hq + g * G + flat % G;
       const bool rest = first_unit > 0;  // the piece continues an earlier worker's
@@ -588,7 +592,8 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     uint2 pb[kUnit], pl[kUnit];  // P^T fragments; over bf16 pages what their rounding left, as bf16 again
     // no key seen yet: the reference is still -inf, and every weight is 0
     auto neg = [](float m) { return m == -INFINITY ? 0.f : -m; };
-    const float2 rl = make_float2(neg(m_l.x), neg(m_l.y)), ro = make_float2(neg(m_o.x), neg(m_o.y));
+    const float2 rl = make_float2(neg(m_l.x), neg(m_l.y));
+    const float2 ro = make_float2(neg(m_o.x) + kLift, neg(m_o.y) + kLift);  // e4m3 only
 #pragma unroll
     for (int k = 0; k < 2 * kUnit; ++k) {
       const float2 x = add2(sc[k], rl);
