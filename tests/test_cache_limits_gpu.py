@@ -272,6 +272,53 @@ def test_attention_of_hundreds_of_sequences(kind, seqs, max_q):
         check_attention(pool, q, None if max_q == 1 else offs, lens, prefix, False, max_q=max_q)
 
 
+@pytest.mark.parametrize("seqs", [60, 5000])
+@pytest.mark.parametrize("prefix", [0, 16])
+@pytest.mark.parametrize("bad,value", [(None, 0), (5, 1 << 20), (0.6, -5), (0.6, 10), (0.59, 1 << 30), (0.3, 0)])
+def test_attention_bad_offsets_void_their_own_rows(seqs, prefix, bad, value, way):
+    """Sequences of 0 to 2 queries, rows before the first and behind the last; an offset that makes nonsense of the two
+    sequences it bounds leaves the others' rows right, and rows of no sequence as they were."""
+    import trie_label_scoring_gb300 as Q
+    hq, hkv, n, skip = 4, 2, 20 + prefix, 3
+    rng = np.random.RandomState(1)
+    nq = rng.randint(0, 3, size=seqs)
+    offs = skip + np.concatenate([[0], np.cumsum(nq)])
+    pool = Pool("bf16", hkv, [n] * 8, prefix)
+    pool.fill([n] * 8)
+    which = torch.from_numpy(rng.randint(0, 8, size=seqs)).cuda()
+    cache = Q.KVCache(pool.k, pool.v, pool.table[which].contiguous())
+    total = int(offs[-1]) + 4
+    q = torch.randn((total, hq, D), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").bfloat16()
+    of = torch.from_numpy(offs.astype(np.int32)).cuda()
+    row_seq = torch.from_numpy(np.repeat(np.arange(seqs), nq)).cuda()
+    o = torch.zeros((total, hq, D), dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(o)
+    for doc in range(8):  # all rows on one document at once
+        rows = skip + torch.nonzero(which[row_seq] == doc)[:, 0]
+        at = [0 if d <= doc else rows.numel() for d in range(9)]
+        r = attention_64(pool, q[rows], at, [n if d == doc else 0 for d in range(8)], prefix, False, D ** -0.5)
+        o[rows], tol[rows] = r[0], r[2]
+    live = torch.zeros(total, dtype=torch.bool, device="cuda")
+    live[skip:int(offs[-1])] = True
+    if bad is not None:
+        bad = int(bad if bad > 1 else bad * seqs)
+        of[bad] = value
+        live[skip:int(offs[-1])] = (row_seq != bad) & (row_seq != bad - 1)
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(Q.workspace_size_attention(cache, hq, total, 2, n, prefix), dtype=torch.uint8, device="cuda")
+    L = torch.full((seqs,), n, dtype=torch.int32, device="cuda")
+    Q.attention_shared(cache, q, of, L, 2, n, pool.prefix_pages, out, ws, causal=False)
+    if bad is None:
+        status()
+    else:
+        with pytest.raises(Q.QuailError) as e:
+            status()
+        assert e.value.name == "QUAIL_ERR_DEVICE_BOUNDS"
+    err = ((out.double() - o).abs() <= tol).all(-1).all(-1)
+    assert bool(err[live].all()), f"{int((~err[live]).sum())} rows wrong"
+    assert bool((out[:skip] == 5).all()) and bool((out[int(offs[-1]):] == 5).all())
+
+
 # ------------------------------------------------------------------ bits of the streamed weights
 @pytest.fixture
 def streamed():

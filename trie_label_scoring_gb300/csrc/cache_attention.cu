@@ -777,8 +777,11 @@ __global__ void __launch_bounds__(32 * WARPS) attention_join_kernel(SharedAttnAr
   if (a.q_offsets != nullptr) {  // the sequence that has row t
     if (threadIdx.x == 0) s_b = -1;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.c.num_seqs; i += 32 * WARPS)
-      if (a.q_offsets[i] <= t && t < a.q_offsets[i + 1]) s_b = i;
+    for (int i = threadIdx.x; i < a.c.num_seqs; i += 32 * WARPS) {
+      const int lo = a.q_offsets[i], hi = a.q_offsets[i + 1];
+      // a range that is none (query_range) has no row: it would take those of others
+      if (lo <= t && t < hi && lo >= 0 && hi <= a.total_q && hi - lo <= a.max_q) s_b = i;
+    }
     __syncthreads();
     b = s_b;
     if (b < 0) return;  // of no sequence: left as it was
