@@ -146,14 +146,18 @@ quail_status quail_trie_upload(quail_trie* trie, quail_stream_t stream);
  * Ultra-High Throughput AI-SQL Engine", sec. 3.2.4): writing it, reading it
  * back, and attention over it for sequences that share their first tokens. A
  * bf16 cache filled by quail_cache_append is what quail_paged_kv describes
- * (same pools, same page table).
+ * (same pools, same page table). An e4m3 cache, and a prefix read once for all
+ * sequences, are for the calls of this section and quail_classify_letters_cached;
+ * the other classify calls read bf16 pages, a shared prefix's once per document.
  *
  * dtype QUAIL_DTYPE_BF16: k_pool, v_pool bf16 [num_pages, n_kv_heads, 16, 128];
  *                k_scale, v_scale NULL.
  * dtype QUAIL_DTYPE_E4M3: the pools hold e4m3 codes in one byte, and k_scale,
- *                v_scale [num_pages, n_kv_heads, 16] one byte e (1..254) per
+ *                v_scale [num_pages, n_kv_heads, 16] one byte e (3..246) per
  *                (page, head, slot): element = code * 2^(e - 127), a bf16 value
- *                exactly.
+ *                exactly. (quail_cache_append writes 27..246, and 247 for a row
+ *                with an element above 1.75 * 2^127, whose largest code may stand
+ *                for an infinity as the element's bf16 rounding may.)
  * page_table:    device int32 [num_seqs, max_pages]; entry (b, p) = physical
  *                page of positions [16p, 16p + 16) of sequence b. */
 typedef enum { QUAIL_DTYPE_BF16 = 0, QUAIL_DTYPE_F32 = 1, QUAIL_DTYPE_E4M3 = 2 } quail_dtype;

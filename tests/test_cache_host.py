@@ -224,7 +224,7 @@ def test_attention_workspace_serves_all_smaller_bounds(dtype):
 def test_attention_workspace_grows_with_the_length():
     """64 sequences of one query behind 512 shared keys, 32 heads on 8; and 16 sequences of one."""
     for seqs, prefix in ((64, 512), (16, 0)):
-        sizes = [_size(Q.DTYPE_BF16, [8, 32, seqs, seqs, 1, n, prefix]) for n in (512, 1024, 2048, 3072, 8192, 16384)]
+        sizes = [_size(Q.DTYPE_BF16, [8, 32, seqs, seqs, 1, n, prefix]) for n in (512, 1024, 2048, 4096, 8192, 16384)]
         assert sizes == sorted(sizes)
 
 
@@ -237,6 +237,6 @@ def test_letters_workspace_grows_with_its_bounds(seqs):
     def size(letters, n, prefix):
         return Q.lib().quail_workspace_size_letters_cached(ctypes.byref(m), ctypes.byref(d), letters, n, prefix)
 
-    for sizes in ([size(26, n, 512) for n in (512, 1024, 3072, 8192, 16384, 100000)],
+    for sizes in ([size(26, n, 512) for n in (512, 1024, 4096, 8192, 16384, 100000)],
                   [size(26, 8192, p) for p in (0, 16, 512, 2048, 8192)], [size(k, 8192, 0) for k in (2, 26, 300, 8192)]):
         assert sizes[0] > 0 and sizes == sorted(sizes)

@@ -660,6 +660,7 @@ def cache_read(cache: KVCache, token_seq, token_pos, k_out, v_out, stream=None) 
 
 def workspace_size_attention(cache: KVCache, n_q_heads: int, total_q: int, max_q_len: int, max_seq_len: int,
                              prefix_len: int = 0) -> int:
+    """Bytes that serve these bounds and any smaller ones."""
     n = lib().quail_workspace_size_attention(cache.ref, int(n_q_heads), int(total_q), int(max_q_len),
                                              int(max_seq_len), int(prefix_len))
     if n == 0:
@@ -671,7 +672,7 @@ def attention_shared(cache: KVCache, q, q_offsets, seq_len, max_q_len: int, max_
                      workspace, lse=None, causal: bool = True, scale: float | None = None, stream=None) -> None:
     """q, out [total_q, hq, 128] bf16; q_offsets int32 [num_seqs + 1] or None (one query per sequence);
     seq_len int32 [num_seqs], the shared keys included; prefix_pages int32 [prefix_len / 16] or None;
-    lse fp32 [total_q, hq] or None; workspace uint8, workspace_size_attention bytes."""
+    lse fp32 [total_q, hq] or None; workspace uint8, workspace_size_attention bytes; scale None or 0: 1/sqrt(128)."""
     n, hq, d = q.shape
     if d != 128:
         raise QuailError(-1, "q must be [total_q, hq, 128]")

@@ -1012,7 +1012,9 @@ std::atomic<int> g_attention_way{-1};
 // (the constants fitted to 3,200 sizes, each timed in every way: 1 to 256 sequences
 // of 1 to 100 queries, 1 to 8 heads a group, prefixes to 32,768, own keys to 6,000,
 // both types; the way it takes costs 0.7% more than the fastest on the mean over
-// them.) Measured, 32 heads on 8, us, streamed / streamed + prefix on tiles / tiles
+// them. The bounds are all it sees: it takes every sequence to be max_seq_len long with
+// max_q queries, so one long sequence or prefill among many short ones is estimated as
+// if all were.) Measured, 32 heads on 8, us, streamed / streamed + prefix on tiles / tiles
 // apart / one pass:
 //   bf16 256 x 1 query  prefix  2048,  300 own keys  120 /  82 / 165 / 446
 //   bf16  64 x 1        prefix   512, 1500 own keys   76 /  78 / 111 / 112

@@ -158,9 +158,9 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 //   A = g_j cos, B = -g_j+64 sin, C = g_j+64 cos, D = g_j sin,
 // so a row costs four products a pair and one by r: with angles and gains
 // applied row by row the kernel was bound by its instructions, not by memory.
-// 23,100 tokens of 48 heads (bf16 in, e4m3 cache): 103 us, 5.1 TB/s, L1 at 79%. The
-// rotations kept in registers (a warp to a token) cost occupancy, 107 us; two rows
-// ahead 131, 16 tokens a block 109.
+// 23,100 tokens of 48 heads, bf16 in: e4m3 cache 103 us, 5.1 TB/s, L1 at 78%; bf16 cache
+// 102 us, 5.6 TB/s. The rotations kept in registers (a warp to a token) cost occupancy,
+// 107 us (e4m3); two rows ahead 131, 16 tokens a block 109.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendGroups = kAppendThreads / kRowLanes;
 
@@ -298,8 +298,9 @@ __device__ __forceinline__ void store_codes_bf16(bf16* out, int l, const uint4& 
 }
 
 // Block = a few consecutive tokens: their pages are looked up once, then every
-// group copies kReadRows rows at a time, loads first. 131,072 e4m3 tokens of 8 heads:
-// 124 us, 6.5 TB/s, 96% of a plain copy.
+// group copies kReadRows rows at a time, loads first. 131,072 tokens of 8 heads: e4m3
+// 124 us, 6.5 TB/s, 96% of a plain copy; bf16 159 us, 6.8 TB/s (five blocks an SM leave it
+// 48 registers, and it spills 44 bytes).
 constexpr int kReadRows = 4;
 constexpr int kReadTokens = 64;  // at most
 

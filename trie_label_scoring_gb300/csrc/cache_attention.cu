@@ -45,7 +45,7 @@ namespace {
 // scale neither overflow P nor starve the sum.
 //
 // Bound, with up to 8 rows, by HBM: 64 sequences of 2,048 own keys (8 KV heads, bf16)
-// take 89 us, 6.1 TB/s; e4m3, 4,096 keys, 98 us, 5.7 TB/s. With more rows by the
+// take 91 us, 5.9 TB/s; e4m3, 4,096 keys, 95 us, 5.9 TB/s. With more rows by the
 // latency of its products and softmax, three workers to a scheduler: 160 clocks of an
 // SM for a pass of 8 rows over an e4m3 page. Taking the units' maxima only when some
 // weight would pass 2^8, without their shuffles, was 2% slower.

@@ -20,6 +20,14 @@
 // tile's chain, 1.45 us a block; e4m3 1.9 us, the widening warps competing with it
 // for shared memory.
 //
+// P is one bf16 term, so o is off by 0.0023 relative where its own rounding alone gives
+// 0.0017. A second term in the other half of S's columns gives that 0.0017 and costs half
+// as many products again (3,072 clocks a block); written the plain way, which spills 650 to
+// 800 bytes, the 16 prefills took 732 us.
+//
+// The softmax keeps 128 scores, 32 columns of P and its sums in 200 registers, and spills a
+// little for it: 32 and 44 bytes (bf16), 120 and 136 (e4m3, launched with 128).
+//
 // Few CTAs' worth of rows: their keys are cut into up to eight ranges, a CTA each in one
 // cluster, which leave their parts in shared memory and join them there row by row
 // (more ranges, and parts of other kernels, go through memory and the join kernel).
