@@ -109,3 +109,64 @@ def test_layer_stack_capture_and_replay():
             torch.empty((N,), dtype=torch.int32, device="cuda")]
     pools = [x for group in kv.tensors[:2] for x in group]
     _replays_like_eager(lambda: Q.classify_trie_tree_ml(model, kv, t, N, ws, *outs), outs, pools)
+
+
+def _trie_case(seed=0):
+    import trie_label_scoring_gb300 as Q
+    w = S.WORKLOADS["tiny-support10-4x128"]
+    docs, kv, k, v, table, lens = _docs(w)
+    ls = S.make_labels(w, seed)
+    trie = Q.Trie(ls.labels, ls.root_token, w.shape.vocab, ls.continuation)
+    N, M = w.num_docs, len(ls.labels)
+    outs = [torch.empty((N, M), device="cuda"), torch.empty((N, M), device="cuda"),
+            torch.empty((N,), dtype=torch.int32, device="cuda")]
+    return C.device_model(w.shape), docs, kv, [k, v], trie, N, outs
+
+
+def test_trie_tree_capture_and_replay():
+    import trie_label_scoring_gb300 as Q
+    model, docs, kv, pools, trie, N, outs = _trie_case()
+    ws = torch.empty(Q.workspace_size(model, trie, 0, N, docs.max_doc_len, Q.MODE_TRIE_TREE), dtype=torch.uint8, device="cuda")
+    _replays_like_eager(lambda: Q.classify_trie_tree(model, kv, trie, N, ws, *outs), outs, pools)
+
+
+def test_trie_tree_without_allocation_capture_and_replay():
+    import trie_label_scoring_gb300 as Q
+    model, docs, kv, pools, trie, N, outs = _trie_case()
+    _replays_like_eager(lambda: Q.classify_trie_tree_noalloc(model, kv, trie, N, *outs), outs, pools)
+
+
+def test_trie_decode_capture_and_replay():
+    import trie_label_scoring_gb300 as Q
+    w = S.WORKLOADS["tiny-support10-4x128"]
+    docs, kv, k, v, table, lens = _docs(w)
+    model = C.device_model(w.shape)
+    trie = Q.Trie([[5, 6, 7], [5, 6, 8], [5, 9], [10, 11, 12], [10, 13]], 17, w.shape.vocab)
+    N = w.num_docs
+    ws = torch.empty(Q.workspace_size(model, trie, 0, N, docs.max_doc_len, Q.MODE_TRIE_DECODE), dtype=torch.uint8, device="cuda")
+    cur, lab, act = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (N, N, 1))
+
+    def call():  # greedy decoding from the root to the end
+        cur.zero_()
+        lab.fill_(-1)
+        for _ in range(3):
+            Q.classify_trie_decode_step(model, kv, trie, N, cur, lab, act, ws)
+
+    _replays_like_eager(call, [cur, lab, act], [k, v])
+
+
+def test_shortlist_capture_and_replay():
+    import trie_label_scoring_gb300 as Q
+    w = S.WORKLOADS["tiny-support10-4x128"]
+    docs, kv, k, v, table, lens = _docs(w)
+    model = C.device_model(w.shape)
+    rng = np.random.default_rng(4)
+    labels = [[int(a), int(b)] for a in rng.choice(w.shape.vocab, size=12, replace=False)
+              for b in rng.choice(w.shape.vocab, size=5, replace=False)]
+    trie = Q.Trie(labels, 17, w.shape.vocab)
+    sl = Q.Shortlist(trie, 1)
+    N, M = w.num_docs, len(labels)
+    ws = torch.empty(Q.workspace_size_shortlist(model, trie, sl, 3, N, docs.max_doc_len), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((N, M), device="cuda"), torch.empty((N, M), device="cuda"),
+            torch.empty((N,), dtype=torch.int32, device="cuda"), torch.empty((N, 3), dtype=torch.int32, device="cuda")]
+    _replays_like_eager(lambda: Q.classify_trie_tree_shortlist(model, kv, trie, sl, 3, N, ws, *outs), outs, [k, v])

@@ -118,8 +118,8 @@ quail_status encode_2d_codes(CUtensorMap* m, const void* ptr, uint64_t rows, uin
 }
 
 // A call's own integers to the device. A copy that is captured into a graph would
-// read `host` again at every replay, after the call has freed it: there they travel
-// as kernel arguments, which the graph keeps.
+// read `host` again at every replay, when the call (or its trie) may be gone: there they
+// travel as kernel arguments, which the graph keeps.
 quail_status copy_ints(int* dst, const std::vector<int32_t>& host, cudaStream_t st) {
   cudaStreamCaptureStatus capture;
   CUDA_TRY(cudaStreamIsCapturing(st, &capture));
@@ -569,8 +569,10 @@ quail_status copy_trie_tree_image(const quail_trie* t, uint8_t* dst, cudaStream_
                               &img->label_term_eval,    &img->label_term_slot,   &img->label_prefix_eval};
   size_t off = 0;
   for (int i = 0; i < 9; ++i) {
-    if (!arrays[i]->empty())
-      CUDA_TRY(cudaMemcpyAsync(dst + off, arrays[i]->data(), arrays[i]->size() * 4, cudaMemcpyHostToDevice, st));
+    if (!arrays[i]->empty()) {
+      const quail_status s = copy_ints(reinterpret_cast<int*>(dst + off), *arrays[i], st);
+      if (s != QUAIL_OK) return s;
+    }
     *fields[i] = reinterpret_cast<const int32_t*>(dst + off);
     off += round_up(std::max<size_t>(arrays[i]->size(), 1) * 4, 256);
   }
