@@ -371,3 +371,18 @@ def test_streamed_e4m3_weights_keep_small_ones(streamed):
     # a lane adds the weights of 64 keys of the 512 in fp32; beside the first key's 1, whose half step is 2^-24, each of
     # the other 63 adds nothing: 63 2^-26 at most are missing from the sum
     assert bool(((lse.double() - np.log1p(rest)).abs() <= 63 * 2.0 ** -26 + 2.0 ** -23).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nq,prefix", [(1, 0), (1, 1024), (5, 640)])
+def test_attention_of_a_padded_batch(kind, nq, prefix, way):
+    """A batch padded far past its queries: thousands of rows of no sequence, which the bounds count, stay as they are."""
+    lens = [3000 + prefix, 20 + prefix]
+    pool = Pool(kind, 2, lens, prefix)
+    pool.fill(lens)
+    offs = [0, nq, 2 * nq]
+    q = torch.randn((2 * nq, 8, D), generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").bfloat16()
+    o, z, tol_o, tol_l = attention_64(pool, q, offs, lens, prefix, True, D ** -0.5)
+    for rows_after in (0, 5000):
+        out, lse = attend(pool, q, offs, lens, prefix, True, rows_after=rows_after)
+        assert bool(((out.double() - o).abs() <= tol_o).all()) and bool(((lse.double() - z).abs() <= tol_l).all())
