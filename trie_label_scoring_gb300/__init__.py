@@ -491,7 +491,7 @@ def device_status(stream=None) -> None:
 
 def _test_set_pipeline_wait_limit(cycles: int) -> None:
     """Test hook (not in the public header): every pipeline wait gives up
-    after `cycles` cycles (cache attention: below 0 at once, without a try); 0 restores the default limit."""
+    after `cycles` cycles (below 0: the cache attention's cannot but run out); 0 restores the default limit."""
     _check(lib().quail_test_set_pipeline_wait_limit(int(cycles)))
 
 

@@ -1702,7 +1702,7 @@ quail_status quail_classify_trie_decode_step(const quail_model_desc* model, cons
 }
 
 // Test hook, not part of the public header: shortens the limit of every
-// pipeline wait (cycles > 0; below 0 the cache attention's waits give up at once),
+// pipeline wait (cycles > 0; below 0 the cache attention's cannot but run out),
 // or restores the default (0), so that a test can make a wait run out and check that
 // QUAIL_ERR_DEVICE_TIMEOUT comes back through quail_device_status with the context
 // still usable. Waits that drain in-flight copies and MMAs before a block exits keep

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
                                                              Cfg::kScan);
   const long long limit_clk = pipeline_wait_limit();
   if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 32);
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 32 + (limit_clk < 0));
     fence_mbar_init();
     if (warp == 0) *abort_flag = 0;
   }
@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(StreamCfg<CODES>::kThreads, 1)
     // Gave up: no copy, and no arrival that follows one, may land after the CTA's end.
     asm volatile("cp.async.wait_all;" ::: "memory");
     for (int k = max(0, issued - kStages); k < issued; ++k) {
+      if (limit_clk < 0 && lane == 0) mbar_arrive(&bars[k % kStages]);
       const long long t0 = clock64();
       while (!mbar_try_wait(smem_u32(&bars[k % kStages]), static_cast<uint32_t>((k / kStages) & 1)) &&
              clock64() - t0 <= kWaitLimitCycles) {

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(TileCfg<CODES>::kThreads, 1)
       mbar_init(&bars->code_empty[s], 4);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->s_full[t], 1 + (limit_clk < 0));
       mbar_init(&bars->p_full[t], 128);
       mbar_init(&bars->pv_done[t], 1);
     }

@@ -27,8 +27,9 @@ __device__ __forceinline__ QueryRange query_range(const SharedAttnArgs& a, int b
 }
 
 // mbar_wait for waits that are often not over at once: the limit comes in a
-// register instead of a load between two tries. A negative limit (a test's) makes
-// every wait give up without a try.
+// register instead of a load between two tries. With a negative limit (a test's) the
+// kernels begin with barriers that expect an arrival too many, so that the waits for
+// pages (streamed) or scores (tiles) never end.
 __device__ __forceinline__ long long pipeline_wait_limit() {
   return *const_cast<const volatile long long*>(&g_pipeline_wait_limit);
 }
@@ -36,10 +37,10 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   const uint32_t a = smem_u32(bar);
   // A try waits a while by itself; most waits that the first does not see out end in
   // the second, which the checks would hold up.
-  if (limit >= 0 && mbar_try_wait(a, parity)) return true;
+  if (mbar_try_wait(a, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (limit >= 0 && mbar_try_wait(a, parity)) return true;
+    if (mbar_try_wait(a, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > limit) {
       *abort_flag = 1;
