@@ -12,8 +12,8 @@
 // PV_0(j) S_0(j+1) PV_1(j) S_1(j+1) keeps the tensor pipe on one tile while the
 // softmax warpgroup of the other works. The four products of a block are 2,048
 // tensor cycles; with the softmax between them a block takes 2,800 to 3,150, since
-// S -> maximum -> weights -> P of a tile (1,630) and its own two products (1,024) are
-// one chain: the tensor memory has no room for a second S. A CTA takes another 3,000
+// S -> maximum -> weights -> P of a tile (1,630, a thread to a row) and its own two
+// products (1,024) are one chain: the tensor memory has no room for a second S. A CTA takes another 3,000
 // to 5,000 to its first S and 3,000 to write its rows.
 // 16 prefills of 128 to 1,024 tokens behind 2,048 (32 heads on 8): 318 us,
 // 1,160 TFLOP/s. A CTA with one tile's rows is bound by that
