@@ -256,6 +256,148 @@ quail_status quail_attention_shared(const quail_cache_desc* cache, const int32_t
                                     int32_t causal, float scale, void* workspace, size_t workspace_bytes, void* out,
                                     float* lse, quail_stream_t stream);
 
+/* ------------------------------------------------------------ drafted trees
+ * Decoding with a tree of drafted tokens per sequence over the document cache ("Quail
+ * intro", sec. 3.2.4, attends to a tree of continuations in one request; here the tree is
+ * each sequence's own and is cached like any tokens). One step: quail_cache_resize makes
+ * room for every sequence's tree and says where its tokens go; quail_tree_plan turns the
+ * trees' parents into masks and rotary positions; per layer quail_cache_append_rope writes
+ * the drafted tokens and quail_attention_tree attends; quail_tree_accept keeps the branch
+ * that the model would have taken. A trie's nodes (quail_trie_view: parent) are such a
+ * tree. */
+
+/* Page tables and slot maps from the sequences' lengths. A sequence that grows from
+ * old_len to new_len takes the pages that it lacks from the free pages, one that shrinks
+ * gives back those that it no longer needs. The free pages are a ring: free_state[1] of
+ * them from free_ring[free_state[0]] on, around the end; what is given back goes behind the
+ * last and is not taken in the same call. Growing sequences are granted in order, up to the
+ * first for which the free pages or max_tokens do not suffice; from there on none grows.
+ *   cache:        its page_table is written (the pools are not touched): entries of new
+ *                 pages, those of a sequence's first prefix_len positions when it grows
+ *                 from 0, -1 where pages were given back; the rest is left as it was.
+ *   prefix_pages: device int32 [prefix_len / 16], pages that all sequences share; never
+ *                 taken or given back. prefix_len a multiple of 16; 0: NULL.
+ *   old_len, new_len: device int32 [num_seqs], 0 or at least prefix_len, at most
+ *                 16 max_pages
+ *   free_ring:    device int32 [num_pages]; free_state: device int32 [4]: first, count, 0, 0.
+ *                 Both are updated; calls that share them follow one another.
+ *   granted_len:  device int32 [num_seqs] (not old_len or new_len), out: new_len, or
+ *                 old_len where it was not granted
+ *   token_offsets: device int32 [num_seqs + 1], out: the new tokens of sequence b are
+ *                 [token_offsets[b], token_offsets[b + 1]) (none where it shrinks)
+ *   token_seq, token_pos: device int32 [max_tokens], out: sequence and position of each
+ *                 new token, as the calls above take them; -1 and 0 behind the last. Both
+ *                 NULL: the tables only (max_tokens 0 then, and no limit).
+ * The first position of a sequence that grows from 0 is prefix_len. A length out of range
+ * sets QUAIL_ERR_DEVICE_BOUNDS and leaves that sequence as it is; so does a free_state that
+ * is none or would pass num_pages, for all that grow or shrink. */
+quail_status quail_cache_resize(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
+                                const int32_t* old_len, const int32_t* new_len, int32_t* free_ring,
+                                int32_t* free_state, int32_t* granted_len, int32_t* token_offsets, int32_t* token_seq,
+                                int32_t* token_pos, int32_t max_tokens, quail_stream_t stream);
+
+/* Rotary positions. The first rotary_dim of a head's 128 dims turn, the rest pass:
+ * pair j < rotary_dim / 2 is (j, j + rotary_dim / 2) (QUAIL_ROPE_HALF) or (2j, 2j + 1)
+ * (QUAIL_ROPE_INTERLEAVED), its angle the position times w_j, cosine and sine times
+ * magnitude. With r = rotary_dim and w_j = theta^(-2j/r):
+ *   QUAIL_ROPE_PLAIN   w_j
+ *   QUAIL_ROPE_LINEAR  w_j / factor (positions interpolated)
+ *   QUAIL_ROPE_BASE    theta * factor^(r / (r - 2)) in theta's place
+ *   QUAIL_ROPE_PARTS   (1 - s) w_j / factor + s w_j, s = (t - low) / (high - low) held to
+ *                      [0, 1], t = original_len w_j / (2 pi) the turns within the
+ *                      original context: frequencies scaled by parts (YaRN, Peng et al.
+ *                      2023, which also takes magnitude 0.1 ln(factor) + 1). */
+typedef enum { QUAIL_ROPE_HALF = 0, QUAIL_ROPE_INTERLEAVED = 1 } quail_rope_layout;
+typedef enum { QUAIL_ROPE_PLAIN = 0, QUAIL_ROPE_LINEAR = 1, QUAIL_ROPE_BASE = 2, QUAIL_ROPE_PARTS = 3 } quail_rope_scaling;
+
+typedef struct {
+  int32_t layout;
+  int32_t rotary_dim;  /* a multiple of 16, at most 128 */
+  float theta;         /* above 1 */
+  int32_t scaling;
+  float factor;        /* at least 1; not looked at for QUAIL_ROPE_PLAIN */
+  float original_len;  /* QUAIL_ROPE_PARTS only: above 0, and low < high */
+  float low, high;
+  float magnitude;     /* above 0, or 0: 1 */
+} quail_rope_desc;
+
+/* quail_cache_append with the rotation that `rope` describes, and positions for it apart
+ * from the slots: token t goes to position token_pos[t] of its sequence and turns by
+ * rope_pos[t] (device int32 [num_tokens], 0 to 2^24 - 1; NULL: token_pos), so that the
+ * nodes of a tree lie one after the other and turn by their depths. A rope_pos out of
+ * range sets QUAIL_ERR_DEVICE_BOUNDS and drops that token. All else as there; with
+ * QUAIL_ROPE_HALF, rotary_dim 128 and QUAIL_ROPE_PLAIN the results are the same bits. */
+quail_status quail_cache_append_rope(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
+                                     int32_t num_tokens, int32_t n_q_heads, const int32_t* token_seq,
+                                     const int32_t* token_pos, const int32_t* rope_pos, const void* q_norm,
+                                     const void* k_norm, float rms_eps, const quail_rope_desc* rope, void* q_out,
+                                     quail_stream_t stream);
+
+enum { QUAIL_MAX_TREE = 1024 };
+
+/* The masks of num_seqs trees and their nodes' rotary positions.
+ *   parent:    device int32 [total]: the node that node i hangs off, numbered within its
+ *              tree, less than i; -1: none
+ *   q_offsets: device int32 [num_seqs + 1]: sequence b's nodes are [q_offsets[b],
+ *              q_offsets[b + 1]), at most max_q_len, which is at most QUAIL_MAX_TREE
+ *   seq_len:   device int32 [num_seqs], tokens with the tree's
+ *   mask:      device [total, ceil(max_q_len / 32)] 32-bit words, out: bit j % 32 of word
+ *              j / 32 of row i is set if node j is node i's ancestor or itself
+ *   rope_pos:  device int32 [total], out: seq_len - nodes + depth
+ * Rows outside every range are left as they were. A parent out of range sets
+ * QUAIL_ERR_DEVICE_BOUNDS and counts as -1; offsets or lengths out of range void their
+ * tree. */
+quail_status quail_tree_plan(const int32_t* parent, const int32_t* q_offsets, const int32_t* seq_len, int32_t num_seqs,
+                             int32_t total, int32_t max_q_len, void* mask, int32_t* rope_pos, quail_stream_t stream);
+
+/* Bytes of device workspace that quail_attention_tree needs at most for these bounds
+ * and any smaller ones (256-byte aligned base required); 0 on invalid arguments. */
+size_t quail_workspace_size_attention_tree(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
+                                           int32_t max_q_len, int32_t max_seq_len);
+
+/* GQA attention of the nodes of a tree per sequence over the cache, the tree's own tokens
+ * cached already as the sequence's last: o = softmax(scale q K^T) V, lse its log-sum-exp,
+ * over the keys before the tree and those of the tree that the node's mask row has set.
+ *   q, out:    device bf16 [total_q, n_q_heads, 128]
+ *   q_offsets: as quail_tree_plan's; rows outside every range are left as they were
+ *   seq_len:   device int32 [num_seqs], keys of each sequence, the tree's n included: 0
+ *              (no keys at all: o = 0, lse = -inf), or n to max_seq_len (at most 2^30)
+ *   mask:      device [total_q, ceil(max_q_len / 32)] words as quail_tree_plan writes
+ *              them, or any others; bits from n on are not looked at. A node that sees no
+ *              key gets o = 0 and lse = -inf.
+ *   scale:     0: 1/sqrt(128)
+ *   lse:       device fp32 [total_q, n_q_heads] (natural logarithm), or NULL
+ * Errors, statistics and non-finite values as quail_attention_shared's. */
+quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, const int32_t* q_offsets,
+                                  const int32_t* seq_len, const void* mask, int32_t total_q, int32_t max_q_len,
+                                  int32_t max_seq_len, int32_t n_q_heads, float scale, void* workspace,
+                                  size_t workspace_bytes, void* out, float* lse, quail_stream_t stream);
+
+/* The verdict on drafted trees. Node 0 is the sequence's newest token and is right; another
+ * node is right if its parent is, its drafted token is the one that the model took after
+ * its parent, and no earlier child of that parent has the same token. The right nodes are a
+ * path. Their K and V rows move to the tree's first slots, in every cache, so that the
+ * sequence is new_len tokens long and goes on from there (quail_cache_resize gives the
+ * pages behind it back).
+ *   caches:   host array of n_caches caches, one per layer of a model, alike but for their
+ *             pools; may be empty (the verdict only). Pages that two sequences share are
+ *             not among a tree's.
+ *   parent, q_offsets, seq_len, max_q_len, total: as quail_tree_plan's; mask: as it wrote it
+ *   draft:    device int32 [total], the nodes' tokens
+ *   taken:    device int32 [total], the token that the model takes after each node
+ *   path:     device int32 [total], out: the right nodes' numbers in order of depth, -1
+ *             behind the last of each tree
+ *   accepted: device int32 [num_seqs], out: how many are right
+ *   new_len:  device int32 [num_seqs] (not seq_len), out: seq_len - nodes + accepted
+ *   bonus:    device int32 [num_seqs], out: taken of the last right node (-1: no nodes)
+ * Errors as quail_tree_plan; a page id out of range among the path's rows sets
+ * QUAIL_ERR_DEVICE_BOUNDS and moves none of that sequence's. */
+quail_status quail_tree_accept(const quail_cache_desc* caches, int32_t n_caches, const int32_t* parent,
+                               const void* mask, const int32_t* draft, const int32_t* taken, const int32_t* q_offsets,
+                               const int32_t* seq_len, int32_t num_seqs, int32_t total, int32_t max_q_len,
+                               int32_t* path, int32_t* accepted, int32_t* new_len, int32_t* bonus,
+                               quail_stream_t stream);
+
 /* ------------------------------------------------------------------ model
  * One decoder layer's attention block plus the output head, as used at the
  * answer positions: x = E[tok]; x^ = RMSNorm(x)*in_norm; q,k,v = x^ W^T;

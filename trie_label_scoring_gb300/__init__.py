@@ -30,6 +30,12 @@ Entry points (same names as the C ABI, without the quail_ prefix):
                                  -> quail_workspace_size_attention / quail_attention_shared
   workspace_size_letters_cached(...), classify_letters_cached(...)
                                  -> quail_workspace_size_letters_cached / quail_classify_letters_cached
+  cache_resize(...), Rope(...), cache_append_rope(...)
+                                 -> quail_cache_resize / quail_cache_append_rope
+  tree_plan(...), tree_accept(...)
+                                 -> quail_tree_plan / quail_tree_accept
+  workspace_size_attention_tree(...), attention_tree(...)
+                                 -> quail_workspace_size_attention_tree / quail_attention_tree
 """
 from __future__ import annotations
 
@@ -127,6 +133,12 @@ class CacheDesc(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("theta", ctypes.c_float),
+                ("scaling", ctypes.c_int32), ("factor", ctypes.c_float), ("original_len", ctypes.c_float),
+                ("low", ctypes.c_float), ("high", ctypes.c_float), ("magnitude", ctypes.c_float)]
+
+
 class TrieCSR(ctypes.Structure):
     _fields_ = [("n_nodes", ctypes.c_int32), ("num_labels", ctypes.c_int32), ("n_eval", ctypes.c_int32),
                 ("n_eval_children", ctypes.c_int32), ("max_depth", ctypes.c_int32),
@@ -205,6 +217,23 @@ _SIGNATURES = {
                                                      ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                                      ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p,
                                                      ctypes.c_void_p, ctypes.c_void_p]),
+    "quail_cache_resize": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_void_p, ctypes.c_int32,
+                                          *[ctypes.c_void_p] * 8, ctypes.c_int32, ctypes.c_void_p]),
+    "quail_cache_append_rope": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_void_p, ctypes.c_int,
+                                               ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                               *[ctypes.c_void_p] * 5, ctypes.c_float, ctypes.POINTER(RopeDesc),
+                                               ctypes.c_void_p, ctypes.c_void_p]),
+    "quail_tree_plan": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
+    "quail_workspace_size_attention_tree": (ctypes.c_size_t, [ctypes.POINTER(CacheDesc), ctypes.c_int32,
+                                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "quail_attention_tree": (ctypes.c_int, [ctypes.POINTER(CacheDesc), *[ctypes.c_void_p] * 4, ctypes.c_int32,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                            ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p]),
+    "quail_tree_accept": (ctypes.c_int, [ctypes.POINTER(CacheDesc), ctypes.c_int32, *[ctypes.c_void_p] * 6,
+                                         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, *[ctypes.c_void_p] * 5]),
     "quail_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "quail_set_stage_events": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32]),
     "quail_launch_count": (ctypes.c_int32, []),
@@ -712,3 +741,141 @@ def classify_letters_cached(model: Model, cache: KVCache, prefix_pages, doc_len,
         _at(cache, workspace, _torch.uint8, workspace.numel(), "workspace"), workspace.numel(),
         _at(cache, letter_logprob, f32, N * M, "letter_logprob"), _at(cache, letter_prob, f32, N * M, "letter_prob"),
         _at(cache, letter_argmax, i32, N, "letter_argmax"), _cache_stream(cache, stream)))
+
+
+# ------------------------------------------------------------------ drafted trees
+ROPE_LAYOUTS = ("half", "interleaved")
+ROPE_SCALINGS = ("none", "linear", "base", "parts")
+MAX_TREE = 1024
+
+
+class Rope:
+    """quail_rope_desc: which dims of a head turn in which pairs, and how fast. layout "half" (pairs (j, j + r/2))
+    or "interleaved" ((2j, 2j + 1)) over the first rotary_dim = r dims; scaling "none", "linear", "base" or "parts"
+    (with original_len, low, high) by `factor`; magnitude None: 1."""
+
+    def __init__(self, theta: float, layout: str = "half", rotary_dim: int = 128, scaling: str = "none",
+                 factor: float = 1.0, original_len: float = 0.0, low: float = 1.0, high: float = 32.0,
+                 magnitude: float | None = None):
+        _need(layout in ROPE_LAYOUTS, f"layout must be one of {ROPE_LAYOUTS}")
+        _need(scaling in ROPE_SCALINGS, f"scaling must be one of {ROPE_SCALINGS}")
+        _need(magnitude is None or magnitude > 0, "magnitude must be positive")
+        self.desc = RopeDesc(ROPE_LAYOUTS.index(layout), int(rotary_dim), theta, ROPE_SCALINGS.index(scaling), factor,
+                             original_len, low, high, 0.0 if magnitude is None else magnitude)
+        self.ref = ctypes.byref(self.desc)
+
+
+def cache_append_rope(cache: KVCache, qkv, n_q_heads: int, token_seq, token_pos, rope: Rope, rope_pos=None, q_out=None,
+                      q_norm=None, k_norm=None, rms_eps: float = 1e-6, stream=None) -> None:
+    """cache_append with the rotation that `rope` describes, by rope_pos [T] int32 where a token's slot
+    token_pos[t] is not its position (None: it is)."""
+    n, width = qkv.shape
+    ld = qkv.stride(0) if n > 1 else width
+    dtype = qkv.dtype
+    if (qkv.stride(1) != 1 or width < (n_q_heads + 2 * cache.n_kv_heads) * 128 or qkv.get_device() != cache.index or
+            (dtype is not _torch.bfloat16 and dtype is not _torch.float32)):
+        raise QuailError(-1, "qkv must be bfloat16 or float32 rows of (hq + 2 hkv) * 128 elements on the cache's device")
+    bf16, i32 = _torch.bfloat16, _torch.int32
+    status = lib().quail_cache_append_rope(
+        cache.ref, qkv.data_ptr(), DTYPE_BF16 if dtype is bf16 else DTYPE_F32, ld, n, n_q_heads,
+        _at(cache, token_seq, i32, n, "token_seq"), _at(cache, token_pos, i32, n, "token_pos"),
+        None if rope_pos is None else _at(cache, rope_pos, i32, n, "rope_pos"),
+        None if q_norm is None else _at(cache, q_norm, bf16, 128, "q_norm"),
+        None if k_norm is None else _at(cache, k_norm, bf16, 128, "k_norm"), rms_eps, rope.ref,
+        None if q_out is None else _at(cache, q_out, bf16, n * n_q_heads * 128, "q_out"), _cache_stream(cache, stream))
+    if status:
+        _check(status)
+
+
+def cache_resize(cache: KVCache, old_len, new_len, free_ring, free_state, granted_len, token_offsets, token_seq=None,
+                 token_pos=None, prefix_pages=None, stream=None) -> None:
+    """The cache's page_table from old_len to new_len [num_seqs] int32; free_ring [pages] and free_state
+    [4] = (first, count, 0, 0) int32 hold the free pages. Out: granted_len [num_seqs], token_offsets [num_seqs + 1],
+    and token_seq, token_pos [max_tokens] int32 (both None: the table only)."""
+    i32, B = _torch.int32, cache.num_seqs
+    pages = 0 if prefix_pages is None else prefix_pages.numel()
+    n = 0 if token_seq is None else token_seq.numel()
+    _need((token_seq is None) == (token_pos is None) and (token_seq is None or n > 0),
+          "token_seq and token_pos go together and hold a token at least")
+    status = lib().quail_cache_resize(
+        cache.ref, _at(cache, prefix_pages, i32, pages, "prefix_pages") if pages else None, pages * 16,
+        _at(cache, old_len, i32, B, "old_len"), _at(cache, new_len, i32, B, "new_len"),
+        _at(cache, free_ring, i32, cache.desc.num_pages, "free_ring"), _at(cache, free_state, i32, 4, "free_state"),
+        _at(cache, granted_len, i32, B, "granted_len"), _at(cache, token_offsets, i32, B + 1, "token_offsets"),
+        None if token_seq is None else _at(cache, token_seq, i32, n, "token_seq"),
+        None if token_pos is None else _at(cache, token_pos, i32, n, "token_pos"), n, _cache_stream(cache, stream))
+    if status:
+        _check(status)
+
+
+class _Device:
+    """Where a call without a cache runs: the device of its first tensor."""
+
+    def __init__(self, t):
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        _need(t.is_cuda, "the trees must be device tensors")
+        self.device, self.index = t.device, t.get_device()
+
+
+def tree_plan(parent, q_offsets, seq_len, max_q_len: int, mask, rope_pos, stream=None) -> None:
+    """mask [T, ceil(max_q_len / 32)] int32 bit words and rope_pos [T] int32 of the trees that parent [T] int32
+    (-1: none) holds side by side; q_offsets [num_seqs + 1], seq_len [num_seqs] int32 (the tree's tokens included)."""
+    at, n, B = _Device(parent), parent.numel(), seq_len.numel()
+    i32 = _torch.int32
+    status = lib().quail_tree_plan(
+        _at(at, parent, i32, n, "parent"), _at(at, q_offsets, i32, B + 1, "q_offsets"), _at(at, seq_len, i32, B, "seq_len"),
+        B, n, max_q_len, _at(at, mask, i32, n * ((max_q_len + 31) // 32), "mask"), _at(at, rope_pos, i32, n, "rope_pos"),
+        _cache_stream(at, stream))
+    if status:
+        _check(status)
+
+
+def workspace_size_attention_tree(cache: KVCache, n_q_heads: int, total_q: int, max_q_len: int, max_seq_len: int) -> int:
+    """Bytes that serve these bounds and any smaller ones."""
+    n = lib().quail_workspace_size_attention_tree(cache.ref, int(n_q_heads), int(total_q), int(max_q_len),
+                                                  int(max_seq_len))
+    if n == 0:
+        _check(-1)
+    return int(n)
+
+
+def attention_tree(cache: KVCache, q, q_offsets, seq_len, mask, max_q_len: int, max_seq_len: int, out, workspace,
+                   lse=None, scale: float | None = None, stream=None) -> None:
+    """q, out [total_q, hq, 128] bf16; q_offsets int32 [num_seqs + 1]; seq_len int32 [num_seqs], the trees' tokens
+    included; mask int32 [total_q, ceil(max_q_len / 32)] (tree_plan); lse fp32 [total_q, hq] or None; workspace uint8,
+    workspace_size_attention_tree bytes; scale None or 0: 1/sqrt(128)."""
+    n, hq, d = q.shape
+    if d != 128:
+        raise QuailError(-1, "q must be [total_q, hq, 128]")
+    B, bf16, i32 = cache.num_seqs, _torch.bfloat16, _torch.int32
+    size = workspace.numel()
+    status = lib().quail_attention_tree(
+        cache.ref, _at(cache, q, bf16, n * hq * 128, "q"), _at(cache, q_offsets, i32, B + 1, "q_offsets"),
+        _at(cache, seq_len, i32, B, "seq_len"), _at(cache, mask, i32, n * ((max_q_len + 31) // 32), "mask"), n, max_q_len,
+        max_seq_len, hq, 0.0 if scale is None else scale, _at(cache, workspace, _torch.uint8, size, "workspace"), size,
+        _at(cache, out, bf16, n * hq * 128, "out"), None if lse is None else _at(cache, lse, _torch.float32, n * hq, "lse"),
+        _cache_stream(cache, stream))
+    if status:
+        _check(status)
+
+
+def tree_accept(caches: list, parent, mask, draft, taken, q_offsets, seq_len, max_q_len: int, path, accepted, new_len,
+                bonus, stream=None) -> None:
+    """The branch of every tree that the model would have taken (draft, taken [T] int32: the nodes' tokens and what the
+    model takes after them): path [T], accepted, new_len, bonus [num_seqs] int32; its rows move to the tree's first
+    slots in all of `caches` (one per layer)."""
+    at, n, B = _Device(parent), parent.numel(), seq_len.numel()
+    i32 = _torch.int32
+    _need(all(c.index == at.index for c in caches), "the caches lie on another device than the trees")
+    descs = (CacheDesc * max(1, len(caches)))(*[c.desc for c in caches])
+    status = lib().quail_tree_accept(
+        descs, len(caches), _at(at, parent, i32, n, "parent"), _at(at, mask, i32, n * ((max_q_len + 31) // 32), "mask"),
+        _at(at, draft, i32, n, "draft"), _at(at, taken, i32, n, "taken"), _at(at, q_offsets, i32, B + 1, "q_offsets"),
+        _at(at, seq_len, i32, B, "seq_len"), B, n, max_q_len, _at(at, path, i32, n, "path"),
+        _at(at, accepted, i32, B, "accepted"), _at(at, new_len, i32, B, "new_len"), _at(at, bonus, i32, B, "bonus"),
+        _cache_stream(at, stream))
+    if status:
+        _check(status)

@@ -19,6 +19,7 @@
 #include "quail_internal.h"
 #include "trie.h"
 #include "shortlist.h"
+#include "tree.h"
 
 using namespace quail;
 
@@ -2054,12 +2055,36 @@ quail_status quail_classify_trie_tree_shortlist(const quail_model_desc* model, c
   return QUAIL_OK;
 }
 
-quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
+// Checks and arguments that the two appends share; 0 tokens leave a->num_tokens 0.
+static quail_status open_append(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
                                 int32_t num_tokens, int32_t n_q_heads, const int32_t* token_seq,
                                 const int32_t* token_pos, const void* q_norm, const void* k_norm, float rms_eps,
-                                float rope_theta, void* q_out, quail_stream_t stream) {
-  g_launches = 0;
-  quail_status s = check_cache_shape(cache);
+                                void* q_out, DeviceState** ds, AppendArgs* a) {
+  if (num_tokens == 0) return QUAIL_OK;
+  if (qkv == nullptr || token_seq == nullptr || token_pos == nullptr)
+    return fail(QUAIL_ERR_INVALID_ARG, "a token pointer is null");
+  for (const void* p : {qkv, q_norm, k_norm, static_cast<const void*>(q_out)})
+    if (!aligned16(p)) return fail(QUAIL_ERR_INVALID_ARG, "qkv, the gains and q_out must be 16-byte aligned");
+  int dev = 0;
+  quail_status s = open_cache(cache, ds, &dev, &a->c);
+  if (s != QUAIL_OK) return s;
+  s = check_device_ptr(qkv, "qkv", dev);
+  if (s != QUAIL_OK) return s;
+  a->qkv = qkv;
+  a->ld = ld;
+  a->num_tokens = num_tokens;
+  a->hq = n_q_heads;
+  a->seq = token_seq;
+  a->pos = token_pos;
+  a->gq = static_cast<const bf16*>(q_norm);
+  a->gk = static_cast<const bf16*>(k_norm);
+  a->eps = rms_eps;
+  a->q_out = static_cast<bf16*>(q_out);
+  return QUAIL_OK;
+}
+static quail_status check_append(const quail_cache_desc* cache, quail_dtype qkv_dtype, int64_t ld, int32_t num_tokens,
+                                 int32_t n_q_heads, const void* q_norm, const void* k_norm, float rms_eps) {
+  const quail_status s = check_cache_shape(cache);
   if (s != QUAIL_OK) return s;
   if (qkv_dtype != QUAIL_DTYPE_BF16 && qkv_dtype != QUAIL_DTYPE_F32)
     return fail(QUAIL_ERR_INVALID_ARG, "qkv dtype must be bf16 or f32");
@@ -2069,34 +2094,63 @@ quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, 
     return fail(QUAIL_ERR_INVALID_ARG, "ld must be a multiple of 8 that holds every head");
   if (!(rms_eps > 0.f) && (q_norm != nullptr || k_norm != nullptr))
     return fail(QUAIL_ERR_INVALID_ARG, "rms_eps must be positive");
+  return QUAIL_OK;
+}
+
+quail_status quail_cache_append(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
+                                int32_t num_tokens, int32_t n_q_heads, const int32_t* token_seq,
+                                const int32_t* token_pos, const void* q_norm, const void* k_norm, float rms_eps,
+                                float rope_theta, void* q_out, quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_append(cache, qkv_dtype, ld, num_tokens, n_q_heads, q_norm, k_norm, rms_eps);
+  if (s != QUAIL_OK) return s;
   if (rope_theta != 0.f && !(rope_theta > 1.f && rope_theta < INFINITY))
     return fail(QUAIL_ERR_INVALID_ARG, "rope_theta must be 0 or above 1");
   if (cache->max_pages > (1 << 20) && rope_theta != 0.f)
     return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "rotation is exact for positions below 2^24 only");
-  if (num_tokens == 0) return QUAIL_OK;
-  if (qkv == nullptr || token_seq == nullptr || token_pos == nullptr)
-    return fail(QUAIL_ERR_INVALID_ARG, "a token pointer is null");
-  for (const void* p : {qkv, q_norm, k_norm, static_cast<const void*>(q_out)})
-    if (!aligned16(p)) return fail(QUAIL_ERR_INVALID_ARG, "qkv, the gains and q_out must be 16-byte aligned");
   DeviceState* ds = nullptr;
-  int dev = 0;
   AppendArgs a{};
-  s = open_cache(cache, &ds, &dev, &a.c);
-  if (s != QUAIL_OK) return s;
-  s = check_device_ptr(qkv, "qkv", dev);
-  if (s != QUAIL_OK) return s;
-  a.qkv = qkv;
-  a.ld = ld;
-  a.num_tokens = num_tokens;
-  a.hq = n_q_heads;
-  a.seq = token_seq;
-  a.pos = token_pos;
-  a.gq = static_cast<const bf16*>(q_norm);
-  a.gk = static_cast<const bf16*>(k_norm);
-  a.eps = rms_eps;
+  s = open_append(cache, qkv, qkv_dtype, ld, num_tokens, n_q_heads, token_seq, token_pos, q_norm, k_norm, rms_eps, q_out,
+                  &ds, &a);
+  if (s != QUAIL_OK || num_tokens == 0) return s;
   a.theta = rope_theta;
-  a.q_out = static_cast<bf16*>(q_out);
   CUDA_TRY(launch_cache_append(a, qkv_dtype == QUAIL_DTYPE_F32, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QUAIL_OK;
+}
+
+quail_status quail_cache_append_rope(const quail_cache_desc* cache, const void* qkv, quail_dtype qkv_dtype, int64_t ld,
+                                     int32_t num_tokens, int32_t n_q_heads, const int32_t* token_seq,
+                                     const int32_t* token_pos, const int32_t* rope_pos, const void* q_norm,
+                                     const void* k_norm, float rms_eps, const quail_rope_desc* rope, void* q_out,
+                                     quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_append(cache, qkv_dtype, ld, num_tokens, n_q_heads, q_norm, k_norm, rms_eps);
+  if (s != QUAIL_OK) return s;
+  if (rope == nullptr) return fail(QUAIL_ERR_INVALID_ARG, "rope is null");
+  if (rope->layout != QUAIL_ROPE_HALF && rope->layout != QUAIL_ROPE_INTERLEAVED)
+    return fail(QUAIL_ERR_INVALID_ARG, "rope layout must be half or interleaved");
+  if (rope->rotary_dim < 16 || rope->rotary_dim > 128 || rope->rotary_dim % 16 != 0)
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "rotary_dim must be a multiple of 16, at most 128 (got %d)", rope->rotary_dim);
+  if (!(rope->theta > 1.f && rope->theta < INFINITY)) return fail(QUAIL_ERR_INVALID_ARG, "rope theta must be above 1");
+  if (rope->scaling < QUAIL_ROPE_PLAIN || rope->scaling > QUAIL_ROPE_PARTS)
+    return fail(QUAIL_ERR_INVALID_ARG, "unknown rope scaling %d", rope->scaling);
+  if (rope->scaling != QUAIL_ROPE_PLAIN && !(rope->factor >= 1.f && rope->factor < INFINITY))
+    return fail(QUAIL_ERR_INVALID_ARG, "rope factor must be at least 1");
+  if (rope->scaling == QUAIL_ROPE_PARTS && !(rope->original_len > 0.f && rope->original_len < INFINITY && rope->low >= 0.f &&
+                                             rope->low < rope->high && rope->high < INFINITY))
+    return fail(QUAIL_ERR_INVALID_ARG, "rope by parts needs original_len > 0 and 0 <= low < high");
+  if (!(rope->magnitude >= 0.f && rope->magnitude < INFINITY))
+    return fail(QUAIL_ERR_INVALID_ARG, "rope magnitude must be finite and not negative");
+  if (rope_pos == nullptr && cache->max_pages > (1 << 20))
+    return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "rotation is exact for positions below 2^24 only");
+  DeviceState* ds = nullptr;
+  AppendArgs a{};
+  s = open_append(cache, qkv, qkv_dtype, ld, num_tokens, n_q_heads, token_seq, token_pos, q_norm, k_norm, rms_eps, q_out,
+                  &ds, &a);
+  if (s != QUAIL_OK || num_tokens == 0) return s;
+  a.rope_pos = rope_pos;
+  CUDA_TRY(launch_cache_append_rope(a, *rope, qkv_dtype == QUAIL_DTYPE_F32, ds->num_sms,
+                                    reinterpret_cast<cudaStream_t>(stream)));
   return QUAIL_OK;
 }
 
@@ -2257,6 +2311,195 @@ quail_status quail_classify_letters_cached(const quail_model_desc* model, const 
   CUDA_TRY(launch_letters_head(x.b.z_f32, static_cast<const bf16*>(model->lm_head), x.b.small + 4, num_letters, N,
                                model->hidden, letter_logprob, letter_prob, letter_argmax, st));
   stage_mark(QUAIL_STAGE_HEAD, true, st);
+  return QUAIL_OK;
+}
+
+quail_status quail_cache_resize(const quail_cache_desc* cache, const int32_t* prefix_pages, int32_t prefix_len,
+                                const int32_t* old_len, const int32_t* new_len, int32_t* free_ring,
+                                int32_t* free_state, int32_t* granted_len, int32_t* token_offsets, int32_t* token_seq,
+                                int32_t* token_pos, int32_t max_tokens, quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_cache_shape(cache);
+  if (s != QUAIL_OK) return s;
+  if (prefix_len < 0 || prefix_len % 16 != 0 || prefix_len / 16 > cache->max_pages)
+    return fail(QUAIL_ERR_INVALID_ARG, "prefix_len must be a multiple of 16 within max_pages (got %d)", prefix_len);
+  if ((prefix_len > 0) != (prefix_pages != nullptr))
+    return fail(QUAIL_ERR_INVALID_ARG, "prefix_pages and prefix_len go together");
+  if (cache->max_pages > (1 << 26)) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "max_pages must be at most 2^26");
+  if (max_tokens < 0 || (token_seq == nullptr) != (token_pos == nullptr) || (token_seq == nullptr && max_tokens != 0))
+    return fail(QUAIL_ERR_INVALID_ARG, "token_seq, token_pos and max_tokens go together");
+  if (old_len == nullptr || new_len == nullptr || free_ring == nullptr || free_state == nullptr || granted_len == nullptr ||
+      token_offsets == nullptr)
+    return fail(QUAIL_ERR_INVALID_ARG, "a length, ring or output pointer is null");
+  if (granted_len == old_len || granted_len == new_len)
+    return fail(QUAIL_ERR_INVALID_ARG, "granted_len must not be old_len or new_len");
+  for (const void* p : {static_cast<const void*>(token_seq), static_cast<const void*>(token_pos)})
+    if (!aligned16(p)) return fail(QUAIL_ERR_INVALID_ARG, "token_seq and token_pos must be 16-byte aligned");
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  ResizeArgs a{};
+  s = open_cache(cache, &ds, &dev, &a.c);
+  if (s != QUAIL_OK) return s;
+  a.table = const_cast<int32_t*>(cache->page_table);
+  a.prefix_pages = prefix_pages;
+  a.prefix_len = prefix_len;
+  a.old_len = old_len;
+  a.new_len = new_len;
+  a.ring = free_ring;
+  a.state = free_state;
+  a.granted = granted_len;
+  a.offsets = token_offsets;
+  a.token_seq = token_seq;
+  a.token_pos = token_pos;
+  a.max_tokens = max_tokens;
+  CUDA_TRY(launch_cache_resize(a, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QUAIL_OK;
+}
+
+// Shape of a batch of trees; fills the kernels' view of it but for err.
+static quail_status open_trees(const int32_t* parent, const int32_t* q_offsets, const int32_t* seq_len, int32_t num_seqs,
+                               int32_t total, int32_t max_q_len, TreeView* t) {
+  if (num_seqs < 0 || total < 0 || max_q_len < 1) return fail(QUAIL_ERR_INVALID_ARG, "bad num_seqs, total or max_q_len");
+  if (num_seqs > 65535) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most 65535 sequences per call");
+  if (max_q_len > QUAIL_MAX_TREE) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most %d nodes a tree", QUAIL_MAX_TREE);
+  if (total > (1 << 30)) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "too many nodes");
+  if (num_seqs > 0 && (q_offsets == nullptr || seq_len == nullptr || (total > 0 && parent == nullptr)))
+    return fail(QUAIL_ERR_INVALID_ARG, "parent, q_offsets or seq_len is null");
+  *t = TreeView{parent, q_offsets, seq_len, num_seqs, total, max_q_len, (max_q_len + 31) / 32, nullptr};
+  return QUAIL_OK;
+}
+
+quail_status quail_tree_plan(const int32_t* parent, const int32_t* q_offsets, const int32_t* seq_len, int32_t num_seqs,
+                             int32_t total, int32_t max_q_len, void* mask, int32_t* rope_pos, quail_stream_t stream) {
+  g_launches = 0;
+  TreeView t;
+  quail_status s = open_trees(parent, q_offsets, seq_len, num_seqs, total, max_q_len, &t);
+  if (s != QUAIL_OK) return s;
+  if (num_seqs == 0 || total == 0) return QUAIL_OK;
+  if (mask == nullptr || rope_pos == nullptr) return fail(QUAIL_ERR_INVALID_ARG, "mask or rope_pos is null");
+  if (!aligned16(mask)) return fail(QUAIL_ERR_INVALID_ARG, "mask must be 16-byte aligned");
+  DeviceState* ds = nullptr;
+  s = device_state(&ds);
+  if (s != QUAIL_OK) return s;
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  s = check_device_ptr(mask, "mask", dev);
+  if (s != QUAIL_OK) return s;
+  t.err = ds->err;
+  CUDA_TRY(launch_tree_plan(t, static_cast<uint32_t*>(mask), rope_pos, reinterpret_cast<cudaStream_t>(stream)));
+  return QUAIL_OK;
+}
+
+static quail_status check_attention_tree(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
+                                         int32_t max_q_len, int32_t max_seq_len) {
+  const quail_status s = check_attention_shape(cache, n_q_heads, total_q, max_q_len, max_seq_len, 0);
+  if (s != QUAIL_OK) return s;
+  if (max_q_len > QUAIL_MAX_TREE) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most %d nodes a tree", QUAIL_MAX_TREE);
+  return QUAIL_OK;
+}
+
+size_t quail_workspace_size_attention_tree(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
+                                           int32_t max_q_len, int32_t max_seq_len) {
+  if (check_attention_tree(cache, n_q_heads, total_q, max_q_len, max_seq_len) != QUAIL_OK) return 0;
+  return 256;
+}
+
+quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, const int32_t* q_offsets,
+                                  const int32_t* seq_len, const void* mask, int32_t total_q, int32_t max_q_len,
+                                  int32_t max_seq_len, int32_t n_q_heads, float scale, void* workspace,
+                                  size_t workspace_bytes, void* out, float* lse, quail_stream_t stream) {
+  g_launches = 0;
+  quail_status s = check_attention_tree(cache, n_q_heads, total_q, max_q_len, max_seq_len);
+  if (s != QUAIL_OK) return s;
+  if (!(scale >= 0.f && scale < INFINITY)) return fail(QUAIL_ERR_INVALID_ARG, "scale must be finite and not negative");
+  if (total_q == 0 || cache->num_seqs == 0) return QUAIL_OK;
+  if (q == nullptr || out == nullptr || seq_len == nullptr || q_offsets == nullptr || mask == nullptr)
+    return fail(QUAIL_ERR_INVALID_ARG, "q, out, q_offsets, seq_len or mask is null");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(mask))
+    return fail(QUAIL_ERR_INVALID_ARG, "q, out and mask must be 16-byte aligned");
+  s = check_workspace(workspace, workspace_bytes, 256);
+  if (s != QUAIL_OK) return s;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  TreeAttnArgs a{};
+  s = open_cache(cache, &ds, &dev, &a.c);
+  if (s != QUAIL_OK) return s;
+  s = check_device_ptr(q, "q", dev);
+  if (s != QUAIL_OK) return s;
+  a.hq = n_q_heads;
+  a.q = static_cast<const bf16*>(q);
+  a.q_offsets = q_offsets;
+  a.total_q = total_q;
+  a.max_q = std::min(max_q_len, total_q);
+  a.seq_len = seq_len;
+  a.max_seq_len = max_seq_len;
+  a.mask = static_cast<const uint32_t*>(mask);
+  a.words = (max_q_len + 31) / 32;
+  a.scale_log2 = (scale > 0.f ? scale : 0.08838834764831845f) * 1.4426950408889634f;
+  a.out = static_cast<bf16*>(out);
+  a.lse = lse;
+  CUDA_TRY(launch_tree_attention(a, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  return QUAIL_OK;
+}
+
+quail_status quail_tree_accept(const quail_cache_desc* caches, int32_t n_caches, const int32_t* parent,
+                               const void* mask, const int32_t* draft, const int32_t* taken, const int32_t* q_offsets,
+                               const int32_t* seq_len, int32_t num_seqs, int32_t total, int32_t max_q_len,
+                               int32_t* path, int32_t* accepted, int32_t* new_len, int32_t* bonus,
+                               quail_stream_t stream) {
+  g_launches = 0;
+  AcceptArgs a{};
+  quail_status s = open_trees(parent, q_offsets, seq_len, num_seqs, total, max_q_len, &a.t);
+  if (s != QUAIL_OK) return s;
+  if (n_caches < 0 || (n_caches > 0 && caches == nullptr)) return fail(QUAIL_ERR_INVALID_ARG, "caches is null, or n_caches < 0");
+  for (int i = 0; i < n_caches; ++i) {
+    const quail_cache_desc &c = caches[i], &f = caches[0];
+    s = check_cache_shape(&c);
+    if (s != QUAIL_OK) return s;
+    if (c.num_seqs != num_seqs) return fail(QUAIL_ERR_INVALID_ARG, "cache %d has %d sequences, not %d", i, c.num_seqs, num_seqs);
+    if (c.dtype != f.dtype || c.n_kv_heads != f.n_kv_heads || c.num_pages != f.num_pages || c.page_table != f.page_table ||
+        c.max_pages != f.max_pages)
+      return fail(QUAIL_ERR_INVALID_ARG, "cache %d is not like the first", i);
+  }
+  if (num_seqs == 0) return QUAIL_OK;
+  if (accepted == nullptr || new_len == nullptr || bonus == nullptr ||
+      (total > 0 && (mask == nullptr || draft == nullptr || taken == nullptr || path == nullptr)))
+    return fail(QUAIL_ERR_INVALID_ARG, "a token or output pointer is null");
+  if (new_len == seq_len) return fail(QUAIL_ERR_INVALID_ARG, "new_len must not be seq_len");
+  DeviceState* ds = nullptr;
+  s = device_state(&ds);
+  if (s != QUAIL_OK) return s;
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  s = check_device_ptr(accepted, "accepted", dev);
+  if (s != QUAIL_OK) return s;
+  CacheView v{};
+  for (int i = 0; i < n_caches; ++i) {
+    s = open_cache(&caches[i], &ds, &dev, &v);
+    if (s != QUAIL_OK) return s;
+    if (i == 0) a.c = v;
+  }
+  if (n_caches == 0) a.c.hkv = 1;
+  a.t.err = ds->err;
+  a.mask = static_cast<const uint32_t*>(mask);
+  a.draft = draft;
+  a.taken = taken;
+  a.path = path;
+  a.accepted = accepted;
+  a.new_len = new_len;
+  a.bonus = bonus;
+  // the pools' addresses travel as kernel arguments, kAcceptLayers layers a launch
+  for (int first = 0; first == 0 || first < n_caches; first += kAcceptLayers) {
+    LayerPools pools{};
+    a.layers = std::min(kAcceptLayers, n_caches - first);
+    for (int i = 0; i < a.layers; ++i) {
+      const quail_cache_desc& c = caches[first + i];
+      void* p[4] = {c.k_pool, c.v_pool, c.k_scale, c.v_scale};
+      for (int k = 0; k < 4; ++k) pools.p[i][k] = static_cast<uint8_t*>(p[k]);
+    }
+    if (first > 0) a.path = a.accepted = a.new_len = a.bonus = nullptr;
+    CUDA_TRY(launch_tree_accept(a, pools, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  }
   return QUAIL_OK;
 }
 

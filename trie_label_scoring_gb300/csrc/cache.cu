@@ -15,6 +15,9 @@
 // 16-byte piece of a full 128-byte line, and the row sums take three shuffles.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "cache.h"
 #include "launch.cuh"
@@ -27,18 +30,33 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kRowLanes = 8;
+// Rotary layouts: rotate-half over the whole head, over its first dims, neighbouring pairs.
+enum { kRopeHalf, kRopeHalfPart, kRopeInterleaved };
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
-// A lane's 16 elements of a head row as pairs: x[0..3] = dims 8l.., x[4..7] =
-// dims 64 + 8l.. ; Raw holds them as loaded.
+// The two runs of eight dims of a head row that lane l holds: 8l.. and 64 + 8l..;
+// where rotate-half turns only the first `rotary` dims, lanes below rotary / 16 hold the
+// two members of eight pairs and the others 16 dims that pass.
+struct Chunks {
+  int first, second;
+};
+template <int LAYOUT>
+__device__ __forceinline__ Chunks lane_chunks(int l, int rotary) {
+  if constexpr (LAYOUT != kRopeHalfPart) return {8 * l, 64 + 8 * l};
+  const int i = l - rotary / 16;
+  return i < 0 ? Chunks{8 * l, 8 * l + rotary / 2} : Chunks{rotary + 16 * i, rotary + 16 * i + 8};
+}
+
+// A lane's 16 elements of a head row as pairs: x[0..3] = the first run, x[4..7] = the
+// second; Raw holds them as loaded.
 template <typename T>
 struct Raw {
   uint4 v[sizeof(T)];  // 2 x 16 bytes of bf16, 4 of fp32
-  __device__ __forceinline__ void load(const T* p, int l) {
+  __device__ __forceinline__ void load(const T* p, Chunks c) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
-      v[i] = ldg_stream(p + (2 * i < static_cast<int>(sizeof(T)) ? 0 : 64) + 8 * l + (sizeof(T) == 4 ? 4 * (i & 1) : 0));
+      v[i] = ldg_stream(p + (2 * i < static_cast<int>(sizeof(T)) ? c.first : c.second) + (sizeof(T) == 4 ? 4 * (i & 1) : 0));
   }
   __device__ __forceinline__ void pairs(float2 (&x)[8]) const {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
@@ -52,10 +70,10 @@ struct Raw {
   }
 };
 
-__device__ __forceinline__ void store_row_bf16(bf16* p, int l, const float2 (&x)[8]) {
+__device__ __forceinline__ void store_row_bf16(bf16* p, Chunks c, const float2 (&x)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    *reinterpret_cast<uint4*>(p + 64 * h + 8 * l) =
+    *reinterpret_cast<uint4*>(p + (h ? c.second : c.first)) =
         make_uint4(pack_bf16(x[4 * h].x, x[4 * h].y), pack_bf16(x[4 * h + 1].x, x[4 * h + 1].y),
                    pack_bf16(x[4 * h + 2].x, x[4 * h + 2].y), pack_bf16(x[4 * h + 3].x, x[4 * h + 3].y));
 }
@@ -84,7 +102,7 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 
 // Row x as codes and scale; m is the row's largest finite |x|. An infinity
 // saturates to +-448 * 2^e, a NaN stays one.
-__device__ __forceinline__ void store_row_codes(uint8_t* p, uint8_t* scale, int l, const float2 (&x)[8], float m) {
+__device__ __forceinline__ void store_row_codes(uint8_t* p, uint8_t* scale, int l, Chunks c, const float2 (&x)[8], float m) {
   const int e = scale_exponent(m);
   const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 #pragma unroll
@@ -97,7 +115,7 @@ __device__ __forceinline__ void store_row_codes(uint8_t* p, uint8_t* scale, int 
       const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(b.x * inv, b.y * inv), __NV_SATFINITE, __NV_E4M3);
       w[i] = lo | hi << 16;
     }
-    *reinterpret_cast<uint2*>(p + 64 * h + 8 * l) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(p + (h ? c.second : c.first)) = make_uint2(w[0], w[1]);
   }
   if (l == 0) *scale = static_cast<uint8_t>(e);
 }
@@ -161,10 +179,16 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 // 23,100 tokens of 48 heads, bf16 in: e4m3 cache 103 us, 5.1 TB/s, L1 at 78%; bf16 cache
 // 102 us, 5.6 TB/s. The rotations kept in registers (a warp to a token) cost occupancy,
 // 107 us (e4m3); two rows ahead 131, 16 tokens a block 109.
+//
+// The rotary layouts differ in which dims make a pair and in the table's rows: rotate-half
+// as above, over the whole head or its first dims (the partners are then two runs of one
+// lane again, and dims past them pass, times their gains alone, so that an infinity beside
+// them stays there); interleaved, pairs (2j, 2j + 1) within a run. The angle may go by a
+// position of its own, so a drafted token's slot need not be its position.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendGroups = kAppendThreads / kRowLanes;
 
-template <typename T, int TOK>
+template <typename T, int TOK, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs a, RopeTable rt) {
   __shared__ __align__(16) float s_turn[TOK][2][4][64];  // queries, keys; A, B, C, D
   __shared__ int s_page[TOK], s_slot[TOK];               // page -1: nothing of the token is written
@@ -172,26 +196,49 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
   grid_launch_dependents();
   const int t0 = blockIdx.x * TOK;
   const int l = threadIdx.x % kRowLanes, heads = a.hq + 2 * a.c.hkv;
+  const Chunks ch2 = lane_chunks<LAYOUT>(l, a.rotary);
+  // whether the lane's runs turn; the layouts that turn part of a head have lanes that do not
+  const bool turns0 = LAYOUT == kRopeHalf || (LAYOUT == kRopeHalfPart ? l < a.rotary / 16 : 8 * l < a.rotary);
+  const bool turns1 = LAYOUT == kRopeHalf || (LAYOUT == kRopeHalfPart ? turns0 : 64 + 8 * l < a.rotary);
   const int rows = min(TOK, a.num_tokens - t0) * heads;
   int r = threadIdx.x / kRowLanes, tok = r / heads, h = r - tok * heads;
   const T* qkv = static_cast<const T*>(a.qkv);
   Raw<T> next;
-  if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, l);
+  if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, ch2);
   if (threadIdx.x < 64 * TOK) {
     const int i = threadIdx.x / 64, j = threadIdx.x % 64, t = t0 + i;
     const int seq = t < a.num_tokens ? a.seq[t] : -1;
     const int pos = seq >= 0 ? a.pos[t] : 0;
+    const int at = seq >= 0 && a.rope_pos != nullptr ? a.rope_pos[t] : pos;  // where the angle is taken
     if (j == 0) {
-      s_page[i] = seq < 0 ? -1 : page_of(a.c, seq, pos, t);
+      const bool far = a.rope_pos != nullptr && (at < 0 || at >= 1 << 24);
+      if (far) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, t);
+      s_page[i] = seq < 0 || far ? -1 : page_of(a.c, seq, pos, t);
       s_slot[i] = pos % kPage;
     }
     float c = 1.f, sn = 0.f;
-    if (a.theta > 0.f) cos_sin(pos, rt.w[j], c, sn);
+    int d1 = j, d2 = j + 64;  // the pair's dims
+    bool turned = a.theta > 0.f;
+    if constexpr (LAYOUT == kRopeHalfPart) {
+      const Chunks own = lane_chunks<LAYOUT>(j / 8, a.rotary);
+      d1 = own.first + j % 8;
+      d2 = own.second + j % 8;
+      turned = j < a.rotary / 2;
+    } else if constexpr (LAYOUT == kRopeInterleaved) {
+      d1 = 2 * j;
+      d2 = 2 * j + 1;
+      turned = j < a.rotary / 2;
+    }
+    if (turned) cos_sin(at, rt.w[j], c, sn);
+    if (LAYOUT != kRopeHalf || a.magnitude != 1.f) {
+      c *= turned ? a.magnitude : 1.f;
+      sn *= a.magnitude;
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const bf16* g = k == 0 ? a.gq : a.gk;
-      const float g1 = g != nullptr ? __bfloat162float(g[j]) : 1.f;
-      const float g2 = g != nullptr ? __bfloat162float(g[j + 64]) : 1.f;
+      const float g1 = g != nullptr ? __bfloat162float(g[d1]) : 1.f;
+      const float g2 = g != nullptr ? __bfloat162float(g[d2]) : 1.f;
       s_turn[i][k][0][j] = g1 * c;
       s_turn[i][k][1][j] = -g2 * sn;
       s_turn[i][k][2][j] = g2 * c;
@@ -211,7 +258,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       h -= heads;
       ++tok;
     }
-    if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, l);
+    if (r < rows) next.load(qkv + (t0 + tok) * a.ld + h * 128, ch2);
     const int page = in ? s_page[ct] : -1;
     const bool live = page >= 0;
     const bool is_q = ch < a.hq, is_k = !is_q && ch < a.hq + a.c.hkv;
@@ -225,17 +272,32 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       for (int i = 1; i < 8; ++i) ss = fma2(x[i], x[i], ss);
       const float f = row_sum(ss.x + ss.y);
       if (turn) {
-        const float4* tab = reinterpret_cast<const float4*>(&s_turn[ct][is_q ? 0 : 1][0][8 * l]);
+        const float4* tab = reinterpret_cast<const float4*>(&s_turn[ct][is_q ? 0 : 1][0][LAYOUT == kRopeInterleaved ? 4 * l : 8 * l]);
+        if constexpr (LAYOUT == kRopeInterleaved) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 A = tab[i], B = tab[16 + i], C = tab[32 + i], D = tab[48 + i];
+          for (int i = 0; i < 2; ++i) {  // pairs 4l.. of the first run, 32 + 4l.. of the second
+            const float4 A = tab[8 * i], B = tab[16 + 8 * i], C = tab[32 + 8 * i], D = tab[48 + 8 * i];
+            const float a4[4] = {A.x, A.y, A.z, A.w}, b4[4] = {B.x, B.y, B.z, B.w};
+            const float c4[4] = {C.x, C.y, C.z, C.w}, d4[4] = {D.x, D.y, D.z, D.w};
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 x1 = x[2 * i + k], x2 = x[2 * i + k + 4];
-            x[2 * i + k] = fma2(x1, k ? make_float2(A.z, A.w) : make_float2(A.x, A.y),
-                                mul2(x2, k ? make_float2(B.z, B.w) : make_float2(B.x, B.y)));
-            x[2 * i + k + 4] = fma2(x2, k ? make_float2(C.z, C.w) : make_float2(C.x, C.y),
-                                    mul2(x1, k ? make_float2(D.z, D.w) : make_float2(D.x, D.y)));
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = x[4 * i + k];
+              const bool mix = i == 0 ? turns0 : turns1;
+              x[4 * i + k] = make_float2(fmaf(v.x, a4[k], mix ? v.y * b4[k] : 0.f), fmaf(v.y, c4[k], mix ? v.x * d4[k] : 0.f));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 A = tab[i], B = tab[16 + i], C = tab[32 + i], D = tab[48 + i];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 x1 = x[2 * i + k], x2 = x[2 * i + k + 4], none = make_float2(0.f, 0.f);
+              const float2 m1 = mul2(x2, k ? make_float2(B.z, B.w) : make_float2(B.x, B.y));
+              const float2 m2 = mul2(x1, k ? make_float2(D.z, D.w) : make_float2(D.x, D.y));
+              x[2 * i + k] = fma2(x1, k ? make_float2(A.z, A.w) : make_float2(A.x, A.y), turns0 ? m1 : none);
+              x[2 * i + k + 4] = fma2(x2, k ? make_float2(C.z, C.w) : make_float2(C.x, C.y), turns0 ? m2 : none);
+            }
           }
         }
         if (norm) {
@@ -246,12 +308,12 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       }
     }
     if (live && is_q && a.q_out != nullptr)
-      store_row_bf16(a.q_out + (static_cast<size_t>(t0 + ct) * a.hq + ch) * 128, l, x);
+      store_row_bf16(a.q_out + (static_cast<size_t>(t0 + ct) * a.hq + ch) * 128, ch2, x);
     const bool kv = live && !is_q;
     const int g = ch - a.hq - (is_k ? 0 : a.c.hkv);
     const size_t at = (static_cast<size_t>(page) * a.c.hkv + g) * kPage + s_slot[ct];
     if (!a.c.codes) {
-      if (kv) store_row_bf16(static_cast<bf16*>(is_k ? a.c.k : a.c.v) + at * 128, l, x);
+      if (kv) store_row_bf16(static_cast<bf16*>(is_k ? a.c.k : a.c.v) + at * 128, ch2, x);
     } else if (__any_sync(0xffffffffu, kv)) {
       float m = 0.f;
 #pragma unroll
@@ -262,7 +324,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       m = row_max(m);
       if (kv)
         store_row_codes(static_cast<uint8_t*>(is_k ? a.c.k : a.c.v) + at * 128, (is_k ? a.c.k_scale : a.c.v_scale) + at,
-                        l, x, m);
+                        l, ch2, x, m);
     }
   }
 }
@@ -450,15 +512,38 @@ cudaError_t launch_answer_join(const float* qkv, const bf16* o, const float* lse
 
 namespace {
 
-template <typename T>
-cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const RopeTable rt = a.theta > 0.f ? angle_table(a.theta) : RopeTable{};
+// Frequencies w_j of the rotary pairs as the scaling has them; running powers, as above.
+RopeTable scaled_table(const quail_rope_desc& d) {
+  RopeTable t{};
+  const int r = d.rotary_dim;
+  const double f = d.factor;
+  double theta = d.theta;
+  if (d.scaling == QUAIL_ROPE_BASE) theta *= std::pow(f, static_cast<double>(r) / (r - 2));
+  const double step = std::pow(theta, -2.0 / r);
+  double w = 1.0;
+  for (int j = 0; j < r / 2; ++j) {
+    double v = w;
+    if (d.scaling == QUAIL_ROPE_LINEAR) v = w / f;
+    if (d.scaling == QUAIL_ROPE_PARTS) {
+      const double turns = d.original_len * w / 6.283185307179586477;
+      const double s = std::min(1.0, std::max(0.0, (turns - d.low) / (static_cast<double>(d.high) - d.low)));
+      v = (1.0 - s) * w / f + s * w;
+    }
+    t.w[j].x = static_cast<float>(v);
+    t.w[j].y = static_cast<float>(v - static_cast<double>(t.w[j].x));
+    w *= step;
+  }
+  return t;
+}
+
+template <typename T, int LAYOUT>
+cudaError_t launch_append(const AppendArgs& a, const RopeTable& rt, int num_sms, cudaStream_t st) {
   // Few tokens: a block each, so that they spread over the SMs. One / four a block, us:
   // 4 tokens 3.2 / 5.5, 256 3.9 / 5.7, 608 5.0 / 5.8, 800 7.7 / 7.4, 1,216 8.7 / 7.6
   // (48 heads, bf16; e4m3 9.8 / 10.1 at 608, 12.7 / 11.7 at 800).
   if (a.num_tokens <= 4 * num_sms)
-    return launch_pdl(cache_append_kernel<T, 1>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt);
-  return launch_pdl(cache_append_kernel<T, 4>, dim3((a.num_tokens - 1) / 4 + 1), dim3(kAppendThreads), 0, st, a, rt);
+    return launch_pdl(cache_append_kernel<T, 1, LAYOUT>, dim3(a.num_tokens), dim3(kAppendThreads), 0, st, a, rt);
+  return launch_pdl(cache_append_kernel<T, 4, LAYOUT>, dim3((a.num_tokens - 1) / 4 + 1), dim3(kAppendThreads), 0, st, a, rt);
 }
 
 }  // namespace
@@ -466,7 +551,24 @@ cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t st) {
 cudaError_t launch_cache_append(const AppendArgs& a, bool f32, int num_sms, cudaStream_t st) {
   if (a.num_tokens <= 0) return cudaSuccess;
   count_launch();
-  return f32 ? launch_append<float>(a, num_sms, st) : launch_append<bf16>(a, num_sms, st);
+  const RopeTable rt = a.theta > 0.f ? angle_table(a.theta) : RopeTable{};
+  return f32 ? launch_append<float, kRopeHalf>(a, rt, num_sms, st) : launch_append<bf16, kRopeHalf>(a, rt, num_sms, st);
+}
+
+cudaError_t launch_cache_append_rope(AppendArgs a, const quail_rope_desc& d, bool f32, int num_sms, cudaStream_t st) {
+  if (a.num_tokens <= 0) return cudaSuccess;
+  count_launch();
+  const RopeTable rt = scaled_table(d);
+  a.theta = d.theta;
+  a.rotary = d.rotary_dim;
+  a.magnitude = d.magnitude == 0.f ? 1.f : d.magnitude;
+  const auto launch = [&](auto layout) {
+    constexpr int kLayout = decltype(layout)::value;
+    return f32 ? launch_append<float, kLayout>(a, rt, num_sms, st) : launch_append<bf16, kLayout>(a, rt, num_sms, st);
+  };
+  if (d.layout == QUAIL_ROPE_INTERLEAVED) return launch(std::integral_constant<int, kRopeInterleaved>{});
+  if (d.rotary_dim < 128) return launch(std::integral_constant<int, kRopeHalfPart>{});
+  return launch(std::integral_constant<int, kRopeHalf>{});
 }
 
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens, bf16* k_out,

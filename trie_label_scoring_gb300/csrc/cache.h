@@ -9,6 +9,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "quail_internal.h"
+
 namespace quail {
 
 // A paged K/V pool and its page table. codes: one byte an element plus one
@@ -38,8 +40,13 @@ struct AppendArgs {
   float eps;
   float theta;  // 0: no rotation
   __nv_bfloat16* q_out;  // nullable
+  const int* rope_pos = nullptr;  // nullable: the angle goes by pos
+  int rotary = 128;               // leading dims of a head that turn
+  float magnitude = 1.f;          // of cosine and sine
 };
 cudaError_t launch_cache_append(const AppendArgs& a, bool f32, int num_sms, cudaStream_t st);
+// a.theta, rotary and magnitude follow from d.
+cudaError_t launch_cache_append_rope(AppendArgs a, const quail_rope_desc& d, bool f32, int num_sms, cudaStream_t st);
 
 // k_out / v_out [num_tokens, hkv, 128] bf16 (either may be null).
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens,
