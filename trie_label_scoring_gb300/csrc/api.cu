@@ -105,6 +105,21 @@ quail_status encode_2d_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint
   return QUAIL_OK;
 }
 
+// 3D bf16 tensor [planes, rows, cols], contiguous, boxes of box_cols x box_rows x
+// box_planes, 128-byte swizzle (box_cols * 2 must be 128).
+quail_status encode_3d_bf16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t planes,
+                            uint32_t box_cols, uint32_t box_rows, uint32_t box_planes) {
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+  cuuint32_t box[3] = {box_cols, box_rows, box_planes};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QUAIL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return QUAIL_OK;
+}
+
 // e4m3 codes [rows, 128] (one byte each), boxes of 128 x box_rows, 128-byte swizzle.
 quail_status encode_2d_codes(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
   cuuint64_t dims[2] = {128, rows};
@@ -1719,6 +1734,7 @@ quail_status quail_test_set_pipeline_wait_limit(long long cycles) {
   CUDA_TRY(set_pipeline_wait_limit_attention_tc(v));
   CUDA_TRY(set_pipeline_wait_limit_cache_attention(v));
   CUDA_TRY(set_pipeline_wait_limit_cache_attention_tc(v));
+  CUDA_TRY(set_pipeline_wait_limit_tree_attention(v));
   CUDA_TRY(cudaDeviceSynchronize());
   return QUAIL_OK;
 }
@@ -2398,10 +2414,37 @@ static quail_status check_attention_tree(const quail_cache_desc* cache, int32_t 
   return QUAIL_OK;
 }
 
+// How one call is carried out, and its workspace (as if in runs, when a is null: what
+// these bounds and any smaller ones need at most, since fewer rows take no more columns).
+static size_t plan_attention_tree(uint8_t* base, const quail_cache_desc* c, int hq, int total_q, int max_q, int max_seq_len,
+                                  TreeAttnArgs* a) {
+  const int G = hq / c->n_kv_heads, sms = planning_sms();
+  max_q = std::max(1, std::min(max_q, total_q));
+  const int rows = max_q * G;
+  TreeAttnArgs t{};
+  t.tile_cols = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  t.tile_tokens = t.tile_cols / G;
+  const long blocks = (max_seq_len + 127) / 128;
+  const long items = static_cast<long>(c->num_seqs) * c->n_kv_heads * ((max_q + t.tile_tokens - 1) / t.tile_tokens);
+  t.ctas = sms;
+  constexpr long kBegin = 4, kJoin = 6;
+  const long whole = (items + sms - 1) / sms * (blocks + kBegin), runs = (items * blocks + sms - 1) / sms + kBegin + kJoin;
+  t.direct = a != nullptr && whole <= runs;
+  if (t.direct) t.ctas = static_cast<int>(std::max(1L, std::min<long>(sms, items)));
+  Carver k{base};
+  if (!t.direct) {
+    t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
+    t.part_o = k.take<float>(static_cast<size_t>(sms) * 2 * t.tile_cols * 128);
+    t.part_st = k.take<PartStat>(static_cast<size_t>(sms) * 2 * t.tile_cols);
+  }
+  if (a != nullptr) *a = t;
+  return k.off + 256;
+}
+
 size_t quail_workspace_size_attention_tree(const quail_cache_desc* cache, int32_t n_q_heads, int32_t total_q,
                                            int32_t max_q_len, int32_t max_seq_len) {
   if (check_attention_tree(cache, n_q_heads, total_q, max_q_len, max_seq_len) != QUAIL_OK) return 0;
-  return 256;
+  return plan_attention_tree(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, nullptr);
 }
 
 quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, const int32_t* q_offsets,
@@ -2417,11 +2460,13 @@ quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, 
     return fail(QUAIL_ERR_INVALID_ARG, "q, out, q_offsets, seq_len or mask is null");
   if (!aligned16(q) || !aligned16(out) || !aligned16(mask))
     return fail(QUAIL_ERR_INVALID_ARG, "q, out and mask must be 16-byte aligned");
-  s = check_workspace(workspace, workspace_bytes, 256);
+  TreeAttnArgs a{};
+  const size_t need = plan_attention_tree(nullptr, cache, n_q_heads, total_q, max_q_len, max_seq_len, &a);
+  s = check_workspace(workspace, workspace_bytes, need);
   if (s != QUAIL_OK) return s;
   DeviceState* ds = nullptr;
   int dev = 0;
-  TreeAttnArgs a{};
+  plan_attention_tree(static_cast<uint8_t*>(workspace), cache, n_q_heads, total_q, max_q_len, max_seq_len, &a);
   s = open_cache(cache, &ds, &dev, &a.c);
   if (s != QUAIL_OK) return s;
   s = check_device_ptr(q, "q", dev);
@@ -2435,10 +2480,21 @@ quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, 
   a.max_seq_len = max_seq_len;
   a.mask = static_cast<const uint32_t*>(mask);
   a.words = (max_q_len + 31) / 32;
-  a.scale_log2 = (scale > 0.f ? scale : 0.08838834764831845f) * 1.4426950408889634f;
+  a.scale_log2 = std::max((scale > 0.f ? scale : 0.08838834764831845f) * 1.4426950408889634f, 1.17549435e-38f);
   a.out = static_cast<bf16*>(out);
   a.lse = lse;
-  CUDA_TRY(launch_tree_attention(a, ds->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+  CUtensorMap tK, tV, tQ;
+  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->n_kv_heads * 16;
+  for (int i = 0; i < 2; ++i) {
+    const void* pool = i == 0 ? cache->k_pool : cache->v_pool;
+    CUtensorMap* m = i == 0 ? &tK : &tV;
+    s = a.c.codes ? encode_2d_codes(m, pool, rows, 16) : encode_2d_bf16(m, pool, rows, 128, 128, 64, 16);
+    if (s != QUAIL_OK) return s;
+  }
+  // query tiles: 64 dims of the heads of a group, for a tile's nodes
+  s = encode_3d_bf16(&tQ, q, 128, n_q_heads, total_q, 64, n_q_heads / cache->n_kv_heads, a.tile_tokens);
+  if (s != QUAIL_OK) return s;
+  CUDA_TRY(launch_tree_attention(a, tK, tV, tQ, reinterpret_cast<cudaStream_t>(stream)));
   return QUAIL_OK;
 }
 

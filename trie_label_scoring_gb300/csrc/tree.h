@@ -69,7 +69,19 @@ struct TreeAttnArgs {
   float scale_log2;  // score factor times log2(e)
   __nv_bfloat16* out;
   float* lse;  // nullable
+
+  int tile_cols;    // query columns of a tile: 16, 32, 64 or 128
+  int tile_tokens;  // nodes of a tile, tile_cols / (hq / hkv)
+  int ctas;
+  bool direct;  // whole (sequence, head, tile) items by turns; else equal runs of the work list
+  // of the runs: plan [0] blocks of a run, [2 + b] first block of sequence b; two parts of a
+  // CTA, of tile_cols rows of 128 each: what it began of an item and left, what it went on with
+  long long* plan;
+  float* part_o;
+  PartStat* part_st;
 };
-cudaError_t launch_tree_attention(const TreeAttnArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_tree_attention(const TreeAttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                  const CUtensorMap& tmQ, cudaStream_t st);
+cudaError_t set_pipeline_wait_limit_tree_attention(long long cycles);
 
 }  // namespace quail
