@@ -2422,7 +2422,7 @@ static size_t plan_attention_tree(uint8_t* base, const quail_cache_desc* c, int 
   max_q = std::max(1, std::min(max_q, total_q));
   const int rows = max_q * G;
   TreeAttnArgs t{};
-  t.tile_cols = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  t.tile_cols = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
   t.tile_tokens = t.tile_cols / G;
   const long blocks = (max_seq_len + 127) / 128;
   const long items = static_cast<long>(c->num_seqs) * c->n_kv_heads * ((max_q + t.tile_tokens - 1) / t.tile_tokens);

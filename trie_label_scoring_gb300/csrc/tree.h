@@ -70,7 +70,7 @@ struct TreeAttnArgs {
   __nv_bfloat16* out;
   float* lse;  // nullable
 
-  int tile_cols;    // query columns of a tile: 16, 32, 64 or 128
+  int tile_cols;    // query columns of a tile: 16, 32, 64, 96 or 128
   int tile_tokens;  // nodes of a tile, tile_cols / (hq / hkv)
   int ctas;
   bool direct;  // whole (sequence, head, tile) items by turns; else equal runs of the work list

@@ -54,12 +54,10 @@ constexpr float kNone = 3e38f;  // minus the reference of a row that has seen no
 
 template <int N, bool CODES>
 struct Cfg {
-  static constexpr int kWgs = N >= 64 ? 2 : 1;   // softmax warpgroups
+  static constexpr int kCols = N < 32 ? N : 32;  // columns of a softmax warpgroup
+  static constexpr int kWgs = N / kCols;
   static constexpr int kThreads = 128 + 128 * kWgs;
-  static constexpr int kCols = N / kWgs;         // columns of a warpgroup
-  static constexpr int kChunk = kCols < 32 ? kCols : 32;
-  static constexpr int kChunks = kCols / kChunk;
-  static constexpr int kTerms = CODES ? 3 : N == 128 ? 1 : 2;  // of a weight
+  static constexpr int kTerms = CODES ? 3 : N > 64 ? 1 : 2;  // of a weight
   static constexpr uint32_t kRow = CODES ? 128 : 256;  // bytes of a key
   static constexpr uint32_t kSlot = kBlk * kRow;
   static constexpr int kDepth = CODES ? 4 : 2;   // blocks of K, and of V, in flight or at work
@@ -68,17 +66,18 @@ struct Cfg {
   // P: rows of 128 bytes by key, in blocks of 128 keys; the terms side by side in a block's
   // rows where they fit
   static constexpr int kColBytes = CODES ? 1 : 2;
+  static constexpr int kTermBytes = N == 96 ? (CODES ? 128 : 256) : N * kColBytes;
   static constexpr int kPBlock = kBlk * 128;
-  static constexpr int kPBlocks = (N * kColBytes * kTerms + 127) / 128;
+  static constexpr int kPBlocks = (kTermBytes * kTerms + 127) / 128;
   static constexpr uint32_t kP = kPBlocks * kPBlock;
-  static constexpr int kPBufs = N == 128 ? 1 : 2;
+  static constexpr int kPBufs = N == 128 || (N == 96 && CODES) ? 1 : 2;
   static constexpr uint32_t kOffV = kDepth * kSlot;
   static constexpr uint32_t kOffQ = kOffV + kDepth * kSlot;
   static constexpr uint32_t kOffP = kOffQ + kQ;
   static constexpr uint32_t kOffStats = kOffP + kPBufs * kP;
-  static constexpr int kTmem = N == 16 ? 64 : 4 * N;  // columns: two S, one O
-  static constexpr int kMargin = CODES ? 1 : 8;  // a score may pass the reference by, base 2
-  static constexpr int kLift = 14;               // of codes' weights
+  static constexpr int kTmem = N == 16 ? 64 : N == 32 ? 128 : N == 64 ? 256 : 512;  // columns: two S, one O
+  static constexpr int kMargin = CODES ? 2 : 8;  // a score may pass the reference by, base 2
+  static constexpr int kLift = 13;               // of codes' weights
 };
 
 struct Piece {
@@ -93,13 +92,16 @@ template <int N, bool CODES>
 struct Shared {
   float neg_ref[N];    // minus the reference maxima
   float row_factor[N]; // codes: score factor times the query row's power of two
-  float part[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kChunk];  // of a warp's keys
+  float part[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kCols];  // maxima of a warp's keys
+  float sums[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kCols];
   int part_e[Cfg<N, CODES>::kWgs][4];
+  int moved[Cfg<N, CODES>::kWgs][2];  // block, plus one, for which a warp asks to move the reference
   Piece piece[kPieces];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t k_full[Cfg<N, CODES>::kDepth], k_empty[Cfg<N, CODES>::kDepth];
   uint64_t v_full[Cfg<N, CODES>::kDepth], v_empty[Cfg<N, CODES>::kDepth];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], drain;
+  uint64_t vote[Cfg<N, CODES>::kWgs][2], wg_sync[Cfg<N, CODES>::kWgs];
   uint32_t tmem;
   int abort_flag;
 };
@@ -125,26 +127,14 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs& a, int b) {
   return s;
 }
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBlk - 1) / kBlk; }
-// Blocks of a sequence in the work list, and its (head, row tile) items.
+// Units of a sequence in the work list, and its (head, row tile) items: an item is kBegin
+// units, what it costs to begin and end it, and then its blocks.
+constexpr int kBegin = 2;
 __device__ __forceinline__ long long units_of(const TreeAttnArgs& a, int b, int* items) {
   const Seq s = b < a.c.num_seqs ? seq_of(a, b) : Seq{0, 0, 0, false};
   *items = s.ok ? (s.n + a.tile_tokens - 1) / a.tile_tokens * a.c.hkv : 0;
-  return s.ok ? static_cast<long long>(blocks_of(s.len)) * *items : 0;
+  return s.ok && s.len > 0 ? static_cast<long long>(blocks_of(s.len) + kBegin) * *items : 0;
 }
-
-__device__ __forceinline__ bool any_of_warpgroup(bool p, int bar) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(p)), "r"(bar)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void sync_warpgroup(int bar) { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
 
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -290,6 +280,12 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       mbar_init(&sh.p_empty[s], 1);
     }
     mbar_init(&sh.drain, 1);
+    for (int g = 0; g < C::kWgs; ++g) {
+      mbar_init(&sh.vote[g][0], 4);
+      mbar_init(&sh.vote[g][1], 4);
+      mbar_init(&sh.wg_sync[g], 4);
+      sh.moved[g][0] = sh.moved[g][1] = 0;
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -352,10 +348,10 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
         int items;
         const long long n = units_of(a, b, &items);
         if (at + n > u0 || b >= B) {
-          const int blks = b < B ? blocks_of(a.seq_len[b]) : 1;
+          const int per_item = (b < B ? blocks_of(a.seq_len[b]) : 0) + kBegin;
           b_at = b;
-          x_at = static_cast<int>((u0 - at) / blks);
-          j_at = static_cast<int>((u0 - at) % blks);
+          x_at = static_cast<int>((u0 - at) / per_item);
+          j_at = static_cast<int>((u0 - at) % per_item);
           break;
         }
         at += n;
@@ -366,9 +362,11 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
 
   // ---- a role's way along the pieces
   int piece_no = 0;
+  auto piece_there = [&]() {
+    return __all_sync(0xffffffffu, wait_bar(&sh.piece_full[piece_no % kPieces], static_cast<uint32_t>((piece_no / kPieces) & 1), abort_flag, limit_clk)) != 0;
+  };
   auto take_piece = [&](Piece& p) {
-    if (!__all_sync(0xffffffffu, wait_bar(&sh.piece_full[piece_no % kPieces], static_cast<uint32_t>((piece_no / kPieces) & 1), abort_flag, limit_clk)))
-      return false;
+    if (!piece_there()) return false;
     p = sh.piece[piece_no % kPieces];
     return true;
   };
@@ -461,13 +459,14 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
         p.n = s.n;
         p.len = s.len;
         for (; ok && left > 0 && x < tiles * a.c.hkv; ++x, j = 0) {
+          const int units = static_cast<int>(min(left, static_cast<long long>(blks + kBegin - j)));
           p.g = x / tiles;
           p.tok0 = x % tiles * a.tile_tokens;
-          p.blk0 = j;
-          p.blks = static_cast<int>(min(left, static_cast<long long>(blks - j)));
-          p.slot = p.blks == blks ? -1 : j > 0 ? 1 : 0;
-          publish(p);
-          left -= p.blks;
+          p.blk0 = max(0, j - kBegin);
+          p.blks = max(0, j + units - kBegin) - p.blk0;
+          p.slot = p.blks == blks ? -1 : p.blk0 > 0 ? 1 : 0;
+          if (p.blks > 0) publish(p);
+          left -= units;
         }
       }
     }
@@ -561,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
 #pragma unroll
       for (int term = 0; term < C::kTerms; ++term) {
         constexpr int kKeys = CODES ? 32 : 16;  // an instruction's
-        const int at = term * N * C::kColBytes, off = at / 128 * C::kPBlock + at % 128;
+        const int at = term * C::kTermBytes, off = at / 128 * C::kPBlock + at % 128;
 #pragma unroll
         for (int kk = 0; kk < kBlk / kKeys; ++kk) {
           const uint64_t av = v + ((kk * kKeys * 128) >> 4), bp = w + ((off + kk * kKeys * 128) >> 4);
@@ -614,55 +613,46 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------ softmax: thread <-> key of a block, dim of O
-    const int wg = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane, bar = 2 + wg;
-    constexpr int W = C::kChunk;
+    constexpr int W = C::kCols;
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane, c0 = wg * W;
     tc_fence_before();
     asm volatile("bar.sync 1, %0;" ::"n"(32 + 128 * C::kWgs) : "memory");
     tc_fence_after();
-    const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int col0 = wg * C::kCols;  // the warpgroup's first column
+    const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(quarter * 32) << 16), o_at = tmem + 2 * N + c0;
+    auto wait_warp = [&](uint64_t* bars, int of, int n) { return __all_sync(0xffffffffu, wait_use(bars, of, n)) != 0; };
+    // The warpgroup's barrier; like every wait here it ends when another role has given up.
+    int syncs = 0;
+    auto sync_warpgroup = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.wg_sync[wg]);
+      return wait_warp(&sh.wg_sync[wg], 1, syncs++);
+    };
     int t = 0;
-    while (true) {
-      Piece p;
-      const bool got = take_piece(p);
-      if (any_of_warpgroup(!got, bar)) break;
-      if (p.blks < 0) break;
-      // where column c0 + i's row of the result lies: its node and head, step by step
-      auto for_columns = [&](int c0, auto&& f) {
-        int node = c0 / G, h = c0 % G;
-#pragma unroll
+    while (piece_there()) {
+      const Piece& p = sh.piece[piece_no % kPieces];  // until done_piece
+      const int blks = p.blks;
+      if (blks < 0) break;
+      // the result's row of this lane's column (of the warpgroup's)
+      const int c = lane % W, c_node = (c0 + c) / G;
+      const bool c_there = c_node < a.tile_tokens && p.tok0 + c_node < p.n;
+      const int c_row = c_there ? (p.lo + p.tok0 + c_node) * a.hq + p.g * G + (c0 + c) % G : -1;
+      if (blks == 0) {  // no key: zeros
         for (int i = 0; i < W; ++i) {
-          const bool there = node < a.tile_tokens && p.tok0 + node < p.n;
-          f(i, there, static_cast<size_t>(p.lo + p.tok0 + node) * a.hq + p.g * G + h);
-          if (++h == G) {
-            h = 0;
-            ++node;
-          }
+          const int r = __shfl_sync(0xffffffffu, c_row, i);
+          if (r >= 0) a.out[static_cast<size_t>(r) * 128 + row] = __float2bfloat16(0.f);
         }
-      };
-      if (p.blks == 0) {  // no key: zeros
-#pragma unroll 1
-        for (int ch = 0; ch < C::kChunks; ++ch)
-          for_columns(col0 + ch * W, [&](int, bool there, size_t r) {
-            if (!there) return;
-            a.out[r * 128 + row] = __float2bfloat16(0.f);
-            if (row == 0 && a.lse != nullptr) a.lse[r] = -INFINITY;
-          });
+        if (quarter == 0 && lane < W && c_there && a.lse != nullptr) a.lse[c_row] = -INFINITY;
         done_piece();
         continue;
       }
-      // Outcomes of waits that fail are carried on to the next vote: every thread takes part
-      // in every barrier.
-      bool ok = true;
       if constexpr (CODES) {
-        // the warpgroup's query rows as two terms: 128 / kCols threads a row, 16-byte pieces
-        constexpr int kTpr = 128 / C::kCols, kPer = 128 / kTpr;  // threads a row, elements a thread
-        const int tid = threadIdx.x & 127, c = col0 + tid / kTpr, part = tid % kTpr;
-        const int node = c / G;
+        // the warpgroup's query rows as two terms, 128 / W threads a row
+        constexpr int kTpr = 128 / W, kPer = 128 / kTpr;  // threads a row, elements a thread
+        const int qc = c0 + row / kTpr, part = row % kTpr, node = qc / G;
         uint4 x[kPer / 8];
         const bool there = node < a.tile_tokens && p.tok0 + node < p.n;
         const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (static_cast<size_t>(p.lo + p.tok0 + (there ? node : 0)) * a.hq + p.g * G + (there ? c % G : 0)) * 128 + part * kPer);
+            a.q + (static_cast<size_t>(p.lo + p.tok0 + (there ? node : 0)) * a.hq + p.g * G + (there ? qc % G : 0)) * 128 + part * kPer);
 #pragma unroll
         for (int i = 0; i < kPer / 8; ++i) x[i] = there ? src[i] : make_uint4(0u, 0u, 0u, 0u);
         float am = 0.f;
@@ -683,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
         // times 2^(7 - e): the largest in [128, 256)
         const int e = am > 0.f && !odd_row ? min(127, max(-119, static_cast<int>(__float_as_uint(am) >> 23) - 127)) : 0;
         const float up = pow2_int(7 - e);
-        uint8_t* q0 = base + C::kOffQ + c * 128;
+        uint8_t* q0 = base + C::kOffQ + qc * 128;
 #pragma unroll
         for (int i = 0; i < kPer / 16; ++i) {
           uint32_t w0[4], w1[4];
@@ -701,233 +691,227 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
             w0[k] = odd_row ? 0x7f7f7f7fu : hi[0] | hi[1] << 16;
             w1[k] = odd_row ? 0u : lo[0] | lo[1] << 16;
           }
-          const int chunk = (part * kPer / 16 + i) ^ (c & 7);
+          const int chunk = (part * kPer / 16 + i) ^ (qc & 7);
           *reinterpret_cast<uint4*>(q0 + (chunk << 4)) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
           *reinterpret_cast<uint4*>(q0 + N * 128 + (chunk << 4)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
         }
-        if (part == 0) sh.row_factor[c] = fmaxf(a.scale_log2 * pow2_int(e - 7), 1.17549435e-38f);
+        if (part == 0) sh.row_factor[qc] = fmaxf(a.scale_log2 * pow2_int(e - 7), 1.17549435e-38f);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
+        if (!sync_warpgroup()) break;
       }
-      if (threadIdx.x - (128 + 128 * wg) < C::kCols) sh.neg_ref[col0 + threadIdx.x - (128 + 128 * wg)] = kNone;
-      float2 l[C::kCols / 2];  // this key lane's sums
+      float2 l[W / 2];  // this key lane's sums
 #pragma unroll
-      for (int i = 0; i < C::kCols / 2; ++i) l[i] = make_float2(0.f, 0.f);
-      int e_ref[C::kChunks] = {};  // codes: the largest power of the values seen, biased
-      sync_warpgroup(bar);
+      for (int i = 0; i < W / 2; ++i) l[i] = make_float2(0.f, 0.f);
+      int e_ref = 0;  // codes: the largest power of the values seen, biased
       // codes: this thread's key's powers, read a block ahead, its page's id two
-      const int* table = a.c.table + static_cast<size_t>(p.b) * a.c.max_pages;
       auto page_id = [&](int j) {
         const int key = (p.blk0 + j) * kBlk + row;
-        const int page = j < p.blks && key < p.len ? table[key / kPage] : -1;
+        const int page = j < blks && key < p.len ? a.c.table[static_cast<size_t>(p.b) * a.c.max_pages + key / kPage] : -1;
         return page < a.c.num_pages ? page : -1;
       };
       int page1 = -1;
-      uint32_t ek1 = 0, ev1 = 0;
+      uint32_t e1 = 0;  // the key's power, the value's << 8
       auto read_powers = [&](int page) {
-        ek1 = ev1 = 0;
+        e1 = 0;
         if (page < 0) return;
         const size_t at = static_cast<size_t>(page * a.c.hkv + p.g) * kPage + row % kPage;
-        ek1 = a.c.k_scale[at];
-        ev1 = a.c.v_scale[at];
+        e1 = a.c.k_scale[at] | static_cast<uint32_t>(a.c.v_scale[at]) << 8;
       };
       if constexpr (CODES) {
         read_powers(page_id(0));
         page1 = page_id(1);
       }
-      bool lost = false;  // a vote has found a wait that failed
+      int j = 0;
 #pragma unroll 1
-      for (int j = 0; j < p.blks; ++j, ++t) {
-        const int key0 = (p.blk0 + j) * kBlk, key = key0 + row;
-        const uint32_t ek = ek1, ev = ev1;
+      for (; j < blks; ++j, ++t) {
+        const uint32_t ek = e1 & 255u, ev = e1 >> 8;
         if constexpr (CODES) {
           read_powers(page1);
           page1 = page_id(j + 2);
         }
         // which columns see this thread's key
-        const bool border = key0 + kBlk > p.len - p.n;
-        uint32_t vis[C::kChunks];
-#pragma unroll
-        for (int ch = 0; ch < C::kChunks; ++ch) vis[ch] = 0xffffffffu;
+        const bool border = (p.blk0 + j + 1) * kBlk > p.len - p.n;
+        uint32_t vis = 0xffffffffu;
         if (border) {
-          const int in_tree = key - (p.len - p.n);
-#pragma unroll
-          for (int ch = 0; ch < C::kChunks; ++ch) {
-            if (key >= p.len) vis[ch] = 0;
-            if (key < p.len && in_tree >= 0) {
-              const int c0 = col0 + ch * W;
-              const uint32_t* word = a.mask + static_cast<size_t>(p.lo + p.tok0) * a.words + in_tree / 32;
-              uint32_t v = 0;
-#pragma unroll 8
-              for (int node = c0 / G; node * G < c0 + W; ++node) {
-                const uint32_t m = p.tok0 + node < p.n ? word[static_cast<size_t>(node) * a.words] : 0u;
-                const int from = max(node * G - c0, 0), to = min(node * G + G - c0, W);
-                const uint32_t cols = (to == 32 ? 0u : 1u << to) - (1u << from);
-                if ((m >> (in_tree % 32)) & 1) v |= cols;
-              }
-              vis[ch] = v;
+          const int key = (p.blk0 + j) * kBlk + row, in_tree = key - (p.len - p.n);
+          if (key >= p.len) vis = 0;
+          if (key < p.len && in_tree >= 0) {
+            const uint32_t* word = a.mask + static_cast<size_t>(p.lo + p.tok0) * a.words + in_tree / 32;
+            const int left = p.n - p.tok0;
+            vis = 0;
+#pragma unroll 4
+            for (int node = c0 / G; node * G < c0 + W; ++node) {
+              const uint32_t m = node < left ? word[static_cast<size_t>(node) * a.words] : 0u;
+              const int from = max(node * G - c0, 0), to = min(node * G + G - c0, W);
+              const uint32_t cols = (to == 32 ? 0u : 1u << to) - (1u << from);
+              if ((m >> (in_tree % 32)) & 1) vis |= cols;
             }
           }
         }
-        ok = ok && wait_use(sh.s_full, 2, t);
-        ok = __all_sync(0xffffffffu, ok);
+        if (!wait_warp(sh.s_full, 2, t)) break;
         tc_fence_after();
-        const float k_factor = CODES ? (ek == 0 ? 1.f : pow2_byte(ek)) : 1.f;
+        const uint32_t s_at = tmem + (t & 1) * N + c0;
+        float x[W];
+        // scores, less their references where they have one, base 2
+        auto scores = [&](bool plain) {
+          const float k_factor = CODES ? (ek == 0 ? 1.f : pow2_byte(ek)) : 1.f;
+          tmem_ld_cols<W>(s_at, x);
 #pragma unroll
-        for (int ch = 0; ch < C::kChunks; ++ch) {
-          const int c0 = col0 + ch * W;
-          const uint32_t s_at = tmem + (t & 1) * N + c0, o_at = tmem + 2 * N + c0;
-          float x[W];
-          // scores less their references, base 2
-          auto scores = [&](bool plain) {
-            tmem_ld_cols<W>(s_at, x);
-#pragma unroll
-            for (int i = 0; i < W; i += 4) {
-              const float4 r = plain ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(&sh.neg_ref[c0 + i]);
-              float2 f0 = make_float2(a.scale_log2, a.scale_log2), f1 = f0;
-              if constexpr (CODES) {
-                const float4 f = *reinterpret_cast<const float4*>(&sh.row_factor[c0 + i]);
-                const float2 kf = make_float2(k_factor, k_factor);
-                f0 = mul2(make_float2(f.x, f.y), kf);
-                f1 = mul2(make_float2(f.z, f.w), kf);
-              }
-              const float2 y0 = fma2(make_float2(x[i], x[i + 1]), f0, make_float2(r.x, r.y));
-              const float2 y1 = fma2(make_float2(x[i + 2], x[i + 3]), f1, make_float2(r.z, r.w));
-              x[i] = y0.x;
-              x[i + 1] = y0.y;
-              x[i + 2] = y1.x;
-              x[i + 3] = y1.y;
-            }
-            if (border) {
-#pragma unroll
-              for (int i = 0; i < W; ++i) x[i] = (vis[ch] >> i) & 1 ? x[i] : -INFINITY;
-            }
-          };
-          bool grows = j == 0;
-          if (j > 0) {
-            scores(false);
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i < W; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-            grows = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > static_cast<float>(C::kMargin);
-            if constexpr (CODES) grows = grows || static_cast<int>(ev) > e_ref[ch];
-          }
-          if (j == 0 || any_of_warpgroup(grows || !ok, bar)) {
-            if (any_of_warpgroup(!ok, bar)) {
-              lost = true;
-              break;
-            }
-            scores(true);
-            const float top = over_lanes<W>(x, lane, [](float u, float v) { return fmaxf(u, v); });
-            if (lane < W) sh.part[wg][quarter][lane] = top;
+          for (int i = 0; i < W; i += 4) {
+            const float4 r = plain ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(&sh.neg_ref[c0 + i]);
+            float2 f0 = make_float2(a.scale_log2, a.scale_log2), f1 = f0;
             if constexpr (CODES) {
-              const int e = __reduce_max_sync(0xffffffffu, static_cast<int>(ev));
-              if (lane == 0) sh.part_e[wg][quarter] = e;
+              const float4 f = *reinterpret_cast<const float4*>(&sh.row_factor[c0 + i]);
+              const float2 kf = make_float2(k_factor, k_factor);
+              f0 = mul2(make_float2(f.x, f.y), kf);
+              f1 = mul2(make_float2(f.z, f.w), kf);
             }
-            const int c = lane % W;
-            sync_warpgroup(bar);
-            const float was = -sh.neg_ref[c0 + c];
-            const float now = fmaxf(was, fmaxf(fmaxf(sh.part[wg][0][c], sh.part[wg][1][c]), fmaxf(sh.part[wg][2][c], sh.part[wg][3][c])));
-            int e_now = e_ref[ch];
-            if constexpr (CODES)
-              e_now = max(e_now, max(max(sh.part_e[wg][0], sh.part_e[wg][1]), max(sh.part_e[wg][2], sh.part_e[wg][3])));
-            const float fl = exp2f(was - now), fo = CODES ? fl * pow2_int(e_ref[ch] - e_now) : fl;
-            e_ref[ch] = e_now;
-            sync_warpgroup(bar);
-            if (quarter == 0 && lane < W) sh.neg_ref[c0 + c] = -now;
-            if (j > 0) {
-#pragma unroll
-              for (int i = 0; i < W; i += 2)
-                l[ch * W / 2 + i / 2] = mul2(l[ch * W / 2 + i / 2],
-                                             make_float2(__shfl_sync(0xffffffffu, fl, i), __shfl_sync(0xffffffffu, fl, i + 1)));
-              // O holds every product up to the block before once that is done
-              ok = __all_sync(0xffffffffu, ok && wait_use(sh.p_empty, C::kPBufs, t - 1));
-              tc_fence_after();
-              tmem_ld_cols<W>(o_at, x);
-#pragma unroll
-              for (int i = 0; i < W; ++i) x[i] *= __shfl_sync(0xffffffffu, fo, i);
-              tmem_st_cols<W>(o_at, x);
-            }
-            sync_warpgroup(bar);
-            scores(false);
+            const float2 y0 = fma2(make_float2(x[i], x[i + 1]), f0, make_float2(r.x, r.y));
+            const float2 y1 = fma2(make_float2(x[i + 2], x[i + 3]), f1, make_float2(r.z, r.w));
+            x[i] = y0.x;
+            x[i + 1] = y0.y;
+            x[i + 2] = y1.x;
+            x[i + 3] = y1.y;
           }
-          if (ch == C::kChunks - 1) {  // the scores have been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_empty[t & 1]);
+          if (border) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[i] = (vis >> i) & 1 ? x[i] : -INFINITY;
           }
-          // weights, their sums, and their terms in the threads' rows of P
-          if (ch == 0) ok = __all_sync(0xffffffffu, ok && (t < C::kPBufs || wait_use(sh.p_empty, C::kPBufs, t - C::kPBufs)));
-          uint8_t* prow = base + C::kOffP + t % C::kPBufs * C::kP + (row >> 3) * 1024 + (row & 7) * 128;
-          auto put = [&](int term, int byte, const uint4& v) {  // 16 bytes of the term's columns from `byte` on
-            const int at = term * N * C::kColBytes + byte;
-            *reinterpret_cast<uint4*>(prow + at / 128 * C::kPBlock + ((((at % 128) >> 4) ^ (row & 7)) << 4)) = v;
-          };
+        };
+        auto weights = [&]() {
+#pragma unroll
+          for (int i = 0; i < W; ++i) x[i] = fast_exp2(x[i]);
+        };
+        // The weights are taken before it is known that no warp has a score past its
+        // reference by more than the margin; the rare block that has takes them again.
+        bool moves = true;
+        if (j > 0) {
+          scores(false);
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < W; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+          bool grows = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > static_cast<float>(C::kMargin);
+          if constexpr (CODES) grows = grows || static_cast<int>(ev) > e_ref;
+          grows = __any_sync(0xffffffffu, grows);
+          if (lane == 0) {
+            if (grows) *const_cast<volatile int*>(&sh.moved[wg][t & 1]) = t + 1;
+            mbar_arrive(&sh.vote[wg][t & 1]);
+          }
+          weights();
+          if (!wait_warp(sh.vote[wg], 2, t)) break;
+          moves = *const_cast<volatile int*>(&sh.moved[wg][t & 1]) == t + 1;
+        } else if (lane == 0) {
+          mbar_arrive(&sh.vote[wg][t & 1]);
+        }
+        if (moves) {
+          scores(true);
+          const float top = over_lanes<W>(x, lane, [](float u, float v) { return fmaxf(u, v); });
+          if (lane < W) sh.part[wg][quarter][lane] = top;
           if constexpr (CODES) {
-            const float up = pow2_int(static_cast<int>(ev) - e_ref[ch] + C::kLift);
+            const int e = __reduce_max_sync(0xffffffffu, static_cast<int>(ev));
+            if (lane == 0) sh.part_e[wg][quarter] = e;
+          }
+          if (!sync_warpgroup()) break;
+          const float was = j > 0 ? -sh.neg_ref[c0 + c] : -kNone;
+          const float now = fmaxf(was, fmaxf(fmaxf(sh.part[wg][0][c], sh.part[wg][1][c]), fmaxf(sh.part[wg][2][c], sh.part[wg][3][c])));
+          int e_now = e_ref;
+          if constexpr (CODES)
+            e_now = max(e_now, max(max(sh.part_e[wg][0], sh.part_e[wg][1]), max(sh.part_e[wg][2], sh.part_e[wg][3])));
+          const float fl = exp2f(was - now), fo = CODES ? fl * pow2_int(e_ref - e_now) : fl;
+          e_ref = e_now;
+          if (!sync_warpgroup()) break;
+          if (quarter == 0 && lane < W) sh.neg_ref[c0 + c] = -now;
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < W; i += 2)
+              l[i / 2] = mul2(l[i / 2], make_float2(__shfl_sync(0xffffffffu, fl, i), __shfl_sync(0xffffffffu, fl, i + 1)));
+            // O holds every product up to the block before once that is done
+            if (!wait_warp(sh.p_empty, C::kPBufs, t - 1)) break;
+            tc_fence_after();
 #pragma unroll
             for (int i0 = 0; i0 < W; i0 += 16) {
-              uint32_t w[3][4];
+              float o[16];
+              tmem_ld_cols<16>(o_at + i0, o);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t two[3][2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int i = i0 + 4 * k + 2 * h;
-                  const float2 e = make_float2(fast_exp2(x[i]), fast_exp2(x[i + 1]));
-                  l[(ch * W + i) / 2] = add2(l[(ch * W + i) / 2], e);
-                  float2 v = mul2(e, make_float2(up, up));
-                  const float2 minus = make_float2(-1.f, -1.f);
-#pragma unroll
-                  for (int term = 0; term < 3; ++term) {
-                    // the leading three bits; what is left, exactly
-                    const float2 top = term == 2 ? v
-                                                 : make_float2(__uint_as_float(__float_as_uint(v.x) & 0xffe00000u),
-                                                               __uint_as_float(__float_as_uint(v.y) & 0xffe00000u));
-                    two[term][h] = e5m2x2(top.x, top.y);
-                    if (term < 2) v = fma2(top, minus, v);
-                  }
-                }
-#pragma unroll
-                for (int term = 0; term < 3; ++term) w[term][k] = two[term][0] | two[term][1] << 16;
-              }
-#pragma unroll
-              for (int term = 0; term < 3; ++term)
-                put(term, c0 + i0, make_uint4(w[term][0], w[term][1], w[term][2], w[term][3]));
-            }
-          } else {
-#pragma unroll
-            for (int i0 = 0; i0 < W; i0 += 8) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int i = i0 + 2 * k;
-                const float2 e = make_float2(fast_exp2(x[i]), fast_exp2(x[i + 1]));
-                l[(ch * W + i) / 2] = add2(l[(ch * W + i) / 2], e);
-                if constexpr (C::kTerms == 1) {
-                  hi[k] = pack_bf16(e.x, e.y);
-                } else {
-                  // the high term cut off, not rounded, and the low one not 0 beside it: an
-                  // infinite value times both is that infinity, not a NaN
-                  const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
-                  hi[k] = __byte_perm(ux, uy, 0x7632);
-                  const float2 h = make_float2(__uint_as_float(ux & 0xffff0000u), __uint_as_float(uy & 0xffff0000u));
-                  const float2 rest = fma2(h, make_float2(-1.f, -1.f), e), least = mul2(h, make_float2(0x1p-30f, 0x1p-30f));
-                  lo[k] = pack_bf16(fmaxf(rest.x, least.x), fmaxf(rest.y, least.y));
-                }
-              }
-              put(0, 2 * (c0 + i0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-              if constexpr (C::kTerms == 2) put(1, 2 * (c0 + i0), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+              for (int i = 0; i < 16; ++i) o[i] *= __shfl_sync(0xffffffffu, fo, i0 + i);
+              tmem_st_cols<16>(o_at + i0, o);
             }
           }
+          if (!sync_warpgroup()) break;
+          scores(false);
+          weights();
         }
-        if (lost) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_empty[t & 1]);  // the scores have been read
+        // the weights' sums, and their terms in the threads' rows of P
+        if (t >= C::kPBufs && !wait_warp(sh.p_empty, C::kPBufs, t - C::kPBufs)) break;
+        uint8_t* prow = base + C::kOffP + t % C::kPBufs * C::kP + (row >> 3) * 1024 + (row & 7) * 128;
+        auto put = [&](int term, int byte, const uint4& v) {  // 16 bytes of the term's columns from `byte` on
+          const int at = term * C::kTermBytes + byte;
+          *reinterpret_cast<uint4*>(prow + at / 128 * C::kPBlock + ((((at % 128) >> 4) ^ (row & 7)) << 4)) = v;
+        };
+#pragma unroll
+        for (int i = 0; i < W; i += 2) l[i / 2] = add2(l[i / 2], make_float2(x[i], x[i + 1]));
+        if constexpr (CODES) {
+          const float up = pow2_int(static_cast<int>(ev) - e_ref + C::kLift);
+#pragma unroll
+          for (int i0 = 0; i0 < W; i0 += 16) {
+            uint32_t w[3][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t two[3][2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int i = i0 + 4 * k + 2 * h;
+                float2 v = mul2(make_float2(x[i], x[i + 1]), make_float2(up, up));
+#pragma unroll
+                for (int term = 0; term < 3; ++term) {
+                  // the leading three bits; what is left, exactly
+                  const float2 top = term == 2 ? v
+                                               : make_float2(__uint_as_float(__float_as_uint(v.x) & 0xffe00000u),
+                                                             __uint_as_float(__float_as_uint(v.y) & 0xffe00000u));
+                  two[term][h] = e5m2x2(top.x, top.y);
+                  if (term < 2) v = fma2(top, make_float2(-1.f, -1.f), v);
+                }
+              }
+#pragma unroll
+              for (int term = 0; term < 3; ++term) w[term][k] = two[term][0] | two[term][1] << 16;
+            }
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+              put(term, c0 + i0, make_uint4(w[term][0], w[term][1], w[term][2], w[term][3]));
+          }
+        } else {
+#pragma unroll
+          for (int i0 = 0; i0 < W; i0 += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 e = make_float2(x[i0 + 2 * k], x[i0 + 2 * k + 1]);
+              if constexpr (C::kTerms == 1) {
+                hi[k] = pack_bf16(e.x, e.y);
+              } else {
+                // the high term cut off, not rounded, and the low one not 0 beside it: an
+                // infinite value times both is that infinity, not a NaN
+                const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
+                hi[k] = __byte_perm(ux, uy, 0x7632);
+                const float2 h = make_float2(__uint_as_float(ux & 0xffff0000u), __uint_as_float(uy & 0xffff0000u));
+                const float2 rest = fma2(h, make_float2(-1.f, -1.f), e), least = mul2(h, make_float2(0x1p-30f, 0x1p-30f));
+                lo[k] = pack_bf16(fmaxf(rest.x, least.x), fmaxf(rest.y, least.y));
+              }
+            }
+            put(0, 2 * (c0 + i0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            if constexpr (C::kTerms == 2) put(1, 2 * (c0 + i0), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          }
+        }
         // Value rows past the sequence's end (the tail of the last page, pages not loaded) are
         // zeroed: what their slots hold must not reach O as 0 * NaN.
-        if (wg == 0 && key0 + kBlk > p.len) {
-          ok = __all_sync(0xffffffffu, ok && wait_use(sh.v_full, C::kDepth, t));
-          if (key >= p.len) {
+        if (wg == 0 && (p.blk0 + j + 1) * kBlk > p.len) {
+          if (!wait_warp(sh.v_full, C::kDepth, t)) break;
+          if ((p.blk0 + j) * kBlk + row >= p.len) {
             uint8_t* v = base + C::kOffV + t % C::kDepth * C::kSlot + row * 128;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -937,55 +921,46 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[t % C::kPBufs]);
       }
-      if (lost) break;
+      if (j < blks) break;  // a wait has failed
       // ---- the piece's rows: the sums over the keys, then O, column by column
-      ok = __all_sync(0xffffffffu, ok && wait_use(sh.p_empty, C::kPBufs, t - 1));
-      if (any_of_warpgroup(!ok, bar)) break;
+      float x[W];
+#pragma unroll
+      for (int i = 0; i < W; i += 2) {
+        x[i] = l[i / 2].x;
+        x[i + 1] = l[i / 2].y;
+      }
+      const float of_warp = over_lanes<W>(x, lane, [](float u, float v) { return u + v; });
+      if (lane < W) sh.sums[wg][quarter][lane] = of_warp;
+      if (!sync_warpgroup() || !wait_warp(sh.p_empty, C::kPBufs, t - 1)) break;
       tc_fence_after();
-      const size_t part0 = p.slot < 0 ? 0 : (static_cast<size_t>(blockIdx.x) * 2 + p.slot) * N;
+      const float sum = (sh.sums[wg][0][c] + sh.sums[wg][1][c]) + (sh.sums[wg][2][c] + sh.sums[wg][3][c]);
+      const float ref = -sh.neg_ref[c0 + c];
+      // no key seen (scores that are all NaN move no reference either)
+      const bool none = ref == -kNone && sum == 0.f;
+      tmem_ld_cols<W>(o_at, x);
+      if (p.slot < 0) {
+        const float f = none ? 0.f : (CODES ? 1.f / static_cast<float>(1 << C::kLift) : 1.f) / sum;
+        const float f2 = CODES ? pow2_int(e_ref - 127) : 1.f;
 #pragma unroll
-      for (int ch = 0; ch < C::kChunks; ++ch) {
-        const int c0 = col0 + ch * W, c = lane % W;
-        float x[W];
+        for (int i = 0; i < W; ++i) {
+          const int r = __shfl_sync(0xffffffffu, c_row, i);
+          const float fi = __shfl_sync(0xffffffffu, f, i);
+          if (r >= 0) a.out[static_cast<size_t>(r) * 128 + row] = __float2bfloat16(fi == 0.f ? 0.f : x[i] * fi * f2);
+        }
+        if (quarter == 0 && lane < W && c_there && a.lse != nullptr)
+          a.lse[c_row] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      } else {
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + p.slot) * N + c0;
+        const uint32_t there = __ballot_sync(0xffffffffu, c_there);
 #pragma unroll
-        for (int i = 0; i < W; i += 2) {
-          x[i] = l[ch * W / 2 + i / 2].x;
-          x[i + 1] = l[ch * W / 2 + i / 2].y;
-        }
-        const float sum_w = over_lanes<W>(x, lane, [](float u, float v) { return u + v; });
-        sync_warpgroup(bar);  // the parts before have been read
-        if (lane < W) sh.part[wg][quarter][lane] = sum_w;
-        sync_warpgroup(bar);
-        const float sum = (sh.part[wg][0][c] + sh.part[wg][1][c]) + (sh.part[wg][2][c] + sh.part[wg][3][c]);
-        const float ref = -sh.neg_ref[c0 + c];
-        const bool none = ref == -kNone && sum == 0.f;  // no key seen (scores that are all NaN move no reference either)
-        const float f = none ? 0.f : CODES ? 0x1p-14f / sum : 1.f / sum;
-        const float f2 = CODES ? pow2_int(e_ref[ch] - 127) : 1.f;
-        tmem_ld_cols<W>(tmem + 2 * N + c0, x);
-        if (p.slot < 0) {
-          for_columns(c0, [&](int i, bool there, size_t r) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            if (there) a.out[r * 128 + row] = __float2bfloat16(fi == 0.f ? 0.f : x[i] * fi * f2);
-          });
-        } else {
-          for_columns(c0, [&](int i, bool there, size_t) {
-            if (there) a.part_o[(part0 + c0 + i) * 128 + row] = x[i];
-          });
-        }
-        if (quarter == 0) {
-          for_columns(c0, [&](int i, bool there, size_t r) {
-            if (lane != i || !there) return;
-            if (p.slot >= 0)
-              a.part_st[part0 + c0 + i] = none ? PartStat{-INFINITY, -INFINITY, 0.f, 0.f}
-                                               : PartStat{CODES ? ref + static_cast<float>(e_ref[ch] - 127 - C::kLift) : ref, ref, sum, 0.f};
-            else if (a.lse != nullptr)
-              a.lse[r] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-          });
-        }
+        for (int i = 0; i < W; ++i)
+          if ((there >> i) & 1) a.part_o[(part + i) * 128 + row] = x[i];
+        if (quarter == 0 && lane < W && c_there)
+          a.part_st[part + lane] = none ? PartStat{-INFINITY, -INFINITY, 0.f, 0.f}
+                                        : PartStat{CODES ? ref + static_cast<float>(e_ref - 127 - C::kLift) : ref, ref, sum, 0.f};
       }
       tc_fence_before();
       done_piece();
@@ -1020,7 +995,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(TreeAttnArgs
       if (lane == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
       continue;
     }
-    const long long u = first + (static_cast<long long>(h / G) * tiles + node / a.tile_tokens) * blks;
+    const long long u = first + (static_cast<long long>(h / G) * tiles + node / a.tile_tokens) * (blks + kBegin) + kBegin;
     const int w0 = static_cast<int>(u / chunk), parts = static_cast<int>((u + blks - 1) / chunk) - w0 + 1;
     if (parts == 1) continue;  // written by its only CTA
     const int col = node % a.tile_tokens * G + h % G;
@@ -1093,6 +1068,7 @@ cudaError_t launch_tree_attention(const TreeAttnArgs& a, const CUtensorMap& tmK,
     case 16: e = go(std::integral_constant<int, 16>{}); break;
     case 32: e = go(std::integral_constant<int, 32>{}); break;
     case 64: e = go(std::integral_constant<int, 64>{}); break;
+    case 96: e = go(std::integral_constant<int, 96>{}); break;
     default: e = go(std::integral_constant<int, 128>{}); break;
   }
   if (e != cudaSuccess || a.direct) return e;
