@@ -75,7 +75,13 @@ struct Cfg {
   static constexpr uint32_t kOffQ = kOffV + kDepth * kSlot;
   static constexpr uint32_t kOffP = kOffQ + kQ;
   static constexpr uint32_t kOffStats = kOffP + kPBufs * kP;
-  static constexpr int kTmem = N == 16 ? 64 : N == 32 ? 128 : N == 64 ? 256 : 512;  // columns: two S, one O
+  // The terms of a weight as columns of one product, with sums of their own, where that makes
+  // it no wider than an instruction (which takes at least 46 clocks, as for 32 columns); else
+  // one after the other into the same sums.
+  static constexpr bool kWide = N <= 64;
+  static constexpr int kOCols = kWide ? kTerms * N : N;
+  static constexpr int kTmemUsed = 2 * N + kOCols;  // two S, one O
+  static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static constexpr int kMargin = CODES ? 2 : 8;  // a score may pass the reference by, base 2
   static constexpr int kLift = 13;               // of codes' weights
 };
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       const uint64_t v = dv + ((t % C::kDepth * C::kSlot) >> 4), w = dp + ((t % C::kPBufs * C::kP) >> 4);
       const uint32_t d = tmem + 2 * N;
 #pragma unroll
-      for (int term = 0; term < C::kTerms; ++term) {
+      for (int term = 0; term < (C::kWide ? 1 : C::kTerms); ++term) {
         constexpr int kKeys = CODES ? 32 : 16;  // an instruction's
         const int at = term * C::kTermBytes, off = at / 128 * C::kPBlock + at % 128;
 #pragma unroll
@@ -566,9 +572,9 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           const uint64_t av = v + ((kk * kKeys * 128) >> 4), bp = w + ((off + kk * kKeys * 128) >> 4);
           const uint32_t acc = !first || term + kk != 0;
           if constexpr (CODES)
-            umma_f8(d, av, bp, idesc_f8(N, true) | kAlongM | kAlongN, acc);
+            umma_f8(d, av, bp, idesc_f8(C::kOCols, true) | kAlongM | kAlongN, acc);
           else
-            umma_bf16(d, av, bp, umma_idesc_bf16_f32(128, N) | kAlongM | kAlongN, acc);
+            umma_bf16(d, av, bp, umma_idesc_bf16_f32(128, C::kOCols) | kAlongM | kAlongN, acc);
         }
       }
     };
@@ -708,16 +714,16 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       // codes: this thread's key's powers, read a block ahead, its page's id two
       auto page_id = [&](int j) {
         const int key = (p.blk0 + j) * kBlk + row;
-        const int page = j < blks && key < p.len ? a.c.table[static_cast<size_t>(p.b) * a.c.max_pages + key / kPage] : -1;
-        return page < a.c.num_pages ? page : -1;
+        return j < blks && key < p.len ? a.c.table[static_cast<size_t>(p.b) * a.c.max_pages + key / kPage] : -1;
       };
       int page1 = -1;
-      uint32_t e1 = 0;  // the key's power, the value's << 8
-      auto read_powers = [&](int page) {
-        e1 = 0;
-        if (page < 0) return;
+      uint32_t ek1 = 0, ev1 = 0;
+      auto read_powers = [&](int page) {  // nothing here waits for what it reads
+        ek1 = ev1 = 0;
+        if (page < 0 || page >= a.c.num_pages) return;
         const size_t at = static_cast<size_t>(page * a.c.hkv + p.g) * kPage + row % kPage;
-        e1 = a.c.k_scale[at] | static_cast<uint32_t>(a.c.v_scale[at]) << 8;
+        ek1 = a.c.k_scale[at];
+        ev1 = a.c.v_scale[at];
       };
       if constexpr (CODES) {
         read_powers(page_id(0));
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       int j = 0;
 #pragma unroll 1
       for (; j < blks; ++j, ++t) {
-        const uint32_t ek = e1 & 255u, ev = e1 >> 8;
+        const uint32_t ek = ek1, ev = ev1;
         if constexpr (CODES) {
           read_powers(page1);
           page1 = page_id(j + 2);
@@ -739,14 +745,18 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           if (key >= p.len) vis = 0;
           if (key < p.len && in_tree >= 0) {
             const uint32_t* word = a.mask + static_cast<size_t>(p.lo + p.tok0) * a.words + in_tree / 32;
-            const int left = p.n - p.tok0;
+            const int left = p.n - p.tok0, words = a.words;
             vis = 0;
-#pragma unroll 4
-            for (int node = c0 / G; node * G < c0 + W; ++node) {
-              const uint32_t m = node < left ? word[static_cast<size_t>(node) * a.words] : 0u;
-              const int from = max(node * G - c0, 0), to = min(node * G + G - c0, W);
-              const uint32_t cols = (to == 32 ? 0u : 1u << to) - (1u << from);
-              if ((m >> (in_tree % 32)) & 1) vis |= cols;
+            for (int node0 = c0 / G; node0 * G < c0 + W; node0 += 8) {
+              uint32_t m[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) m[i] = node0 + i < left ? word[(node0 + i) * words] : 0u;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int from = max((node0 + i) * G - c0, 0), to = min((node0 + i + 1) * G - c0, W);
+                const uint32_t cols = (to >= 32 ? 0u : 1u << to) - (1u << (from & 31));
+                if (from < to && ((m[i] >> (in_tree % 32)) & 1)) vis |= cols;
+              }
             }
           }
         }
@@ -830,13 +840,16 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
             // O holds every product up to the block before once that is done
             if (!wait_warp(sh.p_empty, C::kPBufs, t - 1)) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int i0 = 0; i0 < W; i0 += 16) {
-              float o[16];
-              tmem_ld_cols<16>(o_at + i0, o);
+#pragma unroll 1
+              for (int at = 0; at < C::kOCols; at += N) {
+                float o[16];
+                tmem_ld_cols<16>(o_at + at + i0, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= __shfl_sync(0xffffffffu, fo, i0 + i);
-              tmem_st_cols<16>(o_at + i0, o);
+                for (int i = 0; i < 16; ++i) o[i] *= __shfl_sync(0xffffffffu, fo, i0 + i);
+                tmem_st_cols<16>(o_at + at + i0, o);
+              }
             }
           }
           if (!sync_warpgroup()) break;
@@ -862,23 +875,24 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
             uint32_t w[3][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+              // an fp16's upper byte is an e5m2, cut off; what is left is exact in fp16
               uint32_t two[3][2];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int i = i0 + 4 * k + 2 * h;
-                float2 v = mul2(make_float2(x[i], x[i + 1]), make_float2(up, up));
+                const float2 v = mul2(make_float2(x[i], x[i + 1]), make_float2(up, up));
+                __half2 rest = __floats2half2_rn(v.x, v.y);
 #pragma unroll
                 for (int term = 0; term < 3; ++term) {
-                  // the leading three bits; what is left, exactly
-                  const float2 top = term == 2 ? v
-                                               : make_float2(__uint_as_float(__float_as_uint(v.x) & 0xffe00000u),
-                                                             __uint_as_float(__float_as_uint(v.y) & 0xffe00000u));
-                  two[term][h] = e5m2x2(top.x, top.y);
-                  if (term < 2) v = fma2(top, make_float2(-1.f, -1.f), v);
+                  uint32_t& u = two[term][h];
+                  u = *reinterpret_cast<const uint32_t*>(&rest);
+                  if (term == 2) u += 0x00800080u;  // the last one is rounded
+                  u &= 0xff00ff00u;
+                  if (term < 2) rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&u));
                 }
               }
 #pragma unroll
-              for (int term = 0; term < 3; ++term) w[term][k] = two[term][0] | two[term][1] << 16;
+              for (int term = 0; term < 3; ++term) w[term][k] = __byte_perm(two[term][0], two[term][1], 0x7531);
             }
 #pragma unroll
             for (int term = 0; term < 3; ++term)
@@ -940,27 +954,38 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       const float ref = -sh.neg_ref[c0 + c];
       // no key seen (scores that are all NaN move no reference either)
       const bool none = ref == -kNone && sum == 0.f;
-      tmem_ld_cols<W>(o_at, x);
-      if (p.slot < 0) {
-        const float f = none ? 0.f : (CODES ? 1.f / static_cast<float>(1 << C::kLift) : 1.f) / sum;
-        const float f2 = CODES ? pow2_int(e_ref - 127) : 1.f;
+      const float f = none ? 0.f : (CODES ? 1.f / static_cast<float>(1 << C::kLift) : 1.f) / sum;
+      const float f2 = CODES ? pow2_int(e_ref - 127) : 1.f;
+      const int slot = p.slot;
+      const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * N + c0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < W; i0 += 16) {  // 16 columns at a time: the code runs once a piece, and is fetched for it
+        float o[16];
+        tmem_ld_cols<16>(o_at + i0, o);
+#pragma unroll 1
+        for (int at = N; at < C::kOCols; at += N) {
+          float more[16];
+          tmem_ld_cols<16>(o_at + at + i0, more);
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const int r = __shfl_sync(0xffffffffu, c_row, i);
-          const float fi = __shfl_sync(0xffffffffu, f, i);
-          if (r >= 0) a.out[static_cast<size_t>(r) * 128 + row] = __float2bfloat16(fi == 0.f ? 0.f : x[i] * fi * f2);
+          for (int i = 0; i < 16; ++i) o[i] += more[i];
         }
-        if (quarter == 0 && lane < W && c_there && a.lse != nullptr)
-          a.lse[c_row] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-      } else {
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + p.slot) * N + c0;
-        const uint32_t there = __ballot_sync(0xffffffffu, c_there);
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-          if ((there >> i) & 1) a.part_o[(part + i) * 128 + row] = x[i];
-        if (quarter == 0 && lane < W && c_there)
+        for (int i = 0; i < 16; ++i) {
+          const int r = __shfl_sync(0xffffffffu, c_row, i0 + i);
+          const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
+          if (r < 0) continue;
+          if (slot < 0)
+            a.out[static_cast<size_t>(r) * 128 + row] = __float2bfloat16(fi == 0.f ? 0.f : o[i] * fi * f2);
+          else
+            a.part_o[(part + i0 + i) * 128 + row] = o[i];
+        }
+      }
+      if (quarter == 0 && lane < W && c_there) {
+        if (slot >= 0)
           a.part_st[part + lane] = none ? PartStat{-INFINITY, -INFINITY, 0.f, 0.f}
                                         : PartStat{CODES ? ref + static_cast<float>(e_ref - 127 - C::kLift) : ref, ref, sum, 0.f};
+        else if (a.lse != nullptr)
+          a.lse[c_row] = none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       }
       tc_fence_before();
       done_piece();
