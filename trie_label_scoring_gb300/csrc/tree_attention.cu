@@ -96,11 +96,16 @@ struct Piece {
 
 template <int N, bool CODES>
 struct Shared {
-  float neg_ref[N];    // minus the reference maxima
+  float neg_ref[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kCols];  // minus the reference maxima, every warp's own copy
   float row_factor[N]; // codes: score factor times the query row's power of two
-  float part[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kCols];  // maxima of a warp's keys
-  float sums[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kCols];
-  int part_e[Cfg<N, CODES>::kWgs][4];
+  // maxima or sums of a warp's keys, in turn by the warpgroup's barriers: what was written
+  // before one is read before the next, and written over behind that
+  float part[Cfg<N, CODES>::kWgs][2][4][Cfg<N, CODES>::kCols];
+  int part_e[Cfg<N, CODES>::kWgs][2][4];
+  struct {
+    int row;  // of the result, -1: none
+    float factor;
+  } last[Cfg<N, CODES>::kWgs][4][Cfg<N, CODES>::kCols];
   int moved[Cfg<N, CODES>::kWgs][2];  // block, plus one, for which a warp asks to move the reference
   Piece piece[kPieces];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
@@ -633,6 +638,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       if (lane == 0) mbar_arrive(&sh.wg_sync[wg]);
       return wait_warp(&sh.wg_sync[wg], 1, syncs++);
     };
+    float* neg_ref = sh.neg_ref[wg][quarter];
     int t = 0;
     while (piece_there()) {
       const Piece& p = sh.piece[piece_no % kPieces];  // until done_piece
@@ -770,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           tmem_ld_cols<W>(s_at, x);
 #pragma unroll
           for (int i = 0; i < W; i += 4) {
-            const float4 r = plain ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(&sh.neg_ref[c0 + i]);
+            const float4 r = plain ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(&neg_ref[i]);
             float2 f0 = make_float2(a.scale_log2, a.scale_log2), f1 = f0;
             if constexpr (CODES) {
               const float4 f = *reinterpret_cast<const float4*>(&sh.row_factor[c0 + i]);
@@ -786,6 +792,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
             x[i + 3] = y1.y;
           }
           if (border) {
+            asm volatile("");  // a branch, not 32 selections in every block
 #pragma unroll
             for (int i = 0; i < W; ++i) x[i] = (vis >> i) & 1 ? x[i] : -INFINITY;
           }
@@ -801,7 +808,11 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           scores(false);
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 4; i < W; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+          for (int i = 4; i + 8 <= W; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[i + k]), x[i + k + 4]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[W - 4 + k]);
           bool grows = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > static_cast<float>(C::kMargin);
           if constexpr (CODES) grows = grows || static_cast<int>(ev) > e_ref;
           grows = __any_sync(0xffffffffu, grows);
@@ -818,21 +829,26 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
         if (moves) {
           scores(true);
           const float top = over_lanes<W>(x, lane, [](float u, float v) { return fmaxf(u, v); });
-          if (lane < W) sh.part[wg][quarter][lane] = top;
+          const int turn = syncs & 1;
+          if (lane < W) sh.part[wg][turn][quarter][lane] = top;
           if constexpr (CODES) {
             const int e = __reduce_max_sync(0xffffffffu, static_cast<int>(ev));
-            if (lane == 0) sh.part_e[wg][quarter] = e;
+            if (lane == 0) sh.part_e[wg][turn][quarter] = e;
           }
           if (!sync_warpgroup()) break;
-          const float was = j > 0 ? -sh.neg_ref[c0 + c] : -kNone;
-          const float now = fmaxf(was, fmaxf(fmaxf(sh.part[wg][0][c], sh.part[wg][1][c]), fmaxf(sh.part[wg][2][c], sh.part[wg][3][c])));
+          const auto& of = sh.part[wg][turn];
+          const float was = j > 0 ? -neg_ref[c] : -kNone;
+          const float now = fmaxf(was, fmaxf(fmaxf(of[0][c], of[1][c]), fmaxf(of[2][c], of[3][c])));
           int e_now = e_ref;
-          if constexpr (CODES)
-            e_now = max(e_now, max(max(sh.part_e[wg][0], sh.part_e[wg][1]), max(sh.part_e[wg][2], sh.part_e[wg][3])));
+          if constexpr (CODES) {
+            const int* e = sh.part_e[wg][turn];
+            e_now = max(e_now, max(max(e[0], e[1]), max(e[2], e[3])));
+          }
           const float fl = exp2f(was - now), fo = CODES ? fl * pow2_int(e_ref - e_now) : fl;
           e_ref = e_now;
-          if (!sync_warpgroup()) break;
-          if (quarter == 0 && lane < W) sh.neg_ref[c0 + c] = -now;
+          __syncwarp();
+          if (lane < W) neg_ref[lane] = -now;
+          __syncwarp();
           if (j > 0) {
 #pragma unroll
             for (int i = 0; i < W; i += 2)
@@ -852,7 +868,6 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
               }
             }
           }
-          if (!sync_warpgroup()) break;
           scores(false);
           weights();
         }
@@ -886,9 +901,12 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
                 for (int term = 0; term < 3; ++term) {
                   uint32_t& u = two[term][h];
                   u = *reinterpret_cast<const uint32_t*>(&rest);
-                  if (term == 2) u += 0x00800080u;  // the last one is rounded
-                  u &= 0xff00ff00u;
-                  if (term < 2) rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&u));
+                  if (term == 2) {
+                    u += 0x00800080u;  // the last one is rounded
+                  } else {
+                    u &= 0xff00ff00u;
+                    rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&u));
+                  }
                 }
               }
 #pragma unroll
@@ -947,17 +965,28 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
         x[i + 1] = l[i / 2].y;
       }
       const float of_warp = over_lanes<W>(x, lane, [](float u, float v) { return u + v; });
-      if (lane < W) sh.sums[wg][quarter][lane] = of_warp;
-      if (!sync_warpgroup() || !wait_warp(sh.p_empty, C::kPBufs, t - 1)) break;
-      tc_fence_after();
-      const float sum = (sh.sums[wg][0][c] + sh.sums[wg][1][c]) + (sh.sums[wg][2][c] + sh.sums[wg][3][c]);
-      const float ref = -sh.neg_ref[c0 + c];
+      const int turn = syncs & 1;
+      if (lane < W) sh.part[wg][turn][quarter][lane] = of_warp;
+      if (!sync_warpgroup()) break;
+      const auto& of = sh.part[wg][turn];
+      const float sum = (of[0][c] + of[1][c]) + (of[2][c] + of[3][c]);
+      const float ref = -neg_ref[c];
       // no key seen (scores that are all NaN move no reference either)
       const bool none = ref == -kNone && sum == 0.f;
-      const float f = none ? 0.f : (CODES ? 1.f / static_cast<float>(1 << C::kLift) : 1.f) / sum;
-      const float f2 = CODES ? pow2_int(e_ref - 127) : 1.f;
       const int slot = p.slot;
       const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * N + c0;
+      // every column's row and factor, for all lanes
+      auto* last = sh.last[wg][quarter];
+      if (lane < W) {
+        last[lane].row = c_row;
+        last[lane].factor = none ? 0.f : (CODES ? 1.f / static_cast<float>(1 << C::kLift) : 1.f) / sum;
+      }
+      const float f2 = CODES ? pow2_int(e_ref - 127) : 1.f;
+      __syncwarp();
+      if (!wait_warp(sh.p_empty, C::kPBufs, t - 1)) break;
+      tc_fence_after();
+      bf16* out = a.out + row;
+      float* out_part = a.part_o + part * 128 + row;
 #pragma unroll 1
       for (int i0 = 0; i0 < W; i0 += 16) {  // 16 columns at a time: the code runs once a piece, and is fetched for it
         float o[16];
@@ -969,15 +998,17 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] += more[i];
         }
+        if (slot < 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = __shfl_sync(0xffffffffu, c_row, i0 + i);
-          const float fi = __shfl_sync(0xffffffffu, f, i0 + i);
-          if (r < 0) continue;
-          if (slot < 0)
-            a.out[static_cast<size_t>(r) * 128 + row] = __float2bfloat16(fi == 0.f ? 0.f : o[i] * fi * f2);
-          else
-            a.part_o[(part + i0 + i) * 128 + row] = o[i];
+          for (int i = 0; i < 16; ++i) {
+            const int r = last[i0 + i].row;
+            const float fi = last[i0 + i].factor;
+            if (r >= 0) out[static_cast<size_t>(r) * 128] = __float2bfloat16(fi == 0.f ? 0.f : o[i] * fi * f2);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (last[i0 + i].row >= 0) out_part[(i0 + i) * 128] = o[i];
         }
       }
       if (quarter == 0 && lane < W && c_there) {
