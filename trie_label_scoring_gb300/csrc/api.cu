@@ -2433,7 +2433,7 @@ static size_t plan_attention_tree(uint8_t* base, const quail_cache_desc* c, int 
   if (t.direct) t.ctas = static_cast<int>(std::max(1L, std::min<long>(sms, items)));
   Carver k{base};
   if (!t.direct) {
-    t.plan = k.take<long long>(static_cast<size_t>(c->num_seqs) + 3);
+    t.shared_items = k.take<SharedItem>(sms);
     t.part_o = k.take<float>(static_cast<size_t>(sms) * 2 * t.tile_cols * 128);
     t.part_st = k.take<PartStat>(static_cast<size_t>(sms) * 2 * t.tile_cols);
   }

@@ -21,7 +21,7 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // after this kernel's own grid_dependency_wait, so everything before this
 // kernel is complete when the next one starts, and the next one need wait
 // only before it reads this kernel's outputs. Only kernels that hold no
-// tensor memory call it.
+// tensor memory, or whose next kernel takes none, call it.
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

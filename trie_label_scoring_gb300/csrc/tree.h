@@ -56,6 +56,12 @@ struct AcceptArgs {
 };
 cudaError_t launch_tree_accept(const AcceptArgs& a, const LayerPools& pools, int num_sms, cudaStream_t st);
 
+struct SharedItem {
+  int row0, tokens;  // first node's row, nodes
+  int g;             // KV head
+  int parts;         // CTAs that have one, this and those after it; 0: no item
+};
+
 struct TreeAttnArgs {
   CacheView c;
   int hq;
@@ -74,9 +80,9 @@ struct TreeAttnArgs {
   int tile_tokens;  // nodes of a tile, tile_cols / (hq / hkv)
   int ctas;
   bool direct;  // whole (sequence, head, tile) items by turns; else equal runs of the work list
-  // of the runs: plan [0] blocks of a run, [2 + b] first block of sequence b; two parts of a
-  // CTA, of tile_cols rows of 128 each: what it began of an item and left, what it went on with
-  long long* plan;
+  // of the runs: the item that each CTA begins and leaves; two parts of a CTA, of tile_cols
+  // rows of 128 each: what it did of that item, and what it did of one begun before it
+  SharedItem* shared_items;
   float* part_o;
   PartStat* part_st;
 };

@@ -60,7 +60,7 @@ struct Cfg {
   static constexpr int kTerms = CODES ? 3 : N > 64 ? 1 : 2;  // of a weight
   static constexpr uint32_t kRow = CODES ? 128 : 256;  // bytes of a key
   static constexpr uint32_t kSlot = kBlk * kRow;
-  static constexpr int kDepth = CODES ? 4 : 2;   // blocks of K, and of V, in flight or at work
+  static constexpr int kDepth = !CODES ? 2 : N == 96 ? 3 : 4;   // blocks of K, and of V, in flight or at work
   static constexpr uint32_t kHalf = CODES ? 0 : kBlk * 128;  // bf16: 64 dims of a block's rows
   static constexpr uint32_t kQ = N * 256;        // two halves of bf16, or two terms of codes
   // P: rows of 128 bytes by key, in blocks of 128 keys; the terms side by side in a block's
@@ -70,7 +70,7 @@ struct Cfg {
   static constexpr int kPBlock = kBlk * 128;
   static constexpr int kPBlocks = (kTermBytes * kTerms + 127) / 128;
   static constexpr uint32_t kP = kPBlocks * kPBlock;
-  static constexpr int kPBufs = N == 128 || (N == 96 && CODES) ? 1 : 2;
+  static constexpr int kPBufs = N == 128 ? 1 : 2;
   static constexpr uint32_t kOffV = kDepth * kSlot;
   static constexpr uint32_t kOffQ = kOffV + kDepth * kSlot;
   static constexpr uint32_t kOffP = kOffQ + kQ;
@@ -82,8 +82,8 @@ struct Cfg {
   static constexpr int kOCols = kWide ? kTerms * N : N;
   static constexpr int kTmemUsed = 2 * N + kOCols;  // two S, one O
   static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static constexpr int kMargin = CODES ? 2 : 8;  // a score may pass the reference by, base 2
-  static constexpr int kLift = 13;               // of codes' weights
+  static constexpr int kMargin = CODES ? 4 : 8;  // a score may pass the reference by, base 2
+  static constexpr int kLift = 11;               // of codes' weights
 };
 
 struct Piece {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
   fence_proxy_async_smem();
 
   // ---- the plan: thread i counts the blocks of its own run of sequences
-  long long u0 = 0, count = 0;  // this CTA's run of the work list
+  long long chunk = 0, u0 = 0, count = 0;  // blocks of a run; this CTA's
   int b_at = 0, x_at = 0, j_at = 0;
   if (!a.direct) {
     long long* scan = reinterpret_cast<long long*>(base + C::kOffP);  // kThreads + 1 of them
@@ -333,16 +333,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
     scan[threadIdx.x + 1] = x + before;
     __syncthreads();
     const long long units = scan[C::kThreads];
-    const long long chunk = max(1LL, (units + gridDim.x - 1) / gridDim.x);
-    if (blockIdx.x == 0) {
-      long long at = scan[threadIdx.x];
-      for (int b = b0; b < b1; ++b) {
-        a.plan[2 + b] = at;
-        int items;
-        at += units_of(a, b, &items);
-      }
-      if (threadIdx.x == 0) a.plan[0] = chunk;
-    }
+    chunk = max(1LL, (units + gridDim.x - 1) / gridDim.x);
     u0 = blockIdx.x * chunk;
     count = max(0LL, min(units, u0 + chunk) - u0);
     if (warp == 2 && count > 0) {  // where the run begins
@@ -370,6 +361,9 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
     }
   }
   __syncthreads();
+  // the join, which takes no tensor memory, may come up beside this kernel's CTAs; it waits
+  // for their end
+  if (!a.direct) grid_launch_dependents();
 
   // ---- a role's way along the pieces
   int piece_no = 0;
@@ -452,6 +446,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       }
     } else {
       long long left = count;
+      SharedItem begun{0, 0, 0, 0};  // the item that this CTA begins and leaves
       for (int b = b_at, x = x_at, j = j_at; ok && left > 0; ++b, x = 0) {
         // the next sequence with keys and nodes, 32 looked at at a time
         for (; b < a.c.num_seqs; b += 32) {
@@ -477,9 +472,13 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           p.blks = max(0, j + units - kBegin) - p.blk0;
           p.slot = p.blks == blks ? -1 : p.blk0 > 0 ? 1 : 0;
           if (p.blks > 0) publish(p);
+          if (p.blks > 0 && p.slot == 0)
+            begun = SharedItem{s.lo + p.tok0, min(a.tile_tokens, s.n - p.tok0), p.g,
+                               1 + static_cast<int>((blks - p.blk0 - p.blks + chunk - 1) / chunk)};
           left -= units;
         }
       }
+      if (lane == 0) a.shared_items[blockIdx.x] = begun;
     }
     p.blks = -1;
     if (ok) publish(p);
@@ -1033,63 +1032,64 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// A row whose item several CTAs shared: the first's part (slot 0 of its two), then the
-// others' (slot 1), brought to one maximum. A warp a row, 4 dims a lane.
+// Rows whose item several CTAs shared: the part of the one that began it (slot 0 of its
+// two), then those of the CTAs after it (slot 1), brought to one maximum. A block for 8
+// columns of a CTA's item, a warp a row, 4 dims a lane; most find that their CTA left
+// none. And the rows of sequences without keys, which are in no CTA's work.
 constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(TreeAttnArgs a) {
   grid_dependency_wait();
-  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Seq s = seq_of(a, b);
-  if (!s.ok) return;
-  const int G = a.hq / a.c.hkv, tiles = (s.n + a.tile_tokens - 1) / a.tile_tokens, blks = blocks_of(s.len);
-  const long long chunk = s.len > 0 ? a.plan[0] : 1, first = s.len > 0 ? a.plan[2 + b] : 0;
-  for (int r = blockIdx.y * kJoinWarps + warp; r < s.n * a.hq; r += gridDim.y * kJoinWarps) {
-    const int node = r / a.hq, h = r % a.hq;
-    const size_t row = static_cast<size_t>(s.lo + node) * a.hq + h;
-    if (s.len == 0) {
-      *reinterpret_cast<uint2*>(a.out + row * 128 + 4 * lane) = make_uint2(0u, 0u);
-      if (lane == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
-      continue;
-    }
-    const long long u = first + (static_cast<long long>(h / G) * tiles + node / a.tile_tokens) * (blks + kBegin) + kBegin;
-    const int w0 = static_cast<int>(u / chunk), parts = static_cast<int>((u + blks - 1) / chunk) - w0 + 1;
-    if (parts == 1) continue;  // written by its only CTA
-    const int col = node % a.tile_tokens * G + h % G;
-    auto at = [&](int i) { return (static_cast<size_t>(w0 + i) * 2 + (i > 0)) * a.tile_cols + col; };
-    PartStat st{-INFINITY, -INFINITY, 0.f, 0.f};
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto pow2_or_0 = [](float x, float ref) { return x == -INFINITY ? 0.f : exp2f(x - ref); };
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      const int n = min(32, parts - i0);
-      const PartStat mine = lane < n ? a.part_st[at(i0 + lane)] : PartStat{-INFINITY, -INFINITY, 0.f, 0.f};
-      float mo = fmaxf(mine.m_o, st.m_o), ml = fmaxf(mine.m_l, st.m_l);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, d));
-        ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, d));
-      }
-      const float f = pow2_or_0(mine.m_o, mo), was = pow2_or_0(st.m_o, mo);
-      float l = mine.l != mine.l ? mine.l : mine.l * pow2_or_0(mine.m_l, ml);  // a NaN sum stays one
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
-      st.l = (st.l != st.l ? st.l : st.l * pow2_or_0(st.m_l, ml)) + l;
-      st.m_l = ml;
-      st.m_o = mo;
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(i0 + i) * 128 + 4 * lane);
-        const float w = __shfl_sync(0xffffffffu, f, i);
-        acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.hq / a.c.hkv;
+  if (blockIdx.y == 0) {
+    for (int b0 = 32 * (blockIdx.x * kJoinWarps + warp); b0 < a.c.num_seqs; b0 += 32 * kJoinWarps * gridDim.x) {
+      const Seq mine = b0 + lane < a.c.num_seqs ? seq_of(a, b0 + lane) : Seq{0, 0, 0, false};
+      for (uint32_t empty = __ballot_sync(0xffffffffu, mine.ok && mine.len == 0 && mine.n > 0); empty != 0; empty &= empty - 1) {
+        const int from = __ffs(empty) - 1;
+        const size_t row0 = static_cast<size_t>(__shfl_sync(0xffffffffu, mine.lo, from)) * a.hq;
+        const int rows = __shfl_sync(0xffffffffu, mine.n, from) * a.hq;
+        for (int i = lane; i < rows * 16; i += 32) reinterpret_cast<uint4*>(a.out + row0 * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = lane; a.lse != nullptr && i < rows; i += 32) a.lse[row0 + i] = -INFINITY;
       }
     }
-    const bool none = st.m_l == -INFINITY && st.l == 0.f;
-    const float f = none ? 0.f : st.l != st.l ? st.l : exp2f(st.m_o - st.m_l) / st.l;
-    if (none) acc = make_float4(0.f, 0.f, 0.f, 0.f);  // whatever weights of 0 made of the values
-    *reinterpret_cast<uint2*>(a.out + row * 128 + 4 * lane) =
-        make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
-    if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : (st.m_l + log2f(st.l)) * 0.6931471805599453f;
   }
+  const SharedItem it = a.shared_items[blockIdx.x];
+  const int col = blockIdx.y * kJoinWarps + warp;
+  if (it.parts < 2 || col >= it.tokens * G) return;
+  const size_t row = static_cast<size_t>(it.row0 + col / G) * a.hq + it.g * G + col % G;
+  auto at = [&](int i) { return (static_cast<size_t>(blockIdx.x + i) * 2 + (i > 0)) * a.tile_cols + col; };
+  PartStat st{-INFINITY, -INFINITY, 0.f, 0.f};
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto pow2_or_0 = [](float x, float ref) { return x == -INFINITY ? 0.f : exp2f(x - ref); };
+  for (int i0 = 0; i0 < it.parts; i0 += 32) {
+    const int n = min(32, it.parts - i0);
+    const PartStat mine = lane < n ? a.part_st[at(i0 + lane)] : PartStat{-INFINITY, -INFINITY, 0.f, 0.f};
+    float mo = fmaxf(mine.m_o, st.m_o), ml = fmaxf(mine.m_l, st.m_l);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, d));
+      ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, d));
+    }
+    const float f = pow2_or_0(mine.m_o, mo), was = pow2_or_0(st.m_o, mo);
+    float l = mine.l != mine.l ? mine.l : mine.l * pow2_or_0(mine.m_l, ml);  // a NaN sum stays one
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
+    st.l = (st.l != st.l ? st.l : st.l * pow2_or_0(st.m_l, ml)) + l;
+    st.m_l = ml;
+    st.m_o = mo;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(i0 + i) * 128 + 4 * lane);
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+    }
+  }
+  const bool none = st.m_l == -INFINITY && st.l == 0.f;
+  const float f = none ? 0.f : st.l != st.l ? st.l : exp2f(st.m_o - st.m_l) / st.l;
+  if (none) acc = make_float4(0.f, 0.f, 0.f, 0.f);  // whatever weights of 0 made of the values
+  *reinterpret_cast<uint2*>(a.out + row * 128 + 4 * lane) =
+      make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : (st.m_l + log2f(st.l)) * 0.6931471805599453f;
 }
 
 template <int N, bool CODES>
@@ -1128,11 +1128,8 @@ cudaError_t launch_tree_attention(const TreeAttnArgs& a, const CUtensorMap& tmK,
     default: e = go(std::integral_constant<int, 128>{}); break;
   }
   if (e != cudaSuccess || a.direct) return e;
-  // a few rows a warp
-  const long long rows = static_cast<long long>(a.max_q) * a.hq;
-  const int slices = static_cast<int>(std::max(1LL, std::min(1024LL, (rows + kJoinWarps - 1) / kJoinWarps)));
   count_launch();
-  return launch_pdl(tree_join_kernel, dim3(a.c.num_seqs, slices), dim3(32 * kJoinWarps), 0, st, a);
+  return launch_pdl(tree_join_kernel, dim3(a.ctas, a.tile_cols / kJoinWarps), dim3(32 * kJoinWarps), 0, st, a);
 }
 
 // Test hook: this translation unit's copy of the pipeline wait limit.
