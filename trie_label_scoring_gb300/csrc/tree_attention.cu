@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr int kCols = N < 32 ? N : 32;  // columns of a softmax warpgroup
   static constexpr int kWgs = N / kCols;
   static constexpr int kThreads = 128 + 128 * kWgs;
-  static constexpr int kTerms = CODES ? 3 : N > 64 ? 1 : 2;  // of a weight
+  static constexpr int kTerms = CODES ? 3 : N > 32 ? 1 : 2;  // of a weight
   static constexpr uint32_t kRow = CODES ? 128 : 256;  // bytes of a key
   static constexpr uint32_t kSlot = kBlk * kRow;
   static constexpr int kDepth = !CODES ? 2 : N == 96 ? 3 : 4;   // blocks of K, and of V, in flight or at work
@@ -111,7 +111,7 @@ struct Shared {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t k_full[Cfg<N, CODES>::kDepth], k_empty[Cfg<N, CODES>::kDepth];
   uint64_t v_full[Cfg<N, CODES>::kDepth], v_empty[Cfg<N, CODES>::kDepth];
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], p_empty[2], drain;
   uint64_t vote[Cfg<N, CODES>::kWgs][2], wg_sync[Cfg<N, CODES>::kWgs];
   uint32_t tmem;
   int abort_flag;
@@ -286,7 +286,6 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
     mbar_init(&sh.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.s_full[s], 1 + (limit_clk < 0));
-      mbar_init(&sh.s_empty[s], 4 * C::kWgs);
       mbar_init(&sh.p_full[s], 4 * C::kWgs);
       mbar_init(&sh.p_empty[s], 1);
     }
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
       if (p.blks == 0) continue;
       if (lane == 0) {
         auto scores = [&](int j) {
-          ok = wait_use(sh.k_full, C::kDepth, t + j) && (t + j < 2 || wait_use(sh.s_empty, 2, t + j - 2));
+          ok = wait_use(sh.k_full, C::kDepth, t + j);
           if (!ok) return;
           tc_fence_after();
           issue_s(t + j);
@@ -870,11 +869,9 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           scores(false);
           weights();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.s_empty[t & 1]);  // the scores have been read
-        // the weights' sums, and their terms in the threads' rows of P
-        if (t >= C::kPBufs && !wait_warp(sh.p_empty, C::kPBufs, t - C::kPBufs)) break;
+        // The weights' sums, and their terms in the threads' rows of P. Where there are two of
+        // it, the product of two blocks ago has read this one: it was issued before these scores.
+        if (C::kPBufs == 1 && t >= 1 && !wait_warp(sh.p_empty, 1, t - 1)) break;
         uint8_t* prow = base + C::kOffP + t % C::kPBufs * C::kP + (row >> 3) * 1024 + (row & 7) * 128;
         auto put = [&](int term, int byte, const uint4& v) {  // 16 bytes of the term's columns from `byte` on
           const int at = term * C::kTermBytes + byte;
@@ -952,7 +949,10 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           }
         }
         fence_proxy_async_smem();
+        tc_fence_before();
         __syncwarp();
+        // P is there, and the scores have been read: two blocks on they are written over, behind
+        // the product that waits for this
         if (lane == 0) mbar_arrive(&sh.p_full[t % C::kPBufs]);
       }
       if (j < blks) break;  // a wait has failed
