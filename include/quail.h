@@ -367,7 +367,12 @@ size_t quail_workspace_size_attention_tree(const quail_cache_desc* cache, int32_
  *              key gets o = 0 and lse = -inf.
  *   scale:     0: 1/sqrt(128)
  *   lse:       device fp32 [total_q, n_q_heads] (natural logarithm), or NULL
- * Errors, statistics and non-finite values as quail_attention_shared's. */
+ * Sums and softmax statistics are fp32. For the product with V a weight is two bf16 terms
+ * over bf16 pages, one where a sequence has more than 32 rows of nodes and heads to a KV
+ * head; over e4m3 pages it is three e5m2 terms, 9 bits, lost below 2^-28 of the largest
+ * weight times the largest power of two of a value row, and a query element is two terms,
+ * exact down to 2^-17 of the row's largest. Non-finite values and errors as
+ * quail_attention_shared's. */
 quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, const int32_t* q_offsets,
                                   const int32_t* seq_len, const void* mask, int32_t total_q, int32_t max_q_len,
                                   int32_t max_seq_len, int32_t n_q_heads, float scale, void* workspace,
@@ -379,9 +384,10 @@ quail_status quail_attention_tree(const quail_cache_desc* cache, const void* q, 
  * path. Their K and V rows move to the tree's first slots, in every cache, so that the
  * sequence is new_len tokens long and goes on from there (quail_cache_resize gives the
  * pages behind it back).
- *   caches:   host array of n_caches caches, one per layer of a model, alike but for their
- *             pools; may be empty (the verdict only). Pages that two sequences share are
- *             not among a tree's.
+ *   caches:   host array of n_caches caches, one per layer of a model (at most
+ *             QUAIL_MAX_LAYERS), alike but for their pools, which are all different; may be
+ *             empty (the verdict only). Pages that two sequences share are not among a
+ *             tree's.
  *   parent, q_offsets, seq_len, max_q_len, total: as quail_tree_plan's; mask: as it wrote it
  *   draft:    device int32 [total], the nodes' tokens
  *   taken:    device int32 [total], the token that the model takes after each node

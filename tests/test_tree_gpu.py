@@ -678,6 +678,50 @@ def test_attention_reports_bad_indices(n, what):
     status()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("limit", [-1, 200])
+@pytest.mark.parametrize("n,hq,hkv,lens", [(3, 8, 2, [40, 300]), (8, 8, 2, [700] * 3), (16, 32, 8, [3000] * 24),
+                                           (24, 32, 8, [2000] * 9), (3, 128, 1, [5000] * 2), (100, 16, 4, [2500] * 5)])
+def test_waits_that_run_out_are_reported(kind, limit, n, hq, hkv, lens):
+    """Every width of tile, whole items and runs: a wait that gives up is reported and ends the call; the next one is right."""
+    import trie_label_scoring_gb300 as Q
+    pool = Pool(kind, hkv, lens)
+    pool.fill(lens)
+    rng = np.random.RandomState(1)
+    seen = [ancestors(random_parents(rng, n)) for _ in lens]
+    offs = [n * b for b in range(len(lens) + 1)]
+    q = torch.randn((offs[-1], hq, D), device="cuda").bfloat16()
+    attend(pool, q, offs, lens, seen)
+    Q._test_set_pipeline_wait_limit(limit)
+    try:
+        # 200 cycles are not sure to run out, below 0 is
+        try:
+            attend(pool, q, offs, lens, seen)
+            gave_up = False
+        except Q.QuailError as e:
+            assert e.name == "QUAIL_ERR_DEVICE_TIMEOUT"
+            gave_up = True
+    finally:
+        Q._test_set_pipeline_wait_limit(0)
+    assert gave_up or limit > 0
+    check_attention(pool, q, offs, lens, seen)
+
+
+def test_two_ways_of_carrying_out_a_call_agree():
+    """Bounds far above the lengths take a call from whole items to runs of the work list: the same results."""
+    rng = np.random.RandomState(5)
+    n, lens = [9, 0, 30, 1], [500, 0, 260, 0]
+    seen = [ancestors(random_parents(rng, k)) if k else np.zeros((0, 0), dtype=bool) for k in n]
+    for kind in ("bf16", "e4m3"):
+        pool = Pool(kind, 2, lens, extra_pages=4000)
+        pool.fill(lens)
+        offs = [0] + list(np.cumsum(n))
+        q = torch.randn((offs[-1], 8, D), device="cuda").bfloat16()
+        check_attention(pool, q, offs, lens, seen)
+        check_attention(pool, q, offs, lens, seen, slack=60000)
+        check_attention(pool, q, offs, lens, seen, slack=60000, more=500)
+
+
 # ------------------------------------------------------------------ the verdict
 def verdict(parent, draft, taken):
     node, path = 0, [0] if parent else []

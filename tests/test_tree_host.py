@@ -160,6 +160,21 @@ def test_accept_refusals(kw):
     refused(accept([desc()], **kw), "QUAIL_ERR_INVALID_ARG")
 
 
+@pytest.mark.parametrize("pools", [dict(k_pool=0x1000, v_pool=0x8000), dict(k_pool=0x8000, v_pool=0x2000),
+                                   dict(k_pool=0x2000, v_pool=0x8000), dict(k_pool=0x8000, v_pool=0x1000),
+                                   dict(k_pool=0x8000, v_pool=0x8000)])
+def test_accept_refuses_a_pool_that_is_there_twice(pools):
+    refused(accept([desc(), desc(**pools)]), "QUAIL_ERR_INVALID_ARG")
+
+
+def test_accept_refuses_too_many_layers():
+    refused(accept([desc()], n=1025), "QUAIL_ERR_UNSUPPORTED_SHAPE")
+
+
+def test_resize_refuses_a_cache_without_sequences():
+    refused(resize(desc(num_seqs=0)), "QUAIL_ERR_INVALID_ARG")
+
+
 @pytest.mark.parametrize("other", [dict(n_kv_heads=4), dict(num_pages=9), dict(page_table=0x3010), dict(max_pages=5),
                                    dict(num_seqs=2), dict(dtype=Q.DTYPE_E4M3, k_scale=0x4000, v_scale=0x4100)])
 def test_accept_refuses_caches_that_differ(other):

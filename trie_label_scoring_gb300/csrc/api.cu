@@ -2342,6 +2342,7 @@ quail_status quail_cache_resize(const quail_cache_desc* cache, const int32_t* pr
   if ((prefix_len > 0) != (prefix_pages != nullptr))
     return fail(QUAIL_ERR_INVALID_ARG, "prefix_pages and prefix_len go together");
   if (cache->max_pages > (1 << 26)) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "max_pages must be at most 2^26");
+  if (cache->num_seqs == 0) return fail(QUAIL_ERR_INVALID_ARG, "the cache has no sequences");
   if (max_tokens < 0 || (token_seq == nullptr) != (token_pos == nullptr) || (token_seq == nullptr && max_tokens != 0))
     return fail(QUAIL_ERR_INVALID_ARG, "token_seq, token_pos and max_tokens go together");
   if (old_len == nullptr || new_len == nullptr || free_ring == nullptr || free_state == nullptr || granted_len == nullptr ||
@@ -2425,7 +2426,7 @@ static size_t plan_attention_tree(uint8_t* base, const quail_cache_desc* c, int 
   // The narrowest tile that holds a sequence's rows. More than 96 rows: tiles of 96 or of 128,
   // whichever cost less; one of 128 takes 1.3 times as long as one of 96 (codes 1.5).
   t.tile_cols = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
-  if (rows > 96 && G <= 96) {
+  if (rows > 96 && G <= 96 && a != nullptr) {  // a smaller call may take 128 where this one does not
     const auto tiles = [&](int cols) { return (max_q + cols / G - 1) / (cols / G); };
     if (tiles(96) <= (c->dtype == QUAIL_DTYPE_E4M3 ? 1.5 : 1.3) * tiles(128)) t.tile_cols = 96;
   }
@@ -2514,6 +2515,7 @@ quail_status quail_tree_accept(const quail_cache_desc* caches, int32_t n_caches,
   quail_status s = open_trees(parent, q_offsets, seq_len, num_seqs, total, max_q_len, &a.t);
   if (s != QUAIL_OK) return s;
   if (n_caches < 0 || (n_caches > 0 && caches == nullptr)) return fail(QUAIL_ERR_INVALID_ARG, "caches is null, or n_caches < 0");
+  if (n_caches > QUAIL_MAX_LAYERS) return fail(QUAIL_ERR_UNSUPPORTED_SHAPE, "at most %d caches", QUAIL_MAX_LAYERS);
   for (int i = 0; i < n_caches; ++i) {
     const quail_cache_desc &c = caches[i], &f = caches[0];
     s = check_cache_shape(&c);
@@ -2522,6 +2524,10 @@ quail_status quail_tree_accept(const quail_cache_desc* caches, int32_t n_caches,
     if (c.dtype != f.dtype || c.n_kv_heads != f.n_kv_heads || c.num_pages != f.num_pages || c.page_table != f.page_table ||
         c.max_pages != f.max_pages)
       return fail(QUAIL_ERR_INVALID_ARG, "cache %d is not like the first", i);
+    // a pool that is there twice would have its rows moved twice
+    for (int j = 0; j <= i; ++j)
+      if (c.k_pool == caches[j].v_pool || (j < i && (c.k_pool == caches[j].k_pool || c.v_pool == caches[j].v_pool || c.v_pool == caches[j].k_pool)))
+        return fail(QUAIL_ERR_INVALID_ARG, "cache %d has a pool that is among the others", i);
   }
   if (num_seqs == 0) return QUAIL_OK;
   if (accepted == nullptr || new_len == nullptr || bonus == nullptr ||

@@ -140,7 +140,7 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs& a, int b) {
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBlk - 1) / kBlk; }
 // Units of a sequence in the work list, and its (head, row tile) items: an item is kBegin
 // units, what it costs to begin and end it, and then its blocks.
-constexpr int kBegin = 2;
+constexpr int kBegin = 3;
 __device__ __forceinline__ long long units_of(const TreeAttnArgs& a, int b, int* items) {
   const Seq s = b < a.c.num_seqs ? seq_of(a, b) : Seq{0, 0, 0, false};
   *items = s.ok ? (s.n + a.tile_tokens - 1) / a.tile_tokens * a.c.hkv : 0;
