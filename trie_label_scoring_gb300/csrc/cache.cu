@@ -30,8 +30,11 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kRowLanes = 8;
-// Rotary layouts: rotate-half over the whole head, over its first dims, neighbouring pairs.
-enum { kRopeHalf, kRopeHalfPart, kRopeInterleaved };
+// Rotary layouts: rotate-half over the whole head by the token's position (quail_cache_append),
+// and, by a position of its own and with a magnitude: over the whole head, over its first
+// dims, neighbouring pairs. (One form for the first two cost the first 0.7%.)
+enum { kRopeHalf, kRopeHalfAt, kRopeHalfPart, kRopeInterleaved };
+__host__ __device__ constexpr bool whole_half(int layout) { return layout == kRopeHalf || layout == kRopeHalfAt; }
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
@@ -184,7 +187,9 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 // as above, over the whole head or its first dims (the partners are then two runs of one
 // lane again, and dims past them pass, times their gains alone, so that an infinity beside
 // them stays there); interleaved, pairs (2j, 2j + 1) within a run. The angle may go by a
-// position of its own, so a drafted token's slot need not be its position.
+// position of its own, so a drafted token's slot need not be its position. 23,100 tokens,
+// bf16 and e4m3 cache: whole head 106 and 102 us, its first 64 dims 112 and 108 (lanes whose
+// dims pass have rows of a line cut in two), interleaved 103 and 98.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendGroups = kAppendThreads / kRowLanes;
 
@@ -198,8 +203,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
   const int l = threadIdx.x % kRowLanes, heads = a.hq + 2 * a.c.hkv;
   const Chunks ch2 = lane_chunks<LAYOUT>(l, a.rotary);
   // whether the lane's runs turn; the layouts that turn part of a head have lanes that do not
-  const bool turns0 = LAYOUT == kRopeHalf || (LAYOUT == kRopeHalfPart ? l < a.rotary / 16 : 8 * l < a.rotary);
-  const bool turns1 = LAYOUT == kRopeHalf || (LAYOUT == kRopeHalfPart ? turns0 : 64 + 8 * l < a.rotary);
+  const bool turns0 = whole_half(LAYOUT) || (LAYOUT == kRopeHalfPart ? l < a.rotary / 16 : 8 * l < a.rotary);
+  const bool turns1 = whole_half(LAYOUT) || (LAYOUT == kRopeHalfPart ? turns0 : 64 + 8 * l < a.rotary);
   const int rows = min(TOK, a.num_tokens - t0) * heads;
   int r = threadIdx.x / kRowLanes, tok = r / heads, h = r - tok * heads;
   const T* qkv = static_cast<const T*>(a.qkv);
@@ -209,9 +214,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
     const int i = threadIdx.x / 64, j = threadIdx.x % 64, t = t0 + i;
     const int seq = t < a.num_tokens ? a.seq[t] : -1;
     const int pos = seq >= 0 ? a.pos[t] : 0;
-    const int at = seq >= 0 && a.rope_pos != nullptr ? a.rope_pos[t] : pos;  // where the angle is taken
+    const int at = LAYOUT != kRopeHalf && seq >= 0 && a.rope_pos != nullptr ? a.rope_pos[t] : pos;  // where the angle is taken
     if (j == 0) {
-      const bool far = a.rope_pos != nullptr && (at < 0 || at >= 1 << 24);
+      const bool far = LAYOUT != kRopeHalf && a.rope_pos != nullptr && (at < 0 || at >= 1 << 24);
       if (far) raise_device_error(a.c.err, QUAIL_ERR_DEVICE_BOUNDS, t);
       s_page[i] = seq < 0 || far ? -1 : page_of(a.c, seq, pos, t);
       s_slot[i] = pos % kPage;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       turned = j < a.rotary / 2;
     }
     if (turned) cos_sin(at, rt.w[j], c, sn);
-    if (LAYOUT != kRopeHalf || a.magnitude != 1.f) {
+    if constexpr (LAYOUT != kRopeHalf) {
       c *= turned ? a.magnitude : 1.f;
       sn *= a.magnitude;
     }
@@ -568,7 +573,7 @@ cudaError_t launch_cache_append_rope(AppendArgs a, const quail_rope_desc& d, boo
   };
   if (d.layout == QUAIL_ROPE_INTERLEAVED) return launch(std::integral_constant<int, kRopeInterleaved>{});
   if (d.rotary_dim < 128) return launch(std::integral_constant<int, kRopeHalfPart>{});
-  return launch(std::integral_constant<int, kRopeHalf>{});
+  return launch(std::integral_constant<int, kRopeHalfAt>{});
 }
 
 cudaError_t launch_cache_read(const CacheView& c, const int* seq, const int* pos, int num_tokens, bf16* k_out,
