@@ -32,7 +32,7 @@ constexpr int kPage = 16;
 constexpr int kRowLanes = 8;
 // Rotary layouts: rotate-half over the whole head by the token's position (quail_cache_append),
 // and, by a position of its own and with a magnitude: over the whole head, over its first
-// dims, neighbouring pairs. (One form for the first two cost the first 0.7%.)
+// dims, neighbouring pairs. (One form for the first two took the first 0.3% longer.)
 enum { kRopeHalf, kRopeHalfAt, kRopeHalfPart, kRopeInterleaved };
 __host__ __device__ constexpr bool whole_half(int layout) { return layout == kRopeHalf || layout == kRopeHalfAt; }
 

@@ -8,31 +8,48 @@
 // 16 to 128 of them, on tcgen05:
 //   S^T = K Q^T    M 128 keys, N query rows, K 128 dims
 //   O^T += V^T P^T M 128 dims, N query rows, K 128 keys
-// K and V pages go from memory to the products as they lie (V^T is V read along its rows:
-// the operand's major dimension is the dims). A thread of the softmax has one key and N
-// scores: a key's own factors are scalars of its thread, and no row waits for a shuffle.
-// The maximum of a query row would need one, over all 128 keys; so rows keep a reference
-// that moves only when some score passes it by a margin (an OR over the warpgroup, rarely
-// true after a piece's first block), and the sums of the weights stay in the threads until
-// the end. P^T is laid into shared memory key by key.
+// (an instruction takes 46 clocks up to 32 columns, 49 for 64, 57 for 96, 65 for 128,
+// whichever way its operands lie in shared memory). K and V pages go from memory to the
+// products as they lie: V^T is V read along its rows. A thread of the softmax has one key
+// and 32 scores: a key's own factors are scalars of its thread, and no row waits for a
+// shuffle. The maximum of a query row would need one, over all 128 keys; so rows keep a
+// reference that moves only when some score passes it by a margin (2^8, codes 2^4), and the
+// sums of the weights stay in the threads until the end. Whether one does is a vote of the
+// four warps that runs while they take the weights; the block that moves a reference (the
+// first of a piece, then one in thirty with codes) takes them again. P^T is laid into shared
+// memory key by key.
 //
 // Over an e4m3 cache the codes are operands as they are (kind::f8f6f4): no widening. A query
 // element, 8 significant bits, is an e4m3 and an e5m2 term exactly (down to 2^-17 of the
-// row's largest; below, off by up to 2^-21 of it); a weight, times its value row's power of two,
-// is cut into three e5m2 terms, 9 bits, which are products of their own into the same sums.
-// e5m2 because its exponents reach from 2^-16 to 2^15: weights are taken times 2^14, at
-// most 2^15, and terms are lost below 2^-30 of the largest weight times the largest power.
-// Over a bf16 cache a weight is two bf16 terms (one with 128 columns, where the products
-// are what counts).
+// row's largest; below, off by up to 2^-21 of it); a weight, times its value row's power of
+// two, is cut into three e5m2 terms, 9 bits. e5m2 because its exponents reach from 2^-16 to
+// 2^15: weights are taken times 2^11, at most 2^15, and lost below 2^-28 of the largest
+// weight times the largest power. The terms come out of an fp16's upper bytes: converting
+// fp32 to e5m2 three times took 238 us where this takes 202 (32 sequences of 24 nodes).
+// Over a bf16 cache a weight is two bf16 terms up to 32 columns (o's error is that of its
+// own rounding, 0.0017 relative) and one beyond (0.0023; two there cost 6 us of 65).
+// Up to 64 columns a weight's terms are columns of one product, with sums of their own.
 //
-// Work: blocks of 128 keys of every (sequence, KV head, row tile) in one list, cut into
-// equal runs, one per CTA, whatever the lengths are (or, where no sequence is long, whole
-// (sequence, head, tile) items in turn, so that nothing is left to join). The pieces of an
-// item that several CTAs share are joined by a second kernel.
+// Work: an item is a (sequence, KV head, row tile), its blocks 128 keys each. Where no
+// sequence is long the CTAs take whole items in turn, and nothing is left to join. Else the
+// blocks of all items, with three units ahead of each for what an item costs to begin and
+// end, are one list that is cut into equal runs, one per CTA, whatever the lengths are, and
+// the pieces of an item that several CTAs share are joined by a second kernel, which comes up
+// beside the last of these CTAs.
+//
+// What bounds it. 64 sequences of 1 to 12 nodes, 128 to 2,048 keys (32 heads on 8): 59 us,
+// 4.9 TB/s; a block takes 2,200 clocks where reading its 64 KB takes 2,900 at full rate, so
+// memory is what counts, and a piece another 5,000 to begin and end, in part hidden by the
+// pages that come in meanwhile. 16 sequences of 40 to 100 nodes, 1,024 to 4,096 keys: 94 us,
+// three or four tiles of 96 columns; 32 of 24 nodes over 7,000 to 8,192 codes: 167 us. There a
+// block takes 2,600 and 3,000 clocks, the softmax: three warps a scheduler issue 40 and 52%
+// of the time, each an instruction in 6 to 8 clocks (latency of dependent instructions); with
+// codes 520 instructions of a warp and block, 28% of them the terms, and the ALU pipe 40% busy.
 //
 // Roles: warp 0 and 3 load K and V pages (TMA, a page a lane), warp 1 issues the products,
 // warp 2 walks the work list, publishes its pieces and loads bf16 queries, warps 4.. are
-// the softmax: one warpgroup, from 64 columns on two with half the columns each.
+// the softmax, a warpgroup per 32 columns (a thread per key of a block, per dim of O). Its
+// barriers are mbarriers like all others here, so that a wait that gives up ends them all.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
