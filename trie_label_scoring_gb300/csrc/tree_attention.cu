@@ -8,7 +8,7 @@
 // 16 to 128 of them, on tcgen05:
 //   S^T = K Q^T    M 128 keys, N query rows, K 128 dims
 //   O^T += V^T P^T M 128 dims, N query rows, K 128 keys
-// (an instruction takes 46 clocks up to 32 columns, 49 for 64, 57 for 96, 65 for 128,
+// (an instruction takes 46 clocks up to 32 columns, 49 for 64, 65 for 128,
 // whichever way its operands lie in shared memory). K and V pages go from memory to the
 // products as they lie: V^T is V read along its rows. A thread of the softmax has one key
 // and 32 scores: a key's own factors are scalars of its thread, and no row waits for a
@@ -27,7 +27,8 @@
 // weight times the largest power. The terms come out of an fp16's upper bytes: converting
 // fp32 to e5m2 three times took 238 us where this takes 202 (32 sequences of 24 nodes).
 // Over a bf16 cache a weight is two bf16 terms up to 32 columns (o's error is that of its
-// own rounding, 0.0017 relative) and one beyond (0.0023; two there cost 6 us of 65).
+// own rounding, 0.0017 relative) and one beyond (0.0023; with two, and two barriers a block
+// more, the first case below took 65 us).
 // Up to 64 columns a weight's terms are columns of one product, with sums of their own.
 //
 // Work: an item is a (sequence, KV head, row tile), its blocks 128 keys each. Where no
@@ -349,7 +350,8 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
     scan[threadIdx.x + 1] = x + before;
     __syncthreads();
     const long long units = scan[C::kThreads];
-    chunk = max(1LL, (units + gridDim.x - 1) / gridDim.x);
+    // two at least: a part per block is more to join than it saves (5,205 keys of one head 15.1 us, 13.7)
+    chunk = max(2LL, (units + gridDim.x - 1) / gridDim.x);
     u0 = blockIdx.x * chunk;
     count = max(0LL, min(units, u0 + chunk) - u0);
     if (warp == 2 && count > 0) {  // where the run begins
