@@ -509,6 +509,27 @@ def test_any_mask_and_rows_that_see_nothing(kind, hq, hkv):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,slack", [(8, 2, 0), (16, 1, 0), (5, 5, 0), (8, 2, 200000), (32, 8, 200000)])
+def test_masks_of_large_trees_that_end_early(kind, hq, hkv, slack):
+    """Row tiles whose nodes see nothing behind some key, or nothing at all, or only the last; whole items and runs."""
+    rng = np.random.RandomState(11)
+    n, lens = [300, 300, 129, 700, 257], [300, 1500, 129, 701, 600]
+    seen = [np.tril(rng.random_sample((k, k)) < 0.2) for k in n]
+    seen[0][:, 40:] = False
+    seen[0][::7] = False
+    seen[1][:200] = False            # the keys before the tree only
+    seen[2][:] = False               # nothing
+    seen[3][5:9, 699] = True
+    seen[3][:, 650:] &= rng.random_sample((700, 50)) < 0.02
+    seen[4][:, 128:] = False
+    pool = Pool(kind, hkv, lens, extra_pages=slack // 16)
+    pool.fill(lens)
+    offs = [0] + list(np.cumsum(n))
+    q = torch.randn((offs[-1], hq, D), device="cuda").bfloat16()
+    check_attention(pool, q, offs, lens, seen, slack=slack)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n", [1, 6, 20, 60])
 @pytest.mark.parametrize("q_scale,scale", [(60.0, None), (1e-4, None), (1.0, 1.5), (3e4, 1e-6)])
 def test_attention_score_ranges(kind, n, q_scale, scale):

@@ -270,6 +270,25 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// Blocks up to the last one that some node of the row tile sees, one at least: in a tree
+// larger than a block, ancestors come first, so the tiles of its early nodes end early. By a
+// whole warp.
+__device__ __forceinline__ int blocks_seen(const TreeAttnArgs& a, const Seq& s, int tok0, int lane) {
+  if (s.n <= kBlk) return blocks_of(s.len);
+  const int used = (s.n + 31) / 32, words = min(a.tile_tokens, s.n - tok0) * used;
+  const uint32_t* rows = a.mask + static_cast<size_t>(s.lo + tok0) * a.words;
+  int top = -1;
+#pragma unroll 4
+  for (int i = lane; i < words; i += 32) {
+    const int w = i % used;
+    uint32_t m = rows[i / used * a.words + w];
+    if (w == used - 1 && s.n % 32 != 0) m &= (1u << (s.n % 32)) - 1;
+    if (m != 0) top = max(top, w);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  return max(1, blocks_of(min(s.len, s.len - s.n + 32 * (top + 1))));
+}
+
 // 2^e for any e, 0 and infinity past the ends.
 __device__ __forceinline__ float pow2_int(int e) {
   return e < -126 ? 0.f : e > 127 ? INFINITY : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
@@ -458,7 +477,7 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
         p.n = s.n;
         p.len = s.len;
         p.blk0 = 0;
-        p.blks = blocks_of(s.len);
+        p.blks = s.len > 0 ? blocks_seen(a, s, p.tok0, lane) : 0;
         p.slot = -1;
         publish(p);
       }
@@ -486,13 +505,14 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
           const int units = static_cast<int>(min(left, static_cast<long long>(blks + kBegin - j)));
           p.g = x / tiles;
           p.tok0 = x % tiles * a.tile_tokens;
+          const int seen = blocks_seen(a, s, p.tok0, lane);  // what lies behind is nobody's
           p.blk0 = max(0, j - kBegin);
-          p.blks = max(0, j + units - kBegin) - p.blk0;
-          p.slot = p.blks == blks ? -1 : p.blk0 > 0 ? 1 : 0;
+          p.blks = min(seen, max(0, j + units - kBegin)) - p.blk0;
+          p.slot = p.blks == seen ? -1 : p.blk0 > 0 ? 1 : 0;
           if (p.blks > 0) publish(p);
           if (p.blks > 0 && p.slot == 0)
             begun = SharedItem{s.lo + p.tok0, min(a.tile_tokens, s.n - p.tok0), p.g,
-                               1 + static_cast<int>((blks - p.blk0 - p.blks + chunk - 1) / chunk)};
+                               1 + static_cast<int>((seen - p.blks + chunk - 1) / chunk)};
           left -= units;
         }
       }
