@@ -489,6 +489,45 @@ def test_attention_of_trees(kind, hq, hkv, case):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [1, 3, 6, 7, 11, 17, 31, 33, 48, 63, 65, 96, 97, 100, 127])
+@pytest.mark.parametrize("slack", [0, 1 << 20])
+def test_groups_of_all_sizes(kind, group, slack):
+    """Heads to a KV head that divide no tile; bounds a thousand times the lengths."""
+    rng = np.random.RandomState(group)
+    n, lens = [1, 2, 0, 9, 14, 1], [130, 2, 0, 300, 14, 1]
+    seen = [ancestors(random_parents(rng, k, roots=0.2)) if k else np.zeros((0, 0), dtype=bool) for k in n]
+    pool = Pool(kind, 1, lens, extra_pages=slack // 16)
+    pool.fill(lens)
+    offs = [0] + list(np.cumsum(n))
+    q = torch.randn((offs[-1], group, D), device="cuda").bfloat16()
+    check_attention(pool, q, offs, lens, seen, slack=slack, more=group % 3 * 100)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_the_most_heads_and_nodes(kind):
+    """128 KV heads; a tree of 1,024 nodes; 3,000 sequences of a node."""
+    rng = np.random.RandomState(1)
+    for n, lens, hq, hkv in (([1024, 3], [1200, 3], 4, 1), ([5, 40], [200, 50], 128, 128), ([1] * 3000, [1 + i % 40 for i in range(3000)], 8, 2)):
+        seen = [ancestors(random_parents(rng, k)) for k in n]
+        pool = Pool(kind, hkv, lens)
+        pool.fill(lens[:40])
+        if len(lens) > 40:  # the same rows in every fortieth sequence
+            for i in range(40, len(lens)):
+                pool.table[i] = pool.table[i % 40]
+        offs = [0] + list(np.cumsum(n))
+        q = torch.randn((offs[-1], hq, D), device="cuda").bfloat16()
+        if len(lens) <= 40:
+            check_attention(pool, q, offs, lens, seen)
+        else:
+            out, lse = attend(pool, q, offs, lens, seen)
+            o, z, tol_o, tol_l = attention_64(pool, q[:400], offs[:401], lens[:400], seen[:400], D ** -0.5)
+            assert bool(((out[:400].double() - o).abs() <= tol_o).all())
+            q[2000:2040] = q[:40]
+            again, _ = attend(pool, q, offs, lens, seen)
+            assert torch.equal(again[2000:2040], again[:40]) and torch.equal(again[:40], out[:40])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (16, 1), (5, 5)])
 def test_any_mask_and_rows_that_see_nothing(kind, hq, hkv):
     """Masks that are no tree's; nodes that see no key: o = 0, lse = -inf, also beside others that do; no keys at all."""
