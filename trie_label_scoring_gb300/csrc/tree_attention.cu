@@ -235,6 +235,13 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[C]
   }
 }
 
+// `width` bits from bit `lo` on, as far as there are 32.
+__device__ __forceinline__ uint32_t bits_from(int lo, int width) {
+  uint32_t r;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(width));
+  return r;
+}
+
 // Column i of v over the warp's lanes, to lane i (mod C): each step halves the columns a
 // lane keeps and doubles the lanes that they stand for.
 template <int C, class Op>
@@ -794,11 +801,12 @@ __global__ void __launch_bounds__(Cfg<N, CODES>::kThreads, 1)
               uint32_t m[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) m[i] = node0 + i < left ? word[(node0 + i) * words] : 0u;
+              int from = node0 * G - c0;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int from = max((node0 + i) * G - c0, 0), to = min((node0 + i + 1) * G - c0, W);
-                const uint32_t cols = (to >= 32 ? 0u : 1u << to) - (1u << (from & 31));
-                if (from < to && ((m[i] >> (in_tree % 32)) & 1)) vis |= cols;
+              for (int i = 0; i < 8; ++i, from += G) {
+                const int lo = i == 0 ? max(from, 0) : from;
+                // its columns, where its bit is set
+                vis |= bits_from(lo, from + G - lo) & static_cast<uint32_t>(static_cast<int>(m[i] << (~in_tree & 31)) >> 31);
               }
             }
           }
