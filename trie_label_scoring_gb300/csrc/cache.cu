@@ -235,19 +235,25 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
       turned = j < a.rotary / 2;
     }
     if (turned) cos_sin(at, rt.w[j], c, sn);
-    if constexpr (LAYOUT != kRopeHalf) {
-      c *= turned ? a.magnitude : 1.f;
-      sn *= a.magnitude;
-    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const bf16* g = k == 0 ? a.gq : a.gk;
       const float g1 = g != nullptr ? __bfloat162float(g[d1]) : 1.f;
       const float g2 = g != nullptr ? __bfloat162float(g[d2]) : 1.f;
-      s_turn[i][k][0][j] = g1 * c;
-      s_turn[i][k][1][j] = -g2 * sn;
-      s_turn[i][k][2][j] = g2 * c;
-      s_turn[i][k][3][j] = g1 * sn;
+      if constexpr (LAYOUT == kRopeHalf) {
+        s_turn[i][k][0][j] = g1 * c;
+        s_turn[i][k][1][j] = -g2 * sn;
+        s_turn[i][k][2][j] = g2 * c;
+        s_turn[i][k][3][j] = g1 * sn;
+      } else {
+        // gain and magnitude in two floats, so that an entry is rounded once, as above
+        const float mag = turned ? a.magnitude : 1.f;
+        const float h1 = g1 * mag, l1 = fmaf(g1, mag, -h1), h2 = g2 * mag, l2 = fmaf(g2, mag, -h2);
+        s_turn[i][k][0][j] = fmaf(h1, c, l1 * c);
+        s_turn[i][k][1][j] = -fmaf(h2, sn, l2 * sn);
+        s_turn[i][k][2][j] = fmaf(h2, c, l2 * c);
+        s_turn[i][k][3][j] = fmaf(h1, sn, l1 * sn);
+      }
     }
   }
   __syncthreads();
